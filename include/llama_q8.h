@@ -447,6 +447,211 @@ llama_q8_status llama_q8_attention_decode_noalloc(const float* q, const float* k
                                                   int32_t n_head_kv, int32_t head_dim,
                                                   int32_t cache_stride, float* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Batched decoding over a paged KV cache. No counterpart on the pages (their
+ * forward has one sequence and a contiguous cache): the operators of a program
+ * that decodes several sequences, or several beams of one, and keeps their
+ * keys and values in pages that sequences can share.
+ *
+ * A step of such a program, every call on one stream:
+ *   projections -> llama_q8_rope_append -> llama_q8_attention_paged (each layer)
+ *   -> lm_head -> llama_q8_beam_select -> llama_q8_pages_fork
+ *
+ * Conventions, beside those of the device-level entry points above:
+ *   - A row is one token. pos[row] is its position in its sequence (pos < 0: a
+ *     padding row, for which nothing is read or written, except that attention
+ *     writes the result of an empty mask), seq[row] the sequence; with seq ==
+ *     NULL row r belongs to sequence r (then rows <= n_seq, else LQ8_ERR_ARG).
+ *   - table[n_seq][table_stride] holds the page of each block of `page`
+ *     positions of a sequence: position p is slot p % page of page
+ *     table[seq][p / page]; entries < 0 are holes.
+ *   - pos, seq, table and the other int32 arrays are device memory and not seen
+ *     by the host. `err` (device int32, zeroed by the caller) receives the
+ *     largest llama_q8_status of what a kernel found wrong in them and stays as
+ *     it is otherwise: LQ8_ERR_CTX for a position past the table, LQ8_ERR_ARG
+ *     for a sequence or page number out of range. Nothing is read or written out
+ *     of range for them: such an append is skipped, such a position is masked.
+ *   - Every call runs on the calling thread's current device, on which `stream`
+ *     and every device pointer live. The calls keep nothing between them but
+ *     what their arguments hold, and may be captured in CUDA graphs.
+ *   - A workspace has at least the bytes its query returns, is 16-byte aligned,
+ *     zeroed before its first use and left with zeroed counters by every call.
+ *     Calls that share one (or graphs that captured such calls) must not overlap
+ *     on the GPU.
+ * ------------------------------------------------------------------------- */
+#define LLAMA_Q8_GGUF_F32 0
+#define LLAMA_Q8_GGUF_F16 1
+#define LLAMA_Q8_GGUF_BF16 30
+
+/* A pool of pages in device memory: k and v, each
+ * [n_layer][n_pages][n_head_kv][page][head_dim] of `type`, 16-byte aligned,
+ * caller-owned. n_pages, n_layer, n_head_kv > 0 (LQ8_ERR_ARG); page a power of
+ * two in 8..256, head_dim 64 or 128, a type above (LQ8_ERR_UNSUPPORTED). The
+ * f32 values written to F16 / BF16 pages are rounded to nearest even. */
+typedef struct llama_q8_pages {
+    void* k;
+    void* v;
+    int32_t type;      /* LLAMA_Q8_GGUF_F32, _F16 or _BF16 */
+    int32_t n_layer;
+    int32_t n_pages;
+    int32_t page;      /* positions per page */
+    int32_t n_head_kv;
+    int32_t head_dim;
+} llama_q8_pages;
+
+/* Frequencies of the rotation, in radians per position, for the leading
+ * rot_dim values of a head: freq[i] = theta^(-2i/rot_dim), i < rot_dim / 2,
+ * scaled for contexts `factor` times as long as trained:
+ *   LQ8_ROPE_NONE    as they are (factor and the rest ignored)
+ *   LQ8_ROPE_LINEAR  freq / factor (position interpolation)
+ *   LQ8_ROPE_BASE    theta replaced by theta * factor^(rot_dim / (rot_dim - 2))
+ *   LQ8_ROPE_RAMP    by parts: with r = trained_ctx * freq / 2 pi rotations in
+ *                    the trained context, freq / factor where r <= low, freq
+ *                    where r >= high, and between them the mixture with weight
+ *                    (r - low) / (high - low) on freq
+ *   LQ8_ROPE_RAMP_M  the same, and *magnitude = 0.1 ln(factor) + 1
+ * freq: host double[rot_dim / 2]; *magnitude, the factor on cos and sin, is 1
+ * otherwise. rot_dim even and >= 2 (> 2 for BASE), theta > 0, factor >= 1,
+ * trained_ctx > 0 and 0 <= low < high for the ramps, all finite; else
+ * LQ8_ERR_ARG. Host arithmetic in double; no GPU is used. */
+#define LQ8_ROPE_NONE 0
+#define LQ8_ROPE_LINEAR 1
+#define LQ8_ROPE_BASE 2
+#define LQ8_ROPE_RAMP 3
+#define LQ8_ROPE_RAMP_M 4
+typedef struct llama_q8_rope_scaling {
+    int32_t kind;
+    int32_t trained_ctx;
+    double factor;
+    double low, high;
+} llama_q8_rope_scaling;
+llama_q8_status llama_q8_rope_frequencies(int32_t rot_dim, double theta, const llama_q8_rope_scaling* scaling,
+                                          double* freq, float* magnitude);
+
+/* The rotation of llama_q8_rope_append: the leading rot_dim values of every
+ * query and key head, the others unchanged. rot_dim a multiple of 8, at most
+ * head_dim (LQ8_ERR_UNSUPPORTED otherwise); style as llama_q8_config.rope_style:
+ * 0 pairs values 2i and 2i + 1, 1 (NEOX) values i and i + rot_dim / 2. */
+typedef struct llama_q8_rope {
+    const double* freq;  /* device [rot_dim / 2], radians per position */
+    int32_t rot_dim;
+    int32_t style;
+    float magnitude;     /* factor on cos and sin; finite */
+} llama_q8_rope;
+
+/* Rotary positions and KV append. qkv: f32 rows of [n_head query heads |
+ * n_head_kv key heads | n_head_kv value heads] * head_dim, the layout of the
+ * concatenated projection; row r starts at qkv + r * qkv_stride (floats, a
+ * multiple of 4). q_out[rows][n_head][head_dim] receives the rotated queries;
+ * the rotated keys and the values of row r go to its position's slot of layer
+ * `layer`. The angle pos * freq is reduced to one turn in double and its cosine
+ * and sine taken in f32, so far positions keep f32 accuracy. n_head %
+ * n_head_kv == 0. rows == 0 does nothing. Rows of one call name different
+ * (sequence, position) pairs; of rows that name the same one, each written
+ * value is one of theirs. A row whose sequence or position is out of range, or
+ * whose page is a hole or out of range, still gets its q_out (with the position
+ * it names); its append is skipped and reported in err (may be NULL). qkv, q_out
+ * 16-byte aligned. Enqueues one kernel. */
+llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer, const float* qkv,
+                                     int64_t qkv_stride, int32_t rows, const int32_t* pos, const int32_t* seq,
+                                     int32_t n_head, const llama_q8_rope* rope, const int32_t* table,
+                                     int32_t n_seq, int32_t table_stride, float* q_out, int32_t* err,
+                                     void* stream);
+
+/* Grouped-query attention of single tokens over the pages: row r attends to
+ * the positions max(0, pos - window + 1) .. pos of its sequence (window == 0:
+ * all of 0 .. pos), out = softmax(scale q k^T) v in one pass, query head h
+ * reading KV head h / (n_head / n_head_kv). scale == 0 means 1 /
+ * sqrt(head_dim). q, out [rows][n_head][head_dim] f32; lse[rows][n_head] (may
+ * be NULL) receives the natural log of the sum of the exponentials, so that
+ * results over parts of a cache can be joined. Positions in holes or in pages
+ * out of range are masked (the latter reported in err, as is a position past
+ * the table, of which the part inside counts); a row that sees nothing gets
+ * zeros and lse -infinity. What lies in masked slots, also infinities and NaN,
+ * does not matter; visible keys and values must be finite. Rows may share a
+ * sequence (several new tokens of one sequence, each with its own pos).
+ * Products with F16 / BF16 pages run on the tensor cores on q and the
+ * probabilities split into parts that keep 22 bits or more (probabilities: 16
+ * with BF16), summed in f32; F32 pages are multiplied in f32. The visible
+ * positions of all rows are dealt evenly to the GPU's blocks, whatever their
+ * lengths; parts of one row meet through the workspace, always added in the
+ * order of the positions, so equal calls give equal bits.
+ * n_head / n_head_kv <= 8 (LQ8_ERR_UNSUPPORTED); rows * n_head_kv < 2^24
+ * (LQ8_ERR_UNSUPPORTED); window >= 0, scale finite and >= 0 (LQ8_ERR_ARG);
+ * rows == 0 does nothing. q, out 16-byte aligned. Enqueues one kernel. */
+size_t llama_q8_attention_paged_workspace_bytes(int32_t rows, int32_t n_head, int32_t n_head_kv, int32_t head_dim);
+llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t layer, const float* q, int32_t rows,
+                                         const int32_t* pos, const int32_t* seq, int32_t n_head, float scale,
+                                         int32_t window, const int32_t* table, int32_t n_seq,
+                                         int32_t table_stride, float* out, float* lse, void* workspace,
+                                         size_t workspace_bytes, int32_t* err, void* stream);
+
+/* Fork, extend and free: rows_out sequences that continue rows_in ones, as
+ * after a beam search step, in bookkeeping that goes from the _in arrays to the
+ * _out arrays (which must not overlap; a program swaps two sets). refs_in
+ * [n_pages] counts the table entries that name each page (0: free); a caller
+ * may hold counts of its own on pages it wants kept. Child i continues sequence
+ * parent[i] (-1: empty, length 0) with len_out[i] = len_in[parent[i]] = n:
+ *   - pages filled entirely (blocks below n / page) are shared, holes stay;
+ *   - the blocks from there on are written next, so they belong to one sequence:
+ *     the first child of a parent (lowest i) keeps those whose count is 1; for
+ *     the blocks below ceil((n + reserve) / page) that it does not keep, and all
+ *     of these blocks of the other children, a free page is taken, and the n %
+ *     page positions of a partly filled one are copied to it, in every layer;
+ *   - other entries of table_out[rows_out][table_stride] are -1.
+ * The counts of a parent's pages are passed on to its children and dropped with
+ * a parent that has none, so a row that is nobody's parent is freed. Free pages
+ * are those with count 0 in refs_in, taken lowest number first in the order of
+ * (child, block): pages freed by a call are free for the next one.
+ * A call that cannot be done leaves pages and _in arrays as they are, the _out
+ * arrays unspecified, and reports in err (not NULL): LQ8_ERR_OOM (too few free
+ * pages), LQ8_ERR_CTX (n < 0, or n + reserve past the table), LQ8_ERR_ARG (a
+ * parent outside [-1, rows_in)). A page number >= n_pages in a row that is
+ * continued or freed counts as a hole and is reported as LQ8_ERR_ARG. rows_in,
+ * rows_out in 1 .. 65536, reserve >= 0. Enqueues two kernels. */
+size_t llama_q8_pages_fork_workspace_bytes(int32_t rows_in, int32_t rows_out, int32_t table_stride);
+llama_q8_status llama_q8_pages_fork(const llama_q8_pages* pages, int32_t rows_in, const int32_t* len_in,
+                                    const int32_t* table_in, int32_t table_stride, const int32_t* refs_in,
+                                    int32_t rows_out, const int32_t* parent, int32_t reserve, int32_t* len_out,
+                                    int32_t* table_out, int32_t* refs_out, void* workspace,
+                                    size_t workspace_bytes, int32_t* err, void* stream);
+
+/* Compaction: with U pages in use (count > 0), the pages in use with numbers
+ * >= U move, in every layer, to the free numbers < U (both ascending), after
+ * which pages U .. n_pages - 1 are free. table_out[rows][table_stride] names the
+ * new numbers (entries that are holes, out of range or name a free page become
+ * -1; the last two are reported in err as LQ8_ERR_ARG), refs_out[n_pages] the
+ * counts, *n_used (device) is U. Every table that names pages of the pool has to
+ * be in table_in. The _out arrays do not overlap the _in arrays; the moved
+ * pages' old contents stay until they are written again. rows == 0 (no tables)
+ * is allowed. err is not NULL. Enqueues two kernels. */
+size_t llama_q8_pages_compact_workspace_bytes(int32_t n_pages);
+llama_q8_status llama_q8_pages_compact(const llama_q8_pages* pages, int32_t rows, const int32_t* table_in,
+                                       int32_t table_stride, const int32_t* refs_in, int32_t* table_out,
+                                       int32_t* refs_out, int32_t* n_used, void* workspace,
+                                       size_t workspace_bytes, int32_t* err, void* stream);
+
+/* Beam search's selection, the batched counterpart of the greedy argmax:
+ * logits[groups * beams] rows of n_vocab f32, row r at logits + r *
+ * logits_stride (>= n_vocab); scores[groups * beams] the beams' sums of log
+ * probabilities so far. Of each group's beams * n_vocab continuations with
+ * totals scores[beam] + logit - log(sum(exp(logits of the row))), the n_out
+ * largest, in falling order, equal totals with the lowest (beam, token) first:
+ * out_scores[groups][n_out], out_parent (the row, group * beams + beam: the
+ * parent array of llama_q8_pages_fork when n_out == beams) and out_token.
+ * Totals are formed in double and rounded to f32 at the end. A logit of -inf
+ * forbids its token (total -inf). A beam whose score is not finite (a padding
+ * or finished beam), or whose row has a NaN or +inf or nothing but -inf, has
+ * totals -inf: it is chosen only where a group has fewer than n_out others.
+ * groups, beams, n_vocab > 0, n_out in 1 .. beams * n_vocab (LQ8_ERR_ARG); beams
+ * and n_out <= 64, groups * beams <= 65535 (LQ8_ERR_UNSUPPORTED). groups == 0
+ * does nothing. Enqueues one kernel. */
+size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out);
+llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride, int32_t groups, int32_t beams,
+                                     int32_t n_vocab, const float* scores, int32_t n_out, float* out_scores,
+                                     int32_t* out_parent, int32_t* out_token, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,8 +32,13 @@ EXPORTS = ("llama_q8_load", "llama_q8_forward", "llama_q8_forward_argmax", "llam
            "llama_q8_attention_workspace_bytes", "llama_q8_attention", "llama_q8_launch_count",
            "llama_q8_profile_decode", "llama_q8_attention_decode_noalloc", "llama_q8_attention_decode",
            "llama_q8_selftest_wait_timeout", "llama_q8_rope_style_for_arch", "llama_q8_gguf_config",
-           "llama_q8_load_gguf", "llama_q8_packed_bytes_fmt", "llama_q8_pack_fmt", "llama_q8_matvec_fmt")
+           "llama_q8_load_gguf", "llama_q8_packed_bytes_fmt", "llama_q8_pack_fmt", "llama_q8_matvec_fmt",
+           "llama_q8_rope_frequencies", "llama_q8_rope_append", "llama_q8_attention_paged_workspace_bytes",
+           "llama_q8_attention_paged", "llama_q8_pages_fork_workspace_bytes", "llama_q8_pages_fork",
+           "llama_q8_pages_compact_workspace_bytes", "llama_q8_pages_compact",
+           "llama_q8_beam_select_workspace_bytes", "llama_q8_beam_select")
 GGUF_Q5_0, GGUF_Q8_0, GGUF_Q4_K, GGUF_Q6_K = 6, 8, 12, 14
+GGUF_F32, GGUF_F16, GGUF_BF16 = 0, 1, 30
 
 
 class Q8Error(RuntimeError):
@@ -64,6 +69,20 @@ class llama_q8_layer_weights(C.Structure):
 class llama_q8_weights(C.Structure):
     _fields_ = [("token_embd", C.c_void_p), ("output_norm", C.c_void_p), ("output", C.c_void_p),
                 ("layers", C.POINTER(llama_q8_layer_weights)), ("on_device", C.c_int32)]
+
+
+class llama_q8_pages(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("type", C.c_int32), ("n_layer", C.c_int32),
+                ("n_pages", C.c_int32), ("page", C.c_int32), ("n_head_kv", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class llama_q8_rope_scaling(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("trained_ctx", C.c_int32), ("factor", C.c_double), ("low", C.c_double),
+                ("high", C.c_double)]
+
+
+class llama_q8_rope(C.Structure):
+    _fields_ = [("freq", C.c_void_p), ("rot_dim", C.c_int32), ("style", C.c_int32), ("magnitude", C.c_float)]
 
 
 _lib = None
@@ -110,6 +129,17 @@ def lib() -> C.CDLL:
         "llama_q8_packed_bytes_fmt": (sz, [i32, i64, i64]),
         "llama_q8_pack_fmt": (i32, [i32, vp, i64, i64, vp, vp]),
         "llama_q8_matvec_fmt": (i32, [i32, vp, i64, i64, vp, vp, i32, vp]),
+        "llama_q8_rope_frequencies": (i32, [i32, C.c_double, vp, vp, vp]),
+        "llama_q8_rope_append": (i32, [vp, i32, vp, i64, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp]),
+        "llama_q8_attention_paged_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "llama_q8_attention_paged": (i32, [vp, i32, vp, i32, vp, vp, i32, C.c_float, i32, vp, i32, i32, vp, vp, vp,
+                                           sz, vp, vp]),
+        "llama_q8_pages_fork_workspace_bytes": (sz, [i32, i32, i32]),
+        "llama_q8_pages_fork": (i32, [vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp, vp]),
+        "llama_q8_pages_compact_workspace_bytes": (sz, [i32]),
+        "llama_q8_pages_compact": (i32, [vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp]),
+        "llama_q8_beam_select_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "llama_q8_beam_select": (i32, [vp, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -360,6 +390,118 @@ def llama_q8_attention_decode_noalloc(q, k_cache, v_cache, kv_len: int, n_head: 
     check(lib().llama_q8_attention_decode_noalloc(ptr(q), ptr(k_cache), ptr(v_cache), kv_len, n_head, n_head_kv,
                                                   head_dim, cache_stride, ptr(out), stream or None),
           "llama_q8_attention_decode_noalloc")
+
+
+# ---- batched decoding over a paged KV cache ---------------------------------------
+
+LQ8_ROPE_NONE, LQ8_ROPE_LINEAR, LQ8_ROPE_BASE, LQ8_ROPE_RAMP, LQ8_ROPE_RAMP_M = 0, 1, 2, 3, 4
+
+
+def _dev(a, dtype: str) -> int | None:
+    """Address of a contiguous device array of the given element type (a torch
+    tensor), of a raw address, or None."""
+    if a is None or isinstance(a, int):
+        return a
+    if not a.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    if str(a.dtype) != dtype:
+        raise TypeError(f"tensor must be {dtype}, got {a.dtype}")
+    return a.data_ptr()
+
+
+_F32, _I32, _F64, _U8 = "torch.float32", "torch.int32", "torch.float64", "torch.uint8"
+_PAGE_TYPES = {"torch.float32": GGUF_F32, "torch.float16": GGUF_F16, "torch.bfloat16": GGUF_BF16}
+
+
+def make_pages(k, v) -> llama_q8_pages:
+    """The pool of K and V page tensors, each [n_layer][n_pages][n_head_kv][page][head_dim]."""
+    if tuple(k.shape) != tuple(v.shape) or len(k.shape) != 5 or k.dtype != v.dtype:
+        raise ValueError("k and v must be 5-dimensional, of one shape and type")
+    kind = _PAGE_TYPES.get(str(k.dtype))
+    if kind is None:
+        raise TypeError(f"pages must be float32, float16 or bfloat16, got {k.dtype}")
+    n_layer, n_pages, n_head_kv, page, head_dim = k.shape
+    p = llama_q8_pages(_dev(k, str(k.dtype)), _dev(v, str(k.dtype)), kind, n_layer, n_pages, page, n_head_kv, head_dim)
+    p.keep = (k, v)
+    return p
+
+
+def llama_q8_rope_frequencies(rot_dim: int, theta: float, kind: int = LQ8_ROPE_NONE, factor: float = 1.0,
+                              trained_ctx: int = 0, low: float = 0.0, high: float = 0.0):
+    """(frequencies f64[rot_dim / 2], magnitude) of the rotation, on the host."""
+    sc = llama_q8_rope_scaling(kind, trained_ctx, factor, low, high)
+    freq = np.zeros(max(rot_dim // 2, 1), np.float64)
+    mag = C.c_float(0.0)
+    check(lib().llama_q8_rope_frequencies(rot_dim, theta, C.addressof(sc), ptr(freq), C.addressof(mag)),
+          "llama_q8_rope_frequencies")
+    return freq, float(mag.value)
+
+
+def make_rope(freq, style: int = 0, magnitude: float = 1.0) -> llama_q8_rope:
+    """The rotation with device frequencies freq (f64[rot_dim / 2])."""
+    r = llama_q8_rope(_dev(freq, _F64), 2 * freq.numel(), style, magnitude)
+    r.keep = freq
+    return r
+
+
+def llama_q8_rope_append(pages: llama_q8_pages, layer: int, qkv, qkv_stride: int, rows: int, pos, seq, n_head: int,
+                         rope: llama_q8_rope, table, n_seq: int, table_stride: int, q_out, err=None,
+                         stream=0) -> None:
+    check(lib().llama_q8_rope_append(C.addressof(pages), layer, _dev(qkv, _F32), qkv_stride, rows, _dev(pos, _I32),
+                                     _dev(seq, _I32), n_head, C.addressof(rope), _dev(table, _I32), n_seq,
+                                     table_stride, _dev(q_out, _F32), _dev(err, _I32), stream or None),
+          "llama_q8_rope_append")
+
+
+def llama_q8_attention_paged_workspace_bytes(rows: int, n_head: int, n_head_kv: int, head_dim: int) -> int:
+    return int(lib().llama_q8_attention_paged_workspace_bytes(rows, n_head, n_head_kv, head_dim))
+
+
+def llama_q8_attention_paged(pages: llama_q8_pages, layer: int, q, rows: int, pos, seq, n_head: int, scale: float,
+                             window: int, table, n_seq: int, table_stride: int, out, lse, workspace,
+                             workspace_bytes: int, err=None, stream=0) -> None:
+    check(lib().llama_q8_attention_paged(C.addressof(pages), layer, _dev(q, _F32), rows, _dev(pos, _I32),
+                                         _dev(seq, _I32), n_head, scale, window, _dev(table, _I32), n_seq,
+                                         table_stride, _dev(out, _F32), _dev(lse, _F32), _dev(workspace, _U8),
+                                         workspace_bytes, _dev(err, _I32), stream or None),
+          "llama_q8_attention_paged")
+
+
+def llama_q8_pages_fork_workspace_bytes(rows_in: int, rows_out: int, table_stride: int) -> int:
+    return int(lib().llama_q8_pages_fork_workspace_bytes(rows_in, rows_out, table_stride))
+
+
+def llama_q8_pages_fork(pages: llama_q8_pages, rows_in: int, len_in, table_in, table_stride: int, refs_in,
+                        rows_out: int, parent, reserve: int, len_out, table_out, refs_out, workspace,
+                        workspace_bytes: int, err, stream=0) -> None:
+    check(lib().llama_q8_pages_fork(C.addressof(pages), rows_in, _dev(len_in, _I32), _dev(table_in, _I32),
+                                    table_stride, _dev(refs_in, _I32), rows_out, _dev(parent, _I32), reserve,
+                                    _dev(len_out, _I32), _dev(table_out, _I32), _dev(refs_out, _I32),
+                                    _dev(workspace, _U8), workspace_bytes, _dev(err, _I32), stream or None),
+          "llama_q8_pages_fork")
+
+
+def llama_q8_pages_compact_workspace_bytes(n_pages: int) -> int:
+    return int(lib().llama_q8_pages_compact_workspace_bytes(n_pages))
+
+
+def llama_q8_pages_compact(pages: llama_q8_pages, rows: int, table_in, table_stride: int, refs_in, table_out,
+                           refs_out, n_used, workspace, workspace_bytes: int, err, stream=0) -> None:
+    check(lib().llama_q8_pages_compact(C.addressof(pages), rows, _dev(table_in, _I32), table_stride,
+                                       _dev(refs_in, _I32), _dev(table_out, _I32), _dev(refs_out, _I32),
+                                       _dev(n_used, _I32), _dev(workspace, _U8), workspace_bytes, _dev(err, _I32),
+                                       stream or None), "llama_q8_pages_compact")
+
+
+def llama_q8_beam_select_workspace_bytes(groups: int, beams: int, n_vocab: int, n_out: int) -> int:
+    return int(lib().llama_q8_beam_select_workspace_bytes(groups, beams, n_vocab, n_out))
+
+
+def llama_q8_beam_select(logits, logits_stride: int, groups: int, beams: int, n_vocab: int, scores, n_out: int,
+                         out_scores, out_parent, out_token, workspace, workspace_bytes: int, stream=0) -> None:
+    check(lib().llama_q8_beam_select(_dev(logits, _F32), logits_stride, groups, beams, n_vocab, _dev(scores, _F32),
+                                     n_out, _dev(out_scores, _F32), _dev(out_parent, _I32), _dev(out_token, _I32),
+                                     _dev(workspace, _U8), workspace_bytes, stream or None), "llama_q8_beam_select")
 
 
 def status_str(s: int) -> str:

@@ -1,0 +1,79 @@
+// The paged KV cache as the kernels see it: one layer of a pool, element types
+// and the checks shared by the entry points of paged.cu and pages.cu.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "llama_q8.h"
+
+namespace lq8 {
+
+constexpr int kPageMin = 8, kPageMax = 256;
+
+inline int page_type_bytes(int type) {
+    return type == LLAMA_Q8_GGUF_F32 ? 4 : (type == LLAMA_Q8_GGUF_F16 || type == LLAMA_Q8_GGUF_BF16) ? 2 : 0;
+}
+
+// One layer of a pool. page_elems = n_kv * page * head_dim values per page.
+template <typename T>
+struct PageView {
+    T* k;
+    T* v;
+    int n_pages, page_shift, n_kv;
+    int64_t page_elems;
+};
+
+// Page table of the sequences; entries outside [0, n_pages) are holes.
+struct TableView {
+    const int32_t* table;
+    int n_seq, stride;
+};
+
+inline int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+// LQ8_OK, or what is wrong with a pool's description.
+inline llama_q8_status check_pages(const llama_q8_pages* p) {
+    if (!p || !p->k || !p->v || p->n_layer <= 0 || p->n_pages <= 0 || p->n_head_kv <= 0) return LQ8_ERR_ARG;
+    if (!page_type_bytes(p->type)) return LQ8_ERR_UNSUPPORTED;
+    if (p->page < kPageMin || p->page > kPageMax || (p->page & (p->page - 1))) return LQ8_ERR_UNSUPPORTED;
+    if (p->head_dim != 64 && p->head_dim != 128) return LQ8_ERR_UNSUPPORTED;
+    if (((uintptr_t)p->k | (uintptr_t)p->v) & 15) return LQ8_ERR_ARG;
+    return LQ8_OK;
+}
+
+template <typename T>
+inline PageView<T> page_view(const llama_q8_pages* p, int layer) {
+    PageView<T> w;
+    w.page_elems = (int64_t)p->n_head_kv * p->page * p->head_dim;
+    const int64_t off = (int64_t)layer * p->n_pages * w.page_elems;
+    w.k = reinterpret_cast<T*>(p->k) + off;
+    w.v = reinterpret_cast<T*>(p->v) + off;
+    w.n_pages = p->n_pages;
+    w.page_shift = log2_of(p->page);
+    w.n_kv = p->n_head_kv;
+    return w;
+}
+
+// Report a status found on the device: the largest one stays.
+__device__ __forceinline__ void report(int32_t* err, int status) {
+    if (err) atomicMax(err, status);
+}
+
+__device__ __forceinline__ int page_of(const TableView& t, int seq, int block, int n_pages) {
+    const int p = t.table[(int64_t)seq * t.stride + block];
+    return p < n_pages ? p : -1;
+}
+
+// attention_paged.cu
+cudaError_t init_attention_paged_attributes();
+// pages.cu, beam.cu: nothing to initialise
+
+}  // namespace lq8

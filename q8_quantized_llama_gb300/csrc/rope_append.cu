@@ -1,0 +1,213 @@
+// Rotary positions and the append of keys and values to the pages of a cache,
+// one kernel for all rows of a step or a prompt.
+//
+// A row is [q heads | k heads | v heads] * head_dim floats. Value pairs (x, y)
+// of the leading rot_dim values of a q or k head become (x c - y s, x s + y c)
+// with c, s = magnitude * cos, sin of pos * freq_i. The product is taken in
+// double and reduced to a fraction of a turn there (a position of 2^20 leaves
+// an f32 product no digits of the angle); cos and sin of the fraction are f32.
+// They are computed once per row and pair into shared memory and used by all
+// heads.
+//
+// Bound: memory. Each thread moves items of 8 values (two 16-byte loads, one or
+// two stores): the two halves of 4 pairs for the half layout, so that no value
+// is read twice; the loads are issued before the angles are computed, whose
+// latency (double multiply, sincospif) they cover. One CTA per row: 8 or more
+// resident per SM, enough bytes in flight without a pipeline.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "paged.cuh"
+
+namespace lq8 {
+namespace {
+
+struct RopeArgs {
+    const float* qkv;
+    int64_t qkv_stride;
+    const int32_t* pos;
+    const int32_t* seq;
+    int n_head;
+    const double* freq;
+    int rot_dim, style;
+    float magnitude;
+    float* q_out;
+    int32_t* err;
+};
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+    __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
+}
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeItems = 4;  // items loaded ahead per thread
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, PageView<T> pg, TableView tb) {
+    __shared__ float2 cs[HD / 2];
+    constexpr int IPH = HD / 8;  // items per head
+    const int row = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
+    const int p = a.pos[row];
+    if (p < 0) return;
+    const int half = a.rot_dim >> 1, rot_items = a.rot_dim >> 3;
+    const int heads = a.n_head + 2 * pg.n_kv, items = heads * IPH;
+    const float* x = a.qkv + row * a.qkv_stride;
+
+    // where the first and second four values of item `it` of a head lie
+    auto first = [&](int it, bool rot) { return (rot && a.style) ? 4 * it : 8 * it; };
+    auto second = [&](int it, bool rot) { return (rot && a.style) ? 4 * it + half : 8 * it + 4; };
+    float4 u[kRopeItems], w[kRopeItems];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < kRopeItems; ++j) {
+            const int i = i0 + j * threads;
+            if (i < items) {
+                const int h = i / IPH, it = i % IPH;
+                const bool rot = h < a.n_head + pg.n_kv && it < rot_items;
+                u[j] = __ldcs(reinterpret_cast<const float4*>(x + h * HD + first(it, rot)));
+                w[j] = __ldcs(reinterpret_cast<const float4*>(x + h * HD + second(it, rot)));
+            }
+        }
+    };
+    load(tid);
+    if (tid < half) {
+        // angle in turns: the product and its reduction in double
+        const double turns = (double)p * (a.freq[tid] * 0.15915494309189533577);  // 1 / 2 pi
+        float s, c;
+        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+        cs[tid] = make_float2(c * a.magnitude, s * a.magnitude);
+    }
+    const int sq = a.seq ? a.seq[row] : row;
+    const int block = p >> pg.page_shift, slot = p & ((1 << pg.page_shift) - 1);
+    int page = -1;
+    if (sq < 0 || sq >= tb.n_seq) {
+        if (tid == 0) report(a.err, LQ8_ERR_ARG);
+    } else if (block >= tb.stride) {
+        if (tid == 0) report(a.err, LQ8_ERR_CTX);
+    } else {
+        page = page_of(tb, sq, block, pg.n_pages);
+        if (page < 0 && tid == 0) report(a.err, LQ8_ERR_ARG);
+    }
+    __syncthreads();
+
+    for (int i0 = tid; i0 < items;) {
+#pragma unroll
+        for (int j = 0; j < kRopeItems; ++j) {
+            const int i = i0 + j * threads;
+            if (i >= items) break;
+            const int h = i / IPH, it = i % IPH;
+            const bool rot = h < a.n_head + pg.n_kv && it < rot_items;
+            float4 y = u[j], z = w[j];
+            if (rot && a.style) {  // y holds values 4 it .. + 3, z their partners
+                const float2 c0 = cs[4 * it], c1 = cs[4 * it + 1], c2 = cs[4 * it + 2], c3 = cs[4 * it + 3];
+                y = make_float4(u[j].x * c0.x - w[j].x * c0.y, u[j].y * c1.x - w[j].y * c1.y,
+                                u[j].z * c2.x - w[j].z * c2.y, u[j].w * c3.x - w[j].w * c3.y);
+                z = make_float4(u[j].x * c0.y + w[j].x * c0.x, u[j].y * c1.y + w[j].y * c1.x,
+                                u[j].z * c2.y + w[j].z * c2.x, u[j].w * c3.y + w[j].w * c3.x);
+            } else if (rot) {  // pairs side by side
+                const float2 c0 = cs[4 * it], c1 = cs[4 * it + 1], c2 = cs[4 * it + 2], c3 = cs[4 * it + 3];
+                y = make_float4(u[j].x * c0.x - u[j].y * c0.y, u[j].x * c0.y + u[j].y * c0.x,
+                                u[j].z * c1.x - u[j].w * c1.y, u[j].z * c1.y + u[j].w * c1.x);
+                z = make_float4(w[j].x * c2.x - w[j].y * c2.y, w[j].x * c2.y + w[j].y * c2.x,
+                                w[j].z * c3.x - w[j].w * c3.y, w[j].z * c3.y + w[j].w * c3.x);
+            }
+            const int o1 = first(it, rot), o2 = second(it, rot);
+            if (h < a.n_head) {
+                float* q = a.q_out + ((int64_t)row * a.n_head + h) * HD;
+                store4(q + o1, y);
+                store4(q + o2, z);
+            } else if (page >= 0) {
+                const int kh = h - a.n_head;
+                const bool is_v = kh >= pg.n_kv;
+                T* dst = (is_v ? pg.v : pg.k) + page * pg.page_elems +
+                         ((int64_t)((is_v ? kh - pg.n_kv : kh) << pg.page_shift) + slot) * HD;
+                store4(dst + o1, y);
+                store4(dst + o2, z);
+            }
+        }
+        i0 += kRopeItems * threads;
+        load(i0);
+    }
+}
+
+template <typename T>
+cudaError_t launch_rope(const RopeArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, int rows,
+                        cudaStream_t s) {
+    const int items = (a.n_head + 2 * p->n_head_kv) * (p->head_dim / 8);
+    // as many warps as one pass over the row's items needs, at least those that compute the angles
+    const int threads = std::min(kRopeThreads, std::max((items + 31) / 32 * 32, p->head_dim / 2));
+    if (p->head_dim == 64)
+        return launch_ex(rope_append_kernel<T, 64>, dim3(rows), dim3(threads), 0, s, false, a, page_view<T>(p, layer), tb);
+    return launch_ex(rope_append_kernel<T, 128>, dim3(rows), dim3(threads), 0, s, false, a, page_view<T>(p, layer), tb);
+}
+
+}  // namespace
+}  // namespace lq8
+
+using namespace lq8;
+
+extern "C" {
+
+llama_q8_status llama_q8_rope_frequencies(int32_t rot_dim, double theta, const llama_q8_rope_scaling* sc, double* freq,
+                                          float* magnitude) {
+    if (!sc || !freq || !magnitude || rot_dim < 2 || rot_dim % 2 || !(theta > 0) || !std::isfinite(theta))
+        return LQ8_ERR_ARG;
+    if (sc->kind < LQ8_ROPE_NONE || sc->kind > LQ8_ROPE_RAMP_M) return LQ8_ERR_ARG;
+    const bool ramp = sc->kind == LQ8_ROPE_RAMP || sc->kind == LQ8_ROPE_RAMP_M;
+    if (sc->kind != LQ8_ROPE_NONE && !(sc->factor >= 1 && std::isfinite(sc->factor))) return LQ8_ERR_ARG;
+    if (sc->kind == LQ8_ROPE_BASE && rot_dim == 2) return LQ8_ERR_ARG;
+    if (ramp && !(sc->trained_ctx > 0 && sc->low >= 0 && sc->high > sc->low && std::isfinite(sc->high)))
+        return LQ8_ERR_ARG;
+    if (sc->kind == LQ8_ROPE_BASE) theta *= std::pow(sc->factor, (double)rot_dim / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / rot_dim);
+        if (sc->kind == LQ8_ROPE_LINEAR) f /= sc->factor;
+        if (ramp) {
+            const double turns = sc->trained_ctx * f / 6.283185307179586477;
+            const double t = (turns - sc->low) / (sc->high - sc->low);
+            const double keep = t < 0 ? 0 : t > 1 ? 1 : t;
+            f = f * keep + f / sc->factor * (1 - keep);
+        }
+        freq[i] = f;
+    }
+    *magnitude = sc->kind == LQ8_ROPE_RAMP_M ? (float)(0.1 * std::log(sc->factor) + 1.0) : 1.0f;
+    return LQ8_OK;
+}
+
+llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer, const float* qkv, int64_t qkv_stride,
+                                     int32_t rows, const int32_t* pos, const int32_t* seq, int32_t n_head,
+                                     const llama_q8_rope* rope, const int32_t* table, int32_t n_seq,
+                                     int32_t table_stride, float* q_out, int32_t* err, void* stream) {
+    const llama_q8_status st = check_pages(pages);
+    if (st != LQ8_OK) return st;
+    if (!rope || !rope->freq || !qkv || !pos || !table || !q_out || rows < 0 || n_head <= 0 || n_seq <= 0 ||
+        table_stride <= 0 || layer < 0 || layer >= pages->n_layer || n_head % pages->n_head_kv)
+        return LQ8_ERR_ARG;
+    if (!seq && rows > n_seq) return LQ8_ERR_ARG;
+    if (rope->style != 0 && rope->style != 1) return LQ8_ERR_ARG;
+    if (!std::isfinite(rope->magnitude)) return LQ8_ERR_ARG;
+    if (rope->rot_dim <= 0 || rope->rot_dim % 8 || rope->rot_dim > pages->head_dim) return LQ8_ERR_UNSUPPORTED;
+    const int64_t width = ((int64_t)n_head + 2 * (int64_t)pages->n_head_kv) * pages->head_dim;
+    if (width > INT32_MAX) return LQ8_ERR_UNSUPPORTED;
+    if (qkv_stride < width || qkv_stride % 4) return LQ8_ERR_ARG;
+    // rows move in 16-byte pieces
+    if (((uintptr_t)qkv | (uintptr_t)q_out) & 15) return LQ8_ERR_ARG;
+    if (((uintptr_t)rope->freq & 7) || (((uintptr_t)pos | (uintptr_t)seq | (uintptr_t)table | (uintptr_t)err) & 3))
+        return LQ8_ERR_ARG;
+    if (rows == 0) return LQ8_OK;
+    RopeArgs a{qkv, qkv_stride, pos, seq, n_head, rope->freq, rope->rot_dim, rope->style, rope->magnitude, q_out, err};
+    const TableView tb{table, n_seq, table_stride};
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = pages->type == LLAMA_Q8_GGUF_F32   ? launch_rope<float>(a, pages, layer, tb, rows, s)
+                    : pages->type == LLAMA_Q8_GGUF_F16 ? launch_rope<__half>(a, pages, layer, tb, rows, s)
+                                                       : launch_rope<__nv_bfloat16>(a, pages, layer, tb, rows, s);
+    return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
+}
+
+}  // extern "C"
