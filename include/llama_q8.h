@@ -475,9 +475,10 @@ llama_q8_status llama_q8_attention_decode_noalloc(const float* q, const float* k
  *     and every device pointer live. The calls keep nothing between them but
  *     what their arguments hold, and may be captured in CUDA graphs.
  *   - A workspace has at least the bytes its query returns, is 16-byte aligned,
- *     zeroed before its first use and left with zeroed counters by every call.
- *     Calls that share one (or graphs that captured such calls) must not overlap
- *     on the GPU.
+ *     zeroed before its first use and left with zeroed counters by every call;
+ *     calls of any sizes and of all of these operators can use the same one in
+ *     turn. Calls that share one (or graphs that captured such calls) must not
+ *     overlap on the GPU.
  * ------------------------------------------------------------------------- */
 #define LLAMA_Q8_GGUF_F32 0
 #define LLAMA_Q8_GGUF_F16 1

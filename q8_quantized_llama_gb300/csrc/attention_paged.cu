@@ -1,122 +1,714 @@
 // Grouped-query attention of single tokens over the pages of a KV cache.
 //
 // For a row and KV head: s_j = scale q . k_j over the visible positions, m =
-// max s, l = sum exp(s_j - m), out = sum exp(s_j - m) v_j / l, lse = m + ln l.
-// One CTA per (KV head, row) goes through the positions in tiles of 32 with a
-// running maximum and sum.
+// max s, l = sum exp(s_j - m), out = sum exp(s_j - m) v_j / l, lse = m + ln l,
+// in one pass with a running m and l (in units of log2: q is multiplied by
+// scale * log2 e once).
+//
+// Bound: memory; each visible K and V row is read once, for all query heads of
+// its group.
+//
+// Split. The visible positions of all (row, KV head) pairs are laid end to end
+// in units of a few tiles and dealt evenly to the CTAs, whatever the lengths:
+// every CTA adds up the rows' units itself (positions live on the device) and
+// takes the same share. Pairs that lie in one CTA's share are finished there;
+// the parts of the others go to the workspace and the CTA that finishes last
+// (a counter per pair) joins them in the order of the positions.
+//
+// Inside a CTA each of four warps takes one tile of every unit through a ring
+// of its own (cp.async, zero-filled outside the visible range, 16-byte pieces
+// XOR-swizzled by row), keeps its own m, l and output in registers and needs no
+// CTA barrier until the end of the pair. Page numbers are fetched 32 tiles
+// ahead, one per lane.
+//
+// 16-bit pages: mma.sync m16n8k16. A group has at most 8 query heads, so rows
+// 0-7 of the A operand carry the high part of q (or of the probabilities) and
+// rows 8-15 the rest: one product gives both, and their sum is two registers of
+// one thread. tcgen05 (128 rows) would idle 15/16 of its rows and pass the
+// probabilities through tensor memory; the kernel is bound by memory without.
+//  - f16: q is scaled per head by a power of two (largest value into [2^14,
+//    2^15)) and split in two: 22 bits; the probabilities by 2^15.
+//  - bf16: q in three parts, 24 bits (the third in a second product); the
+//    probabilities in two, 16 bits and the rounding's sign.
+// f32 pages: f32 products. Scores: a few lanes per key over the dimensions,
+// q from shared memory; output: a few dimensions per lane.
+#include <algorithm>
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace lq8 {
 namespace {
 
-constexpr int kTile = 32, kThreads = 128, kMaxG = 8;
+constexpr int kWarps = 4, kThreads = kWarps * 32, kMaxG = 8;
+constexpr int kMaxCtas = 2 * 152;
+constexpr int kRingBytes = 24 * 1024;  // per warp
+constexpr int kMinShare = 2;           // units a CTA takes at least
 
 struct AttnArgs {
     const float* q;
     const int32_t* pos;
     const int32_t* seq;
-    int n_head;
-    float scale;
+    int rows, n_head;
+    float scale_log2;
     int window;
     float* out;
     float* lse;
     int32_t* err;
+    // workspace
+    unsigned int* counters;  // [kMaxCtas] by the CTA in whose share a pair starts, zero between launches
+    float2* part_ml;         // [2 * kMaxCtas][G]
+    float* part_o;           // [2 * kMaxCtas][G][HD]
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+size_t attn_paged_workspace(int n_head, int n_kv, int hd, AttnArgs* a, void* ws) {
+    const int G = n_head / n_kv;
+    const size_t c = kCounterBytes;
+    const size_t ml = (sizeof(float2) * 2 * kMaxCtas * G + 255) / 256 * 256;
+    if (a) {
+        uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+        a->counters = reinterpret_cast<unsigned int*>(w);
+        a->part_ml = reinterpret_cast<float2*>(w + c);
+        a->part_o = reinterpret_cast<float*>(w + c + ml);
+    }
+    return c + ml + sizeof(float) * 2 * kMaxCtas * (size_t)G * hd;
+}
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) attention_paged_kernel(AttnArgs a, PageView<T> pg, TableView tb) {
-    __shared__ float ks[kTile][HD + 1], vs[kTile][HD], qs[kMaxG][HD], ps[kMaxG][kTile];
-    __shared__ float sm[kMaxG], sl[kMaxG], sc[kMaxG];
-    __shared__ int ok[kTile];
-    const int kh = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, G = a.n_head / pg.n_kv;
-    const int p = a.pos[row], sq = a.seq ? a.seq[row] : row;
-    int64_t end = p < 0 ? 0 : (int64_t)p + 1;
-    if (end > 0 && (sq < 0 || sq >= tb.n_seq)) {
-        if (tid == 0) report(a.err, LQ8_ERR_ARG);
-        end = 0;
+struct Shape {
+    static constexpr int kTile = sizeof(T) == 2 ? 16 : 1024 / HD;  // keys per warp and step
+    static constexpr int kRowBytes = HD * (int)sizeof(T);
+    static constexpr int kTileBytes = kTile * kRowBytes;           // of K or of V
+    static constexpr int kStages = kRingBytes / (2 * kTileBytes);
+    static constexpr int kUnit = kWarps * kTile;                   // positions
+    static constexpr int kChunks = kRowBytes / 16;
+    static_assert(kMaxG * HD * 4 <= kRingBytes, "a warp's output waits in its ring");
+};
+constexpr int kSmemRing = kWarps * kRingBytes;
+constexpr int kSmemQ = kSmemRing;                                  // f32: [8][HD] q; joins: weights
+constexpr int kSmemP = kSmemQ + kMaxG * 128 * 4;                   // f32: [warp][tile][8] probabilities
+constexpr int kSmemMl = kSmemP + kWarps * 16 * kMaxG * 4;          // [warp][8] m, l
+constexpr int kSmemBytes = kSmemMl + kWarps * kMaxG * 8;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// (x, y) rounded to the type; x, y left with what the rounding dropped
+__device__ __forceinline__ uint32_t take_part(float& x, float& y, __half) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    x -= f.x;
+    y -= f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t take_part(float& x, float& y, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    x -= f.x;
+    y -= f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ int order_int(float x) {
+    const int b = __float_as_int(x);
+    return b >= 0 ? b : b ^ 0x7fffffff;
+}
+__device__ __forceinline__ float order_float(int b) { return __int_as_float(b >= 0 ? b : b ^ 0x7fffffff); }
+
+// Visible positions [lo, hi) of a row; status: what is wrong with it.
+struct Range {
+    int lo, hi, seq, status;
+};
+__device__ __forceinline__ Range row_range(const AttnArgs& a, const TableView& tb, int shift, int row) {
+    Range g{0, 0, 0, 0};
+    const int p = a.pos[row];
+    g.seq = a.seq ? a.seq[row] : row;
+    if (p < 0) return g;
+    if (g.seq < 0 || g.seq >= tb.n_seq) {
+        g.status = LQ8_ERR_ARG;
+        return g;
     }
-    const int lo = (int)(a.window > 0 && end > a.window ? end - a.window : 0);
-    const int64_t cap = (int64_t)tb.stride << pg.page_shift;
-    if (end > cap && tid == 0) report(a.err, LQ8_ERR_CTX);
-    const int hi = (int)min(end, cap);
-    const int64_t ob = ((int64_t)row * a.n_head + kh * G) * HD;
-    for (int i = tid; i < G * HD; i += kThreads) qs[i / HD][i % HD] = a.q[ob + i] * a.scale;
-    if (tid < kMaxG) { sm[tid] = -INFINITY; sl[tid] = 0.0f; }
-    float acc[kMaxG][HD / 128 ? HD / 128 : 1] = {};
+    const int64_t end = (int64_t)p + 1, cap = min((int64_t)tb.stride << shift, (int64_t)INT32_MAX - 1023);
+    if (end > cap) g.status = LQ8_ERR_CTX;
+    const int64_t lo = a.window > 0 && end > a.window ? end - a.window : 0;
+    g.hi = (int)min(end, cap);
+    g.lo = (int)min(lo, (int64_t)g.hi);
+    return g;
+}
+template <int UNIT>
+__device__ __forceinline__ int range_units(const Range& g) {
+    return g.hi > g.lo ? (g.hi + UNIT - 1) / UNIT - g.lo / UNIT : 0;
+}
+
+// One warp's running state over one (row, KV head).
+template <typename T, int HD>
+struct State16 {
+    uint32_t q[HD / 16][4];
+    uint32_t q3[HD / 16][2];  // bf16: third part
+    float o[HD / 8][4];
+    float m, l, q_inv;
+};
+template <int HD>
+struct State32 {
+    float o[kMaxG][HD / 32];
+    float m[kMaxG], l[kMaxG];  // m the same in every lane, l a part per lane
+};
+
+template <typename T, int HD>
+__device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, int G, float scale, int lane) {
+    constexpr bool kHalf = sizeof(T) == 2 && std::is_same<T, __half>::value;
+    const int g = lane >> 2, t = lane & 3;
+    const T tag{};
+    float v[HD / 16][4];
+    float mx = 0.0f;
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+        float2 x = make_float2(0.f, 0.f), y = x;
+        if (g < G) {
+            x = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 2 * t);
+            y = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 8 + 2 * t);
+        }
+        v[k][0] = x.x * scale; v[k][1] = x.y * scale;
+        v[k][2] = y.x * scale; v[k][3] = y.y * scale;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fabsf(v[k][j]));
+    }
+    float up = 1.0f;
+    s.q_inv = 1.0f;
+    if (kHalf) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int sh = row_shift(mx);
+        up = pow2f(sh);
+        s.q_inv = pow2f(-sh);
+    }
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[k][j] *= up;
+        s.q[k][0] = take_part(v[k][0], v[k][1], tag);
+        s.q[k][1] = take_part(v[k][0], v[k][1], tag);
+        s.q[k][2] = take_part(v[k][2], v[k][3], tag);
+        s.q[k][3] = take_part(v[k][2], v[k][3], tag);
+        if (!kHalf) {
+            s.q3[k][0] = take_part(v[k][0], v[k][1], tag);
+            s.q3[k][1] = take_part(v[k][2], v[k][3], tag);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.o[d][j] = 0.0f;
+    s.m = -INFINITY;
+    s.l = 0.0f;
+}
+
+// A tile of 16 keys: K at ks, V at vs (shared addresses); key j of the tile counts if bit j of see is set.
+template <typename T, int HD>
+__device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint32_t vs, unsigned see, int lane) {
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    constexpr int RB = HD * 2;
+    const T tag{};
+    const int l8 = lane & 7, mi = lane >> 3, t = lane & 3;
+    float c[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < HD / 32; ++k) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t b[4];
+            ldsm4(b, ks + (n * 8 + l8) * RB + (((k * 4 + mi) ^ l8) << 4));
+            mma16(c[n], s.q[2 * k], b[0], b[1], tag);
+            mma16(c[n], s.q[2 * k + 1], b[2], b[3], tag);
+            if (!kHalf) {
+                const uint32_t a0[4] = {s.q3[2 * k][0], 0, s.q3[2 * k][1], 0};
+                const uint32_t a1[4] = {s.q3[2 * k + 1][0], 0, s.q3[2 * k + 1][1], 0};
+                mma16(c[n], a0, b[0], b[1], tag);
+                mma16(c[n], a1, b[2], b[3], tag);
+            }
+        }
+    }
+    float x[4] = {c[0][0] + c[0][2], c[0][1] + c[0][3], c[1][0] + c[1][2], c[1][1] + c[1][3]};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (kHalf) x[j] *= s.q_inv;
+        if (!((see >> ((j >> 1) * 8 + 2 * t + (j & 1))) & 1)) x[j] = -INFINITY;
+    }
+    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float m = fmaxf(s.m, mx);  // finite: a tile in which nothing counts is not given to this function
+    if (__any_sync(0xffffffffu, m > s.m)) {
+        const float f = ex2(s.m - m);
+        s.m = m;
+        s.l *= f;
+#pragma unroll
+        for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s.o[d][j] *= f;
+    }
+    // f16: probabilities times 2^15, so that the second part of a small one is not lost below f16's range
+    const float ref = kHalf ? m - 15.0f : m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] = ex2(x[j] - ref);
+        s.l += x[j];
+    }
+    uint32_t a[4];
+    a[0] = take_part(x[0], x[1], tag);
+    a[1] = take_part(x[0], x[1], tag);
+    a[2] = take_part(x[2], x[3], tag);
+    a[3] = take_part(x[2], x[3], tag);
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) {
+        uint32_t b[4];
+        ldsm4_t(b, vs + ((mi & 1) * 8 + l8) * RB + (((2 * d + (mi >> 1)) ^ l8) << 4));
+        mma16(s.o[2 * d], a, b[0], b[1], tag);
+        mma16(s.o[2 * d + 1], a, b[2], b[3], tag);
+    }
+}
+
+// The warp's part: output [8][HD] to ob, m and l of its heads to ml (l of f16 pages carries the factor 2^15).
+template <typename T, int HD>
+__device__ __forceinline__ void state_store(State16<T, HD>& s, float* ob, float2* ml, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float l = s.l;
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (t == 0) ml[g] = make_float2(s.m, l);
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d)
+        *reinterpret_cast<float2*>(ob + g * HD + d * 8 + 2 * t) =
+            make_float2(s.o[d][0] + s.o[d][2], s.o[d][1] + s.o[d][3]);
+}
+
+template <int HD, int GP>
+__device__ __forceinline__ void state_init(State32<HD>& s) {
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) s.o[g][d] = 0.0f;
+        s.m[g] = -INFINITY;
+        s.l[g] = 0.0f;
+    }
+}
+
+// A tile of 1024 / HD keys; q [GP][HD] and the warp's probabilities [tile][8] in shared memory.
+template <int HD, int GP>
+__device__ __forceinline__ void state_tile(State32<HD>& s, const uint8_t* ks, const uint8_t* vs, const float* q,
+                                           float* pb, unsigned see, int lane) {
+    constexpr int TK = 1024 / HD, LPK = 32 / TK, CPL = HD / 4 / LPK;  // keys, lanes per key, 16-byte pieces per lane
+    constexpr int RB = HD * 4;
+    const int key = lane % TK, part = lane / TK;
+    uint64_t acc[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) acc[g] = 0;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+        const int ch = part * CPL + i;
+        const ulonglong2 kv = *reinterpret_cast<const ulonglong2*>(ks + key * RB + ((ch ^ (key & 7)) << 4));
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(q + g * HD + ch * 4);
+            acc[g] = fma_f2(kv.x, qv.x, acc[g]);
+            acc[g] = fma_f2(kv.y, qv.y, acc[g]);
+        }
+    }
+    const bool in = (see >> key) & 1;
+    float p[GP];
+    bool grew = false;
+    float f[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+        float x = f2_lo(acc[g]) + f2_hi(acc[g]);
+#pragma unroll
+        for (int o = TK; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (!in) x = -INFINITY;
+        const float mx = order_float(__reduce_max_sync(0xffffffffu, order_int(x)));
+        const float m = fmaxf(s.m[g], mx);
+        f[g] = ex2(s.m[g] - m);
+        grew |= m > s.m[g];
+        s.m[g] = m;
+        p[g] = ex2(x - m);
+        s.l[g] = s.l[g] * f[g] + (part == 0 ? p[g] : 0.0f);
+    }
+    if (grew) {  // the same in every lane
+#pragma unroll
+        for (int g = 0; g < GP; ++g)
+#pragma unroll
+            for (int d = 0; d < HD / 32; ++d) s.o[g][d] *= f[g];
+    }
+    __syncwarp();  // the last tile's probabilities have been read
+    if (part == 0) {
+#pragma unroll
+        for (int g = 0; g < GP; g += 4)
+            *reinterpret_cast<float4*>(pb + key * kMaxG + g) = make_float4(p[g], p[g + 1], p[g + 2], p[g + 3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < TK; ++j) {
+        float v[HD / 32];
+        if (HD == 128) {
+            const float4 x = *reinterpret_cast<const float4*>(vs + j * RB + ((lane ^ (j & 7)) << 4));
+            v[0] = x.x; v[1] = x.y; v[HD / 32 - 2] = x.z; v[HD / 32 - 1] = x.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(vs + j * RB + (((lane >> 1) ^ (j & 7)) << 4) + (lane & 1) * 8);
+            v[0] = x.x; v[1] = x.y;
+        }
+#pragma unroll
+        for (int g4 = 0; g4 < GP; g4 += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(pb + j * kMaxG + g4);
+            const float ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int d = 0; d < HD / 32; ++d) s.o[g4 + g][d] = fmaf(ww[g], v[d], s.o[g4 + g][d]);
+        }
+    }
+}
+
+template <int HD, int GP>
+__device__ __forceinline__ void state_store(State32<HD>& s, float* ob, float2* ml, int lane) {
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+        const float l = warp_sum(s.l[g]);
+        if (lane == 0) ml[g] = make_float2(s.m[g], l);
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) ob[g * HD + lane * (HD / 32) + d] = s.o[g][d];
+    }
+}
+
+// GP: query heads the f32 form carries (4 or 8); the tensor cores' rows hold 8 in any case.
+template <typename T, int HD, int GP>
+__global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a, PageView<T> pg, TableView tb) {
+    using S = Shape<T, HD>;
+    constexpr bool kF32 = sizeof(T) == 4;
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_scan[kWarps], s_base;
+    __shared__ int s_row, s_last;
+    __shared__ unsigned s_see[kWarps][S::kStages];  // keys that count in each stage's tile
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.n_head / pg.n_kv, shift = pg.page_shift;
+    uint8_t* ring = smem + warp * kRingBytes;
+    float* qs = reinterpret_cast<float*>(smem + kSmemQ);
+    float* pb = reinterpret_cast<float*>(smem + kSmemP) + warp * 16 * kMaxG;
+    float2* ml = reinterpret_cast<float2*>(smem + kSmemMl);
+
+    // ---- this CTA's share of the units of all rows -------------------------------------
+    const int per = (a.rows + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int r = tid * per + i;
+        if (r < a.rows) mine += range_units<S::kUnit>(row_range(a, tb, shift, r));
+    }
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) s_scan[warp] = before;
     __syncthreads();
-    for (int j0 = lo; j0 < hi; j0 += kTile) {
-        const int n = min(kTile, hi - j0);
-        for (int i = tid; i < kTile * HD; i += kThreads) {
-            const int r = i / HD, d = i % HD;
-            float kv = 0.0f, vv = 0.0f;
-            bool good = false;
-            if (r < n) {
-                const int j = j0 + r, page = page_of(tb, sq, j >> pg.page_shift, pg.n_pages);
-                if (page >= 0) {
-                    const int64_t o = page * pg.page_elems +
-                                      (((int64_t)kh << pg.page_shift) + (j & ((1 << pg.page_shift) - 1))) * HD + d;
-                    kv = to_f32(pg.k[o]);
-                    vv = to_f32(pg.v[o]);
-                    good = true;
-                } else if (d == 0 && tb.table[(int64_t)sq * tb.stride + (j >> pg.page_shift)] >= pg.n_pages) {
-                    report(a.err, LQ8_ERR_ARG);
+    long long total = 0;
+    before -= mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    total *= pg.n_kv;
+    const long long share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
+    long long w0 = share * blockIdx.x;
+    const long long w1 = min(total, w0 + share);
+    if (w0 < w1 && before * pg.n_kv <= w0 && w0 < (before + mine) * pg.n_kv) {
+        for (int r = tid * per;; ++r) {
+            const int u = range_units<S::kUnit>(row_range(a, tb, shift, r));
+            if (w0 < (before + u) * pg.n_kv) {
+                s_row = r;
+                s_base = before * pg.n_kv;
+                break;
+            }
+            before += u;
+        }
+    }
+    __syncthreads();
+    int row = s_row;
+    long long base = s_base;  // units before the row
+    bool first = true;        // of this CTA's pieces
+    while (w0 < w1) {
+        const Range rg = row_range(a, tb, shift, row);
+        const int units = range_units<S::kUnit>(rg);
+        if (units == 0) {
+            ++row;
+            continue;
+        }
+        const int kh = (int)((w0 - base) / units), u = (int)((w0 - base) % units);
+        const int n = (int)min((long long)(units - u), w1 - w0);
+        const int tile0 = (rg.lo / S::kUnit + u) * kWarps + warp;  // the warp's first tile
+        const int32_t* trow = tb.table + (int64_t)rg.seq * tb.stride;
+
+        // Page of the warp's tile j (16-key tiles can end in a second page of 8), -1: nothing to read
+        auto page_entry = [&](int j, int off) {
+            const int64_t p = (int64_t)(tile0 + j * kWarps) * S::kTile + off;
+            if (j >= n || p >= rg.hi || p + min(S::kTile, 1 << shift) <= rg.lo) return -1;
+            const int e = trow[p >> shift];
+            if (e >= pg.n_pages) {
+                report(a.err, LQ8_ERR_ARG);
+                return -1;
+            }
+            return e;
+        };
+        const bool two = S::kTile > (1 << shift);
+        int ent = page_entry(lane, 0), ent2 = two ? page_entry(lane, 8) : -1;
+        int nxt = page_entry(32 + lane, 0), nxt2 = two ? page_entry(32 + lane, 8) : -1;
+        // keys of tile j that count, as bits
+        auto see_bits = [&](int j, int e, int e2) {
+            const int p = (tile0 + j * kWarps) * S::kTile;
+            unsigned bits = (1u << S::kTile) - 1;
+            if (p + S::kTile > rg.hi) bits &= (1u << max(0, rg.hi - p)) - 1;
+            if (p < rg.lo) bits &= rg.lo - p >= S::kTile ? 0u : ~0u << (rg.lo - p);
+            if (e < 0) bits &= two ? 0xff00u : 0u;
+            if (two && e2 < 0) bits &= 0x00ffu;
+            return bits;
+        };
+        int i_issue = 0;  // tiles asked for
+        auto issue = [&]() {
+            const int j = i_issue++;
+            if (j < n) {
+                if ((j & 31) == 0 && j > 0) {
+                    ent = nxt;
+                    ent2 = nxt2;
+                    nxt = page_entry(j + 32 + lane, 0);
+                    nxt2 = two ? page_entry(j + 32 + lane, 8) : -1;
+                }
+                const int e = __shfl_sync(0xffffffffu, ent, j & 31);
+                const int e2 = two ? __shfl_sync(0xffffffffu, ent2, j & 31) : e;
+                const unsigned bits = see_bits(j, e, e2);
+                if (lane == 0) s_see[warp][j % S::kStages] = bits;
+                const int p = (tile0 + j * kWarps) * S::kTile;
+                uint8_t* dst = ring + (j % S::kStages) * 2 * S::kTileBytes;
+                constexpr int RPI = 32 / S::kChunks >= 1 ? 32 / S::kChunks : 1;  // rows per warp-wide copy
+                const int ch = lane % S::kChunks, r0 = lane / S::kChunks;
+#pragma unroll
+                for (int i = 0; i < S::kTile / RPI; ++i) {
+                    const int r = i * RPI + r0;
+                    const int pe = max(0, two && r >= 8 ? e2 : e);
+                    const int64_t off = pe * pg.page_elems +
+                                        (((int64_t)kh << shift) + ((p + r) & ((1 << shift) - 1))) * HD +
+                                        ch * (16 / (int)sizeof(T));
+                    const uint32_t bytes = (bits >> r) & 1 ? 16u : 0u;
+                    uint8_t* d = dst + r * S::kRowBytes + ((ch ^ (r & 7)) << 4);
+                    cp_async16(d, pg.k + off, bytes);
+                    cp_async16(d + S::kTileBytes, pg.v + off, bytes);
                 }
             }
-            ks[r][d] = kv;
-            vs[r][d] = vv;
-            if (d == 0) ok[r] = good;
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) issue();
+
+        const float* q = a.q + ((int64_t)row * a.n_head + kh * G) * HD;
+        State16<T, HD> s16;
+        State32<HD> s32;
+        if constexpr (kF32) {
+            for (int i = tid; i < GP * HD; i += kThreads) qs[i] = i < G * HD ? q[i] * a.scale_log2 : 0.0f;
+            state_init<HD, GP>(s32);
+            __syncthreads();
+        } else {
+            state_init(s16, q, G, a.scale_log2, lane);
         }
-        __syncthreads();
-        for (int i = tid; i < G * kTile; i += kThreads) {
-            const int g = i / kTile, r = i % kTile;
-            float s = 0.0f;
-            for (int d = 0; d < HD; ++d) s = fmaf(qs[g][d], ks[r][d], s);
-            ps[g][r] = ok[r] ? s : -INFINITY;
-        }
-        __syncthreads();
-        const int warp = tid >> 5, lane = tid & 31;
-        for (int g = warp; g < G; g += kThreads / 32) {
-            const float s = ps[g][lane], m0 = sm[g];
-            const float m1 = fmaxf(m0, warp_max(s));
-            const float e = m1 == -INFINITY ? 0.0f : expf(s - m1);
-            const float c = m1 == -INFINITY ? 0.0f : expf(m0 - m1);
-            const float t = warp_sum(e);
-            ps[g][lane] = e;
-            __syncwarp();
-            if (lane == 0) { sm[g] = m1; sl[g] = sl[g] * c + t; sc[g] = c; }
-        }
-        __syncthreads();
-        for (int g = 0; g < G; ++g)
-            for (int u = 0; u * kThreads + tid < HD; ++u) {
-                float x = acc[g][u] * sc[g];
-                for (int r = 0; r < kTile; ++r) x = fmaf(ps[g][r], vs[r][u * kThreads + tid], x);
-                acc[g][u] = x;
+        for (int j = 0; j < n; ++j) {
+            cp_async_wait<S::kStages - 2>();
+            __syncwarp();  // every lane's pieces of tile j have arrived, and tile j - 1 has been read
+            const unsigned bits = s_see[warp][j % S::kStages];
+            issue();
+            if (bits) {
+                const uint8_t* t = ring + (j % S::kStages) * 2 * S::kTileBytes;
+                if constexpr (kF32)
+                    state_tile<HD, GP>(s32, t, t + S::kTileBytes, qs, pb, bits, lane);
+                else
+                    state_tile(s16, smem_u32(t), smem_u32(t + S::kTileBytes), bits, lane);
             }
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+        if constexpr (kF32)
+            state_store<HD, GP>(s32, reinterpret_cast<float*>(ring), ml + warp * kMaxG, lane);
+        else
+            state_store(s16, reinterpret_cast<float*>(ring), ml + warp * kMaxG, lane);
         __syncthreads();
+
+        // ---- join the warps: the result, or a part of it -----------------------------------
+        const bool whole = n == units;
+        const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+        const int64_t ob = ((int64_t)row * a.n_head + kh * G) * HD;
+        for (int e = tid; e < G * (HD / 4); e += kThreads) {
+            const int g = e / (HD / 4);
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kMaxG + g].x);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 x = ml[w * kMaxG + g];
+                const float f = x.x > -INFINITY ? ex2(x.x - m) : 0.0f;
+                const float4 y = reinterpret_cast<const float4*>(smem + w * kRingBytes)[e];
+                l = fmaf(f, x.y, l);
+                o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y);
+                o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+            }
+            if (whole) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                reinterpret_cast<float4*>(a.out + ob)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                if (a.lse && e % (HD / 4) == 0)
+                    a.lse[(int64_t)row * a.n_head + kh * G + g] =
+                        l > 0.0f ? (m - (kHalf ? 15.0f : 0.0f)) * 0.69314718055994531f + logf(l) : -INFINITY;
+            } else {
+                reinterpret_cast<float4*>(a.part_o + (int64_t)slot * G * HD)[e] = o;
+                if (e % (HD / 4) == 0) a.part_ml[slot * G + g] = make_float2(m, l);
+            }
+        }
+        if (!whole) {
+            // ---- the last CTA of the pair joins its parts, in the order of the positions ------
+            const long long seg0 = base + (long long)kh * units;
+            const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + units - 1) / share), parts = c1 - c0 + 1;
+            unsigned int* counter = a.counters + c0;  // only the last pair of a share goes on behind it
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(parts - 1);
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                if (tid == 0) *counter = 0;
+                // the pair starts inside the first CTA's share unless it starts it
+                const int slot0 = 2 * c0 + (seg0 == c0 * share ? 0 : 1);
+                auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (c0 + i); };
+                float* wgt = reinterpret_cast<float*>(smem);  // [parts][G], then sums of the thread groups
+                for (int g = warp; g < G; g += kWarps) {
+                    float m = -INFINITY, l = 0.0f;
+                    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot_of(i) * G + g].x));
+                    m = warp_max(m);
+                    for (int i = lane; i < parts; i += 32) {
+                        const float2 x = __ldcg(&a.part_ml[slot_of(i) * G + g]);
+                        const float f = x.x > -INFINITY ? ex2(x.x - m) : 0.0f;
+                        wgt[i * G + g] = f;
+                        l = fmaf(f, x.y, l);
+                    }
+                    l = warp_sum(l);
+                    if (lane == 0) ml[g] = make_float2(m, l);
+                }
+                __syncthreads();
+                // few heads: several groups of threads share the parts
+                const int vecs = G * (HD / 4), groups = max(1, kThreads / vecs);
+                const int chunk = (parts + groups - 1) / groups;
+                float4* sums = reinterpret_cast<float4*>(smem + kRingBytes);
+                for (int e0 = tid; e0 < vecs * groups; e0 += kThreads) {
+                    const int e = e0 % vecs, gr = e0 / vecs, g = e / (HD / 4);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int i1 = min(parts, (gr + 1) * chunk);
+#pragma unroll 8
+                    for (int i = gr * chunk; i < i1; ++i) {
+                        const float f = wgt[i * G + g];
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + (int64_t)slot_of(i) * G * HD) + e);
+                        o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y);
+                        o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+                    }
+                    sums[e0] = o;
+                }
+                __syncthreads();
+                for (int e = tid; e < vecs; e += kThreads) {
+                    const int g = e / (HD / 4);
+                    float4 o = sums[e];
+                    for (int gr = 1; gr < groups; ++gr) {
+                        const float4 y = sums[gr * vecs + e];
+                        o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+                    }
+                    const float l = ml[g].y, inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    reinterpret_cast<float4*>(a.out + ob)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                    if (a.lse && e % (HD / 4) == 0)
+                        a.lse[(int64_t)row * a.n_head + kh * G + g] =
+                            l > 0.0f ? (ml[g].x - (kHalf ? 15.0f : 0.0f)) * 0.69314718055994531f + logf(l) : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();  // shared memory is free for the next piece
+        first = false;
+        w0 += n;
+        if (kh == pg.n_kv - 1 && u + n == units) {
+            base += (long long)units * pg.n_kv;
+            ++row;
+        }
     }
-    for (int g = 0; g < G; ++g) {
-        for (int u = 0; u * kThreads + tid < HD; ++u)
-            a.out[ob + g * HD + u * kThreads + tid] = sl[g] > 0.0f ? acc[g][u] / sl[g] : 0.0f;
-        if (a.lse && tid == 0)
-            a.lse[(int64_t)row * a.n_head + kh * G + g] = sl[g] > 0.0f ? sm[g] + logf(sl[g]) : -INFINITY;
+    // ---- rows that see nothing, and what is wrong with rows -------------------------------
+    for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const Range rg = row_range(a, tb, shift, r);
+        if (rg.status && tid == 0) report(a.err, rg.status);
+        if (rg.hi > rg.lo) continue;
+        for (int i = tid; i < a.n_head * (HD / 4); i += kThreads)
+            reinterpret_cast<float4*>(a.out + (int64_t)r * a.n_head * HD)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.lse)
+            for (int i = tid; i < a.n_head; i += kThreads) a.lse[(int64_t)r * a.n_head + i] = -INFINITY;
     }
+}
+
+template <typename T, int HD, int GP>
+cudaError_t launch_one(const AttnArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, cudaStream_t s) {
+    // no more CTAs than units the table can hold, or than rows where those are more
+    const int64_t units = (((int64_t)tb.stride * p->page + Shape<T, HD>::kUnit - 1) / Shape<T, HD>::kUnit + 1) *
+                          a.rows * p->n_head_kv;
+    const int64_t grid = std::min<int64_t>(kMaxCtas, std::max<int64_t>(1, (units + kMinShare - 1) / kMinShare));
+    return launch_ex(attention_paged_kernel<T, HD, GP>, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, s, false, a,
+                     page_view<T>(p, layer), tb);
 }
 
 template <typename T>
-cudaError_t launch_attention(const AttnArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, int rows,
-                             cudaStream_t s) {
-    const dim3 grid(p->n_head_kv, rows);
-    if (p->head_dim == 64)
-        return launch_ex(attention_paged_kernel<T, 64>, grid, dim3(kThreads), 0, s, false, a, page_view<T>(p, layer), tb);
-    return launch_ex(attention_paged_kernel<T, 128>, grid, dim3(kThreads), 0, s, false, a, page_view<T>(p, layer), tb);
+cudaError_t launch_attention(const AttnArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, cudaStream_t s) {
+    if constexpr (sizeof(T) == 4) {
+        if (a.n_head / p->n_head_kv > 4)
+            return p->head_dim == 64 ? launch_one<T, 64, 8>(a, p, layer, tb, s) : launch_one<T, 128, 8>(a, p, layer, tb, s);
+    }
+    return p->head_dim == 64 ? launch_one<T, 64, 4>(a, p, layer, tb, s) : launch_one<T, 128, 4>(a, p, layer, tb, s);
+}
+
+template <typename T, int HD, int GP>
+cudaError_t set_attr() {
+    return cudaFuncSetAttribute(attention_paged_kernel<T, HD, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
 
 }  // namespace
+
+cudaError_t init_attention_paged_attributes() {
+    cudaError_t e = set_attr<float, 64, 4>();
+    if (e == cudaSuccess) e = set_attr<float, 64, 8>();
+    if (e == cudaSuccess) e = set_attr<float, 128, 4>();
+    if (e == cudaSuccess) e = set_attr<float, 128, 8>();
+    if (e == cudaSuccess) e = set_attr<__half, 64, 4>();
+    if (e == cudaSuccess) e = set_attr<__half, 128, 4>();
+    if (e == cudaSuccess) e = set_attr<__nv_bfloat16, 64, 4>();
+    if (e == cudaSuccess) e = set_attr<__nv_bfloat16, 128, 4>();
+    return e;
+}
 }  // namespace lq8
 
 using namespace lq8;
@@ -125,7 +717,7 @@ extern "C" {
 
 size_t llama_q8_attention_paged_workspace_bytes(int32_t rows, int32_t n_head, int32_t n_head_kv, int32_t head_dim) {
     if (rows < 0 || n_head <= 0 || n_head_kv <= 0 || n_head % n_head_kv || head_dim <= 0) return 0;
-    return 256;
+    return attn_paged_workspace(n_head, n_head_kv, head_dim, nullptr, nullptr);
 }
 
 llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t layer, const float* q, int32_t rows,
@@ -144,15 +736,19 @@ llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t la
     if ((int64_t)rows * pages->n_head_kv >= (1 << 24)) return LQ8_ERR_UNSUPPORTED;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15) return LQ8_ERR_ARG;
     if (((uintptr_t)pos | (uintptr_t)seq | (uintptr_t)table | (uintptr_t)lse | (uintptr_t)err) & 3) return LQ8_ERR_ARG;
-    if (workspace_bytes < llama_q8_attention_paged_workspace_bytes(rows, n_head, pages->n_head_kv, pages->head_dim))
+    AttnArgs a{};
+    if (workspace_bytes < attn_paged_workspace(n_head, pages->n_head_kv, pages->head_dim, &a, workspace))
         return LQ8_ERR_ARG;
     if (rows == 0) return LQ8_OK;
-    AttnArgs a{q, pos, seq, n_head, scale > 0.0f ? scale : 1.0f / sqrtf((float)pages->head_dim), window, out, lse, err};
+    if (ensure_kernel_attributes() != cudaSuccess) return LQ8_ERR_CUDA;
+    a.q = q, a.pos = pos, a.seq = seq, a.rows = rows, a.n_head = n_head, a.window = window;
+    a.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)pages->head_dim)) * 1.4426950408889634f;
+    a.out = out, a.lse = lse, a.err = err;
     const TableView tb{table, n_seq, table_stride};
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = pages->type == LLAMA_Q8_GGUF_F32   ? launch_attention<float>(a, pages, layer, tb, rows, s)
-                    : pages->type == LLAMA_Q8_GGUF_F16 ? launch_attention<__half>(a, pages, layer, tb, rows, s)
-                                                       : launch_attention<__nv_bfloat16>(a, pages, layer, tb, rows, s);
+    cudaError_t e = pages->type == LLAMA_Q8_GGUF_F32   ? launch_attention<float>(a, pages, layer, tb, s)
+                    : pages->type == LLAMA_Q8_GGUF_F16 ? launch_attention<__half>(a, pages, layer, tb, s)
+                                                       : launch_attention<__nv_bfloat16>(a, pages, layer, tb, s);
     return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
 

@@ -16,7 +16,7 @@
 //
 // Bound: memory (each logit read once).
 #include "kernels.cuh"
-#include "llama_q8.h"
+#include "paged.cuh"
 
 namespace lq8 {
 namespace {
@@ -62,7 +62,7 @@ size_t beam_workspace(int groups, int beams, int n_vocab, int n_out, BeamArgs* a
         o += (bytes + 255) / 256 * 256;
         return at;
     };
-    const size_t c = take(4 * (size_t)groups), t = take(sizeof(ChunkStat) * (size_t)(rows * chunks)),
+    const size_t c = take(kCounterBytes), t = take(sizeof(ChunkStat) * (size_t)(rows * chunks)),
                  d = take(sizeof(ChunkCand) * (size_t)(rows * chunks) * n_out);
     if (a) {
         uint8_t* w = reinterpret_cast<uint8_t*>(ws);
@@ -291,7 +291,7 @@ static bool beam_sizes_ok(int32_t groups, int32_t beams, int32_t n_vocab, int32_
     return groups >= 0 && beams > 0 && n_vocab > 0 && n_out > 0 && n_out <= (int64_t)beams * n_vocab;
 }
 static bool beam_sizes_supported(int32_t groups, int32_t beams, int32_t n_out) {
-    return beams <= kBeamMax && n_out <= kBeamMax && (int64_t)groups * beams <= 65535;
+    return beams <= kBeamMax && n_out <= kBeamMax && (int64_t)groups * beams < kMaxCounters;
 }
 
 size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out) {

@@ -14,6 +14,12 @@ namespace lq8 {
 
 constexpr int kPageMin = 8, kPageMax = 256;
 
+// Every workspace starts with the completion counters, in an area of one size,
+// so that no call's data lie where another call (of other sizes, or of another
+// operator) has its counters.
+constexpr int kMaxCounters = 65536;
+constexpr size_t kCounterBytes = 4 * (size_t)kMaxCounters;
+
 inline int page_type_bytes(int type) {
     return type == LLAMA_Q8_GGUF_F32 ? 4 : (type == LLAMA_Q8_GGUF_F16 || type == LLAMA_Q8_GGUF_BF16) ? 2 : 0;
 }
@@ -71,9 +77,5 @@ __device__ __forceinline__ int page_of(const TableView& t, int seq, int block, i
     const int p = t.table[(int64_t)seq * t.stride + block];
     return p < n_pages ? p : -1;
 }
-
-// attention_paged.cu
-cudaError_t init_attention_paged_attributes();
-// pages.cu, beam.cu: nothing to initialise
 
 }  // namespace lq8

@@ -71,7 +71,7 @@ struct ForkArgs {
 };
 
 size_t fork_workspace(int rows_in, int rows_out, int width, ForkArgs* a, void* ws) {
-    size_t o = 0;
+    size_t o = kCounterBytes;
     auto take = [&](size_t bytes) {
         const size_t at = o;
         o += (bytes + 255) / 256 * 256;
@@ -306,13 +306,13 @@ struct CompactArgs {
 size_t compact_workspace(int n_pages, CompactArgs* a, void* ws) {
     const size_t all = (4 * (size_t)n_pages + 255) / 256 * 256, part = (4 * ((size_t)n_pages / 2 + 1) + 255) / 256 * 256;
     if (a) {
-        uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+        uint8_t* w = reinterpret_cast<uint8_t*>(ws) + kCounterBytes;
         a->n_moves = reinterpret_cast<int32_t*>(w);
         a->to = reinterpret_cast<int32_t*>(w + 256);
         a->from = reinterpret_cast<int32_t*>(w + 256 + all);
         a->hole = reinterpret_cast<int32_t*>(w + 256 + all + part);
     }
-    return 256 + all + 2 * part;
+    return kCounterBytes + 256 + all + 2 * part;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs a) {

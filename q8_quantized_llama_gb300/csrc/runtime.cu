@@ -25,6 +25,7 @@ using namespace lq8;
 namespace lq8 {
 cudaError_t init_gemv_attributes();
 cudaError_t init_attention_attributes();
+cudaError_t init_attention_paged_attributes();
 
 namespace {
 constexpr int kMaxDevices = 64;
@@ -45,6 +46,7 @@ cudaError_t ensure_kernel_attributes() {
     if (err == cudaSuccess) err = init_attention_attributes();
     if (err == cudaSuccess) err = init_gemm_tc_attributes();
     if (err == cudaSuccess) err = init_gemv_fmt_attributes();
+    if (err == cudaSuccess) err = init_attention_paged_attributes();
     if (err == cudaSuccess) g_init_done[dev] = true;
     return err;
 }

@@ -720,6 +720,35 @@ def test_beam_search_captured_in_a_graph():
     assert int(lp.err[0]) == 0
 
 
+def test_one_workspace_for_all_operators_in_turn():
+    """Calls of every operator and of other sizes leave the counters of the next call alone."""
+    B = binding()
+    attn = [paged_case([900] * 3, 32, 8, 128, 32, "bf16", 31), paged_case([4000], 7, 1, 128, 8, "f32", 32)]
+    want = [run_attention(B, *c[:3], c[3], c[4])[0] for c in attn]
+    ws = zeros(64 << 20)
+    table, refs = held([40, 41], 8, 40, 8, 1)
+    for groups, beams in [(1, 2), (300, 4), (5, 64), (9000, 1)]:
+        x = torch.randn((groups * beams, 500), device="cuda")
+        s = torch.zeros(groups * beams, device="cuda")
+        first = run_beam(B, x, s, beams, 5)
+        for c, w in zip(attn, want):
+            assert torch.equal(run_attention(B, *c[:3], c[3], c[4], ws=ws)[0], w)
+            got = run_beam(B, x, s, beams, 5, ws=ws)
+            for a, b in zip(first, got):
+                np.testing.assert_array_equal(a, b)
+            k, v = pool(1, 40, 1, 8, 64, "f32", 1)
+            out = [i32([0] * 3), i32(np.zeros((3, 8))), i32([0] * 40), i32([0])]
+            B.llama_q8_pages_fork(B.make_pages(k, v), 2, i32([40, 41]), i32(table), 8, i32(refs), 3, i32([0, 1, 1]), 1,
+                                  out[0], out[1], out[2], ws, ws.numel(), out[3])
+            wl, wt, wr, _ = P.fork(np.array([40, 41]), table, refs, [0, 1, 1], 1, 8)
+            np.testing.assert_array_equal(host(out[1]), wt)
+            np.testing.assert_array_equal(host(out[2]), wr)
+            used = i32([0])
+            B.llama_q8_pages_compact(B.make_pages(k, v), 3, out[1], 8, out[2], i32(np.zeros((3, 8))), i32([0] * 40),
+                                     used, ws, ws.numel(), out[3])
+            assert int(used[0]) == (wr > 0).sum() and int(out[3][0]) == 0
+
+
 def test_calls_on_two_streams_with_their_own_workspaces():
     B = binding()
     cases = [paged_case([1500, 3, 800], 32, 8, 128, 16, "bf16", 21), paged_case([40, 2500], 9, 3, 64, 32, "f32", 22)]
