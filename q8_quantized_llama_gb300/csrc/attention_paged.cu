@@ -231,24 +231,31 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
     constexpr int RB = HD * 2;
     const T tag{};
     const int l8 = lane & 7, mi = lane >> 3, t = lane & 3;
-    float c[2][4] = {};
+    // short chains: even and odd steps, and the third part of q, each in sums of their own (the tensor cores cut
+    // digits off at every addition to a sum, in proportion to the sum)
+    float c[2][2][4] = {}, c3[2][4] = {};
 #pragma unroll
     for (int k = 0; k < HD / 32; ++k) {
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             uint32_t b[4];
             ldsm4(b, ks + (n * 8 + l8) * RB + (((k * 4 + mi) ^ l8) << 4));
-            mma16(c[n], s.q[2 * k], b[0], b[1], tag);
-            mma16(c[n], s.q[2 * k + 1], b[2], b[3], tag);
+            mma16(c[n][0], s.q[2 * k], b[0], b[1], tag);
+            mma16(c[n][1], s.q[2 * k + 1], b[2], b[3], tag);
             if (!kHalf) {
                 const uint32_t a0[4] = {s.q3[2 * k][0], 0, s.q3[2 * k][1], 0};
                 const uint32_t a1[4] = {s.q3[2 * k + 1][0], 0, s.q3[2 * k + 1][1], 0};
-                mma16(c[n], a0, b[0], b[1], tag);
-                mma16(c[n], a1, b[2], b[3], tag);
+                mma16(c3[n], a0, b[0], b[1], tag);
+                mma16(c3[n], a1, b[2], b[3], tag);
             }
         }
     }
-    float x[4] = {c[0][0] + c[0][2], c[0][1] + c[0][3], c[1][0] + c[1][2], c[1][1] + c[1][3]};
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int n = j >> 1, i = j & 1;
+        x[j] = (c[n][0][i] + c[n][1][i]) + (c[n][0][i + 2] + c[n][1][i + 2] + c3[n][i]);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (kHalf) x[j] *= s.q_inv;
