@@ -8,13 +8,17 @@
 // chosen. The last CTA of a group to finish (a counter in the workspace) joins
 // the chunks' sums in double and picks the n_out largest totals.
 //
-// Largest of many by a threshold: of the 256 threads' own maxima the n_out-th
-// largest is a bound that at least n_out values reach, and at most n_out
-// threads hold any that do; those few values are ranked by counting the larger
-// ones. Values compare as (value, lowest index) keys, all different, so ties,
-// also rows of equal values, keep the bound exact.
+// Largest of many by a bound: lanes form groups (32, 64 or 128 per CTA, at
+// least twice n_out); n_out groups reach the n_out-th largest of the groups'
+// maxima, so at least n_out values do, and only a few more. Those few are
+// ranked by counting the larger ones, as keys (value, lowest index) that all
+// differ. Where equal values leave too many of them (a row of one value, say),
+// the bound is taken again over the threads' keys, which leaves at most IT per
+// chosen thread.
 //
-// Bound: memory (each logit read once).
+// Bound: memory (each logit read once); issue slots are next: about 8 per value
+// (load, maximum, subtract, scale, ex2 and add, packed in pairs where there is
+// a packed form, and one comparison).
 #include "kernels.cuh"
 #include "paged.cuh"
 
@@ -94,21 +98,43 @@ __device__ __forceinline__ double f64_of_key(unsigned long long k) {
     return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
+// Lanes per group: 32, 64 or 128 groups of the CTA's 256 threads.
+__device__ __forceinline__ int group_lanes(int n_out) { return n_out <= 16 ? 8 : n_out <= 32 ? 4 : 2; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 template <int IT>
 __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(BeamArgs a) {
-    constexpr int kCand = kBeamMax * IT, kFinal = kBeamMax * kPickItems;
+    constexpr int kCand = kBeamMax * IT;
+    constexpr int kFew = 256;                          // candidates the first bound may leave
+    constexpr int kFinal = 16 * 8 * kPickItems;        // n_out groups of group_lanes threads: 16 x 8, 32 x 4, 64 x 2
     // the chunk's part and the group's part use the memory one after the other
     __shared__ __align__(16) union {
         struct {
             unsigned long long best[kBeamThreads], cand[kCand];
         } c;
         struct {
-            Pick best[kBeamThreads], cand[kFinal], keep[kBeamMax];
+            Pick best[kBeamThreads / 2], cand[kFinal], keep[kBeamMax];
             double lse[kBeamMax];
         } g;
     } sm;
-    __shared__ float red_m[kBeamThreads / 32], red_s[kBeamThreads / 32];
+    __shared__ float red_m[kBeamThreads / 32], red_s[kBeamThreads / 32], s_top[kBeamThreads / 2];
     __shared__ unsigned long long s_bound;
+    __shared__ float s_floor;
     __shared__ Pick s_pick;
     __shared__ int s_n, s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -117,69 +143,113 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(BeamArgs a) {
     const int64_t base = (int64_t)chunk * kBeamThreads * IT;
     const int n = (int)min((int64_t)kBeamThreads * IT, a.n_vocab - base);
     const float* x = a.logits + row * a.stride + base;
+    const int gl = group_lanes(a.n_out), groups = kBeamThreads / gl;
 
     float v[IT];
+    if (n == kBeamThreads * IT) {
 #pragma unroll
-    for (int j = 0; j < IT; ++j) {
-        const int i = j * kBeamThreads + tid;
-        v[j] = i < n ? __ldcs(x + i) : -INFINITY;
-    }
-    float m = -INFINITY, s = 0.0f;
-    bool nan = false;
-    int at = -1;
+        for (int j = 0; j < IT; ++j) v[j] = __ldcs(x + j * kBeamThreads + tid);
+    } else {
 #pragma unroll
-    for (int j = 0; j < IT; ++j) {
-        nan |= v[j] != v[j];
-        v[j] = v[j] != v[j] ? -INFINITY : v[j] + 0.0f;  // -0 and 0 are one value
-        const int i = j * kBeamThreads + tid;
-        if (i < n && (at < 0 || v[j] > m)) { m = v[j]; at = i; }
+        for (int j = 0; j < IT; ++j) v[j] = j * kBeamThreads + tid < n ? __ldcs(x + j * kBeamThreads + tid) : -INFINITY;
     }
-    if (m > -INFINITY) {
+    float m = v[0];
 #pragma unroll
-        for (int j = 0; j < IT; ++j) s += expf(v[j] - m);
+    for (int j = 1; j < IT; ++j) m = fmaxf(m, v[j]);  // of the numbers; -inf if there is none
+    if (m != m) m = -INFINITY;
+    // exponentials of the differences; a NaN or +inf makes the sum NaN
+    const float ref = m > -INFINITY ? m : 0.0f;
+    uint64_t sum2 = 0;
+    const uint64_t ref2 = pack_f2(ref, ref), log2e = pack_f2(1.4426950408889634f, 1.4426950408889634f);
+#pragma unroll
+    for (int j = 0; j < IT; j += 2) {
+        const uint64_t t = mul_f2(sub_f2(pack_f2(v[j], v[j + 1]), ref2), log2e);
+        sum2 = add_f2(sum2, pack_f2(ex2(f2_lo(t)), ex2(f2_hi(t))));
     }
-    if (nan) s = NAN;
-    const unsigned long long mine = at >= 0 ? argmax_key(m, at) : 0ull;
-    sm.c.best[tid] = mine;
-    if (tid == 0) { s_bound = 0; s_n = 0; }
-    // sum of the chunk
-    float wm = warp_max(m);
-    float ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
-    if (lane == 0) { red_m[warp] = wm; red_s[warp] = ws; }
+    const float s = f2_lo(sum2) + f2_hi(sum2);
+    // the groups' maxima, the chunk's maximum and sum
+    float gm = m;
+    for (int o = 1; o < gl; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+    if (tid % gl == 0) s_top[tid / gl] = gm;
+    {
+        const float wm = warp_max(gm);
+        const float ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
+        if (lane == 0) { red_m[warp] = wm; red_s[warp] = ws; }
+    }
+    if (tid == 0) s_n = 0;
     __syncthreads();
-    if (warp == 0) {
-        m = lane < kBeamThreads / 32 ? red_m[lane] : -INFINITY;
-        s = lane < kBeamThreads / 32 ? red_s[lane] : 0.0f;
-        wm = warp_max(m);
-        ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
+    if (tid < groups) {
+        const float mine = s_top[tid];
+        int over = 0, same = 0;
+#pragma unroll 8
+        for (int t = 0; t < groups; ++t) {
+            over += s_top[t] > mine;
+            same += s_top[t] == mine;
+        }
+        // the same value from every group that has it
+        if (over < a.n_out && over + same >= a.n_out) s_floor = mine;
+    }
+    if (warp == kBeamThreads / 32 - 1) {
+        const float wm0 = lane < kBeamThreads / 32 ? red_m[lane] : -INFINITY;
+        const float ws0 = lane < kBeamThreads / 32 ? red_s[lane] : 0.0f;
+        const float wm = warp_max(wm0);
+        const float ws = warp_sum(wm0 > -INFINITY ? ws0 * expf(wm0 - wm) : ws0);
         if (lane == 0) a.stat[row * a.chunks + chunk] = ChunkStat{wm, ws};
     }
-    // the n_out-th largest of the threads' maxima
-    if (mine) {
-        int above_me = 0;
-        for (int t = 0; t < kBeamThreads; ++t) above_me += sm.c.best[t] > mine;
-        if (above_me == a.n_out - 1) s_bound = mine;
-    }
     __syncthreads();
-    const unsigned long long bound = s_bound;
-    if (mine && mine >= bound) {
+    const float floor = s_floor;
+    if (m >= floor) {
 #pragma unroll
         for (int j = 0; j < IT; ++j) {
             const int i = j * kBeamThreads + tid;
-            const unsigned long long key = argmax_key(v[j], i);
-            if (i < n && key >= bound) sm.c.cand[atomicAdd(&s_n, 1)] = key;
+            if (v[j] >= floor && i < n) {
+                const int at = atomicAdd(&s_n, 1);
+                if (at < kFew) sm.c.cand[at] = argmax_key(v[j] + 0.0f, i);  // -0 and 0 are one value
+            }
         }
     }
     __syncthreads();
+    int nc = s_n;
+    if (nc > kFew) {
+        // many equal values: the n_out-th largest of the threads' keys (m and its first place)
+        int at = -1;
+#pragma unroll
+        for (int j = IT - 1; j >= 0; --j) {
+            if (v[j] != v[j]) v[j] = -INFINITY;
+            if (v[j] == m && j * kBeamThreads + tid < n) at = j * kBeamThreads + tid;
+        }
+        const unsigned long long mine = at >= 0 ? argmax_key(m + 0.0f, at) : 0ull;
+        sm.c.best[tid] = mine;
+        __syncthreads();
+        if (tid == 0) { s_bound = 0; s_n = 0; }
+        __syncthreads();
+        if (mine) {
+            int above_me = 0;
+            for (int t = 0; t < kBeamThreads; ++t) above_me += sm.c.best[t] > mine;
+            if (above_me == a.n_out - 1) s_bound = mine;
+        }
+        __syncthreads();
+        const unsigned long long bound = s_bound;
+        if (mine && mine >= bound) {
+#pragma unroll
+            for (int j = 0; j < IT; ++j) {
+                const int i = j * kBeamThreads + tid;
+                const unsigned long long key = argmax_key(v[j] + 0.0f, i);
+                if (i < n && key >= bound) sm.c.cand[atomicAdd(&s_n, 1)] = key;
+            }
+        }
+        __syncthreads();
+        nc = s_n;
+    }
     ChunkCand* out = a.cand + (row * a.chunks + chunk) * a.n_out;
-    const int nc = s_n;
     for (int c = tid; c < nc; c += kBeamThreads) {
         const unsigned long long key = sm.c.cand[c];
         int r = 0;
         for (int t = 0; t < nc; ++t) r += sm.c.cand[t] > key;
         if (r < a.n_out) out[r] = ChunkCand{key_value(key), (int32_t)base + argmax_key_index(key)};
     }
-    for (int r = n + tid; r < a.n_out; r += kBeamThreads) out[r] = ChunkCand{-INFINITY, -1};
+    // fewer values than n_out (NaN are none: their row is not chosen from)
+    for (int r = nc + tid; r < a.n_out; r += kBeamThreads) out[r] = ChunkCand{-INFINITY, -1};
 
     __threadfence();
     __syncthreads();
@@ -203,7 +273,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(BeamArgs a) {
         for (int c = lane; c < a.chunks; c += 32) {
             const float cm = __ldcg(&st[c].m);
             const double cs = (double)__ldcg(&st[c].s);
-            sum += cm > -INFINITY ? cs * exp((double)cm - (double)top) : cs;  // a chunk of NaN alone: cs is NaN
+            sum += cm > -INFINITY ? cs * (double)expf(cm - top) : cs;  // a chunk of NaN alone: cs is NaN
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -245,14 +315,20 @@ __global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(BeamArgs a) {
             if (above(p[j], best)) best = p[j];
         }
         i0 += fresh;
+        for (int o = 1; o < gl; o <<= 1) {
+            const Pick y{__shfl_xor_sync(0xffffffffu, best.hi, o), __shfl_xor_sync(0xffffffffu, best.lo, o)};
+            if (above(y, best)) best = y;
+        }
         __syncthreads();
-        sm.g.best[tid] = best;
+        if (tid % gl == 0) sm.g.best[tid / gl] = best;
         if (tid == 0) { s_pick = Pick{0, 0}; s_n = 0; }
         __syncthreads();
-        if (best.lo) {
+        if (tid < groups) {
+            const Pick mine = sm.g.best[tid];
             int above_me = 0;
-            for (int t = 0; t < kBeamThreads; ++t) above_me += above(sm.g.best[t], best);
-            if (above_me == a.n_out - 1) s_pick = best;
+#pragma unroll 8
+            for (int t = 0; t < groups; ++t) above_me += above(sm.g.best[t], mine);
+            if (mine.lo && above_me == a.n_out - 1) s_pick = mine;
         }
         __syncthreads();
         const Pick bnd = s_pick;
