@@ -640,12 +640,13 @@ llama_q8_status llama_q8_pages_compact(const llama_q8_pages* pages, int32_t rows
  * largest, in falling order, equal totals with the lowest (beam, token) first:
  * out_scores[groups][n_out], out_parent (the row, group * beams + beam: the
  * parent array of llama_q8_pages_fork when n_out == beams) and out_token.
- * Totals are formed in double and rounded to f32 at the end. A logit of -inf
+ * With n_out == beams, out_scores may be scores; no other array may overlap.
+ * Totals are formed in two f32 parts (48 bits) and rounded to f32 at the end. A logit of -inf
  * forbids its token (total -inf). A beam whose score is not finite (a padding
  * or finished beam), or whose row has a NaN or +inf or nothing but -inf, has
  * totals -inf: it is chosen only where a group has fewer than n_out others.
  * groups, beams, n_vocab > 0, n_out in 1 .. beams * n_vocab (LQ8_ERR_ARG); beams
- * and n_out <= 64, groups * beams <= 65535 (LQ8_ERR_UNSUPPORTED). groups == 0
+ * and n_out <= 64, groups * beams <= 65535, n_vocab <= 2^28 (LQ8_ERR_UNSUPPORTED). groups == 0
  * does nothing. Enqueues one kernel. */
 size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out);
 llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride, int32_t groups, int32_t beams,

@@ -601,12 +601,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             const long long seg0 = base + (long long)kh * units;
             const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + units - 1) / share), parts = c1 - c0 + 1;
             unsigned int* counter = a.counters + c0;  // only the last pair of a share goes on behind it
-            __threadfence();
             __syncthreads();
-            if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(parts - 1);
+            if (tid == 0) s_last = take_ticket(counter) == (unsigned)(parts - 1);
             __syncthreads();
             if (s_last) {
-                __threadfence();
                 if (tid == 0) *counter = 0;
                 // the pair starts inside the first CTA's share unless it starts it
                 const int slot0 = 2 * c0 + (seg0 == c0 * share ? 0 : 1);

@@ -2,23 +2,29 @@
 // over beams x vocabulary, in one kernel that reads the logits once.
 //
 // total(beam, token) = score[beam] + logit - lse[beam], lse = ln sum exp(logit).
-// A CTA takes one chunk of one row's logits into registers and gets from them
-// the chunk's maximum, its sum of exponentials and its n_out largest logits:
-// within a row totals rise with logits, so no other value of the chunk can be
-// chosen. The last CTA of a group to finish (a counter in the workspace) joins
-// the chunks' sums in double and picks the n_out largest totals.
+// A CTA goes through its piece of a row, a block of values per thread at a time
+// with the next block's loads in flight, and gets the piece's sum of exponentials
+// (a running maximum and sum per thread) and its n_out largest logits: within a
+// row totals rise with logits, so no other value of the piece can be chosen. The
+// last CTA of a group to finish (a counter in the workspace) joins the pieces'
+// sums and picks the n_out largest totals.
 //
-// Largest of many by a bound: lanes form groups (32, 64 or 128 per CTA, at
-// least twice n_out); n_out groups reach the n_out-th largest of the groups'
-// maxima, so at least n_out values do, and only a few more. Those few are
-// ranked by counting the larger ones, as keys (value, lowest index) that all
-// differ. Where equal values leave too many of them (a row of one value, say),
-// the bound is taken again over the threads' keys, which leaves at most IT per
-// chosen thread.
+// Largest of many by a bound: in the first block lanes form groups (32, 64 or
+// 128 per CTA, at least twice n_out); n_out groups reach the n_out-th largest of
+// the groups' maxima, so at least n_out values do, and only a few more. They
+// are kept, and of the later blocks the values above the bound: an equal one
+// there has a higher index and loses. When the list has grown by 16 or half it is
+// cut to its n_out best, and the bound rises: keys (value, lowest index), which
+// all differ, are ranked by counting the larger ones.
 //
-// Bound: memory (each logit read once); issue slots are next: about 8 per value
-// (load, maximum, subtract, scale, ex2 and add, packed in pairs where there is
-// a packed form, and one comparison).
+// Bound: issue slots and the latency of the first and last steps of a piece
+// rather than memory: 240 rows of 100003 take 34 us, 14 of them for the bytes.
+// Not kept: one CTA per 8192 values without a list (46 us: barriers and fences);
+// a pass of maxima and sums alone, then a second look at the threads that reach
+// the bound (53 us: what they look up again has left L2); a list kept to the
+// bound in every block (35 us).
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "paged.cuh"
 
@@ -28,6 +34,7 @@ namespace {
 constexpr int kBeamThreads = 256;
 constexpr int kBeamMax = 64;   // beams per group, results per group
 constexpr int kPickItems = 4;  // candidates per thread and pass of the final choice
+constexpr int kBeamVocab = 1 << 28;  // longest row: 64 beams x 64 results x its chunks stay below 2^31 - 1024
 
 struct ChunkStat {
     float m, s;  // largest logit and sum of exp(logit - m); NaN s: a NaN or +inf among them
@@ -41,25 +48,39 @@ struct BeamArgs {
     const float* logits;
     int64_t stride;
     const float* scores;
-    int beams, n_vocab, n_out, chunks;
+    int beams, n_vocab, n_out;
+    int chunks, blocks;  // pieces per row at most, blocks per row
+    int share, units;      // blocks per CTA, of all rows
     float* out_scores;
     int32_t *out_parent, *out_token;
     unsigned int* counters;  // [groups], zero between launches
-    ChunkStat* stat;         // [groups * beams][chunks]
+    ChunkStat* stat;         // [groups * beams][chunks], by the CTA's place among the row's
     ChunkCand* cand;         // [groups * beams][chunks][n_out]
 };
 
-// Few rows: short chunks, so that more SMs have one. Long chunks otherwise:
-// fewer candidates to join.
-inline int beam_items(int64_t rows, int n_vocab) {
-    const int64_t ctas = rows * (((int64_t)n_vocab + kBeamThreads * 32 - 1) / (kBeamThreads * 32));
-    return ctas >= 2 * 152 ? 32 : 8;
+// How the work is cut: rows in blocks of 256 * items values, the blocks of all
+// rows dealt evenly to one wave of CTAs (four per SM), `share` blocks each, so
+// that a row is in pieces of up to `chunks` CTAs and a CTA may hold pieces of
+// several rows. Where that would leave most SMs without one, blocks of half the
+// size, one per CTA.
+struct BeamCut {
+    int items, blocks, chunks;
+    int share, ctas;
+};
+constexpr int kBeamWave = 152 * 4;
+inline BeamCut beam_cut(int64_t rows, int n_vocab) {
+    const int64_t big = ((int64_t)n_vocab + kBeamThreads * 16 - 1) / (kBeamThreads * 16);
+    const bool few = rows * big <= kBeamWave / 2;
+    const int64_t blocks = few ? ((int64_t)n_vocab + kBeamThreads * 8 - 1) / (kBeamThreads * 8) : big;
+    const int64_t share = few ? 1 : (rows * blocks + kBeamWave - 1) / kBeamWave;
+    return BeamCut{few ? 8 : 16, (int)blocks, (int)((blocks - 1 + share - 1) / share + 1), (int)share,
+                   (int)((rows * blocks + share - 1) / share)};
 }
 
 size_t beam_workspace(int groups, int beams, int n_vocab, int n_out, BeamArgs* a, void* ws) {
     const int64_t rows = (int64_t)groups * beams;
-    const int per = kBeamThreads * beam_items(rows, n_vocab);
-    const int64_t chunks = ((int64_t)n_vocab + per - 1) / per;
+    const BeamCut cut = beam_cut(std::max<int64_t>(rows, 1), n_vocab);
+    const int64_t chunks = cut.chunks;
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -73,7 +94,10 @@ size_t beam_workspace(int groups, int beams, int n_vocab, int n_out, BeamArgs* a
         a->counters = reinterpret_cast<unsigned int*>(w + c);
         a->stat = reinterpret_cast<ChunkStat*>(w + t);
         a->cand = reinterpret_cast<ChunkCand*>(w + d);
-        a->chunks = (int)chunks;
+        a->chunks = cut.chunks;
+        a->blocks = cut.blocks;
+        a->share = cut.share;
+        a->units = (int)(rows * cut.blocks);
     }
     return o;
 }
@@ -83,23 +107,214 @@ __device__ __forceinline__ float key_value(unsigned long long key) {
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
-// A total and its place as a pair that compares like (total, lowest place).
+// A total and its slot among the group's candidates (beam, chunk, place in the
+// chunk's falling list). Of equal totals the lowest slot is the lowest (beam,
+// token): a chunk's equal values are listed by index.
 struct Pick {
-    unsigned long long hi, lo;  // order-preserving bits of the total; ~(beam << 32 | token)
+    unsigned long long key;  // order-preserving bits of the total, 0: none
+    unsigned slot;
 };
 __device__ __forceinline__ bool above(const Pick& a, const Pick& b) {
-    return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+    // no short circuits: as branches they made the counting loops wait 100 cycles and more per entry
+    return (a.key > b.key) | ((a.key == b.key) & (a.slot < b.slot));
 }
-__device__ __forceinline__ unsigned long long f64_order_key(double v) {
-    const unsigned long long u = (unsigned long long)__double_as_longlong(v);
-    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+// Totals and log sums are unevaluated sums hi + lo of two f32 numbers (about 48
+// bits): double arithmetic runs at a small fraction of f32's rate here.
+struct Sum2 {
+    float hi, lo;
+};
+// a + b exactly: the rounded sum and what the rounding dropped (Knuth's two-sum)
+__device__ __forceinline__ Sum2 two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Sum2{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ double f64_of_key(unsigned long long k) {
-    return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+__device__ __forceinline__ Sum2 add2(Sum2 x, float y) {
+    const Sum2 s = two_sum(x.hi, y);
+    return two_sum(s.hi, __fadd_rn(s.lo, x.lo));
+}
+__device__ __forceinline__ unsigned long long total_key(Sum2 t) {
+    if (!(t.hi > -INFINITY)) t = Sum2{-INFINITY, 0.0f};  // two_sum of an infinity leaves NaN in lo
+    return ((unsigned long long)f32_order_key(t.hi + 0.0f) << 32) | f32_order_key(t.lo + 0.0f);
 }
 
 // Lanes per group: 32, 64 or 128 groups of the CTA's 256 threads.
 __device__ __forceinline__ int group_lanes(int n_out) { return n_out <= 16 ? 8 : n_out <= 32 ? 4 : 2; }
+
+// CTAs that hold a row's pieces: from first_cta on, row_pieces of them.
+__device__ __forceinline__ int first_cta(const BeamArgs& a, int row) { return row * a.blocks / a.share; }
+__device__ __forceinline__ int row_pieces(const BeamArgs& a, int row) {
+    return ((row + 1) * a.blocks - 1) / a.share - first_cta(a, row) + 1;
+}
+
+constexpr int kFinal = 16 * 8 * kPickItems;  // n_out groups of group_lanes threads: 16 x 8, 32 x 4, 64 x 2
+struct ChooseShared {
+    Pick best[kBeamThreads], cand[kFinal], keep[kBeamMax], bound;
+    Sum2 add[kBeamMax];  // score - lse of each beam; not finite: its totals are all -inf
+    int pieces[kBeamMax], n;
+};
+
+// A group whose pieces are all written: the log sums of its rows, then the best totals. All threads of a CTA.
+__device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int group) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gl = group_lanes(a.n_out), groups = kBeamThreads / gl;
+    const int64_t row0 = (int64_t)group * a.beams;
+    const int lists = a.beams * a.chunks, all = lists * a.n_out;  // below 2^31 (kBeamVocab)
+    const ChunkCand* cand = a.cand + row0 * a.chunks * (int64_t)a.n_out;
+    auto fetch = [&](int i) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(cand + i));
+        return ChunkCand{x.x, __float_as_int(x.y)};
+    };
+    auto pick = [&](const ChunkCand& c, int i) {
+        const int list = i / a.n_out, b = list / a.chunks, piece = list - b * a.chunks;
+        const Sum2 add = sm.add[b];
+        Pick p{0ull, (unsigned)i};
+        if (!isfinite(add.hi)) {  // the lowest tokens of the beam
+            if (piece == 0 && i - list * a.n_out < a.n_vocab) p.key = total_key(Sum2{-INFINITY, 0.0f});
+        } else if (piece < sm.pieces[b] && c.token >= 0) {
+            p.key = total_key(add2(add, c.logit));
+        }
+        return p;
+    };
+    auto put = [&](const Pick& p, int r) {
+        const int list = (int)p.slot / a.n_out, b = list / a.chunks;
+        const int64_t o = (int64_t)group * a.n_out + r;
+        a.out_scores[o] = key_value(p.key);
+        a.out_parent[o] = (int32_t)(row0 + b);
+        a.out_token[o] = isfinite(sm.add[b].hi) ? fetch((int)p.slot).token : (int)p.slot - list * a.n_out;
+    };
+    // candidates asked for before the sums: two per thread, or the heads of the lists
+    const bool direct = all <= kFinal;
+    const ChunkCand none{-INFINITY, -1};
+    const int i0 = direct ? tid : tid * a.n_out, i1 = direct ? tid + kBeamThreads : i0 + 1;
+    const ChunkCand c0 = i0 < all ? fetch(i0) : none, c1 = i1 < all ? fetch(i1) : none;
+    for (int b = warp; b < a.beams; b += kBeamThreads / 32) {
+        const ChunkStat* st = a.stat + (row0 + b) * a.chunks;
+        const int pieces = row_pieces(a, (int)row0 + b);
+        const float sc = a.scores[row0 + b];
+        float top = -INFINITY, part = 0.0f;  // the lane's pieces
+        for (int c = lane; c < pieces; c += 32) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(st + c));
+            const float m1 = fmaxf(top, x.x);
+            // a piece of -inf alone adds 0, one of NaN alone NaN
+            part = (top > -INFINITY ? part * expf(top - m1) : part) + (x.x > -INFINITY ? x.y * expf(x.x - m1) : x.y);
+            top = m1;
+        }
+        const float all_top = warp_max(top);
+        Sum2 sum{top > -INFINITY ? part * expf(top - all_top) : part, 0.0f};
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float y = __shfl_xor_sync(0xffffffffu, sum.hi, o), z = __shfl_xor_sync(0xffffffffu, sum.lo, o);
+            sum = add2(add2(sum, y), z);
+        }
+        if (lane == 0) {
+            // ln of 2^e f, f in [1/2, 1): e ln 2 in two parts, the first with few enough bits to be exact, and the
+            // logarithm of f, off by 2^-25 where that of the sum itself would be by 2^-21
+            int e = 0;
+            const float f = frexpf(sum.hi, &e);
+            Sum2 t = two_sum(sc, -all_top);
+            t = add2(t, -0.69140625f * e);  // 177 / 256
+            t = add2(t, -fmaf(1.7409305599453e-3f, (float)e, logf(f)));
+            t = add2(t, -sum.lo / sum.hi);
+            if (!(isfinite(sc) && isfinite(all_top) && isfinite(sum.hi))) t.hi = INFINITY;
+            sm.add[b] = t;
+            sm.pieces[b] = pieces;
+        }
+    }
+    if (tid == 0) {
+        sm.bound = Pick{0, ~0u};
+        sm.n = 0;
+    }
+    __syncthreads();
+    // rank of p among the first n entries
+    auto rank = [](const Pick* list, int n, const Pick& p) {
+        int r = 0;
+#pragma unroll 8
+        for (int t = 0; t < n; ++t) r += above(list[t], p);
+        return r;
+    };
+    if (direct) {
+        if (i0 < all) sm.cand[i0] = pick(c0, i0);
+        if (i1 < all) sm.cand[i1] = pick(c1, i1);
+        __syncthreads();
+        for (int c = tid; c < all; c += kBeamThreads) {
+            const Pick p = sm.cand[c];
+            const int r = p.key ? rank(sm.cand, all, p) : a.n_out;
+            if (r < a.n_out) put(p, r);
+        }
+        return;
+    }
+    if (lists <= kBeamThreads && lists >= a.n_out) {
+        // the n_out-th largest of the lists' first entries is a bound; each list is read down to it
+        Pick head{0, ~0u};
+        if (tid < lists) sm.best[tid] = head = pick(c0, i0);
+        __syncthreads();
+        if (head.key && rank(sm.best, lists, head) == a.n_out - 1) sm.bound = head;
+        __syncthreads();
+        const Pick bound = sm.bound;
+        if (tid < lists) {
+            Pick p = head;
+            for (int r = 0; p.key && !above(bound, p);) {
+                const int at = atomicAdd(&sm.n, 1);
+                if (at < kFinal) sm.cand[at] = p;
+                if (++r == a.n_out) break;
+                p = pick(r == 1 ? c1 : fetch(i0 + r), i0 + r);
+            }
+        }
+        __syncthreads();
+        const int n = sm.n;
+        if (n <= kFinal) {
+            for (int c = tid; c < n; c += kBeamThreads) {
+                const Pick p = sm.cand[c];
+                const int r = rank(sm.cand, n, p);
+                if (r < a.n_out) put(p, r);
+            }
+            return;
+        }
+    }
+    // many lists, or a few long ones: all candidates, 1024 at a time beside the best so far, by a bound from groups of
+    // lanes as in the chunks
+    int kept = 0;
+    for (int at = 0; at < all;) {
+        Pick p[kPickItems], best{0, ~0u};
+#pragma unroll
+        for (int j = 0; j < kPickItems; ++j) {
+            const int slot = j * kBeamThreads + tid, i = at + slot - kept;
+            p[j] = slot < kept ? sm.keep[slot] : i < all ? pick(fetch(i), i) : Pick{0, ~0u};
+            if (above(p[j], best)) best = p[j];
+        }
+        at += kBeamThreads * kPickItems - kept;
+        for (int o = 1; o < gl; o <<= 1) {
+            const Pick y{__shfl_xor_sync(0xffffffffu, best.key, o), __shfl_xor_sync(0xffffffffu, best.slot, o)};
+            if (above(y, best)) best = y;
+        }
+        __syncthreads();
+        if (tid % gl == 0) sm.best[tid / gl] = best;
+        if (tid == 0) {
+            sm.bound = Pick{0, ~0u};
+            sm.n = 0;
+        }
+        __syncthreads();
+        if (tid < groups) {
+            const Pick mine = sm.best[tid];
+            if (mine.key && rank(sm.best, groups, mine) == a.n_out - 1) sm.bound = mine;
+        }
+        __syncthreads();
+        const Pick bound = sm.bound;
+#pragma unroll
+        for (int j = 0; j < kPickItems; ++j)
+            if (p[j].key && !above(bound, p[j])) sm.cand[atomicAdd(&sm.n, 1)] = p[j];
+        __syncthreads();
+        const int n = sm.n;
+        for (int c = tid; c < n; c += kBeamThreads) {
+            const Pick k = sm.cand[c];
+            const int r = rank(sm.cand, n, k);
+            if (r < a.n_out) sm.keep[r] = k;
+        }
+        kept = min(n, a.n_out);
+        __syncthreads();
+    }
+    if (tid < kept) put(sm.keep[tid], tid);
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -117,242 +332,231 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// How many of the first n keys are larger.
+__device__ __forceinline__ int key_rank(const unsigned long long* list, int n, unsigned long long key) {
+    int r = 0;
+#pragma unroll 8
+    for (int t = 0; t < n; ++t) r += list[t] > key;
+    return r;
+}
+
 template <int IT>
-__global__ void __launch_bounds__(kBeamThreads) beam_select_kernel(BeamArgs a) {
-    constexpr int kCand = kBeamMax * IT;
-    constexpr int kFew = 256;                          // candidates the first bound may leave
-    constexpr int kFinal = 16 * 8 * kPickItems;        // n_out groups of group_lanes threads: 16 x 8, 32 x 4, 64 x 2
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(BeamArgs a) {
+    constexpr int kBlock = kBeamThreads * IT;
+    constexpr int kList = 2 * kBeamMax + kBlock;
+    constexpr int kCut = kBeamMax * ((kList + kBeamThreads - 1) / kBeamThreads);
     // the chunk's part and the group's part use the memory one after the other
     __shared__ __align__(16) union {
         struct {
-            unsigned long long best[kBeamThreads], cand[kCand];
+            unsigned long long best[kBeamThreads], list[kList], cut[kCut];
         } c;
-        struct {
-            Pick best[kBeamThreads / 2], cand[kFinal], keep[kBeamMax];
-            double lse[kBeamMax];
-        } g;
+        ChooseShared g;
     } sm;
     __shared__ float red_m[kBeamThreads / 32], red_s[kBeamThreads / 32], s_top[kBeamThreads / 2];
     __shared__ unsigned long long s_bound;
     __shared__ float s_floor;
-    __shared__ Pick s_pick;
-    __shared__ int s_n, s_last;
+    __shared__ int s_n, s_cut, s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int chunk = blockIdx.x, group = blockIdx.y / a.beams;
-    const int64_t row = blockIdx.y;
-    const int64_t base = (int64_t)chunk * kBeamThreads * IT;
-    const int n = (int)min((int64_t)kBeamThreads * IT, a.n_vocab - base);
-    const float* x = a.logits + row * a.stride + base;
     const int gl = group_lanes(a.n_out), groups = kBeamThreads / gl;
+    const int few = a.n_out + max(16, a.n_out / 2);  // keys a block may find in the list: at most 96
+    int unit = blockIdx.x * a.share;
+    const int unit1 = min(a.units - unit, a.share) + unit;
+    while (unit < unit1) {
+        const int row = unit / a.blocks, block0 = unit % a.blocks, n_blocks = min(a.blocks - block0, unit1 - unit);
+        unit += n_blocks;
+        const int group = row / a.beams, chunk = blockIdx.x - first_cta(a, row);
+        const int64_t base = (int64_t)block0 * kBlock;
+        const int n = (int)min((int64_t)n_blocks * kBlock, a.n_vocab - base);
+        const float* x = a.logits + (int64_t)row * a.stride + base;
 
-    float v[IT];
-    if (n == kBeamThreads * IT) {
+        float v[IT], next[IT];
+        auto load = [&](float (&to)[IT], int b0) {
+            if (n - b0 >= kBlock) {
 #pragma unroll
-        for (int j = 0; j < IT; ++j) v[j] = __ldcs(x + j * kBeamThreads + tid);
-    } else {
+                for (int j = 0; j < IT; ++j) to[j] = __ldcs(x + b0 + j * kBeamThreads + tid);
+            } else {
 #pragma unroll
-        for (int j = 0; j < IT; ++j) v[j] = j * kBeamThreads + tid < n ? __ldcs(x + j * kBeamThreads + tid) : -INFINITY;
-    }
-    float m = v[0];
-#pragma unroll
-    for (int j = 1; j < IT; ++j) m = fmaxf(m, v[j]);  // of the numbers; -inf if there is none
-    if (m != m) m = -INFINITY;
-    // exponentials of the differences; a NaN or +inf makes the sum NaN
-    const float ref = m > -INFINITY ? m : 0.0f;
-    uint64_t sum2 = 0;
-    const uint64_t ref2 = pack_f2(ref, ref), log2e = pack_f2(1.4426950408889634f, 1.4426950408889634f);
-#pragma unroll
-    for (int j = 0; j < IT; j += 2) {
-        const uint64_t t = mul_f2(sub_f2(pack_f2(v[j], v[j + 1]), ref2), log2e);
-        sum2 = add_f2(sum2, pack_f2(ex2(f2_lo(t)), ex2(f2_hi(t))));
-    }
-    const float s = f2_lo(sum2) + f2_hi(sum2);
-    // the groups' maxima, the chunk's maximum and sum
-    float gm = m;
-    for (int o = 1; o < gl; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-    if (tid % gl == 0) s_top[tid / gl] = gm;
-    {
-        const float wm = warp_max(gm);
-        const float ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
-        if (lane == 0) { red_m[warp] = wm; red_s[warp] = ws; }
-    }
-    if (tid == 0) s_n = 0;
-    __syncthreads();
-    if (tid < groups) {
-        const float mine = s_top[tid];
-        int over = 0, same = 0;
-#pragma unroll 8
-        for (int t = 0; t < groups; ++t) {
-            over += s_top[t] > mine;
-            same += s_top[t] == mine;
-        }
-        // the same value from every group that has it
-        if (over < a.n_out && over + same >= a.n_out) s_floor = mine;
-    }
-    if (warp == kBeamThreads / 32 - 1) {
-        const float wm0 = lane < kBeamThreads / 32 ? red_m[lane] : -INFINITY;
-        const float ws0 = lane < kBeamThreads / 32 ? red_s[lane] : 0.0f;
-        const float wm = warp_max(wm0);
-        const float ws = warp_sum(wm0 > -INFINITY ? ws0 * expf(wm0 - wm) : ws0);
-        if (lane == 0) a.stat[row * a.chunks + chunk] = ChunkStat{wm, ws};
-    }
-    __syncthreads();
-    const float floor = s_floor;
-    if (m >= floor) {
-#pragma unroll
-        for (int j = 0; j < IT; ++j) {
-            const int i = j * kBeamThreads + tid;
-            if (v[j] >= floor && i < n) {
-                const int at = atomicAdd(&s_n, 1);
-                if (at < kFew) sm.c.cand[at] = argmax_key(v[j] + 0.0f, i);  // -0 and 0 are one value
-            }
-        }
-    }
-    __syncthreads();
-    int nc = s_n;
-    if (nc > kFew) {
-        // many equal values: the n_out-th largest of the threads' keys (m and its first place)
-        int at = -1;
-#pragma unroll
-        for (int j = IT - 1; j >= 0; --j) {
-            if (v[j] != v[j]) v[j] = -INFINITY;
-            if (v[j] == m && j * kBeamThreads + tid < n) at = j * kBeamThreads + tid;
-        }
-        const unsigned long long mine = at >= 0 ? argmax_key(m + 0.0f, at) : 0ull;
-        sm.c.best[tid] = mine;
-        __syncthreads();
-        if (tid == 0) { s_bound = 0; s_n = 0; }
-        __syncthreads();
-        if (mine) {
-            int above_me = 0;
-            for (int t = 0; t < kBeamThreads; ++t) above_me += sm.c.best[t] > mine;
-            if (above_me == a.n_out - 1) s_bound = mine;
-        }
-        __syncthreads();
-        const unsigned long long bound = s_bound;
-        if (mine && mine >= bound) {
-#pragma unroll
-            for (int j = 0; j < IT; ++j) {
-                const int i = j * kBeamThreads + tid;
-                const unsigned long long key = argmax_key(v[j] + 0.0f, i);
-                if (i < n && key >= bound) sm.c.cand[atomicAdd(&s_n, 1)] = key;
-            }
-        }
-        __syncthreads();
-        nc = s_n;
-    }
-    ChunkCand* out = a.cand + (row * a.chunks + chunk) * a.n_out;
-    for (int c = tid; c < nc; c += kBeamThreads) {
-        const unsigned long long key = sm.c.cand[c];
-        int r = 0;
-        for (int t = 0; t < nc; ++t) r += sm.c.cand[t] > key;
-        if (r < a.n_out) out[r] = ChunkCand{key_value(key), (int32_t)base + argmax_key_index(key)};
-    }
-    // fewer values than n_out (NaN are none: their row is not chosen from)
-    for (int r = nc + tid; r < a.n_out; r += kBeamThreads) out[r] = ChunkCand{-INFINITY, -1};
-
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        const unsigned int ticket = atomicAdd(a.counters + group, 1u);
-        s_last = ticket == (unsigned)(a.beams * a.chunks - 1);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    if (tid == 0) a.counters[group] = 0;
-
-    // ---- the group: log sums of its rows, then the best totals -----------------------
-    const int64_t row0 = (int64_t)group * a.beams;
-    for (int b = warp; b < a.beams; b += kBeamThreads / 32) {
-        const ChunkStat* st = a.stat + (row0 + b) * a.chunks;
-        float top = -INFINITY;
-        for (int c = lane; c < a.chunks; c += 32) top = fmaxf(top, __ldcg(&st[c].m));
-        top = warp_max(top);
-        double sum = 0.0;
-        for (int c = lane; c < a.chunks; c += 32) {
-            const float cm = __ldcg(&st[c].m);
-            const double cs = (double)__ldcg(&st[c].s);
-            sum += cm > -INFINITY ? cs * (double)expf(cm - top) : cs;  // a chunk of NaN alone: cs is NaN
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float sc = a.scores[row0 + b];
-        // +inf marks a beam whose totals are all -inf
-        if (lane == 0) {
-            const double lse = (double)top + log(sum);
-            sm.g.lse[b] = isfinite(lse) && isfinite(sc) ? lse : (double)INFINITY;
-        }
-    }
-    __syncthreads();
-    const int per_row = a.chunks * a.n_out;
-    const int64_t all = (int64_t)a.beams * per_row;
-    int kept = 0;
-    for (int64_t i0 = 0; i0 < all;) {
-        const int fresh = kBeamThreads * kPickItems - kept;
-        Pick p[kPickItems];
-        Pick best{0, 0};
-#pragma unroll
-        for (int j = 0; j < kPickItems; ++j) {
-            p[j] = Pick{0, 0};
-            const int slot = j * kBeamThreads + tid;
-            const int64_t i = i0 + slot - kept;
-            if (slot < kept) {
-                p[j] = sm.g.keep[slot];
-            } else if (i < all) {
-                const int b = (int)(i / per_row), r = (int)(i % per_row);
-                const int token = __ldcg(&a.cand[row0 * per_row + i].token);
-                const float logit = __ldcg(&a.cand[row0 * per_row + i].logit);
-                const double lse = sm.g.lse[b];
-                if (lse < (double)INFINITY) {
-                    if (token >= 0)
-                        p[j] = Pick{f64_order_key((double)a.scores[row0 + b] + ((double)logit - lse)),
-                                    ~(((unsigned long long)b << 32) | (unsigned)token)};
-                } else if (r < a.n_out && r < a.n_vocab) {  // its lowest tokens, all -inf
-                    p[j] = Pick{f64_order_key(-(double)INFINITY), ~(((unsigned long long)b << 32) | (unsigned)r)};
+                for (int j = 0; j < IT; ++j) {
+                    const int i = b0 + j * kBeamThreads + tid;
+                    to[j] = i < n ? __ldcs(x + i) : -INFINITY;
                 }
             }
-            if (above(p[j], best)) best = p[j];
-        }
-        i0 += fresh;
-        for (int o = 1; o < gl; o <<= 1) {
-            const Pick y{__shfl_xor_sync(0xffffffffu, best.hi, o), __shfl_xor_sync(0xffffffffu, best.lo, o)};
-            if (above(y, best)) best = y;
-        }
-        __syncthreads();
-        if (tid % gl == 0) sm.g.best[tid / gl] = best;
-        if (tid == 0) { s_pick = Pick{0, 0}; s_n = 0; }
-        __syncthreads();
-        if (tid < groups) {
-            const Pick mine = sm.g.best[tid];
-            int above_me = 0;
-#pragma unroll 8
-            for (int t = 0; t < groups; ++t) above_me += above(sm.g.best[t], mine);
-            if (mine.lo && above_me == a.n_out - 1) s_pick = mine;
-        }
-        __syncthreads();
-        const Pick bnd = s_pick;
+        };
+        // the list's n_out best to its front, in order; s_floor: the smallest of them (all threads; the list is complete
+        // and has n_out keys or more)
+        auto cut_list = [&](int count) {
+            if (count <= kBeamThreads) {  // one key per thread
+                const unsigned long long key = tid < count ? sm.c.list[tid] : 0ull;
+                const int r = tid < count ? key_rank(sm.c.list, count, key) : kBeamThreads;
+                __syncthreads();  // all have read the list
+                if (r < a.n_out) sm.c.list[r] = key;
+                if (r == a.n_out - 1) s_floor = key_value(key);
+            } else {  // first those from the n_out-th largest of the threads' own largest keys on
+                unsigned long long mine = 0;
+                for (int c = tid; c < count; c += kBeamThreads) mine = max(mine, sm.c.list[c]);
+                sm.c.best[tid] = mine;
+                if (tid == 0) s_cut = 0;
+                __syncthreads();
+                if (key_rank(sm.c.best, kBeamThreads, mine) == a.n_out - 1) s_bound = mine;
+                __syncthreads();
+                const unsigned long long bound = s_bound;
+                if (mine >= bound)
+                    for (int c = tid; c < count; c += kBeamThreads)
+                        if (sm.c.list[c] >= bound) sm.c.cut[atomicAdd(&s_cut, 1)] = sm.c.list[c];
+                __syncthreads();
+                const int kept = s_cut;
+                for (int c = tid; c < kept; c += kBeamThreads) {
+                    const unsigned long long key = sm.c.cut[c];
+                    const int r = key_rank(sm.c.cut, kept, key);
+                    if (r < a.n_out) sm.c.list[r] = key;
+                    if (r == a.n_out - 1) s_floor = key_value(key);
+                }
+            }
+            if (tid == 0) s_n = a.n_out;
+            __syncthreads();
+        };
+
+        float m = -INFINITY, s = 0.0f;
+        // largest number of the block's values, and the running maximum and sum; a NaN or +inf makes the sum NaN
+        auto take_block = [&]() {
+            float top = v[0];
 #pragma unroll
-        for (int j = 0; j < kPickItems; ++j)
-            if (p[j].lo && !above(bnd, p[j])) sm.g.cand[atomicAdd(&s_n, 1)] = p[j];
-        __syncthreads();
-        const int np = s_n;
-        for (int c = tid; c < np; c += kBeamThreads) {
-            const Pick k = sm.g.cand[c];
-            int r = 0;
-            for (int t = 0; t < np; ++t) r += above(sm.g.cand[t], k);
-            if (r < a.n_out) sm.g.keep[r] = k;
+            for (int j = 1; j < IT; ++j) top = fmaxf(top, v[j]);
+            if (top != top) top = -INFINITY;
+            const float m1 = fmaxf(m, top), ref = m1 > -INFINITY ? m1 : 0.0f;
+            const uint64_t ref2 = pack_f2(ref, ref), log2e = pack_f2(1.4426950408889634f, 1.4426950408889634f);
+            uint64_t sum2 = pack_f2(m > -INFINITY ? s * ex2((m - ref) * 1.4426950408889634f) : s, 0.0f);
+#pragma unroll
+            for (int j = 0; j < IT; j += 2) {
+                const uint64_t t = mul_f2(sub_f2(pack_f2(v[j], v[j + 1]), ref2), log2e);
+                sum2 = add_f2(sum2, pack_f2(ex2(f2_lo(t)), ex2(f2_hi(t))));
+            }
+            s = f2_lo(sum2) + f2_hi(sum2);
+            m = m1;
+            return top;
+        };
+        // s_floor: the n_out-th largest of the lane groups' values of `top`
+        auto find_floor = [&](float top) {
+            for (int o = 1; o < gl; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (tid % gl == 0) s_top[tid / gl] = top;
+            __syncthreads();
+            if (tid < groups) {
+                const float mine = s_top[tid];
+                int over = 0, same = 0;
+#pragma unroll 8
+                for (int t = 0; t < groups; ++t) {
+                    over += s_top[t] > mine;
+                    same += s_top[t] == mine;
+                }
+                // the same value from every group that has it
+                if (over < a.n_out && over + same >= a.n_out) s_floor = mine;
+            }
+            __syncthreads();
+        };
+        // the block's values above the bound (or at it) to the list
+        auto push_block = [&](bool at_it, float floor, int b0) {
+            // one bit per value, the last in bit 0: the sign of bound - value (of value - bound with at_it; a bound of 0
+            // gets the sign with which -0 and 0 leave no sign)
+            const float fl = floor == 0.0f ? (at_it ? -0.0f : 0.0f) : floor;
+            const uint64_t fl2 = pack_f2(fl, fl);
+            unsigned hit = 0;
+#pragma unroll
+            for (int j = 0; j < IT; j += 2) {
+                const uint64_t x2 = pack_f2(v[j], v[j + 1]);
+                const uint64_t d = at_it ? sub_f2(x2, fl2) : sub_f2(fl2, x2);
+                hit = __funnelshift_l((uint32_t)d, hit, 1);
+                hit = __funnelshift_l((uint32_t)(d >> 32), hit, 1);
+            }
+            if (at_it) hit = ~hit & ((1u << IT) - 1);
+            while (hit) {
+                const int bit = 31 - __clz(hit), j = IT - 1 - bit, i = b0 + j * kBeamThreads + tid;
+                hit ^= 1u << bit;
+                float y[IT];  // y[0] becomes v[j]
+#pragma unroll
+                for (int t = 0; t < IT; ++t) y[t] = v[t];
+#pragma unroll
+                for (int w = IT / 2; w > 0; w >>= 1)
+#pragma unroll
+                    for (int t = 0; t < w; ++t) y[t] = (j & w) ? y[t + w] : y[t];
+                if (i < n) {
+                    const int at = atomicAdd(&s_n, 1);
+                    if (at < kList) sm.c.list[at] = argmax_key(y[0] + 0.0f, i);  // -0 and 0 are one value
+                }
+            }
+        };
+
+        // the list is looked at every fourth block, so that the warps need not keep in step; where that lets it
+        // overflow (rising values), the piece is done again with a look after every block
+        for (bool careful = false;; careful = true) {
+            float floor = -INFINITY;
+            bool full = false;
+            load(v, 0);
+            m = -INFINITY;
+            s = 0.0f;
+            if (tid == 0) s_n = 0;
+            for (int it = 0, b0 = 0; b0 < n; ++it, b0 += kBlock) {
+                if (b0 + kBlock < n) load(next, b0 + kBlock);
+                const float top = take_block();
+                if (it == 0) {
+                    find_floor(top);
+                    floor = s_floor;
+                }
+                // a later value has to be above the bound, one of the first block at it
+                if (it == 0 ? top >= floor : top > floor) push_block(it == 0, floor, b0);
+                if (careful || (it & 3) == 3 || b0 + kBlock >= n) {
+                    __syncthreads();
+                    const int count = s_n;
+                    __syncthreads();  // s_n has been read before anyone adds to it
+                    if (count > kList) {
+                        full = true;
+                        break;
+                    }
+                    if (count > few) {
+                        cut_list(count);
+                        floor = s_floor;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < IT; ++j) v[j] = next[j];
+            }
+            if (!full) break;  // the same in every thread
         }
-        kept = min(np, a.n_out);
+        {
+            const float wm = warp_max(m);
+            const float ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
+            if (lane == 0) { red_m[warp] = wm; red_s[warp] = ws; }
+        }
         __syncthreads();
-    }
-    if (tid < kept) {
-        const Pick k = sm.g.keep[tid];
-        const unsigned long long place = ~k.lo;
-        const int64_t o = (int64_t)group * a.n_out + tid;
-        a.out_scores[o] = (float)f64_of_key(k.hi);
-        a.out_parent[o] = (int32_t)(row0 + (int64_t)(place >> 32));
-        a.out_token[o] = (int32_t)(place & 0xffffffffull);
+        if (warp == kBeamThreads / 32 - 1) {
+            const float wm0 = lane < kBeamThreads / 32 ? red_m[lane] : -INFINITY;
+            const float ws0 = lane < kBeamThreads / 32 ? red_s[lane] : 0.0f;
+            const float wm = warp_max(wm0);
+            const float ws = warp_sum(wm0 > -INFINITY ? ws0 * expf(wm0 - wm) : ws0);
+            if (lane == 0) a.stat[(int64_t)row * a.chunks + chunk] = ChunkStat{wm, ws};
+        }
+        ChunkCand* out = a.cand + ((int64_t)row * a.chunks + chunk) * a.n_out;
+        const int nc = s_n;
+        for (int c = tid; c < nc; c += kBeamThreads) {
+            const unsigned long long key = sm.c.list[c];
+            const int r = key_rank(sm.c.list, nc, key);
+            if (r < a.n_out) out[r] = ChunkCand{key_value(key), (int32_t)base + argmax_key_index(key)};
+        }
+        // fewer values than n_out (NaN are none: their row is not chosen from)
+        for (int r = nc + tid; r < a.n_out; r += kBeamThreads) out[r] = ChunkCand{-INFINITY, -1};
+
+        __syncthreads();
+        if (warp == 0) {
+            int all_pieces = 0;
+            for (int b = lane; b < a.beams; b += 32) all_pieces += row_pieces(a, group * a.beams + b);
+            all_pieces = __reduce_add_sync(0xffffffffu, all_pieces);
+            if (lane == 0) s_last = take_ticket(a.counters + group) == (unsigned)(all_pieces - 1);
+        }
+        __syncthreads();
+        if (!s_last) continue;  // the same in every thread; what the next piece writes first is behind a barrier
+        if (tid == 0) a.counters[group] = 0;
+
+        choose(a, sm.g, group);
+        __syncthreads();  // the shared memory is the next piece's
     }
 }
 
@@ -366,12 +570,14 @@ extern "C" {
 static bool beam_sizes_ok(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out) {
     return groups >= 0 && beams > 0 && n_vocab > 0 && n_out > 0 && n_out <= (int64_t)beams * n_vocab;
 }
-static bool beam_sizes_supported(int32_t groups, int32_t beams, int32_t n_out) {
-    return beams <= kBeamMax && n_out <= kBeamMax && (int64_t)groups * beams < kMaxCounters;
+static bool beam_sizes_supported(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out) {
+    return beams <= kBeamMax && n_out <= kBeamMax && (int64_t)groups * beams < kMaxCounters && n_vocab <= kBeamVocab &&
+           // blocks are counted in 32 bits
+           (int64_t)groups * beams * (n_vocab / (kBeamThreads * 8) + 1) < INT32_MAX - kBeamVocab;
 }
 
 size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out) {
-    if (!beam_sizes_ok(groups, beams, n_vocab, n_out) || !beam_sizes_supported(groups, beams, n_out)) return 0;
+    if (!beam_sizes_ok(groups, beams, n_vocab, n_out) || !beam_sizes_supported(groups, beams, n_vocab, n_out)) return 0;
     return beam_workspace(groups, beams, n_vocab, n_out, nullptr, nullptr);
 }
 
@@ -382,7 +588,7 @@ llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride,
     if (!logits || !scores || !out_scores || !out_parent || !out_token || !workspace ||
         !beam_sizes_ok(groups, beams, n_vocab, n_out) || logits_stride < n_vocab)
         return LQ8_ERR_ARG;
-    if (!beam_sizes_supported(groups, beams, n_out)) return LQ8_ERR_UNSUPPORTED;
+    if (!beam_sizes_supported(groups, beams, n_vocab, n_out)) return LQ8_ERR_UNSUPPORTED;
     if ((((uintptr_t)logits | (uintptr_t)scores | (uintptr_t)out_scores | (uintptr_t)out_parent |
           (uintptr_t)out_token) & 3) || ((uintptr_t)workspace & 15))
         return LQ8_ERR_ARG;
@@ -391,10 +597,11 @@ llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride,
     if (groups == 0) return LQ8_OK;
     a.logits = logits, a.stride = logits_stride, a.scores = scores, a.beams = beams, a.n_vocab = n_vocab;
     a.n_out = n_out, a.out_scores = out_scores, a.out_parent = out_parent, a.out_token = out_token;
-    const dim3 grid(a.chunks, groups * beams);
+    const BeamCut cut = beam_cut((int64_t)groups * beams, n_vocab);
+    const dim3 grid((unsigned)cut.ctas);
     const cudaError_t e =
-        beam_items((int64_t)groups * beams, n_vocab) == 32
-            ? launch_ex(beam_select_kernel<32>, grid, dim3(kBeamThreads), 0, (cudaStream_t)stream, false, a)
+        cut.items == 16
+            ? launch_ex(beam_select_kernel<16>, grid, dim3(kBeamThreads), 0, (cudaStream_t)stream, false, a)
             : launch_ex(beam_select_kernel<8>, grid, dim3(kBeamThreads), 0, (cudaStream_t)stream, false, a);
     return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }

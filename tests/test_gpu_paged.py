@@ -570,6 +570,15 @@ def test_beam_select_one_large_value_per_thread_stripe():
     check_beam(B, x.repeat(80, 1), torch.zeros(320, device="cuda"), 4, 64)
 
 
+@pytest.mark.parametrize("groups,beams", [(2, 2), (300, 2), (700, 1)])
+def test_beam_select_sorted_rows(groups, beams):
+    """Rising rows, where every block holds larger values than all before it, falling ones, and steps of equal values."""
+    B = binding()
+    x = torch.arange(100001, device="cuda", dtype=torch.float32)
+    for row in (x * 1e-3, -x * 1e-3, torch.floor(x / 3000)):
+        check_beam(B, row[None].repeat(groups * beams, 1).contiguous(), torch.zeros(groups * beams, device="cuda"), beams, 7)
+
+
 def test_beam_select_strided_rows_and_repeated_calls():
     B = binding()
     x = torch.randn((8, 1003), device="cuda")
