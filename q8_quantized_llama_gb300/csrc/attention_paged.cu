@@ -175,13 +175,10 @@ struct State32 {
     float m[kMaxG], l[kMaxG];  // m the same in every lane, l a part per lane
 };
 
-template <typename T, int HD>
-__device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, int G, float scale, int lane) {
-    constexpr bool kHalf = sizeof(T) == 2 && std::is_same<T, __half>::value;
+// The lane's values of q as the A operand holds them.
+template <int HD>
+__device__ __forceinline__ void load_q(float (&v)[HD / 16][4], const float* q, int G, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const T tag{};
-    float v[HD / 16][4];
-    float mx = 0.0f;
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k) {
         float2 x = make_float2(0.f, 0.f), y = x;
@@ -189,11 +186,23 @@ __device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, in
             x = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 2 * t);
             y = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 8 + 2 * t);
         }
-        v[k][0] = x.x * scale; v[k][1] = x.y * scale;
-        v[k][2] = y.x * scale; v[k][3] = y.y * scale;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fabsf(v[k][j]));
+        v[k][0] = x.x; v[k][1] = x.y;
+        v[k][2] = y.x; v[k][3] = y.y;
     }
+}
+
+template <typename T, int HD>
+__device__ __forceinline__ void state_init(State16<T, HD>& s, float (&v)[HD / 16][4], float scale) {
+    constexpr bool kHalf = std::is_same<T, __half>::value;
+    const T tag{};
+    float mx = 0.0f;
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[k][j] *= scale;
+            mx = fmaxf(mx, fabsf(v[k][j]));
+        }
     float up = 1.0f;
     s.q_inv = 1.0f;
     if (kHalf) {
@@ -414,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_scan[kWarps], s_base;
     __shared__ int s_row, s_last;
+    __shared__ Range s_range;
     __shared__ unsigned s_see[kWarps][S::kStages];  // keys that count in each stage's tile
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_head / pg.n_kv, shift = pg.page_shift;
@@ -425,9 +435,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     // ---- this CTA's share of the units of all rows -------------------------------------
     const int per = (a.rows + kThreads - 1) / kThreads;
     long long mine = 0;
+    Range own{0, 0, 0, 0};
     for (int i = 0; i < per; ++i) {
         const int r = tid * per + i;
-        if (r < a.rows) mine += range_units<S::kUnit>(row_range(a, tb, shift, r));
+        if (r < a.rows) {
+            own = row_range(a, tb, shift, r);
+            mine += range_units<S::kUnit>(own);
+        }
     }
     long long before = mine;
 #pragma unroll
@@ -450,9 +464,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     const long long w1 = min(total, w0 + share);
     if (w0 < w1 && before * pg.n_kv <= w0 && w0 < (before + mine) * pg.n_kv) {
         for (int r = tid * per;; ++r) {
-            const int u = range_units<S::kUnit>(row_range(a, tb, shift, r));
+            const Range g = per == 1 ? own : row_range(a, tb, shift, r);
+            const int u = range_units<S::kUnit>(g);
             if (w0 < (before + u) * pg.n_kv) {
                 s_row = r;
+                s_range = g;
                 s_base = before * pg.n_kv;
                 break;
             }
@@ -461,13 +477,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     }
     __syncthreads();
     int row = s_row;
+    Range rg = s_range;
     long long base = s_base;  // units before the row
     bool first = true;        // of this CTA's pieces
     while (w0 < w1) {
-        const Range rg = row_range(a, tb, shift, row);
         const int units = range_units<S::kUnit>(rg);
         if (units == 0) {
-            ++row;
+            rg = row_range(a, tb, shift, ++row);
             continue;
         }
         const int kh = (int)((w0 - base) / units), u = (int)((w0 - base) % units);
@@ -475,16 +491,28 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         const int tile0 = (rg.lo / S::kUnit + u) * kWarps + warp;  // the warp's first tile
         const int32_t* trow = tb.table + (int64_t)rg.seq * tb.stride;
 
+        // q is asked for before the keys: behind the ring's copies its loads take 5000 cycles
+        const float* q = a.q + ((int64_t)row * a.n_head + kh * G) * HD;
+        float q16[HD / 16][4], qv[GP * HD / kThreads];
+        if constexpr (kF32) {
+#pragma unroll
+            for (int i = 0; i < GP * HD / kThreads; ++i)
+                qv[i] = i * kThreads + tid < G * HD ? q[i * kThreads + tid] : 0.0f;
+        } else {
+            load_q<HD>(q16, q, G, lane);
+        }
+
         // Page of the warp's tile j (16-key tiles can end in a second page of 8), -1: nothing to read
         auto page_entry = [&](int j, int off) {
             const int64_t p = (int64_t)(tile0 + j * kWarps) * S::kTile + off;
             if (j >= n || p >= rg.hi || p + min(S::kTile, 1 << shift) <= rg.lo) return -1;
-            const int e = trow[p >> shift];
-            if (e >= pg.n_pages) {
-                report(a.err, LQ8_ERR_ARG);
-                return -1;
-            }
-            return e;
+            return trow[p >> shift];
+        };
+        // a number out of range is reported when the tile is asked for
+        auto checked = [&](int e) {
+            if (e < pg.n_pages) return e;
+            if (lane == 0) report(a.err, LQ8_ERR_ARG);
+            return -1;
         };
         const bool two = S::kTile > (1 << shift);
         int ent = page_entry(lane, 0), ent2 = two ? page_entry(lane, 8) : -1;
@@ -509,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
                     nxt = page_entry(j + 32 + lane, 0);
                     nxt2 = two ? page_entry(j + 32 + lane, 8) : -1;
                 }
-                const int e = __shfl_sync(0xffffffffu, ent, j & 31);
-                const int e2 = two ? __shfl_sync(0xffffffffu, ent2, j & 31) : e;
+                const int e = checked(__shfl_sync(0xffffffffu, ent, j & 31));
+                const int e2 = two ? checked(__shfl_sync(0xffffffffu, ent2, j & 31)) : e;
                 const unsigned bits = see_bits(j, e, e2);
                 if (lane == 0) s_see[warp][j % S::kStages] = bits;
                 const int p = (tile0 + j * kWarps) * S::kTile;
@@ -535,15 +563,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) issue();
 
-        const float* q = a.q + ((int64_t)row * a.n_head + kh * G) * HD;
         State16<T, HD> s16;
         State32<HD> s32;
         if constexpr (kF32) {
-            for (int i = tid; i < GP * HD; i += kThreads) qs[i] = i < G * HD ? q[i] * a.scale_log2 : 0.0f;
+#pragma unroll
+            for (int i = 0; i < GP * HD / kThreads; ++i) qs[i * kThreads + tid] = qv[i] * a.scale_log2;
             state_init<HD, GP>(s32);
             __syncthreads();
         } else {
-            state_init(s16, q, G, a.scale_log2, lane);
+            state_init(s16, q16, a.scale_log2);
         }
         for (int j = 0; j < n; ++j) {
             cp_async_wait<S::kStages - 2>();
@@ -662,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         w0 += n;
         if (kh == pg.n_kv - 1 && u + n == units) {
             base += (long long)units * pg.n_kv;
-            ++row;
+            if (w0 < w1) rg = row_range(a, tb, shift, ++row);
         }
     }
     // ---- rows that see nothing, and what is wrong with rows -------------------------------
