@@ -397,13 +397,31 @@ def llama_q8_attention_decode_noalloc(q, k_cache, v_cache, kv_len: int, n_head: 
 LQ8_ROPE_NONE, LQ8_ROPE_LINEAR, LQ8_ROPE_BASE, LQ8_ROPE_RAMP, LQ8_ROPE_RAMP_M = 0, 1, 2, 3, 4
 
 
+_dtype_names: dict = {}
+
+
 def _dev(a, dtype: str) -> int | None:
     """Address of a contiguous device array of the given element type (a torch
     tensor), of a raw address, or None."""
-    if a is None or isinstance(a, int):
+    if a is None or type(a) is int:
         return a
+    kind = a.dtype
+    name = _dtype_names.get(kind)
+    if name is None:
+        name = _dtype_names[kind] = str(kind)
+    if name != dtype:
+        raise TypeError(f"tensor must be {dtype}, got {kind}")
     if not a.is_contiguous():
         raise ValueError("tensor must be contiguous")
+    return a.data_ptr()
+
+
+def _dev_rows(a, dtype: str, stride: int) -> int | None:
+    """As _dev, for rows `stride` values apart: a contiguous tensor, or one whose rows are that far apart."""
+    if a is None or type(a) is int or a.is_contiguous():
+        return _dev(a, dtype)
+    if a.dim() != 2 or a.stride(1) != 1 or a.stride(0) != stride:
+        raise ValueError(f"tensor must be contiguous or have rows {stride} apart")
     if str(a.dtype) != dtype:
         raise TypeError(f"tensor must be {dtype}, got {a.dtype}")
     return a.data_ptr()
@@ -447,7 +465,7 @@ def make_rope(freq, style: int = 0, magnitude: float = 1.0) -> llama_q8_rope:
 def llama_q8_rope_append(pages: llama_q8_pages, layer: int, qkv, qkv_stride: int, rows: int, pos, seq, n_head: int,
                          rope: llama_q8_rope, table, n_seq: int, table_stride: int, q_out, err=None,
                          stream=0) -> None:
-    check(lib().llama_q8_rope_append(C.addressof(pages), layer, _dev(qkv, _F32), qkv_stride, rows, _dev(pos, _I32),
+    check(lib().llama_q8_rope_append(C.addressof(pages), layer, _dev_rows(qkv, _F32, qkv_stride), qkv_stride, rows, _dev(pos, _I32),
                                      _dev(seq, _I32), n_head, C.addressof(rope), _dev(table, _I32), n_seq,
                                      table_stride, _dev(q_out, _F32), _dev(err, _I32), stream or None),
           "llama_q8_rope_append")
@@ -499,7 +517,7 @@ def llama_q8_beam_select_workspace_bytes(groups: int, beams: int, n_vocab: int, 
 
 def llama_q8_beam_select(logits, logits_stride: int, groups: int, beams: int, n_vocab: int, scores, n_out: int,
                          out_scores, out_parent, out_token, workspace, workspace_bytes: int, stream=0) -> None:
-    check(lib().llama_q8_beam_select(_dev(logits, _F32), logits_stride, groups, beams, n_vocab, _dev(scores, _F32),
+    check(lib().llama_q8_beam_select(_dev_rows(logits, _F32, logits_stride), logits_stride, groups, beams, n_vocab, _dev(scores, _F32),
                                      n_out, _dev(out_scores, _F32), _dev(out_parent, _I32), _dev(out_token, _I32),
                                      _dev(workspace, _U8), workspace_bytes, stream or None), "llama_q8_beam_select")
 

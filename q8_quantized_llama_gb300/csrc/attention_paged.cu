@@ -46,6 +46,8 @@ constexpr int kWarps = 4, kThreads = kWarps * 32, kMaxG = 8;
 constexpr int kMaxCtas = 2 * 152;
 constexpr int kRingBytes = 24 * 1024;  // per warp
 constexpr int kMinShare = 2;           // units a CTA takes at least
+constexpr int kJoin = 16;              // parts joined at once where a pair has more than twice as many
+static_assert((kMaxCtas + kJoin - 1) / kJoin <= 32, "one lane per part or group");
 
 struct AttnArgs {
     const float* q;
@@ -58,7 +60,7 @@ struct AttnArgs {
     float* lse;
     int32_t* err;
     // workspace
-    unsigned int* counters;  // [kMaxCtas] by the CTA in whose share a pair starts, zero between launches
+    unsigned int* counters;  // zero between launches: [2 * kMaxCtas] by the first part's slot, [kMaxCtas] by the first CTA
     float2* part_ml;         // [2 * kMaxCtas][G]
     float* part_o;           // [2 * kMaxCtas][G][HD]
 };
@@ -78,19 +80,18 @@ size_t attn_paged_workspace(int n_head, int n_kv, int hd, AttnArgs* a, void* ws)
 
 template <typename T, int HD>
 struct Shape {
-    static constexpr int kTile = sizeof(T) == 2 ? 16 : 1024 / HD;  // keys per warp and step
+    static constexpr int kTile = 4096 / (HD * (int)sizeof(T));     // keys per warp and step: 4 KB of K, 4 KB of V
     static constexpr int kRowBytes = HD * (int)sizeof(T);
-    static constexpr int kTileBytes = kTile * kRowBytes;           // of K or of V
-    static constexpr int kStages = kRingBytes / (2 * kTileBytes);
     static constexpr int kUnit = kWarps * kTile;                   // positions
     static constexpr int kChunks = kRowBytes / 16;
-    static_assert(kMaxG * HD * 4 <= kRingBytes, "a warp's output waits in its ring");
 };
-constexpr int kSmemRing = kWarps * kRingBytes;
-constexpr int kSmemQ = kSmemRing;                                  // f32: [8][HD] q; joins: weights
-constexpr int kSmemP = kSmemQ + kMaxG * 128 * 4;                   // f32: [warp][tile][8] probabilities
-constexpr int kSmemMl = kSmemP + kWarps * 16 * kMaxG * 4;          // [warp][8] m, l
+constexpr int kTileBytes = 4096;                                   // of K or of V
+constexpr int kStages = kRingBytes / (2 * kTileBytes);
+constexpr int kSmemQ = kWarps * kRingBytes;                        // [2][8][HD] q of this piece and the next
+constexpr int kSmemP = kSmemQ + 2 * kMaxG * 128 * 4;               // f32: [warp][tile][8] probabilities, each twice
+constexpr int kSmemMl = kSmemP + kWarps * 16 * kMaxG * 8;          // [warp][8] m, l
 constexpr int kSmemBytes = kSmemMl + kWarps * kMaxG * 8;
+static_assert(kMaxG * 128 * 4 <= kTileBytes, "a warp's output waits in one tile of its ring");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -161,6 +162,8 @@ __device__ __forceinline__ int range_units(const Range& g) {
     return g.hi > g.lo ? (g.hi + UNIT - 1) / UNIT - g.lo / UNIT : 0;
 }
 
+__device__ constexpr int log2_ceil(int x) { return x <= 1 ? 0 : 1 + log2_ceil((x + 1) / 2); }
+
 // One warp's running state over one (row, KV head).
 template <typename T, int HD>
 struct State16 {
@@ -171,38 +174,27 @@ struct State16 {
 };
 template <int HD>
 struct State32 {
-    float o[kMaxG][HD / 32];
+    uint64_t o[kMaxG][HD / 64];  // pairs of dimensions
     float m[kMaxG], l[kMaxG];  // m the same in every lane, l a part per lane
 };
 
-// The lane's values of q as the A operand holds them.
-template <int HD>
-__device__ __forceinline__ void load_q(float (&v)[HD / 16][4], const float* q, int G, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int k = 0; k < HD / 16; ++k) {
-        float2 x = make_float2(0.f, 0.f), y = x;
-        if (g < G) {
-            x = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 2 * t);
-            y = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 8 + 2 * t);
-        }
-        v[k][0] = x.x; v[k][1] = x.y;
-        v[k][2] = y.x; v[k][3] = y.y;
-    }
-}
-
+// q [8][HD] in shared memory
 template <typename T, int HD>
-__device__ __forceinline__ void state_init(State16<T, HD>& s, float (&v)[HD / 16][4], float scale) {
+__device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, float scale, int lane) {
     constexpr bool kHalf = std::is_same<T, __half>::value;
+    const int g = lane >> 2, t = lane & 3;
     const T tag{};
+    float v[HD / 16][4];
     float mx = 0.0f;
 #pragma unroll
-    for (int k = 0; k < HD / 16; ++k)
+    for (int k = 0; k < HD / 16; ++k) {
+        const float2 x = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 2 * t);
+        const float2 y = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 8 + 2 * t);
+        v[k][0] = x.x * scale; v[k][1] = x.y * scale;
+        v[k][2] = y.x * scale; v[k][3] = y.y * scale;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[k][j] *= scale;
-            mx = fmaxf(mx, fabsf(v[k][j]));
-        }
+        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fabsf(v[k][j]));
+    }
     float up = 1.0f;
     s.q_inv = 1.0f;
     if (kHalf) {
@@ -233,44 +225,42 @@ __device__ __forceinline__ void state_init(State16<T, HD>& s, float (&v)[HD / 16
     s.l = 0.0f;
 }
 
-// A tile of 16 keys: K at ks, V at vs (shared addresses); key j of the tile counts if bit j of see is set.
+// A tile of 2048 / HD keys: K at ks, V at vs (shared addresses); key j of the tile counts if bit j of see is set.
 template <typename T, int HD>
 __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint32_t vs, unsigned see, int lane) {
     constexpr bool kHalf = std::is_same<T, __half>::value;
-    constexpr int RB = HD * 2;
+    constexpr int RB = HD * 2, NT = 2048 / HD / 8;  // blocks of 8 keys
     const T tag{};
     const int l8 = lane & 7, mi = lane >> 3, t = lane & 3;
     // short chains: even and odd steps, and the third part of q, each in sums of their own (the tensor cores cut
     // digits off at every addition to a sum, in proportion to the sum)
-    float c[2][2][4] = {}, c3[2][4] = {};
+    float x[2 * NT];
 #pragma unroll
-    for (int k = 0; k < HD / 32; ++k) {
+    for (int n = 0; n < NT; ++n) {
+        float c[2][4] = {}, c3[4] = {};
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int k = 0; k < HD / 32; ++k) {
             uint32_t b[4];
             ldsm4(b, ks + (n * 8 + l8) * RB + (((k * 4 + mi) ^ l8) << 4));
-            mma16(c[n][0], s.q[2 * k], b[0], b[1], tag);
-            mma16(c[n][1], s.q[2 * k + 1], b[2], b[3], tag);
+            mma16(c[0], s.q[2 * k], b[0], b[1], tag);
+            mma16(c[1], s.q[2 * k + 1], b[2], b[3], tag);
             if (!kHalf) {
                 const uint32_t a0[4] = {s.q3[2 * k][0], 0, s.q3[2 * k][1], 0};
                 const uint32_t a1[4] = {s.q3[2 * k + 1][0], 0, s.q3[2 * k + 1][1], 0};
-                mma16(c3[n], a0, b[0], b[1], tag);
-                mma16(c3[n], a1, b[2], b[3], tag);
+                mma16(c3, a0, b[0], b[1], tag);
+                mma16(c3, a1, b[2], b[3], tag);
             }
         }
-    }
-    float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = j >> 1, i = j & 1;
-        x[j] = (c[n][0][i] + c[n][1][i]) + (c[n][0][i + 2] + c[n][1][i + 2] + c3[n][i]);
+        for (int i = 0; i < 2; ++i) {
+            float y = (c[0][i] + c[1][i]) + (c[0][i + 2] + c[1][i + 2] + c3[i]);
+            if (kHalf) y *= s.q_inv;
+            x[2 * n + i] = (see >> (n * 8 + 2 * t + i)) & 1 ? y : -INFINITY;
+        }
     }
+    float mx = x[0];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (kHalf) x[j] *= s.q_inv;
-        if (!((see >> ((j >> 1) * 8 + 2 * t + (j & 1))) & 1)) x[j] = -INFINITY;
-    }
-    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    for (int j = 1; j < 2 * NT; ++j) mx = fmaxf(mx, x[j]);
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float m = fmaxf(s.m, mx);  // finite: a tile in which nothing counts is not given to this function
@@ -285,23 +275,28 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
     }
     // f16: probabilities times 2^15, so that the second part of a small one is not lost below f16's range
     const float ref = kHalf ? m - 15.0f : m;
+    uint32_t a[NT / 2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2 * NT; ++j) {
         x[j] = ex2(x[j] - ref);
         s.l += x[j];
     }
-    uint32_t a[4];
-    a[0] = take_part(x[0], x[1], tag);
-    a[1] = take_part(x[0], x[1], tag);
-    a[2] = take_part(x[2], x[3], tag);
-    a[3] = take_part(x[2], x[3], tag);
 #pragma unroll
-    for (int d = 0; d < HD / 16; ++d) {
-        uint32_t b[4];
-        ldsm4_t(b, vs + ((mi & 1) * 8 + l8) * RB + (((2 * d + (mi >> 1)) ^ l8) << 4));
-        mma16(s.o[2 * d], a, b[0], b[1], tag);
-        mma16(s.o[2 * d + 1], a, b[2], b[3], tag);
+    for (int h = 0; h < NT / 2; ++h) {
+        a[h][0] = take_part(x[4 * h], x[4 * h + 1], tag);
+        a[h][1] = take_part(x[4 * h], x[4 * h + 1], tag);
+        a[h][2] = take_part(x[4 * h + 2], x[4 * h + 3], tag);
+        a[h][3] = take_part(x[4 * h + 2], x[4 * h + 3], tag);
     }
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d)
+#pragma unroll
+        for (int h = 0; h < NT / 2; ++h) {
+            uint32_t b[4];
+            ldsm4_t(b, vs + (h * 16 + (mi & 1) * 8 + l8) * RB + (((2 * d + (mi >> 1)) ^ l8) << 4));
+            mma16(s.o[2 * d], a[h], b[0], b[1], tag);
+            mma16(s.o[2 * d + 1], a[h], b[2], b[3], tag);
+        }
 }
 
 // The warp's part: output [8][HD] to ob, m and l of its heads to ml (l of f16 pages carries the factor 2^15).
@@ -323,16 +318,16 @@ __device__ __forceinline__ void state_init(State32<HD>& s) {
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
 #pragma unroll
-        for (int d = 0; d < HD / 32; ++d) s.o[g][d] = 0.0f;
+        for (int d = 0; d < HD / 64; ++d) s.o[g][d] = 0;
         s.m[g] = -INFINITY;
         s.l[g] = 0.0f;
     }
 }
 
-// A tile of 1024 / HD keys; q [GP][HD] and the warp's probabilities [tile][8] in shared memory.
+// A tile of 1024 / HD keys; q [GP][HD] and the warp's probabilities [tile][8], each twice, in shared memory.
 template <int HD, int GP>
 __device__ __forceinline__ void state_tile(State32<HD>& s, const uint8_t* ks, const uint8_t* vs, const float* q,
-                                           float* pb, unsigned see, int lane) {
+                                           float* pb, float scale, unsigned see, int lane) {
     constexpr int TK = 1024 / HD, LPK = 32 / TK, CPL = HD / 4 / LPK;  // keys, lanes per key, 16-byte pieces per lane
     constexpr int RB = HD * 4;
     const int key = lane % TK, part = lane / TK;
@@ -351,54 +346,55 @@ __device__ __forceinline__ void state_tile(State32<HD>& s, const uint8_t* ks, co
         }
     }
     const bool in = (see >> key) & 1;
-    float p[GP];
+    float p[GP], m[GP];
     bool grew = false;
-    float f[GP];
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
-        float x = f2_lo(acc[g]) + f2_hi(acc[g]);
+        float x = (f2_lo(acc[g]) + f2_hi(acc[g])) * scale;
 #pragma unroll
         for (int o = TK; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (!in) x = -INFINITY;
-        const float mx = order_float(__reduce_max_sync(0xffffffffu, order_int(x)));
-        const float m = fmaxf(s.m[g], mx);
-        f[g] = ex2(s.m[g] - m);
-        grew |= m > s.m[g];
-        s.m[g] = m;
-        p[g] = ex2(x - m);
-        s.l[g] = s.l[g] * f[g] + (part == 0 ? p[g] : 0.0f);
+        m[g] = fmaxf(s.m[g], order_float(__reduce_max_sync(0xffffffffu, order_int(x))));
+        grew |= m[g] > s.m[g];
+        p[g] = ex2(x - m[g]);
     }
     if (grew) {  // the same in every lane
 #pragma unroll
-        for (int g = 0; g < GP; ++g)
+        for (int g = 0; g < GP; ++g) {
+            const float f = ex2(s.m[g] - m[g]);
+            s.m[g] = m[g];
+            s.l[g] *= f;
 #pragma unroll
-            for (int d = 0; d < HD / 32; ++d) s.o[g][d] *= f[g];
+            for (int d = 0; d < HD / 64; ++d) s.o[g][d] = pack_f2(f2_lo(s.o[g][d]) * f, f2_hi(s.o[g][d]) * f);
+        }
     }
     __syncwarp();  // the last tile's probabilities have been read
     if (part == 0) {
 #pragma unroll
-        for (int g = 0; g < GP; g += 4)
-            *reinterpret_cast<float4*>(pb + key * kMaxG + g) = make_float4(p[g], p[g + 1], p[g + 2], p[g + 3]);
+        for (int g = 0; g < GP; ++g) s.l[g] += p[g];
+#pragma unroll
+        for (int g = 0; g < GP; g += 2)
+            *reinterpret_cast<float4*>(pb + (key * kMaxG + g) * 2) = make_float4(p[g], p[g], p[g + 1], p[g + 1]);
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < TK; ++j) {
-        float v[HD / 32];
-        if (HD == 128) {
-            const float4 x = *reinterpret_cast<const float4*>(vs + j * RB + ((lane ^ (j & 7)) << 4));
-            v[0] = x.x; v[1] = x.y; v[HD / 32 - 2] = x.z; v[HD / 32 - 1] = x.w;
+        uint64_t v[HD / 64];
+        if constexpr (HD == 128) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(vs + j * RB + ((lane ^ (j & 7)) << 4));
+            v[0] = x.x;
+            v[1] = x.y;
         } else {
-            const float2 x = *reinterpret_cast<const float2*>(vs + j * RB + (((lane >> 1) ^ (j & 7)) << 4) + (lane & 1) * 8);
-            v[0] = x.x; v[1] = x.y;
+            v[0] = *reinterpret_cast<const uint64_t*>(vs + j * RB + (((lane >> 1) ^ (j & 7)) << 4) + (lane & 1) * 8);
         }
 #pragma unroll
-        for (int g4 = 0; g4 < GP; g4 += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(pb + j * kMaxG + g4);
-            const float ww[4] = {w.x, w.y, w.z, w.w};
+        for (int g = 0; g < GP; g += 2) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(pb + (j * kMaxG + g) * 2);
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-                for (int d = 0; d < HD / 32; ++d) s.o[g4 + g][d] = fmaf(ww[g], v[d], s.o[g4 + g][d]);
+            for (int d = 0; d < HD / 64; ++d) {
+                s.o[g][d] = fma_f2(w.x, v[d], s.o[g][d]);
+                s.o[g + 1][d] = fma_f2(w.y, v[d], s.o[g + 1][d]);
+            }
         }
     }
 }
@@ -410,7 +406,8 @@ __device__ __forceinline__ void state_store(State32<HD>& s, float* ob, float2* m
         const float l = warp_sum(s.l[g]);
         if (lane == 0) ml[g] = make_float2(s.m[g], l);
 #pragma unroll
-        for (int d = 0; d < HD / 32; ++d) ob[g * HD + lane * (HD / 32) + d] = s.o[g][d];
+        for (int d = 0; d < HD / 64; ++d)
+            *reinterpret_cast<uint64_t*>(ob + g * HD + lane * (HD / 32) + 2 * d) = s.o[g][d];
     }
 }
 
@@ -424,13 +421,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     __shared__ long long s_scan[kWarps], s_base;
     __shared__ int s_row, s_last;
     __shared__ Range s_range;
-    __shared__ unsigned s_see[kWarps][S::kStages];  // keys that count in each stage's tile
+    __shared__ unsigned s_see[kWarps][kStages];  // keys that count in each stage's tile
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_head / pg.n_kv, shift = pg.page_shift;
     uint8_t* ring = smem + warp * kRingBytes;
-    float* qs = reinterpret_cast<float*>(smem + kSmemQ);
-    float* pb = reinterpret_cast<float*>(smem + kSmemP) + warp * 16 * kMaxG;
+    float* pb = reinterpret_cast<float*>(smem + kSmemP) + warp * 16 * kMaxG * 2;
     float2* ml = reinterpret_cast<float2*>(smem + kSmemMl);
+    // heads behind the group stay zero
+    for (int i = tid; i < 2 * kMaxG * HD; i += kThreads) reinterpret_cast<float*>(smem + kSmemQ)[i] = 0.0f;
 
     // ---- this CTA's share of the units of all rows -------------------------------------
     const int per = (a.rows + kThreads - 1) / kThreads;
@@ -476,128 +474,172 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         }
     }
     __syncthreads();
-    int row = s_row;
-    Range rg = s_range;
-    long long base = s_base;  // units before the row
-    bool first = true;        // of this CTA's pieces
-    while (w0 < w1) {
-        const int units = range_units<S::kUnit>(rg);
-        if (units == 0) {
+    // ---- the share's pieces: the part of a (row, KV head) pair that lies in it -------------
+    // The next piece's page numbers and q are asked for during a piece, and its first tiles before the piece is
+    // joined, so that only the first waits for the memory.
+    struct Piece {
+        Range rg;
+        int row, kh, units, u, n;  // of the pair's `units` units, n from u on
+        long long base;            // units before the row
+        int tile0;                 // the warp's first tile
+    };
+    auto place = [&](Piece& p, int row, Range rg, long long base, long long w) {  // the piece that starts at unit w
+        int units = range_units<S::kUnit>(rg);
+        while (w >= base + (long long)units * pg.n_kv) {
+            base += (long long)units * pg.n_kv;
             rg = row_range(a, tb, shift, ++row);
-            continue;
+            units = range_units<S::kUnit>(rg);
         }
-        const int kh = (int)((w0 - base) / units), u = (int)((w0 - base) % units);
-        const int n = (int)min((long long)(units - u), w1 - w0);
-        const int tile0 = (rg.lo / S::kUnit + u) * kWarps + warp;  // the warp's first tile
-        const int32_t* trow = tb.table + (int64_t)rg.seq * tb.stride;
-
-        // q is asked for before the keys: behind the ring's copies its loads take 5000 cycles
-        const float* q = a.q + ((int64_t)row * a.n_head + kh * G) * HD;
-        float q16[HD / 16][4], qv[GP * HD / kThreads];
-        if constexpr (kF32) {
+        const unsigned at = (unsigned)(w - base);  // below 2^32: checked by the host
+        p.rg = rg;
+        p.row = row;
+        p.base = base;
+        p.units = units;
+        p.kh = (int)(at / (unsigned)units);
+        p.u = (int)(at % (unsigned)units);
+        p.n = (int)min((long long)(units - p.u), w1 - w);
+        p.tile0 = (rg.lo / S::kUnit + p.u) * kWarps + warp;
+    };
+    // Page numbers, one per lane: entry e is part e % parts of tile e / parts (a tile can lie in 2 or 4 pages)
+    const int part_shift = max(0, log2_ceil(S::kTile) - shift);
+    auto entry = [&](const Piece& p, int e) {
+        const int64_t pos = (int64_t)(p.tile0 + (e >> part_shift) * kWarps) * S::kTile +
+                            ((e & ((1 << part_shift) - 1)) << shift);
+        if ((e >> part_shift) >= p.n || pos >= p.rg.hi || pos + min(S::kTile, 1 << shift) <= p.rg.lo) return -1;
+        return tb.table[(int64_t)p.rg.seq * tb.stride + (pos >> shift)];
+    };
+    auto ask_q = [&](const Piece& p, int buf) {
+        const float* q = a.q + ((int64_t)p.row * a.n_head + p.kh * G) * HD;
+        float* qs = reinterpret_cast<float*>(smem + kSmemQ) + buf * kMaxG * HD;
+        for (int i = tid; i < G * (HD / 4); i += kThreads) cp_async16(qs + 4 * i, q + 4 * i, 16);
+    };
+    // The warp's tile j of p to stage st; ent: the entries of tiles from (j * parts) & ~31 on.
+    auto issue = [&](const Piece& p, int j, int st, int ent) {
+        const int pos = (p.tile0 + j * kWarps) * S::kTile;
+        unsigned bits = S::kTile == 32 ? ~0u : (1u << S::kTile) - 1;
+        if (pos + S::kTile > p.rg.hi) bits &= (1u << max(0, p.rg.hi - pos)) - 1;
+        if (pos < p.rg.lo) bits &= p.rg.lo - pos >= S::kTile ? 0u : ~0u << (p.rg.lo - pos);
+        constexpr int RPI = 32 / S::kChunks >= 1 ? 32 / S::kChunks : 1;  // rows per warp-wide copy
+        const int ch = lane % S::kChunks, r0 = lane / S::kChunks;
+        uint8_t* dst = ring + st * 2 * kTileBytes + r0 * S::kRowBytes;
+        const int64_t lane_off = r0 * HD + ch * (16 / (int)sizeof(T)) + (((int64_t)p.kh << shift) * HD);
+        int64_t off = 0;
 #pragma unroll
-            for (int i = 0; i < GP * HD / kThreads; ++i)
-                qv[i] = i * kThreads + tid < G * HD ? q[i * kThreads + tid] : 0.0f;
-        } else {
-            load_q<HD>(q16, q, G, lane);
-        }
-
-        // Page of the warp's tile j (16-key tiles can end in a second page of 8), -1: nothing to read
-        auto page_entry = [&](int j, int off) {
-            const int64_t p = (int64_t)(tile0 + j * kWarps) * S::kTile + off;
-            if (j >= n || p >= rg.hi || p + min(S::kTile, 1 << shift) <= rg.lo) return -1;
-            return trow[p >> shift];
-        };
-        // a number out of range is reported when the tile is asked for
-        auto checked = [&](int e) {
-            if (e < pg.n_pages) return e;
-            if (lane == 0) report(a.err, LQ8_ERR_ARG);
-            return -1;
-        };
-        const bool two = S::kTile > (1 << shift);
-        int ent = page_entry(lane, 0), ent2 = two ? page_entry(lane, 8) : -1;
-        int nxt = page_entry(32 + lane, 0), nxt2 = two ? page_entry(32 + lane, 8) : -1;
-        // keys of tile j that count, as bits
-        auto see_bits = [&](int j, int e, int e2) {
-            const int p = (tile0 + j * kWarps) * S::kTile;
-            unsigned bits = (1u << S::kTile) - 1;
-            if (p + S::kTile > rg.hi) bits &= (1u << max(0, rg.hi - p)) - 1;
-            if (p < rg.lo) bits &= rg.lo - p >= S::kTile ? 0u : ~0u << (rg.lo - p);
-            if (e < 0) bits &= two ? 0xff00u : 0u;
-            if (two && e2 < 0) bits &= 0x00ffu;
-            return bits;
-        };
-        int i_issue = 0;  // tiles asked for
-        auto issue = [&]() {
-            const int j = i_issue++;
-            if (j < n) {
-                if ((j & 31) == 0 && j > 0) {
-                    ent = nxt;
-                    ent2 = nxt2;
-                    nxt = page_entry(j + 32 + lane, 0);
-                    nxt2 = two ? page_entry(j + 32 + lane, 8) : -1;
+        for (int g8 = 0; g8 < S::kTile / 8; ++g8) {  // 8 rows lie in one page
+            const int part = (g8 * 8) >> shift;
+            if (g8 == 0 || (part_shift && ((g8 * 8) & ((1 << shift) - 1)) == 0)) {
+                int e = __shfl_sync(0xffffffffu, ent, ((j << part_shift) + part) & 31);
+                if (e >= pg.n_pages) {
+                    if (lane == 0) report(a.err, LQ8_ERR_ARG);
+                    e = -1;
                 }
-                const int e = checked(__shfl_sync(0xffffffffu, ent, j & 31));
-                const int e2 = two ? checked(__shfl_sync(0xffffffffu, ent2, j & 31)) : e;
-                const unsigned bits = see_bits(j, e, e2);
-                if (lane == 0) s_see[warp][j % S::kStages] = bits;
-                const int p = (tile0 + j * kWarps) * S::kTile;
-                uint8_t* dst = ring + (j % S::kStages) * 2 * S::kTileBytes;
-                constexpr int RPI = 32 / S::kChunks >= 1 ? 32 / S::kChunks : 1;  // rows per warp-wide copy
-                const int ch = lane % S::kChunks, r0 = lane / S::kChunks;
-#pragma unroll
-                for (int i = 0; i < S::kTile / RPI; ++i) {
-                    const int r = i * RPI + r0;
-                    const int pe = max(0, two && r >= 8 ? e2 : e);
-                    const int64_t off = pe * pg.page_elems +
-                                        (((int64_t)kh << shift) + ((p + r) & ((1 << shift) - 1))) * HD +
-                                        ch * (16 / (int)sizeof(T));
-                    const uint32_t bytes = (bits >> r) & 1 ? 16u : 0u;
-                    uint8_t* d = dst + r * S::kRowBytes + ((ch ^ (r & 7)) << 4);
-                    cp_async16(d, pg.k + off, bytes);
-                    cp_async16(d + S::kTileBytes, pg.v + off, bytes);
-                }
+                if (e < 0) bits &= ~(part_shift ? ((1u << (1 << shift)) - 1) << (part << shift) : ~0u);
+                off = max(e, 0) * pg.page_elems + ((pos + g8 * 8) & ((1 << shift) - 1)) * HD + lane_off;
             }
-            cp_async_commit();
-        };
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) issue();
+            for (int i = 0; i < 8 / RPI; ++i) {
+                const int r = i * RPI;  // + r0: the row of the block
+                const uint32_t bytes = (bits >> (g8 * 8 + r + r0)) & 1 ? 16u : 0u;
+                uint8_t* d = dst + (g8 * 8 + r) * S::kRowBytes + ((ch ^ (r + r0)) << 4);
+                const int64_t o = off + (int64_t)r * HD;
+                cp_async16(d, pg.k + o, bytes);
+                cp_async16(d + kTileBytes, pg.v + o, bytes);
+            }
+            off += 8 * HD;
+        }
+        if (lane == 0) s_see[warp][st] = bits;
+    };
 
+    Piece cur, nxt;
+    int ent = -1, ent_more = -1;  // of the current piece: the entries in use, and the 32 after them
+    const int ent_tiles = 32 >> part_shift;
+    if (w0 < w1) {
+        place(cur, s_row, s_range, s_base, w0);
+        ent = entry(cur, lane);
+        ask_q(cur, 0);
+        cp_async_commit();
+        ent_more = entry(cur, 32 + lane);
+#pragma unroll
+        for (int j = 0; j < kStages - 1; ++j) {
+            if (j < cur.n) issue(cur, j, j, ent);
+            cp_async_commit();
+        }
+        cp_async_wait<kStages - 1>();
+        __syncthreads();  // q of all threads' copies
+    }
+    int buf = 0, st0 = 0;  // q buffer, stage of the piece's first tile
+    bool first = true;     // of this CTA's pieces
+    while (w0 < w1) {
+        const bool more = w0 + cur.n < w1;
+        int nxt_ent = -1, nxt_more = -1;
+        if (more) {
+            place(nxt, cur.row, cur.rg, cur.base, w0 + cur.n);
+            nxt_ent = entry(nxt, lane);
+            nxt_more = entry(nxt, 32 + lane);
+            ask_q(nxt, buf ^ 1);  // arrives with the next tile asked for
+        }
+        const float* qs = reinterpret_cast<const float*>(smem + kSmemQ) + buf * kMaxG * HD;
         State16<T, HD> s16;
         State32<HD> s32;
-        if constexpr (kF32) {
-#pragma unroll
-            for (int i = 0; i < GP * HD / kThreads; ++i) qs[i * kThreads + tid] = qv[i] * a.scale_log2;
-            state_init<HD, GP>(s32);
-            __syncthreads();
-        } else {
-            state_init(s16, q16, a.scale_log2);
-        }
-        for (int j = 0; j < n; ++j) {
-            cp_async_wait<S::kStages - 2>();
-            __syncwarp();  // every lane's pieces of tile j have arrived, and tile j - 1 has been read
-            const unsigned bits = s_see[warp][j % S::kStages];
-            issue();
-            if (bits) {
-                const uint8_t* t = ring + (j % S::kStages) * 2 * S::kTileBytes;
-                if constexpr (kF32)
-                    state_tile<HD, GP>(s32, t, t + S::kTileBytes, qs, pb, bits, lane);
-                else
-                    state_tile(s16, smem_u32(t), smem_u32(t + S::kTileBytes), bits, lane);
-            }
-        }
-        cp_async_wait<0>();
-        __syncwarp();
         if constexpr (kF32)
-            state_store<HD, GP>(s32, reinterpret_cast<float*>(ring), ml + warp * kMaxG, lane);
+            state_init<HD, GP>(s32);
         else
-            state_store(s16, reinterpret_cast<float*>(ring), ml + warp * kMaxG, lane);
+            state_init(s16, qs, a.scale_log2, lane);
+        int st = st0;
+        for (int j = 0; j < cur.n; ++j) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();  // every lane's pieces of tile j have arrived, and tile j - 1 has been read
+            const unsigned bits = s_see[warp][st];
+            const int ja = j + kStages - 1, sta = st == 0 ? kStages - 1 : st - 1;
+            if (ja < cur.n) {
+                if ((ja & (ent_tiles - 1)) == 0) {
+                    ent = ent_more;
+                    ent_more = entry(cur, (ja << part_shift) + 32 + lane);
+                }
+                issue(cur, ja, sta, ent);
+            }
+            cp_async_commit();
+            if (bits) {
+                const uint8_t* t = ring + st * 2 * kTileBytes;
+                if constexpr (kF32)
+                    state_tile<HD, GP>(s32, t, t + kTileBytes, qs, pb, a.scale_log2, bits, lane);
+                else
+                    state_tile(s16, smem_u32(t), smem_u32(t + kTileBytes), bits, lane);
+            }
+            st = st == kStages - 1 ? 0 : st + 1;
+        }
+        // stages st and the one after it are free for the next piece's first tiles; the output waits in the last one's
+        const int stl = st == 0 ? kStages - 1 : st - 1;
+        __syncwarp();
+        if (more) {
+            int sj = st;
+#pragma unroll
+            for (int j = 0; j < kStages - 1; ++j) {
+                if (j < nxt.n) issue(nxt, j, sj, nxt_ent);
+                cp_async_commit();
+                sj = sj == kStages - 1 ? 0 : sj + 1;
+            }
+            cp_async_wait<kStages - 1>();  // q of the next piece
+        }
+        float* ob = reinterpret_cast<float*>(ring + stl * 2 * kTileBytes);
+        if constexpr (kF32)
+            state_store<HD, GP>(s32, ob, ml + warp * kMaxG, lane);
+        else
+            state_store(s16, ob, ml + warp * kMaxG, lane);
         __syncthreads();
 
         // ---- join the warps: the result, or a part of it -----------------------------------
-        const bool whole = n == units;
+        const bool whole = cur.n == cur.units;
         const int slot = 2 * blockIdx.x + (first ? 0 : 1);
-        const int64_t ob = ((int64_t)row * a.n_head + kh * G) * HD;
+        const int64_t orow = (int64_t)cur.row * a.n_head + cur.kh * G;  // first head of the pair
+        const uint8_t* parts_of_warps = smem + stl * 2 * kTileBytes;
+        auto finish = [&](int e, float4 o, float m, float l) {  // value e of the pair from its sums
+            const int g = e / (HD / 4);
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            reinterpret_cast<float4*>(a.out + orow * HD)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            if (a.lse && e % (HD / 4) == 0)
+                a.lse[orow + g] = l > 0.0f ? (m - (kHalf ? 15.0f : 0.0f)) * 0.69314718055994531f + logf(l) : -INFINITY;
+        };
         for (int e = tid; e < G * (HD / 4); e += kThreads) {
             const int g = e / (HD / 4);
             float m = -INFINITY, l = 0.0f;
@@ -608,62 +650,62 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             for (int w = 0; w < kWarps; ++w) {
                 const float2 x = ml[w * kMaxG + g];
                 const float f = x.x > -INFINITY ? ex2(x.x - m) : 0.0f;
-                const float4 y = reinterpret_cast<const float4*>(smem + w * kRingBytes)[e];
+                const float4 y = reinterpret_cast<const float4*>(parts_of_warps + w * kRingBytes)[e];
                 l = fmaf(f, x.y, l);
                 o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y);
                 o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
             }
             if (whole) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                reinterpret_cast<float4*>(a.out + ob)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                if (a.lse && e % (HD / 4) == 0)
-                    a.lse[(int64_t)row * a.n_head + kh * G + g] =
-                        l > 0.0f ? (m - (kHalf ? 15.0f : 0.0f)) * 0.69314718055994531f + logf(l) : -INFINITY;
+                finish(e, o, m, l);
             } else {
                 reinterpret_cast<float4*>(a.part_o + (int64_t)slot * G * HD)[e] = o;
                 if (e % (HD / 4) == 0) a.part_ml[slot * G + g] = make_float2(m, l);
             }
         }
         if (!whole) {
-            // ---- the last CTA of the pair joins its parts, in the order of the positions ------
-            const long long seg0 = base + (long long)kh * units;
-            const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + units - 1) / share), parts = c1 - c0 + 1;
-            unsigned int* counter = a.counters + c0;  // only the last pair of a share goes on behind it
-            __syncthreads();
-            if (tid == 0) s_last = take_ticket(counter) == (unsigned)(parts - 1);
-            __syncthreads();
-            if (s_last) {
-                if (tid == 0) *counter = 0;
-                // the pair starts inside the first CTA's share unless it starts it
-                const int slot0 = 2 * c0 + (seg0 == c0 * share ? 0 : 1);
-                auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (c0 + i); };
-                float* wgt = reinterpret_cast<float*>(smem);  // [parts][G], then sums of the thread groups
+            // ---- the parts of a pair: many of them in groups of kJoin, each group and then the groups' results by
+            // the CTA that finishes last, in the order of the positions -----------------------------
+            const long long seg0 = cur.base + (long long)cur.kh * cur.units;
+            const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + cur.units - 1) / share), parts = c1 - c0 + 1;
+            // the pair starts inside the first CTA's share unless it starts it
+            const int slot0 = 2 * c0 + (seg0 == c0 * share ? 0 : 1);
+            auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (c0 + i); };
+            auto arrive = [&](unsigned int* counter, int all) {
+                __syncthreads();
+                if (tid == 0) {
+                    s_last = take_ticket(counter) == (unsigned)(all - 1);
+                    if (s_last) *counter = 0;
+                }
+                __syncthreads();
+                return s_last != 0;
+            };
+            float* wgt = reinterpret_cast<float*>(smem + stl * 2 * kTileBytes + kTileBytes);  // [count][G]
+            float4* sums = reinterpret_cast<float4*>(smem + kRingBytes + stl * 2 * kTileBytes + kTileBytes);
+            // parts i0, i0 + step, .. (count of them) to the result, or to the place of part i0
+            auto join = [&](int i0, int step, int count, bool last) {
                 for (int g = warp; g < G; g += kWarps) {
                     float m = -INFINITY, l = 0.0f;
-                    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(&a.part_ml[slot_of(i) * G + g].x));
-                    m = warp_max(m);
-                    for (int i = lane; i < parts; i += 32) {
-                        const float2 x = __ldcg(&a.part_ml[slot_of(i) * G + g]);
-                        const float f = x.x > -INFINITY ? ex2(x.x - m) : 0.0f;
-                        wgt[i * G + g] = f;
-                        l = fmaf(f, x.y, l);
-                    }
-                    l = warp_sum(l);
+                    const float2 x = lane < count ? __ldcg(&a.part_ml[slot_of(i0 + lane * step) * G + g])
+                                                  : make_float2(-INFINITY, 0.0f);
+                    m = warp_max(x.x);
+                    const float f = x.x > -INFINITY ? ex2(x.x - m) : 0.0f;
+                    if (lane < count) wgt[lane * G + g] = f;
+                    l = warp_sum(f * x.y);
                     if (lane == 0) ml[g] = make_float2(m, l);
                 }
                 __syncthreads();
                 // few heads: several groups of threads share the parts
                 const int vecs = G * (HD / 4), groups = max(1, kThreads / vecs);
-                const int chunk = (parts + groups - 1) / groups;
-                float4* sums = reinterpret_cast<float4*>(smem + kRingBytes);
+                const int chunk = (count + groups - 1) / groups;
                 for (int e0 = tid; e0 < vecs * groups; e0 += kThreads) {
                     const int e = e0 % vecs, gr = e0 / vecs, g = e / (HD / 4);
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const int i1 = min(parts, (gr + 1) * chunk);
+                    const int i1 = min(count, (gr + 1) * chunk);
 #pragma unroll 8
                     for (int i = gr * chunk; i < i1; ++i) {
                         const float f = wgt[i * G + g];
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + (int64_t)slot_of(i) * G * HD) + e);
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(
+                                                    a.part_o + (int64_t)slot_of(i0 + i * step) * G * HD) + e);
                         o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y);
                         o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
                     }
@@ -671,27 +713,39 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
                 }
                 __syncthreads();
                 for (int e = tid; e < vecs; e += kThreads) {
-                    const int g = e / (HD / 4);
                     float4 o = sums[e];
                     for (int gr = 1; gr < groups; ++gr) {
                         const float4 y = sums[gr * vecs + e];
                         o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
                     }
-                    const float l = ml[g].y, inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    reinterpret_cast<float4*>(a.out + ob)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                    if (a.lse && e % (HD / 4) == 0)
-                        a.lse[(int64_t)row * a.n_head + kh * G + g] =
-                            l > 0.0f ? (ml[g].x - (kHalf ? 15.0f : 0.0f)) * 0.69314718055994531f + logf(l) : -INFINITY;
+                    const int g = e / (HD / 4);
+                    if (last) {
+                        finish(e, o, ml[g].x, ml[g].y);
+                    } else {
+                        reinterpret_cast<float4*>(a.part_o + (int64_t)slot_of(i0) * G * HD)[e] = o;
+                        if (e % (HD / 4) == 0) a.part_ml[slot_of(i0) * G + g] = ml[g];
+                    }
+                }
+            };
+            if (parts <= 2 * kJoin) {
+                if (arrive(a.counters + slot0, parts)) join(0, 1, parts, true);
+            } else {
+                const int i0 = (int)(blockIdx.x - c0) / kJoin * kJoin, groups = (parts + kJoin - 1) / kJoin;
+                const int count = min(kJoin, parts - i0);
+                if (arrive(a.counters + slot_of(i0), count)) {
+                    join(i0, 1, count, false);
+                    if (arrive(a.counters + 2 * kMaxCtas + c0, groups)) join(0, kJoin, groups, true);
                 }
             }
         }
-        __syncthreads();  // shared memory is free for the next piece
+        __syncthreads();  // the last tile's stage and ml are free
         first = false;
-        w0 += n;
-        if (kh == pg.n_kv - 1 && u + n == units) {
-            base += (long long)units * pg.n_kv;
-            if (w0 < w1) rg = row_range(a, tb, shift, ++row);
-        }
+        w0 += cur.n;
+        cur = nxt;
+        ent = nxt_ent;
+        ent_more = nxt_more;
+        buf ^= 1;
+        st0 = st;
     }
     // ---- rows that see nothing, and what is wrong with rows -------------------------------
     for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -767,6 +821,9 @@ llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t la
     if (!(scale >= 0.0f) || !std::isfinite(scale)) return LQ8_ERR_ARG;
     if (n_head / pages->n_head_kv > kMaxG) return LQ8_ERR_UNSUPPORTED;
     if ((int64_t)rows * pages->n_head_kv >= (1 << 24)) return LQ8_ERR_UNSUPPORTED;
+    // a row's units of 32 positions or more over all KV heads are counted in 32 bits
+    const int64_t reach = std::min<int64_t>((int64_t)table_stride * pages->page, INT32_MAX);
+    if ((reach / 32 + 2) * pages->n_head_kv > INT32_MAX) return LQ8_ERR_UNSUPPORTED;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15) return LQ8_ERR_ARG;
     if (((uintptr_t)pos | (uintptr_t)seq | (uintptr_t)table | (uintptr_t)lse | (uintptr_t)err) & 3) return LQ8_ERR_ARG;
     AttnArgs a{};

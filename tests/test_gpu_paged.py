@@ -141,6 +141,8 @@ ATTN = [  # lens, heads, kv, dim, page, kind, window
     ([1000, 77, 513], 7, 1, 128, 256, "bf16", 0), ([700, 31, 33], 5, 5, 64, 8, "bf16", 0),
     ([900, 12, 3], 16, 2, 128, 8, "f32", 0), ([640, 100, 9], 32, 8, 128, 16, "f32", 100),
     ([640, 100, 9], 14, 2, 64, 16, "bf16", 33), ([640, 100, 0, 9], 12, 4, 128, 64, "f16", 1),
+    ([70000], 7, 1, 128, 16, "bf16", 0), ([40000, 30000], 3, 1, 64, 8, "f16", 0), ([50000, 5], 8, 1, 64, 32, "f32", 0),
+    ([33] * 40, 8, 8, 64, 8, "bf16", 0), ([40, 0, 9] * 30, 32, 8, 128, 8, "f16", 0), ([31, 260] * 30, 16, 8, 64, 16, "f16", 20),
     ([5000], 2, 1, 64, 64, "f16", 0), ([4097], 9, 3, 64, 32, "f32", 4096), ([3, 9000], 4, 1, 128, 128, "bf16", 0)]
 
 
@@ -277,6 +279,10 @@ def test_attention_paged_equal_calls_give_equal_bits(kind):
     B = binding()
     k, v, q, pos, table = paged_case([2000, 5, 700, 0, 90], 32, 8, 128, 16, kind, 12)
     ws = zeros(B.llama_q8_attention_paged_workspace_bytes(5, 32, 8, 128))
+    c = paged_case([60000], 8, 1, 64, 16, kind, 13)   # parts joined in groups
+    a = run_attention(B, *c[:3], c[3], c[4], ws=ws)[0]
+    for _ in range(3):
+        assert torch.equal(a, run_attention(B, *c[:3], c[3], c[4], ws=ws)[0])
     a = run_attention(B, k, v, q, pos, table, ws=ws)[0]
     for _ in range(3):
         assert torch.equal(a, run_attention(B, k, v, q, pos, table, ws=ws)[0])

@@ -87,6 +87,7 @@ def _attn_call(B, **kw):
     (dict(scale=math.nan), "ARG"), (dict(scale=math.inf), "ARG"), (dict(n_head=27), "UNSUPPORTED"),
     (dict(seq=None, rows=5), "ARG"), (dict(q=_off(A, 4)), "ARG"), (dict(out=_off(E4, 8)), "ARG"),
     (dict(ws=_off(W, 4)), "ARG"), (dict(lse=_off(F4, 2)), "ARG"), (dict(rows=(1 << 24)), "UNSUPPORTED"),
+    (dict(pool=dict(n_head_kv=64), n_head=64, width=1 << 28), "UNSUPPORTED"),
     (dict(rows=0), "OK")] + [(dict(pool=p), s) for p, s in BAD_POOLS])
 def test_attention_paged_refuses(B, kw, status):
     assert _attn_call(B, **kw) == _status(B, status)
