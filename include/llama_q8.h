@@ -577,8 +577,9 @@ llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer,
  * positions of all rows are dealt evenly to the GPU's blocks, whatever their
  * lengths; parts of one row meet through the workspace, always added in the
  * order of the positions, so equal calls give equal bits.
- * n_head / n_head_kv <= 8, rows * n_head_kv < 2^24 and n_head_kv times the
- * positions a table row holds (2^31 at most) below 2^36 (LQ8_ERR_UNSUPPORTED); window >= 0, scale finite and >= 0 (LQ8_ERR_ARG);
+ * n_head / n_head_kv <= 8, rows * n_head_kv < 2^24, and rows * n_head_kv *
+ * (the positions a table row holds, / 32 + 2) < 2^31 - 4096, which a chunk of
+ * rows at a time meets (LQ8_ERR_UNSUPPORTED); window >= 0, scale finite and >= 0 (LQ8_ERR_ARG);
  * rows == 0 does nothing. q, out 16-byte aligned. Enqueues one kernel. */
 size_t llama_q8_attention_paged_workspace_bytes(int32_t rows, int32_t n_head, int32_t n_head_kv, int32_t head_dim);
 llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t layer, const float* q, int32_t rows,

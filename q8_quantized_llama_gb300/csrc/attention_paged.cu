@@ -178,9 +178,9 @@ struct State32 {
     float m[kMaxG], l[kMaxG];  // m the same in every lane, l a part per lane
 };
 
-// q [8][HD] in shared memory
+// q [G][HD] in shared memory
 template <typename T, int HD>
-__device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, float scale, int lane) {
+__device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, int G, float scale, int lane) {
     constexpr bool kHalf = std::is_same<T, __half>::value;
     const int g = lane >> 2, t = lane & 3;
     const T tag{};
@@ -188,8 +188,11 @@ __device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, fl
     float mx = 0.0f;
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k) {
-        const float2 x = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 2 * t);
-        const float2 y = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 8 + 2 * t);
+        float2 x = make_float2(0.f, 0.f), y = x;
+        if (g < G) {
+            x = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 2 * t);
+            y = *reinterpret_cast<const float2*>(q + g * HD + k * 16 + 8 + 2 * t);
+        }
         v[k][0] = x.x * scale; v[k][1] = x.y * scale;
         v[k][2] = y.x * scale; v[k][3] = y.y * scale;
 #pragma unroll
@@ -418,8 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     constexpr bool kF32 = sizeof(T) == 4;
     constexpr bool kHalf = std::is_same<T, __half>::value;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_scan[kWarps], s_base;
-    __shared__ int s_row, s_last;
+    __shared__ int s_scan[kWarps], s_base, s_row, s_last;
     __shared__ Range s_range;
     __shared__ unsigned s_see[kWarps][kStages];  // keys that count in each stage's tile
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -427,12 +429,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     uint8_t* ring = smem + warp * kRingBytes;
     float* pb = reinterpret_cast<float*>(smem + kSmemP) + warp * 16 * kMaxG * 2;
     float2* ml = reinterpret_cast<float2*>(smem + kSmemMl);
-    // heads behind the group stay zero
-    for (int i = tid; i < 2 * kMaxG * HD; i += kThreads) reinterpret_cast<float*>(smem + kSmemQ)[i] = 0.0f;
+    if constexpr (kF32) {  // heads behind the group stay zero
+        for (int i = G * HD + tid; i < GP * HD; i += kThreads) {
+            reinterpret_cast<float*>(smem + kSmemQ)[i] = 0.0f;
+            reinterpret_cast<float*>(smem + kSmemQ)[kMaxG * HD + i] = 0.0f;
+        }
+    }
 
     // ---- this CTA's share of the units of all rows -------------------------------------
     const int per = (a.rows + kThreads - 1) / kThreads;
-    long long mine = 0;
+    int mine = 0;
     Range own{0, 0, 0, 0};
     for (int i = 0; i < per; ++i) {
         const int r = tid * per + i;
@@ -441,15 +447,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             mine += range_units<S::kUnit>(own);
         }
     }
-    long long before = mine;
+    int before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, before, o);
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += y;
     }
     if (lane == 31) s_scan[warp] = before;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
     before -= mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -457,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         total += s_scan[w];
     }
     total *= pg.n_kv;
-    const long long share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
-    long long w0 = share * blockIdx.x;
-    const long long w1 = min(total, w0 + share);
+    const int share = max(kMinShare, (int)(((unsigned)total + gridDim.x - 1) / gridDim.x));
+    int w0 = min(total, share * (int)blockIdx.x);  // units of all rows are counted in 31 bits (checked by the host)
+    const int w1 = min(total - w0, share) + w0;
     if (w0 < w1 && before * pg.n_kv <= w0 && w0 < (before + mine) * pg.n_kv) {
         for (int r = tid * per;; ++r) {
             const Range g = per == 1 ? own : row_range(a, tb, shift, r);
@@ -480,24 +486,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
     struct Piece {
         Range rg;
         int row, kh, units, u, n;  // of the pair's `units` units, n from u on
-        long long base;            // units before the row
+        int base;                  // units before the row
         int tile0;                 // the warp's first tile
     };
-    auto place = [&](Piece& p, int row, Range rg, long long base, long long w) {  // the piece that starts at unit w
+    auto place = [&](Piece& p, int row, Range rg, int base, int w) {  // the piece that starts at unit w
         int units = range_units<S::kUnit>(rg);
-        while (w >= base + (long long)units * pg.n_kv) {
-            base += (long long)units * pg.n_kv;
+        while (w - base >= units * pg.n_kv) {
+            base += units * pg.n_kv;
             rg = row_range(a, tb, shift, ++row);
             units = range_units<S::kUnit>(rg);
         }
-        const unsigned at = (unsigned)(w - base);  // below 2^32: checked by the host
+        const unsigned at = (unsigned)(w - base);
         p.rg = rg;
         p.row = row;
         p.base = base;
         p.units = units;
         p.kh = (int)(at / (unsigned)units);
         p.u = (int)(at % (unsigned)units);
-        p.n = (int)min((long long)(units - p.u), w1 - w);
+        p.n = min(units - p.u, w1 - w);
         p.tile0 = (rg.lo / S::kUnit + p.u) * kWarps + warp;
     };
     // Page numbers, one per lane: entry e is part e % parts of tile e / parts (a tile can lie in 2 or 4 pages)
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         if constexpr (kF32)
             state_init<HD, GP>(s32);
         else
-            state_init(s16, qs, a.scale_log2, lane);
+            state_init(s16, qs, G, a.scale_log2, lane);
         int st = st0;
         for (int j = 0; j < cur.n; ++j) {
             cp_async_wait<kStages - 2>();
@@ -665,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         if (!whole) {
             // ---- the parts of a pair: many of them in groups of kJoin, each group and then the groups' results by
             // the CTA that finishes last, in the order of the positions -----------------------------
-            const long long seg0 = cur.base + (long long)cur.kh * cur.units;
-            const int c0 = (int)(seg0 / share), c1 = (int)((seg0 + cur.units - 1) / share), parts = c1 - c0 + 1;
+            const int seg0 = cur.base + cur.kh * cur.units;
+            const int c0 = seg0 / share, c1 = (seg0 + cur.units - 1) / share, parts = c1 - c0 + 1;
             // the pair starts inside the first CTA's share unless it starts it
             const int slot0 = 2 * c0 + (seg0 == c0 * share ? 0 : 1);
             auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (c0 + i); };
@@ -821,9 +827,9 @@ llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t la
     if (!(scale >= 0.0f) || !std::isfinite(scale)) return LQ8_ERR_ARG;
     if (n_head / pages->n_head_kv > kMaxG) return LQ8_ERR_UNSUPPORTED;
     if ((int64_t)rows * pages->n_head_kv >= (1 << 24)) return LQ8_ERR_UNSUPPORTED;
-    // a row's units of 32 positions or more over all KV heads are counted in 32 bits
+    // units of 32 positions or more over all rows and KV heads are counted in 31 bits, a CTA's share past them included
     const int64_t reach = std::min<int64_t>((int64_t)table_stride * pages->page, INT32_MAX);
-    if ((reach / 32 + 2) * pages->n_head_kv > INT32_MAX) return LQ8_ERR_UNSUPPORTED;
+    if ((double)(reach / 32 + 2) * rows * pages->n_head_kv > INT32_MAX - 4096.0) return LQ8_ERR_UNSUPPORTED;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15) return LQ8_ERR_ARG;
     if (((uintptr_t)pos | (uintptr_t)seq | (uintptr_t)table | (uintptr_t)lse | (uintptr_t)err) & 3) return LQ8_ERR_ARG;
     AttnArgs a{};

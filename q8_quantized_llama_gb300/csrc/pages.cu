@@ -98,34 +98,60 @@ __device__ __forceinline__ int held_page(const ForkArgs& a, int row, int b) {
     return t < a.n_pages ? (t < 0 ? -1 : t) : -1;
 }
 
+// Counts of 1024 consecutive pages from w0 on, 32 per lane (page w0 + j * 32 + lane); -1 past the pool.
+__device__ __forceinline__ void load_counts(int (&v)[32], const int32_t* refs, int w0, int n_pages, int lane) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const int p = w0 + j * 32 + lane;
+        v[j] = p < n_pages ? refs[p] : -1;
+    }
+}
+
+// The chains of dependent loads are what this kernel waits for: the counts of
+// the first pass are asked for before anything else, the children are counted
+// in shared memory (for up to kSharedRows parents), and copies learn their page
+// from a list there.
+constexpr int kSharedRows = 2048, kSharedFresh = 2048;
+
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
     __shared__ int warp_sums[32];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_first[kSharedRows], s_kids[kSharedRows], s_fresh[kSharedFresh];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();  // the second kernel's CTAs take their places and wait
+    int v[32];
+    load_counts(v, a.refs_in, warp * 1024, a.n_pages, lane);
+    int p0 = tid < a.rows_out ? a.parent[tid] : -1;  // of the first 1024 children
     if (tid == 0) s_bad = 0;
+    int* first = a.rows_in <= kSharedRows ? s_first : a.first;
+    int* kids = a.rows_in <= kSharedRows ? s_kids : a.kids;
     for (int p = tid; p < a.rows_in; p += kPlanThreads) {
-        a.first[p] = INT32_MAX;
-        a.kids[p] = 0;
+        first[p] = INT32_MAX;
+        kids[p] = 0;
     }
     __syncthreads();
     for (int i = tid; i < a.rows_out; i += kPlanThreads) {
-        const int p = a.parent[i];
+        const int p = i == tid ? p0 : a.parent[i];
         if (p < -1 || p >= a.rows_in) {
             atomicMax(&s_bad, (int)LQ8_ERR_ARG);
         } else if (p >= 0) {
-            atomicMin(a.first + p, i);
-            atomicAdd(a.kids + p, 1);
+            atomicMin(first + p, i);
+            atomicAdd(kids + p, 1);
         }
     }
     __syncthreads();
+    if (first == s_first) {
+        for (int p = tid; p < a.rows_in; p += kPlanThreads) {
+            a.first[p] = s_first[p];
+            a.kids[p] = s_kids[p];
+        }
+    }
     // pages each child needs, in the children's order
     int need_all = 0, n_copies = 0;
     for (int i0 = 0; i0 < a.rows_out; i0 += kPlanThreads) {
         const int i = i0 + tid;
         int fresh = 0, src = -1, part = 0;
         if (i < a.rows_out) {
-            const int p = a.parent[i];
+            const int p = i0 == 0 ? p0 : a.parent[i];
             int n = 0;
             if (p >= 0 && p < a.rows_in) {
                 n = a.len_in[p];
@@ -136,7 +162,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
                     const int page = 1 << a.page_shift, full = n >> a.page_shift;
                     const int need = (int)(((int64_t)n + a.reserve + page - 1) >> a.page_shift);
                     part = n & (page - 1);
-                    if (__ldcg(a.first + p) == i) {
+                    // (atomics on global memory leave older values in L1)
+                    if ((first == s_first ? s_first[p] : __ldcg(a.first + p)) == i) {
                         for (int b = full; b < need; ++b) {
                             const int t = held_page(a, p, b);
                             if (t >= 0 && a.refs_in[t] == 1) continue;
@@ -164,12 +191,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
     int found = 0;
     for (int c0 = 0; c0 < a.n_pages; c0 += kPlanChunk) {
         const int w0 = c0 + warp * 1024;
-        int v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const int p = w0 + j * 32 + lane;
-            v[j] = p < a.n_pages ? a.refs_in[p] : -1;
-        }
+        if (c0 > 0) load_counts(v, a.refs_in, w0, a.n_pages, lane);
         unsigned mine = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -180,7 +202,11 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
         }
         int total;
         int at = found + block_scan(__popc(mine), warp_sums, &total);
-        for (; mine && at < need_all; mine &= mine - 1) a.fresh[at++] = w0 + lane * 32 + __ffs(mine) - 1;
+        for (; mine && at < need_all; mine &= mine - 1, ++at) {
+            const int p = w0 + lane * 32 + __ffs(mine) - 1;
+            a.fresh[at] = p;
+            if (at < kSharedFresh) s_fresh[at] = p;
+        }
         found += total;
     }
     __syncthreads();
@@ -192,7 +218,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
         if (s_bad) report(a.err, s_bad);
     }
     if (s_bad) return;
-    for (int c = tid; c < n_copies; c += kPlanThreads) a.copies[c].dst = a.fresh[a.copies[c].dst];
+    for (int c = tid; c < n_copies; c += kPlanThreads) {
+        const int at = a.copies[c].dst;
+        a.copies[c].dst = at < kSharedFresh ? s_fresh[at] : a.fresh[at];
+    }
 }
 
 // Bytes [0, n) (a multiple of 16) from src to dst by one warp, eight 16-byte pieces in flight per lane.
@@ -280,7 +309,9 @@ __global__ void __launch_bounds__(kMoveThreads) fork_apply_kernel(ForkArgs a, Po
     }
     const int per_copy = pool.n_layer * 2 * pool.n_kv;
     const int64_t units = (int64_t)a.head->n_copies * per_copy;
-    for (int64_t u = warp; u < units; u += n_warps) {
+    // from the warps that had no job on
+    const int jobs = min(n_warps - 1, a.rows_out + a.rows_in);
+    for (int64_t u = warp < jobs ? warp + n_warps - jobs : warp - jobs; u < units; u += n_warps) {
         const int c = (int)(u / per_copy);
         int r = (int)(u % per_copy);
         const int h = r % pool.n_kv;
@@ -319,41 +350,49 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs 
     __shared__ int warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
-    int n = 0;
-    for (int p = tid; p < a.n_pages; p += kPlanThreads) n += a.refs_in[p] > 0;
-    int used;
+    int v[32];
+    // bit b of lane l's word: page w0 + l * 32 + b is in use
+    auto words = [&](int w0) {
+        load_counts(v, a.refs_in, w0, a.n_pages, lane);
+        unsigned mine = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const unsigned m = __ballot_sync(0xffffffffu, v[j] > 0);
+            if (lane == j) mine = m;
+        }
+        return mine;
+    };
+    unsigned word = 0;
+    int n = 0, used;
+    for (int c0 = 0; c0 < a.n_pages; c0 += kPlanChunk) {
+        word = words(c0 + warp * 1024);
+        n += __popc(word);
+    }
     block_scan(n, warp_sums, &used);
     // holes below `used`, pages in use from there on: as many of one as of the other
     int moves = 0, holes = 0;
     for (int c0 = 0; c0 < a.n_pages; c0 += kPlanChunk) {
         const int w0 = c0 + warp * 1024;
-        unsigned hole = 0, from = 0;
-        int v[32];
+        if (a.n_pages > kPlanChunk) word = words(w0);  // of one pass the word is still there
+        const int below = min(32, max(0, used - (w0 + lane * 32)));
+        const unsigned low = below == 32 ? ~0u : (1u << below) - 1;
+        unsigned hole = ~word & low, from = word & ~low;
+        int total;
+        int at = holes + block_scan(__popc(hole), warp_sums, &total);
+        holes += total;
+        for (; hole; hole &= hole - 1) a.hole[at++] = w0 + lane * 32 + __ffs(hole) - 1;
+        at = moves + block_scan(__popc(from), warp_sums, &total);
+        moves += total;
+        for (; from; from &= from - 1) a.from[at++] = w0 + lane * 32 + __ffs(from) - 1;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const int p = w0 + j * 32 + lane;
-            v[j] = p < a.n_pages ? a.refs_in[p] : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const int p = w0 + j * 32 + lane;
-            const bool in = v[j] > 0;
-            const unsigned mh = __ballot_sync(0xffffffffu, !in && p < used);
-            const unsigned mf = __ballot_sync(0xffffffffu, in && p >= used);
-            if (lane == j) { hole = mh; from = mf; }
             if (p < a.n_pages) {
-                const bool stays = in && p < used;
-                if (!(in && p >= used)) a.to[p] = stays ? p : -1;
+                const bool in = v[j] > 0, stays = in && p < used;
+                if (!in || stays) a.to[p] = stays ? p : -1;
                 if (stays || p >= used) a.refs_out[p] = stays ? v[j] : 0;
             }
         }
-        int total;
-        int at = holes + block_scan(__popc(hole), warp_sums, &total);
-        for (; hole; hole &= hole - 1) a.hole[at++] = w0 + lane * 32 + __ffs(hole) - 1;
-        holes += total;
-        at = moves + block_scan(__popc(from), warp_sums, &total);
-        for (; from; from &= from - 1) a.from[at++] = w0 + lane * 32 + __ffs(from) - 1;
-        moves += total;
     }
     __syncthreads();
     for (int m = tid; m < moves; m += kPlanThreads) {
