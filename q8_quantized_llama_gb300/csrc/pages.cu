@@ -22,7 +22,7 @@ namespace lq8 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanChunk = kPlanThreads * 32;  // counts ranked per pass
+constexpr int kPlanChunk = kPlanThreads * 32;  // counts ranked per pass at most
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = 152 * 4;
 constexpr int kMaxForkRows = 65536;
@@ -39,15 +39,15 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
     __syncthreads();  // warp_sums of an earlier scan are no longer read
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
+    int w = warp_sums[lane];
 #pragma unroll
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const int t = warp_sums[w];
-        if (w < warp) before += t;
-        all += t;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
-    *total = all;
-    return before + x - v;
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return (warp ? before : 0) + x - v;
 }
 
 // One page copy of a fork: n_rows valid positions of page src to page dst.
@@ -98,10 +98,14 @@ __device__ __forceinline__ int held_page(const ForkArgs& a, int row, int b) {
     return t < a.n_pages ? (t < 0 ? -1 : t) : -1;
 }
 
-// Counts of 1024 consecutive pages from w0 on, 32 per lane (page w0 + j * 32 + lane); -1 past the pool.
-__device__ __forceinline__ void load_counts(int (&v)[32], const int32_t* refs, int w0, int n_pages, int lane) {
+// Counts per lane and pass: a warp has 32 * j_n consecutive pages, w0 + j * 32 + lane.
+__device__ __forceinline__ int counts_per_lane(int n_pages) {
+    return min(32, (n_pages + kPlanThreads - 1) / kPlanThreads);
+}
+__device__ __forceinline__ void load_counts(int (&v)[32], const int32_t* refs, int w0, int j_n, int n_pages, int lane) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
+        if (j >= j_n) break;
         const int p = w0 + j * 32 + lane;
         v[j] = p < n_pages ? refs[p] : -1;
     }
@@ -118,9 +122,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
     __shared__ int s_bad, s_first[kSharedRows], s_kids[kSharedRows], s_fresh[kSharedFresh];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();  // the second kernel's CTAs take their places and wait
+    const int j_n = counts_per_lane(a.n_pages);
     int v[32];
-    load_counts(v, a.refs_in, warp * 1024, a.n_pages, lane);
-    int p0 = tid < a.rows_out ? a.parent[tid] : -1;  // of the first 1024 children
+    load_counts(v, a.refs_in, warp * 32 * j_n, j_n, a.n_pages, lane);
+    const int p0 = tid < a.rows_out ? a.parent[tid] : -1;  // of the first 1024 children
     if (tid == 0) s_bad = 0;
     int* first = a.rows_in <= kSharedRows ? s_first : a.first;
     int* kids = a.rows_in <= kSharedRows ? s_kids : a.kids;
@@ -189,12 +194,13 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a) {
     }
     // the lowest free pages, and the counts as they were
     int found = 0;
-    for (int c0 = 0; c0 < a.n_pages; c0 += kPlanChunk) {
-        const int w0 = c0 + warp * 1024;
-        if (c0 > 0) load_counts(v, a.refs_in, w0, a.n_pages, lane);
+    for (int c0 = 0; c0 < a.n_pages; c0 += kPlanThreads * j_n) {
+        const int w0 = c0 + warp * 32 * j_n;
+        if (c0 > 0) load_counts(v, a.refs_in, w0, j_n, a.n_pages, lane);
         unsigned mine = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
+            if (j >= j_n) break;
             const int p = w0 + j * 32 + lane;
             if (p < a.n_pages) a.refs_out[p] = v[j];
             const unsigned m = __ballot_sync(0xffffffffu, v[j] == 0);
@@ -350,13 +356,15 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs 
     __shared__ int warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
+    const int j_n = counts_per_lane(a.n_pages), step = kPlanThreads * j_n;
     int v[32];
     // bit b of lane l's word: page w0 + l * 32 + b is in use
     auto words = [&](int w0) {
-        load_counts(v, a.refs_in, w0, a.n_pages, lane);
+        load_counts(v, a.refs_in, w0, j_n, a.n_pages, lane);
         unsigned mine = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
+            if (j >= j_n) break;
             const unsigned m = __ballot_sync(0xffffffffu, v[j] > 0);
             if (lane == j) mine = m;
         }
@@ -364,17 +372,17 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs 
     };
     unsigned word = 0;
     int n = 0, used;
-    for (int c0 = 0; c0 < a.n_pages; c0 += kPlanChunk) {
-        word = words(c0 + warp * 1024);
+    for (int c0 = 0; c0 < a.n_pages; c0 += step) {
+        word = words(c0 + warp * 32 * j_n);
         n += __popc(word);
     }
     block_scan(n, warp_sums, &used);
     // holes below `used`, pages in use from there on: as many of one as of the other
     int moves = 0, holes = 0;
-    for (int c0 = 0; c0 < a.n_pages; c0 += kPlanChunk) {
-        const int w0 = c0 + warp * 1024;
+    for (int c0 = 0; c0 < a.n_pages; c0 += step) {
+        const int w0 = c0 + warp * 32 * j_n;
         if (a.n_pages > kPlanChunk) word = words(w0);  // of one pass the word is still there
-        const int below = min(32, max(0, used - (w0 + lane * 32)));
+        const int below = lane < j_n ? min(32, max(0, used - (w0 + lane * 32))) : 0;
         const unsigned low = below == 32 ? ~0u : (1u << below) - 1;
         unsigned hole = ~word & low, from = word & ~low;
         int total;
@@ -386,6 +394,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs 
         for (; from; from &= from - 1) a.from[at++] = w0 + lane * 32 + __ffs(from) - 1;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
+            if (j >= j_n) break;
             const int p = w0 + j * 32 + lane;
             if (p < a.n_pages) {
                 const bool in = v[j] > 0, stays = in && p < used;
