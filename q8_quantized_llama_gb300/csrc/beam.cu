@@ -182,11 +182,10 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
         a.out_parent[o] = (int32_t)(row0 + b);
         a.out_token[o] = isfinite(sm.add[b].hi) ? fetch((int)p.slot).token : (int)p.slot - list * a.n_out;
     };
-    // candidates asked for before the sums: two per thread, or the heads of the lists
-    const bool direct = all <= kFinal;
-    const ChunkCand none{-INFINITY, -1};
-    const int i0 = direct ? tid : tid * a.n_out, i1 = direct ? tid + kBeamThreads : i0 + 1;
-    const ChunkCand c0 = i0 < all ? fetch(i0) : none, c1 = i1 < all ? fetch(i1) : none;
+    // a candidate asked for before the sums: one per thread, or the first of the thread's first list
+    const bool direct = all <= kBeamThreads;
+    const int i0 = direct ? tid : tid * a.n_out;
+    const ChunkCand c0 = i0 < all ? fetch(i0) : ChunkCand{-INFINITY, -1};
     for (int b = warp; b < a.beams; b += kBeamThreads / 32) {
         const ChunkStat* st = a.stat + (row0 + b) * a.chunks;
         const int pieces = row_pieces(a, (int)row0 + b);
@@ -233,32 +232,38 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
         return r;
     };
     if (direct) {
-        if (i0 < all) sm.cand[i0] = pick(c0, i0);
-        if (i1 < all) sm.cand[i1] = pick(c1, i1);
+        const Pick p = i0 < all ? pick(c0, i0) : Pick{0, ~0u};
+        sm.cand[tid] = p;
         __syncthreads();
-        for (int c = tid; c < all; c += kBeamThreads) {
-            const Pick p = sm.cand[c];
-            const int r = p.key ? rank(sm.cand, all, p) : a.n_out;
-            if (r < a.n_out) put(p, r);
-        }
+        const int r = p.key ? rank(sm.cand, all, p) : a.n_out;
+        if (r < a.n_out) put(p, r);
         return;
     }
-    if (lists <= kBeamThreads && lists >= a.n_out) {
-        // the n_out-th largest of the lists' first entries is a bound; each list is read down to it
+    if (lists >= a.n_out) {
+        // the n_out-th largest of the threads' best first entries is a bound; each list is read down to it
         Pick head{0, ~0u};
-        if (tid < lists) sm.best[tid] = head = pick(c0, i0);
+        for (int l = tid; l < lists; l += kBeamThreads) {
+            const Pick p = pick(l == tid ? c0 : fetch(l * a.n_out), l * a.n_out);
+            if (above(p, head)) head = p;
+        }
+        sm.best[tid] = head;
         __syncthreads();
-        if (head.key && rank(sm.best, lists, head) == a.n_out - 1) sm.bound = head;
+        if (head.key && rank(sm.best, min(lists, kBeamThreads), head) == a.n_out - 1) sm.bound = head;
         __syncthreads();
         const Pick bound = sm.bound;
-        if (tid < lists) {
-            Pick p = head;
-            for (int r = 0; p.key && !above(bound, p);) {
-                const int at = atomicAdd(&sm.n, 1);
-                if (at < kFinal) sm.cand[at] = p;
-                if (++r == a.n_out) break;
-                p = pick(r == 1 ? c1 : fetch(i0 + r), i0 + r);
-            }
+        auto take = [&](const Pick& p) {
+            if (!p.key || above(bound, p)) return false;
+            const int at = atomicAdd(&sm.n, 1);
+            if (at < kFinal) sm.cand[at] = p;
+            return true;
+        };
+        if (all <= 16 * kBeamThreads) {  // a few loads per thread, none waiting for another
+#pragma unroll 4
+            for (int i = tid; i < all; i += kBeamThreads) take(pick(fetch(i), i));
+        } else {
+            for (int l = tid; l < lists; l += kBeamThreads)
+                for (int r = 0; r < a.n_out; ++r)
+                    if (!take(pick(fetch(l * a.n_out + r), l * a.n_out + r))) break;  // the list falls
         }
         __syncthreads();
         const int n = sm.n;
@@ -271,7 +276,7 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
             return;
         }
     }
-    // many lists, or a few long ones: all candidates, 1024 at a time beside the best so far, by a bound from groups of
+    // a few long lists, or many equal values: all candidates, 1024 at a time beside the best so far, by a bound from groups of
     // lanes as in the chunks
     int kept = 0;
     for (int at = 0; at < all;) {
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(BeamArgs a
         const int n = (int)min((int64_t)n_blocks * kBlock, a.n_vocab - base);
         const float* x = a.logits + (int64_t)row * a.stride + base;
 
-        float v[IT], next[IT];
+        float v[IT], next[IT] = {};
         auto load = [&](float (&to)[IT], int b0) {
             if (n - b0 >= kBlock) {
 #pragma unroll

@@ -12,8 +12,9 @@
 // Bound: memory. Each thread moves items of 8 values (two 16-byte loads, one or
 // two stores): the two halves of 4 pairs for the half layout, so that no value
 // is read twice; the loads are issued before the angles are computed, whose
-// latency (double multiply, sincospif) they cover. One CTA per row: 8 or more
-// resident per SM, enough bytes in flight without a pipeline.
+// latency (double multiply, sincospif) they cover. One CTA per row or per eight
+// narrow rows: 8 or more resident per SM, enough bytes in flight without a
+// pipeline (8195 rows of 32/8 heads of 128 into bf16: 61 us, 6.0 TB/s).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -27,7 +28,7 @@ struct RopeArgs {
     int64_t qkv_stride;
     const int32_t* pos;
     const int32_t* seq;
-    int n_head;
+    int rows, n_head;
     const double* freq;
     int rot_dim, style;
     float magnitude;
@@ -47,17 +48,19 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeItems = 4;  // items loaded ahead per thread
+constexpr int kRopeRows = 8;   // rows per CTA at most
 
-template <typename T, int HD>
+// RC rows per CTA, from row RC * blockIdx.x on.
+template <typename T, int HD, int RC>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, PageView<T> pg, TableView tb) {
-    __shared__ float2 cs[HD / 2];
+    __shared__ float2 cs_all[RC][HD / 2];
+    __shared__ int s_pos[RC], s_page[RC];
     constexpr int IPH = HD / 8;  // items per head
-    const int row = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
-    const int p = a.pos[row];
-    if (p < 0) return;
+    const int row0 = blockIdx.x * RC, tid = threadIdx.x, threads = blockDim.x;
+    const int rows = RC == 1 ? 1 : min(RC, a.rows - row0);
     const int half = a.rot_dim >> 1, rot_items = a.rot_dim >> 3;
-    const int heads = a.n_head + 2 * pg.n_kv, items = heads * IPH;
-    const float* x = a.qkv + row * a.qkv_stride;
+    const int heads = a.n_head + 2 * pg.n_kv, per_row = heads * IPH, items = rows * per_row;
+    const float* x = a.qkv + row0 * a.qkv_stride;
 
     // where the first and second four values of item `it` of a head lie
     auto first = [&](int it, bool rot) { return (rot && a.style) ? 4 * it : 8 * it; };
@@ -68,31 +71,49 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, P
         for (int j = 0; j < kRopeItems; ++j) {
             const int i = i0 + j * threads;
             if (i < items) {
-                const int h = i / IPH, it = i % IPH;
+                const int r = RC == 1 ? 0 : i / per_row, h = (i - r * per_row) / IPH, it = i % IPH;
                 const bool rot = h < a.n_head + pg.n_kv && it < rot_items;
-                u[j] = __ldcs(reinterpret_cast<const float4*>(x + h * HD + first(it, rot)));
-                w[j] = __ldcs(reinterpret_cast<const float4*>(x + h * HD + second(it, rot)));
+                const float* v = x + r * a.qkv_stride + h * HD;
+                u[j] = __ldcs(reinterpret_cast<const float4*>(v + first(it, rot)));
+                w[j] = __ldcs(reinterpret_cast<const float4*>(v + second(it, rot)));
             }
         }
     };
+    // the position before the row's values: what depends on it does not wait behind their loads
+    int p1 = RC == 1 ? a.pos[row0] : 0, page1 = 0;
+    if (RC == 1 && p1 < 0) return;  // a padding row
     load(tid);
-    if (tid < half) {
-        // angle in turns: the product and its reduction in double
-        const double turns = (double)p * (a.freq[tid] * 0.15915494309189533577);  // 1 / 2 pi
+    auto angle = [&](int r, int k, int p) {
+        // in turns: the product and its reduction in double
+        const double turns = (double)p * (a.freq[k] * 0.15915494309189533577);  // 1 / 2 pi
         float s, c;
         sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-        cs[tid] = make_float2(c * a.magnitude, s * a.magnitude);
-    }
-    const int sq = a.seq ? a.seq[row] : row;
-    const int block = p >> pg.page_shift, slot = p & ((1 << pg.page_shift) - 1);
-    int page = -1;
-    if (sq < 0 || sq >= tb.n_seq) {
-        if (tid == 0) report(a.err, LQ8_ERR_ARG);
-    } else if (block >= tb.stride) {
-        if (tid == 0) report(a.err, LQ8_ERR_CTX);
+        cs_all[r][k] = make_float2(c * a.magnitude, s * a.magnitude);
+    };
+    if (RC == 1) {
+        if (tid < half) angle(0, tid, p1);
     } else {
-        page = page_of(tb, sq, block, pg.n_pages);
-        if (page < 0 && tid == 0) report(a.err, LQ8_ERR_ARG);
+        for (int i = tid; i < rows * half; i += threads) angle(i / half, i % half, a.pos[row0 + i / half]);
+    }
+    // the page of a row's position, -1: no append
+    auto find_page = [&](int row, int p, bool tell) {
+        if (p < 0) return -1;
+        const int sq = a.seq ? a.seq[row] : row, block = p >> pg.page_shift;
+        int page = -1, status = LQ8_ERR_ARG;
+        if (sq >= 0 && sq < tb.n_seq) {
+            if (block < tb.stride)
+                page = page_of(tb, sq, block, pg.n_pages);
+            else
+                status = LQ8_ERR_CTX;
+        }
+        if (page < 0 && tell) report(a.err, status);
+        return page;
+    };
+    if (RC == 1) {
+        page1 = find_page(row0, p1, tid == 0);
+    } else if (tid < rows) {
+        s_pos[tid] = p1 = a.pos[row0 + tid];
+        s_page[tid] = find_page(row0 + tid, p1, true);
     }
     __syncthreads();
 
@@ -101,7 +122,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, P
         for (int j = 0; j < kRopeItems; ++j) {
             const int i = i0 + j * threads;
             if (i >= items) break;
-            const int h = i / IPH, it = i % IPH;
+            const int r = RC == 1 ? 0 : i / per_row, h = (i - r * per_row) / IPH, it = i % IPH;
+            const int p = RC == 1 ? p1 : s_pos[r], page = RC == 1 ? page1 : s_page[r];
+            if (p < 0) continue;
+            const float2* cs = cs_all[r];
             const bool rot = h < a.n_head + pg.n_kv && it < rot_items;
             float4 y = u[j], z = w[j];
             if (rot && a.style) {  // y holds values 4 it .. + 3, z their partners
@@ -119,11 +143,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, P
             }
             const int o1 = first(it, rot), o2 = second(it, rot);
             if (h < a.n_head) {
-                float* q = a.q_out + ((int64_t)row * a.n_head + h) * HD;
+                float* q = a.q_out + ((int64_t)(row0 + r) * a.n_head + h) * HD;
                 store4(q + o1, y);
                 store4(q + o2, z);
             } else if (page >= 0) {
-                const int kh = h - a.n_head;
+                const int kh = h - a.n_head, slot = p & ((1 << pg.page_shift) - 1);
                 const bool is_v = kh >= pg.n_kv;
                 T* dst = (is_v ? pg.v : pg.k) + page * pg.page_elems +
                          ((int64_t)((is_v ? kh - pg.n_kv : kh) << pg.page_shift) + slot) * HD;
@@ -136,15 +160,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeArgs a, P
     }
 }
 
+template <typename T, int HD>
+cudaError_t launch_rope_hd(const RopeArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, cudaStream_t s) {
+    const int items = (a.n_head + 2 * p->n_head_kv) * (HD / 8);
+    const PageView<T> pg = page_view<T>(p, layer);
+    // One row per CTA, as many warps as one pass over its items needs (at least those that compute the angles): the
+    // shortest call. Narrow rows of a prompt, once there are enough to fill the GPU either way: several per CTA
+    // (8195 rows of 9/3 heads of 64: 20.6 us with one, 17.0 with eight).
+    if (items <= kRopeThreads / 2 && a.rows >= 152 * 8 * kRopeRows / 2)
+        return launch_ex(rope_append_kernel<T, HD, kRopeRows>, dim3((a.rows + kRopeRows - 1) / kRopeRows),
+                         dim3(kRopeThreads), 0, s, false, a, pg, tb);
+    const int threads = std::min(kRopeThreads, std::max((items + 31) / 32 * 32, HD / 2));
+    return launch_ex(rope_append_kernel<T, HD, 1>, dim3(a.rows), dim3(threads), 0, s, false, a, pg, tb);
+}
 template <typename T>
-cudaError_t launch_rope(const RopeArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, int rows,
-                        cudaStream_t s) {
-    const int items = (a.n_head + 2 * p->n_head_kv) * (p->head_dim / 8);
-    // as many warps as one pass over the row's items needs, at least those that compute the angles
-    const int threads = std::min(kRopeThreads, std::max((items + 31) / 32 * 32, p->head_dim / 2));
-    if (p->head_dim == 64)
-        return launch_ex(rope_append_kernel<T, 64>, dim3(rows), dim3(threads), 0, s, false, a, page_view<T>(p, layer), tb);
-    return launch_ex(rope_append_kernel<T, 128>, dim3(rows), dim3(threads), 0, s, false, a, page_view<T>(p, layer), tb);
+cudaError_t launch_rope(const RopeArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, cudaStream_t s) {
+    return p->head_dim == 64 ? launch_rope_hd<T, 64>(a, p, layer, tb, s) : launch_rope_hd<T, 128>(a, p, layer, tb, s);
 }
 
 }  // namespace
@@ -201,12 +232,12 @@ llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer,
     if (((uintptr_t)rope->freq & 7) || (((uintptr_t)pos | (uintptr_t)seq | (uintptr_t)table | (uintptr_t)err) & 3))
         return LQ8_ERR_ARG;
     if (rows == 0) return LQ8_OK;
-    RopeArgs a{qkv, qkv_stride, pos, seq, n_head, rope->freq, rope->rot_dim, rope->style, rope->magnitude, q_out, err};
+    RopeArgs a{qkv, qkv_stride, pos, seq, rows, n_head, rope->freq, rope->rot_dim, rope->style, rope->magnitude, q_out, err};
     const TableView tb{table, n_seq, table_stride};
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = pages->type == LLAMA_Q8_GGUF_F32   ? launch_rope<float>(a, pages, layer, tb, rows, s)
-                    : pages->type == LLAMA_Q8_GGUF_F16 ? launch_rope<__half>(a, pages, layer, tb, rows, s)
-                                                       : launch_rope<__nv_bfloat16>(a, pages, layer, tb, rows, s);
+    cudaError_t e = pages->type == LLAMA_Q8_GGUF_F32   ? launch_rope<float>(a, pages, layer, tb, s)
+                    : pages->type == LLAMA_Q8_GGUF_F16 ? launch_rope<__half>(a, pages, layer, tb, s)
+                                                       : launch_rope<__nv_bfloat16>(a, pages, layer, tb, s);
     return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
 

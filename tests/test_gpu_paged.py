@@ -49,7 +49,8 @@ ROPE = [  # rows, heads, kv, dim, rot, style, page, kind, far, pad
     (1, 9, 3, 64, 64, 0, 16, "f32", 0, False), (4, 9, 3, 64, 64, 1, 16, "f16", 330, False),
     (37, 32, 8, 128, 128, 0, 64, "bf16", 1000, True), (5, 32, 8, 128, 64, 1, 8, "f16", 100000, True),
     (3, 5, 5, 64, 8, 0, 256, "f32", 1 << 20, False), (2, 7, 1, 128, 24, 1, 32, "bf16", 77, False),
-    (3, 71, 71, 64, 40, 1, 16, "f32", 12345, False), (129, 8, 1, 64, 32, 0, 8, "f16", 3, True)]
+    (3, 71, 71, 64, 40, 1, 16, "f32", 12345, False), (129, 8, 1, 64, 32, 0, 8, "f16", 3, True),
+    (5003, 9, 3, 64, 64, 0, 16, "f32", 40, True), (6001, 4, 1, 128, 96, 1, 32, "bf16", 9, True)]
 
 
 @pytest.mark.parametrize("rows,heads,kv,dim,rot,style,page,kind,far,pad", ROPE)
