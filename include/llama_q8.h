@@ -572,8 +572,7 @@ llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer,
  * does not matter; visible keys and values must be finite. Rows may share a
  * sequence (several new tokens of one sequence, each with its own pos).
  * Products with F16 / BF16 pages run on the tensor cores on q and the
- * probabilities split into parts that keep 22 bits or more (probabilities: 16
- * with BF16), summed in f32; F32 pages are multiplied in f32. The visible
+ * probabilities split into parts that keep 22 bits or more, summed in f32; F32 pages are multiplied in f32. The visible
  * positions of all rows are dealt evenly to the GPU's blocks, whatever their
  * lengths; parts of one row meet through the workspace, always added in the
  * order of the positions, so equal calls give equal bits.

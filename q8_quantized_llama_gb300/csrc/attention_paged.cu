@@ -18,8 +18,8 @@
 // Inside a CTA each of four warps takes one tile of every unit through a ring
 // of its own (cp.async, zero-filled outside the visible range, 16-byte pieces
 // XOR-swizzled by row), keeps its own m, l and output in registers and needs no
-// CTA barrier until the end of the pair. Page numbers are fetched 32 tiles
-// ahead, one per lane.
+// CTA barrier until the end of the pair. Page numbers are fetched 32 at a time,
+// one per lane; a piece's successor is begun before the piece is joined.
 //
 // 16-bit pages: mma.sync m16n8k16. A group has at most 8 query heads, so rows
 // 0-7 of the A operand carry the high part of q (or of the probabilities) and
@@ -28,10 +28,19 @@
 // probabilities through tensor memory; the kernel is bound by memory without.
 //  - f16: q is scaled per head by a power of two (largest value into [2^14,
 //    2^15)) and split in two: 22 bits; the probabilities by 2^15.
-//  - bf16: q in three parts, 24 bits (the third in a second product); the
-//    probabilities in two, 16 bits and the rounding's sign.
+//  - bf16: q and the probabilities in three parts, 24 bits. Groups of up to 4
+//    heads have the three parts in rows 0-3, 4-7 and 8-11 of one product; larger
+//    ones the third in a second product.
 // f32 pages: f32 products. Scores: a few lanes per key over the dimensions,
 // q from shared memory; output: a few dimensions per lane.
+//
+// Measured (bytes of the visible rows per time, of 6.7 TB/s that a copy reaches):
+// 64 rows up to 8191 positions, f16, 32/8 heads of 128: 150 us, 6.5 TB/s; one
+// row of 131071, bf16: 90 us, 6.0; 48 rows up to 4096, f32, 9/3 heads of 64: 31
+// us, 4.4. Where the bytes are few, the fixed chain is what takes the time:
+// positions (1.3 us), page numbers, first tiles, join, ticket and parts, about 7
+// us in all. f32 groups of 5-8 heads are bound by their arithmetic instead (2900
+// cycles per tile and warp: 16/2 heads of 128, 32 rows: 44 us, 21 for the bytes).
 #include <algorithm>
 #include <type_traits>
 
@@ -43,7 +52,7 @@ namespace lq8 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kMaxG = 8;
-constexpr int kMaxCtas = 2 * 152;
+constexpr int kMaxCtas = 2 * 152;      // two per SM: one joins while the other streams
 constexpr int kRingBytes = 24 * 1024;  // per warp
 constexpr int kMinShare = 2;           // units a CTA takes at least
 constexpr int kJoin = 16;              // parts joined at once where a pair has more than twice as many
@@ -164,14 +173,29 @@ __device__ __forceinline__ int range_units(const Range& g) {
 
 __device__ constexpr int log2_ceil(int x) { return x <= 1 ? 0 : 1 + log2_ceil((x + 1) / 2); }
 
-// One warp's running state over one (row, KV head).
-template <typename T, int HD>
+// One warp's running state over one (row, KV head). A lane's accumulators belong to rows lane / 4 and lane / 4 + 8.
+template <typename T, int HD, int GP>
 struct State16 {
+    static constexpr bool kHalf = std::is_same<T, __half>::value;
+    static constexpr bool kOne = !kHalf && GP == 4;  // three parts in one product: lanes of rows 4-7 have the second
+    static constexpr bool kTwo = !kHalf && GP == 8;  // the third part in a second product
     uint32_t q[HD / 16][4];
-    uint32_t q3[HD / 16][2];  // bf16: third part
+    uint32_t q3[kTwo ? HD / 16 : 1][2];
     float o[HD / 8][4];
     float m, l, q_inv;
 };
+// (x, y) as the two words of an A operand for a row's parts: rows lane / 4 and lane / 4 + 8, and the third part apart.
+template <typename St, typename T>
+__device__ __forceinline__ void split_parts(float x, float y, uint32_t& top, uint32_t& low, uint32_t& third, int lane, T tag) {
+    top = take_part(x, y, tag);
+    low = take_part(x, y, tag);
+    if (St::kTwo) third = take_part(x, y, tag);
+    if (St::kOne) {
+        const bool second = lane >= 16;  // rows 4-7
+        top = second ? low : top;
+        low = second ? 0u : take_part(x, y, tag);
+    }
+}
 template <int HD>
 struct State32 {
     uint64_t o[kMaxG][HD / 64];  // pairs of dimensions
@@ -179,10 +203,10 @@ struct State32 {
 };
 
 // q [G][HD] in shared memory
-template <typename T, int HD>
-__device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, int G, float scale, int lane) {
-    constexpr bool kHalf = std::is_same<T, __half>::value;
-    const int g = lane >> 2, t = lane & 3;
+template <typename T, int HD, int GP>
+__device__ __forceinline__ void state_init(State16<T, HD, GP>& s, const float* q, int G, float scale, int lane) {
+    using St = State16<T, HD, GP>;
+    const int g = St::kOne ? (lane >> 2) & 3 : lane >> 2, t = lane & 3;
     const T tag{};
     float v[HD / 16][4];
     float mx = 0.0f;
@@ -200,7 +224,7 @@ __device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, in
     }
     float up = 1.0f;
     s.q_inv = 1.0f;
-    if (kHalf) {
+    if (St::kHalf) {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int sh = row_shift(mx);
@@ -209,16 +233,9 @@ __device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, in
     }
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[k][j] *= up;
-        s.q[k][0] = take_part(v[k][0], v[k][1], tag);
-        s.q[k][1] = take_part(v[k][0], v[k][1], tag);
-        s.q[k][2] = take_part(v[k][2], v[k][3], tag);
-        s.q[k][3] = take_part(v[k][2], v[k][3], tag);
-        if (!kHalf) {
-            s.q3[k][0] = take_part(v[k][0], v[k][1], tag);
-            s.q3[k][1] = take_part(v[k][2], v[k][3], tag);
-        }
+        uint32_t* third = s.q3[St::kTwo ? k : 0];
+        split_parts<St>(v[k][0] * up, v[k][1] * up, s.q[k][0], s.q[k][1], third[0], lane, tag);
+        split_parts<St>(v[k][2] * up, v[k][3] * up, s.q[k][2], s.q[k][3], third[1], lane, tag);
     }
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d)
@@ -229,9 +246,9 @@ __device__ __forceinline__ void state_init(State16<T, HD>& s, const float* q, in
 }
 
 // A tile of 2048 / HD keys: K at ks, V at vs (shared addresses); key j of the tile counts if bit j of see is set.
-template <typename T, int HD>
-__device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint32_t vs, unsigned see, int lane) {
-    constexpr bool kHalf = std::is_same<T, __half>::value;
+template <typename T, int HD, int GP>
+__device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, uint32_t vs, unsigned see, int lane) {
+    using St = State16<T, HD, GP>;
     constexpr int RB = HD * 2, NT = 2048 / HD / 8;  // blocks of 8 keys
     const T tag{};
     const int l8 = lane & 7, mi = lane >> 3, t = lane & 3;
@@ -247,7 +264,7 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
             ldsm4(b, ks + (n * 8 + l8) * RB + (((k * 4 + mi) ^ l8) << 4));
             mma16(c[0], s.q[2 * k], b[0], b[1], tag);
             mma16(c[1], s.q[2 * k + 1], b[2], b[3], tag);
-            if (!kHalf) {
+            if constexpr (St::kTwo) {
                 const uint32_t a0[4] = {s.q3[2 * k][0], 0, s.q3[2 * k][1], 0};
                 const uint32_t a1[4] = {s.q3[2 * k + 1][0], 0, s.q3[2 * k + 1][1], 0};
                 mma16(c3, a0, b[0], b[1], tag);
@@ -257,7 +274,8 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float y = (c[0][i] + c[1][i]) + (c[0][i + 2] + c[1][i + 2] + c3[i]);
-            if (kHalf) y *= s.q_inv;
+            if (St::kOne) y += __shfl_xor_sync(0xffffffffu, y, 16);  // the first and third part, and the second
+            if (St::kHalf) y *= s.q_inv;
             x[2 * n + i] = (see >> (n * 8 + 2 * t + i)) & 1 ? y : -INFINITY;
         }
     }
@@ -277,8 +295,8 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
             for (int j = 0; j < 4; ++j) s.o[d][j] *= f;
     }
     // f16: probabilities times 2^15, so that the second part of a small one is not lost below f16's range
-    const float ref = kHalf ? m - 15.0f : m;
-    uint32_t a[NT / 2][4];
+    const float ref = St::kHalf ? m - 15.0f : m;
+    uint32_t a[NT / 2][4], a3[NT / 2][4] = {};
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
         x[j] = ex2(x[j] - ref);
@@ -286,10 +304,8 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
     }
 #pragma unroll
     for (int h = 0; h < NT / 2; ++h) {
-        a[h][0] = take_part(x[4 * h], x[4 * h + 1], tag);
-        a[h][1] = take_part(x[4 * h], x[4 * h + 1], tag);
-        a[h][2] = take_part(x[4 * h + 2], x[4 * h + 3], tag);
-        a[h][3] = take_part(x[4 * h + 2], x[4 * h + 3], tag);
+        split_parts<St>(x[4 * h], x[4 * h + 1], a[h][0], a[h][1], a3[h][0], lane, tag);
+        split_parts<St>(x[4 * h + 2], x[4 * h + 3], a[h][2], a[h][3], a3[h][2], lane, tag);
     }
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d)
@@ -299,21 +315,31 @@ __device__ __forceinline__ void state_tile(State16<T, HD>& s, uint32_t ks, uint3
             ldsm4_t(b, vs + (h * 16 + (mi & 1) * 8 + l8) * RB + (((2 * d + (mi >> 1)) ^ l8) << 4));
             mma16(s.o[2 * d], a[h], b[0], b[1], tag);
             mma16(s.o[2 * d + 1], a[h], b[2], b[3], tag);
+            if constexpr (St::kTwo) {
+                mma16(s.o[2 * d], a3[h], b[0], b[1], tag);
+                mma16(s.o[2 * d + 1], a3[h], b[2], b[3], tag);
+            }
         }
 }
 
 // The warp's part: output [8][HD] to ob, m and l of its heads to ml (l of f16 pages carries the factor 2^15).
-template <typename T, int HD>
-__device__ __forceinline__ void state_store(State16<T, HD>& s, float* ob, float2* ml, int lane) {
+template <typename T, int HD, int GP>
+__device__ __forceinline__ void state_store(State16<T, HD, GP>& s, float* ob, float2* ml, int lane) {
+    constexpr bool kOne = State16<T, HD, GP>::kOne;
     const int g = lane >> 2, t = lane & 3;
     float l = s.l;
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (t == 0) ml[g] = make_float2(s.m, l);
 #pragma unroll
-    for (int d = 0; d < HD / 8; ++d)
-        *reinterpret_cast<float2*>(ob + g * HD + d * 8 + 2 * t) =
-            make_float2(s.o[d][0] + s.o[d][2], s.o[d][1] + s.o[d][3]);
+    for (int d = 0; d < HD / 8; ++d) {
+        float x = s.o[d][0] + s.o[d][2], y = s.o[d][1] + s.o[d][3];
+        if (kOne) {
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            y += __shfl_xor_sync(0xffffffffu, y, 16);
+        }
+        if (!kOne || g < 4) *reinterpret_cast<float2*>(ob + g * HD + d * 8 + 2 * t) = make_float2(x, y);
+    }
 }
 
 template <int HD, int GP>
@@ -414,7 +440,7 @@ __device__ __forceinline__ void state_store(State32<HD>& s, float* ob, float2* m
     }
 }
 
-// GP: query heads the f32 form carries (4 or 8); the tensor cores' rows hold 8 in any case.
+// GP: query heads the f32 and bf16 forms carry (4 or 8); f16 has room for 8 in any case.
 template <typename T, int HD, int GP>
 __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a, PageView<T> pg, TableView tb) {
     using S = Shape<T, HD>;
@@ -585,12 +611,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             ask_q(nxt, buf ^ 1);  // arrives with the next tile asked for
         }
         const float* qs = reinterpret_cast<const float*>(smem + kSmemQ) + buf * kMaxG * HD;
-        State16<T, HD> s16;
-        State32<HD> s32;
+        std::conditional_t<kF32, State32<HD>, State16<std::conditional_t<kF32, __half, T>, HD, GP>> state;
         if constexpr (kF32)
-            state_init<HD, GP>(s32);
+            state_init<HD, GP>(state);
         else
-            state_init(s16, qs, G, a.scale_log2, lane);
+            state_init(state, qs, G, a.scale_log2, lane);
         int st = st0;
         for (int j = 0; j < cur.n; ++j) {
             cp_async_wait<kStages - 2>();
@@ -608,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             if (bits) {
                 const uint8_t* t = ring + st * 2 * kTileBytes;
                 if constexpr (kF32)
-                    state_tile<HD, GP>(s32, t, t + kTileBytes, qs, pb, a.scale_log2, bits, lane);
+                    state_tile<HD, GP>(state, t, t + kTileBytes, qs, pb, a.scale_log2, bits, lane);
                 else
-                    state_tile(s16, smem_u32(t), smem_u32(t + kTileBytes), bits, lane);
+                    state_tile(state, smem_u32(t), smem_u32(t + kTileBytes), bits, lane);
             }
             st = st == kStages - 1 ? 0 : st + 1;
         }
@@ -629,9 +654,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         }
         float* ob = reinterpret_cast<float*>(ring + stl * 2 * kTileBytes);
         if constexpr (kF32)
-            state_store<HD, GP>(s32, ob, ml + warp * kMaxG, lane);
+            state_store<HD, GP>(state, ob, ml + warp * kMaxG, lane);
         else
-            state_store(s16, ob, ml + warp * kMaxG, lane);
+            state_store(state, ob, ml + warp * kMaxG, lane);
         __syncthreads();
 
         // ---- join the warps: the result, or a part of it -----------------------------------
@@ -777,7 +802,7 @@ cudaError_t launch_one(const AttnArgs& a, const llama_q8_pages* p, int layer, co
 
 template <typename T>
 cudaError_t launch_attention(const AttnArgs& a, const llama_q8_pages* p, int layer, const TableView& tb, cudaStream_t s) {
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (!std::is_same<T, __half>::value) {
         if (a.n_head / p->n_head_kv > 4)
             return p->head_dim == 64 ? launch_one<T, 64, 8>(a, p, layer, tb, s) : launch_one<T, 128, 8>(a, p, layer, tb, s);
     }
@@ -800,6 +825,8 @@ cudaError_t init_attention_paged_attributes() {
     if (e == cudaSuccess) e = set_attr<__half, 128, 4>();
     if (e == cudaSuccess) e = set_attr<__nv_bfloat16, 64, 4>();
     if (e == cudaSuccess) e = set_attr<__nv_bfloat16, 128, 4>();
+    if (e == cudaSuccess) e = set_attr<__nv_bfloat16, 64, 8>();
+    if (e == cudaSuccess) e = set_attr<__nv_bfloat16, 128, 8>();
     return e;
 }
 }  // namespace lq8

@@ -150,11 +150,10 @@ ATTN = [  # lens, heads, kv, dim, page, kind, window
 def attention_tolerance(kind, dim, mag, reach, count, v_mag=1.0):
     """|out error| / sum p |v|. Scores: dim products and sums in f32, and for 16-bit pages q kept to 22 bits or more:
     ds = (dim + 8) 2^-24 + 2^-22, times the largest scale sum |q k|. Each weight then is off by 2 ds (its own and the
-    sum's), by 2^-21 for the exponential of a rounded argument up to ~8 |arguments| of weight, by the rounding of
-    the probabilities (bf16: two parts, 2^-16; f16: 2^-21), and the sums run over `count` terms in f32 plus 2^-21
-    for joining."""
+    sum's), by 2^-19 for the exponential of a rounded argument and for joining, by the rounding of the probabilities
+    (16-bit pages, in parts: 2^-21), and the sums run over `count` terms in f32."""
     ds = ((dim + 8) * U + 2.0 ** -22) * reach
-    p = {"f32": 0.0, "f16": 2.0 ** -21, "bf16": 2.0 ** -16}[kind]
+    p = 0.0 if kind == "f32" else 2.0 ** -21
     return 2 * ds + 2.0 ** -19 + p + count[:, None] * U
 
 
