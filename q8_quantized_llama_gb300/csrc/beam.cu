@@ -2,12 +2,16 @@
 // over beams x vocabulary, in one kernel that reads the logits once.
 //
 // total(beam, token) = score[beam] + logit - lse[beam], lse = ln sum exp(logit).
-// A CTA goes through its piece of a row, a block of values per thread at a time
-// with the next block's loads in flight, and gets the piece's sum of exponentials
-// (a running maximum and sum per thread) and its n_out largest logits: within a
-// row totals rise with logits, so no other value of the piece can be chosen. The
-// last CTA of a group to finish (a counter in the workspace) joins the pieces'
-// sums and picks the n_out largest totals.
+// A CTA goes through its piece of a row, a block of values per thread at a time,
+// with the next block's loads in flight, and gets the sums of exponentials (a
+// running maximum and sum per thread, given out per segment) and its n_out
+// largest logits: within a row totals rise with logits, so no other value of the
+// piece can be chosen. The last CTA of a group to finish (a counter in the
+// workspace) joins the sums and picks the n_out largest totals.
+//
+// Rows are cut into segments at the same places, and a segment's sums are added
+// in the same order, wherever it lies: equal rows get equal log sums, so that
+// equal totals of different beams are found equal. Pieces are whole segments.
 //
 // Largest of many by a bound: in the first block lanes form groups (32, 64 or
 // 128 per CTA, at least twice n_out); n_out groups reach the n_out-th largest of
@@ -15,14 +19,18 @@
 // are kept, and of the later blocks the values above the bound: an equal one
 // there has a higher index and loses. When the list has grown by 16 or half it is
 // cut to its n_out best, and the bound rises: keys (value, lowest index), which
-// all differ, are ranked by counting the larger ones.
+// all differ, are ranked by counting the larger ones. The list is looked at every
+// fourth block; where it overflows in between (rising values, a row of one
+// value), the piece's list is made again 1024 values at a time.
 //
-// Bound: issue slots and the latency of the first and last steps of a piece
-// rather than memory: 240 rows of 100003 take 34 us, 14 of them for the bytes.
+// Bound: the steps that end a piece and a group, and issue slots, more than
+// memory: 240 rows of 100003 take 36 us, 14 of them for the bytes; the final
+// choice alone is 4 to 5.
 // Not kept: one CTA per 8192 values without a list (46 us: barriers and fences);
 // a pass of maxima and sums alone, then a second look at the threads that reach
-// the bound (53 us: what they look up again has left L2); a list kept to the
-// bound in every block (35 us).
+// the bound (53 us: what they look up again has left L2); a ring of 4-byte
+// cp.async stages (41 us); pieces cut anywhere, the sums with them (34 us, but
+// equal rows got log sums that differed in the last bits).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -36,7 +44,7 @@ constexpr int kBeamMax = 64;   // beams per group, results per group
 constexpr int kPickItems = 4;  // candidates per thread and pass of the final choice
 constexpr int kBeamVocab = 1 << 28;  // longest row: 64 beams x 64 results x its chunks stay below 2^31 - 1024
 
-struct ChunkStat {
+struct SegmentStat {
     float m, s;  // largest logit and sum of exp(logit - m); NaN s: a NaN or +inf among them
 };
 struct ChunkCand {
@@ -49,32 +57,35 @@ struct BeamArgs {
     int64_t stride;
     const float* scores;
     int beams, n_vocab, n_out;
-    int chunks, blocks;  // pieces per row at most, blocks per row
-    int share, units;      // blocks per CTA, of all rows
+    int chunks, segs;     // pieces per row at most, segments per row
+    int share, units;     // segments per CTA, of all rows
     float* out_scores;
     int32_t *out_parent, *out_token;
     unsigned int* counters;  // [groups], zero between launches
-    ChunkStat* stat;         // [groups * beams][chunks], by the CTA's place among the row's
-    ChunkCand* cand;         // [groups * beams][chunks][n_out]
+    SegmentStat* stat;       // [groups * beams][segs]
+    ChunkCand* cand;         // [groups * beams][chunks][n_out], by the CTA's place among the row's
 };
 
-// How the work is cut: rows in blocks of 256 * items values, the blocks of all
-// rows dealt evenly to one wave of CTAs (four per SM), `share` blocks each, so
-// that a row is in pieces of up to `chunks` CTAs and a CTA may hold pieces of
-// several rows. Where that would leave most SMs without one, blocks of half the
-// size, one per CTA.
+// How the work is cut: rows in segments of four blocks of 4096 values, the
+// segments of all rows dealt evenly to one wave of CTAs, `share` each, so that a
+// row is in pieces of up to `chunks` CTAs and a CTA may hold pieces of several
+// rows. Where that would leave most SMs without one: segments of one block of
+// 2048, one per CTA.
 struct BeamCut {
-    int items, blocks, chunks;
+    int j, segs, chunks;
     int share, ctas;
 };
-constexpr int kBeamWave = 152 * 4;
+constexpr int kBeamCtas = 4;  // per SM
+constexpr int kBeamWave = 152 * kBeamCtas;
+template <int J>
+constexpr int kSegBlocks = J == 4 ? 4 : 1;
 inline BeamCut beam_cut(int64_t rows, int n_vocab) {
-    const int64_t big = ((int64_t)n_vocab + kBeamThreads * 16 - 1) / (kBeamThreads * 16);
-    const bool few = rows * big <= kBeamWave / 2;
-    const int64_t blocks = few ? ((int64_t)n_vocab + kBeamThreads * 8 - 1) / (kBeamThreads * 8) : big;
-    const int64_t share = few ? 1 : (rows * blocks + kBeamWave - 1) / kBeamWave;
-    return BeamCut{few ? 8 : 16, (int)blocks, (int)((blocks - 1 + share - 1) / share + 1), (int)share,
-                   (int)((rows * blocks + share - 1) / share)};
+    const bool few = rows * (((int64_t)n_vocab + 4095) / 4096) <= 152 * 2;
+    const int seg = few ? 2048 : 4 * 4096;
+    const int64_t segs = ((int64_t)n_vocab + seg - 1) / seg;
+    const int64_t share = few ? 1 : (rows * segs + kBeamWave - 1) / kBeamWave;
+    return BeamCut{few ? 2 : 4, (int)segs, (int)((segs - 1 + share - 1) / share + 1), (int)share,
+                   (int)((rows * segs + share - 1) / share)};
 }
 
 size_t beam_workspace(int groups, int beams, int n_vocab, int n_out, BeamArgs* a, void* ws) {
@@ -87,17 +98,17 @@ size_t beam_workspace(int groups, int beams, int n_vocab, int n_out, BeamArgs* a
         o += (bytes + 255) / 256 * 256;
         return at;
     };
-    const size_t c = take(kCounterBytes), t = take(sizeof(ChunkStat) * (size_t)(rows * chunks)),
+    const size_t c = take(kCounterBytes), t = take(sizeof(SegmentStat) * (size_t)(rows * cut.segs)),
                  d = take(sizeof(ChunkCand) * (size_t)(rows * chunks) * n_out);
     if (a) {
         uint8_t* w = reinterpret_cast<uint8_t*>(ws);
         a->counters = reinterpret_cast<unsigned int*>(w + c);
-        a->stat = reinterpret_cast<ChunkStat*>(w + t);
+        a->stat = reinterpret_cast<SegmentStat*>(w + t);
         a->cand = reinterpret_cast<ChunkCand*>(w + d);
         a->chunks = cut.chunks;
-        a->blocks = cut.blocks;
+        a->segs = cut.segs;
         a->share = cut.share;
-        a->units = (int)(rows * cut.blocks);
+        a->units = (int)(rows * cut.segs);
     }
     return o;
 }
@@ -141,9 +152,9 @@ __device__ __forceinline__ unsigned long long total_key(Sum2 t) {
 __device__ __forceinline__ int group_lanes(int n_out) { return n_out <= 16 ? 8 : n_out <= 32 ? 4 : 2; }
 
 // CTAs that hold a row's pieces: from first_cta on, row_pieces of them.
-__device__ __forceinline__ int first_cta(const BeamArgs& a, int row) { return row * a.blocks / a.share; }
+__device__ __forceinline__ int first_cta(const BeamArgs& a, int row) { return row * a.segs / a.share; }
 __device__ __forceinline__ int row_pieces(const BeamArgs& a, int row) {
-    return ((row + 1) * a.blocks - 1) / a.share - first_cta(a, row) + 1;
+    return ((row + 1) * a.segs - 1) / a.share - first_cta(a, row) + 1;
 }
 
 constexpr int kFinal = 16 * 8 * kPickItems;  // n_out groups of group_lanes threads: 16 x 8, 32 x 4, 64 x 2
@@ -187,14 +198,14 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
     const int i0 = direct ? tid : tid * a.n_out;
     const ChunkCand c0 = i0 < all ? fetch(i0) : ChunkCand{-INFINITY, -1};
     for (int b = warp; b < a.beams; b += kBeamThreads / 32) {
-        const ChunkStat* st = a.stat + (row0 + b) * a.chunks;
+        const SegmentStat* st = a.stat + (row0 + b) * a.segs;
         const int pieces = row_pieces(a, (int)row0 + b);
         const float sc = a.scores[row0 + b];
-        float top = -INFINITY, part = 0.0f;  // the lane's pieces
-        for (int c = lane; c < pieces; c += 32) {
+        float top = -INFINITY, part = 0.0f;  // the lane's segments
+        for (int c = lane; c < a.segs; c += 32) {
             const float2 x = __ldcg(reinterpret_cast<const float2*>(st + c));
             const float m1 = fmaxf(top, x.x);
-            // a piece of -inf alone adds 0, one of NaN alone NaN
+            // -inf alone adds 0, NaN alone NaN
             part = (top > -INFINITY ? part * expf(top - m1) : part) + (x.x > -INFINITY ? x.y * expf(x.x - m1) : x.y);
             top = m1;
         }
@@ -345,47 +356,128 @@ __device__ __forceinline__ int key_rank(const unsigned long long* list, int n, u
     return r;
 }
 
-template <int IT>
-__global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(BeamArgs a) {
-    constexpr int kBlock = kBeamThreads * IT;
-    constexpr int kList = 2 * kBeamMax + kBlock;
-    constexpr int kCut = kBeamMax * ((kList + kBeamThreads - 1) / kBeamThreads);
-    // the chunk's part and the group's part use the memory one after the other
+constexpr int kList = 1280;  // keys the list holds; a step of the careful form adds at most 1024 to at most 96
+constexpr int kCut = kBeamMax * (kList / kBeamThreads);
+// QUAD: all rows start at 16-byte boundaries; a thread's values lie in groups of four, otherwise 256 apart.
+template <int J, bool QUAD>
+__global__ void __launch_bounds__(kBeamThreads, kBeamCtas) beam_select_kernel(BeamArgs a) {
+    constexpr int IT = 4 * J, kBlock = kBeamThreads * IT, kSeg = kSegBlocks<J>;
+    // the pieces' part and the groups' part use the memory one after the other
     __shared__ __align__(16) union {
         struct {
             unsigned long long best[kBeamThreads], list[kList], cut[kCut];
         } c;
         ChooseShared g;
     } sm;
-    __shared__ float red_m[kBeamThreads / 32], red_s[kBeamThreads / 32], s_top[kBeamThreads / 2];
+    __shared__ float s_top[kBeamThreads / 2];
     __shared__ unsigned long long s_bound;
     __shared__ float s_floor;
     __shared__ int s_n, s_cut, s_last;
+    __shared__ float red_m[2][kBeamThreads / 32], red_s[2][kBeamThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gl = group_lanes(a.n_out), groups = kBeamThreads / gl;
-    const int few = a.n_out + max(16, a.n_out / 2);  // keys a block may find in the list: at most 96
+    const int few = a.n_out + max(16, a.n_out / 2);  // keys a step may find in the list: at most 96
     int unit = blockIdx.x * a.share;
     const int unit1 = min(a.units - unit, a.share) + unit;
     while (unit < unit1) {
-        const int row = unit / a.blocks, block0 = unit % a.blocks, n_blocks = min(a.blocks - block0, unit1 - unit);
-        unit += n_blocks;
+        const int row = unit / a.segs, seg0 = unit % a.segs, n_segs = min(a.segs - seg0, unit1 - unit);
+        unit += n_segs;
         const int group = row / a.beams, chunk = blockIdx.x - first_cta(a, row);
-        const int64_t base = (int64_t)block0 * kBlock;
-        const int n = (int)min((int64_t)n_blocks * kBlock, a.n_vocab - base);
+        const int64_t base = (int64_t)seg0 * (kSeg * kBlock);
+        const int n = (int)min((int64_t)n_segs * (kSeg * kBlock), a.n_vocab - base);
         const float* x = a.logits + (int64_t)row * a.stride + base;
+        const int blocks = (n + kBlock - 1) / kBlock;
 
+        // place in the piece of the thread's value j of block b
+        auto index = [&](int b, int j) {
+            return QUAD ? b * kBlock + ((j >> 2) * kBeamThreads + tid) * 4 + (j & 3) : b * kBlock + j * kBeamThreads + tid;
+        };
+        const float* xt = x + index(0, 0);
         float v[IT], next[IT] = {};
-        auto load = [&](float (&to)[IT], int b0) {
-            if (n - b0 >= kBlock) {
+        auto load = [&](float (&to)[IT], int b) {
+            const float* from = xt + b * kBlock;
+            const int left = n - index(b, 0);  // values from the thread's first on
+            if (QUAD) {
 #pragma unroll
-                for (int j = 0; j < IT; ++j) to[j] = __ldcs(x + b0 + j * kBeamThreads + tid);
+                for (int j = 0; j < IT; j += 4) {
+                    const float4 y = j * kBeamThreads + 3 < left ? __ldcs(reinterpret_cast<const float4*>(from + j * kBeamThreads))
+                                                                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                    to[j] = y.x; to[j + 1] = y.y; to[j + 2] = y.z; to[j + 3] = y.w;
+                }
+                if (left < IT * kBeamThreads && (n & 3)) {  // a row's last one to three values
+#pragma unroll
+                    for (int j = 0; j < IT; j += 4)
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            if (j * kBeamThreads + k < left && j * kBeamThreads + 3 >= left) to[j + k] = from[j * kBeamThreads + k];
+                }
+            } else if (n - b * kBlock >= kBlock) {
+#pragma unroll
+                for (int j = 0; j < IT; ++j) to[j] = __ldcs(from + j * kBeamThreads);
             } else {
 #pragma unroll
-                for (int j = 0; j < IT; ++j) {
-                    const int i = b0 + j * kBeamThreads + tid;
-                    to[j] = i < n ? __ldcs(x + i) : -INFINITY;
-                }
+                for (int j = 0; j < IT; ++j) to[j] = j * kBeamThreads < left ? __ldcs(from + j * kBeamThreads) : -INFINITY;
             }
+        };
+        load(v, 0);
+
+        float m = -INFINITY, s = 0.0f;  // running maximum and sum; a NaN or +inf makes the sum NaN
+        auto take_block = [&]() {       // largest number of the block's values
+            float top = v[0];
+#pragma unroll
+            for (int j = 1; j < IT; ++j) top = fmaxf(top, v[j]);
+            if (top != top) top = -INFINITY;
+            const float m1 = fmaxf(m, top), ref = m1 > -INFINITY ? m1 : 0.0f;
+            const uint64_t ref2 = pack_f2(ref, ref), log2e = pack_f2(1.4426950408889634f, 1.4426950408889634f);
+            uint64_t sum2 = pack_f2(m > -INFINITY ? s * ex2((m - ref) * 1.4426950408889634f) : s, 0.0f);
+#pragma unroll
+            for (int j = 0; j < IT; j += 2) {
+                const uint64_t t = mul_f2(sub_f2(pack_f2(v[j], v[j + 1]), ref2), log2e);
+                sum2 = add_f2(sum2, pack_f2(ex2(f2_lo(t)), ex2(f2_hi(t))));
+            }
+            s = f2_lo(sum2) + f2_hi(sum2);
+            m = m1;
+            return top;
+        };
+        // the CTA's sum of segment seg (two sets of warp sums in turn: the next segment's are written while these are read)
+        auto give_segment = [&](int seg) {
+            const float wm = warp_max(m);
+            const float ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
+            if (lane == 0) {
+                red_m[seg & 1][warp] = wm;
+                red_s[seg & 1][warp] = ws;
+            }
+            m = -INFINITY;
+            s = 0.0f;
+            __syncthreads();
+            if (warp == kBeamThreads / 32 - 1) {
+                const float m0 = lane < kBeamThreads / 32 ? red_m[seg & 1][lane] : -INFINITY;
+                const float s0 = lane < kBeamThreads / 32 ? red_s[seg & 1][lane] : 0.0f;
+                const float m1 = warp_max(m0), s1 = warp_sum(m0 > -INFINITY ? s0 * expf(m0 - m1) : s0);
+                if (lane == 0) a.stat[(int64_t)row * a.segs + seg] = SegmentStat{m1, s1};
+            }
+        };
+        // s_floor: the n_out-th largest of the lane groups' values of `top`
+        auto find_floor = [&](float top) {
+            for (int o = 1; o < gl; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (tid % gl == 0) s_top[tid / gl] = top;
+            __syncthreads();
+            if (tid < groups) {
+                const float mine = s_top[tid];
+                int over = 0, same = 0;
+#pragma unroll 8
+                for (int t = 0; t < groups; ++t) {
+                    over += s_top[t] > mine;
+                    same += s_top[t] == mine;
+                }
+                // the same value from every group that has it
+                if (over < a.n_out && over + same >= a.n_out) s_floor = mine;
+            }
+            __syncthreads();
+        };
+        auto push = [&](float y, int i) {
+            const int at = atomicAdd(&s_n, 1);
+            if (at < kList) sm.c.list[at] = argmax_key(y + 0.0f, i);  // -0 and 0 are one value
         };
         // the list's n_out best to its front, in order; s_floor: the smallest of them (all threads; the list is complete
         // and has n_out keys or more)
@@ -421,123 +513,81 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(BeamArgs a
             __syncthreads();
         };
 
-        float m = -INFINITY, s = 0.0f;
-        // largest number of the block's values, and the running maximum and sum; a NaN or +inf makes the sum NaN
-        auto take_block = [&]() {
-            float top = v[0];
-#pragma unroll
-            for (int j = 1; j < IT; ++j) top = fmaxf(top, v[j]);
-            if (top != top) top = -INFINITY;
-            const float m1 = fmaxf(m, top), ref = m1 > -INFINITY ? m1 : 0.0f;
-            const uint64_t ref2 = pack_f2(ref, ref), log2e = pack_f2(1.4426950408889634f, 1.4426950408889634f);
-            uint64_t sum2 = pack_f2(m > -INFINITY ? s * ex2((m - ref) * 1.4426950408889634f) : s, 0.0f);
-#pragma unroll
-            for (int j = 0; j < IT; j += 2) {
-                const uint64_t t = mul_f2(sub_f2(pack_f2(v[j], v[j + 1]), ref2), log2e);
-                sum2 = add_f2(sum2, pack_f2(ex2(f2_lo(t)), ex2(f2_hi(t))));
+        if (tid == 0) s_n = 0;
+        float floor = -INFINITY;
+        bool full = false;
+        for (int b = 0; b < blocks; ++b) {
+            if (b + 1 < blocks) load(next, b + 1);
+            const float top = take_block();
+            if ((b + 1) % kSeg == 0 || b + 1 == blocks) give_segment(seg0 + b / kSeg);
+            if (b == 0) {
+                find_floor(top);
+                floor = s_floor;
             }
-            s = f2_lo(sum2) + f2_hi(sum2);
-            m = m1;
-            return top;
-        };
-        // s_floor: the n_out-th largest of the lane groups' values of `top`
-        auto find_floor = [&](float top) {
-            for (int o = 1; o < gl; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (tid % gl == 0) s_top[tid / gl] = top;
-            __syncthreads();
-            if (tid < groups) {
-                const float mine = s_top[tid];
-                int over = 0, same = 0;
-#pragma unroll 8
-                for (int t = 0; t < groups; ++t) {
-                    over += s_top[t] > mine;
-                    same += s_top[t] == mine;
+            // a later value has to be above the bound, one of the first block at it
+            if (!full && (b == 0 ? top >= floor : top > floor)) {
+                // one bit per value, the last in bit 0: the sign of bound - value (of value - bound in the first block;
+                // a bound of 0 gets the sign with which -0 and 0 leave no sign)
+                const float fl = floor == 0.0f ? (b == 0 ? -0.0f : 0.0f) : floor;
+                const uint64_t fl2 = pack_f2(fl, fl);
+                unsigned hit = 0;
+#pragma unroll
+                for (int j = 0; j < IT; j += 2) {
+                    const uint64_t x2 = pack_f2(v[j], v[j + 1]);
+                    const uint64_t d = b == 0 ? sub_f2(x2, fl2) : sub_f2(fl2, x2);
+                    hit = __funnelshift_l((uint32_t)d, hit, 1);
+                    hit = __funnelshift_l((uint32_t)(d >> 32), hit, 1);
                 }
-                // the same value from every group that has it
-                if (over < a.n_out && over + same >= a.n_out) s_floor = mine;
-            }
-            __syncthreads();
-        };
-        // the block's values above the bound (or at it) to the list
-        auto push_block = [&](bool at_it, float floor, int b0) {
-            // one bit per value, the last in bit 0: the sign of bound - value (of value - bound with at_it; a bound of 0
-            // gets the sign with which -0 and 0 leave no sign)
-            const float fl = floor == 0.0f ? (at_it ? -0.0f : 0.0f) : floor;
-            const uint64_t fl2 = pack_f2(fl, fl);
-            unsigned hit = 0;
+                if (b == 0) hit = ~hit & ((1u << IT) - 1);
+                while (hit) {
+                    const int bit = 31 - __clz(hit), j = IT - 1 - bit, i = index(b, j);
+                    hit ^= 1u << bit;
+                    float y[IT];  // y[0] becomes v[j]
 #pragma unroll
-            for (int j = 0; j < IT; j += 2) {
-                const uint64_t x2 = pack_f2(v[j], v[j + 1]);
-                const uint64_t d = at_it ? sub_f2(x2, fl2) : sub_f2(fl2, x2);
-                hit = __funnelshift_l((uint32_t)d, hit, 1);
-                hit = __funnelshift_l((uint32_t)(d >> 32), hit, 1);
-            }
-            if (at_it) hit = ~hit & ((1u << IT) - 1);
-            while (hit) {
-                const int bit = 31 - __clz(hit), j = IT - 1 - bit, i = b0 + j * kBeamThreads + tid;
-                hit ^= 1u << bit;
-                float y[IT];  // y[0] becomes v[j]
+                    for (int t = 0; t < IT; ++t) y[t] = v[t];
 #pragma unroll
-                for (int t = 0; t < IT; ++t) y[t] = v[t];
+                    for (int w = IT / 2; w > 0; w >>= 1)
 #pragma unroll
-                for (int w = IT / 2; w > 0; w >>= 1)
-#pragma unroll
-                    for (int t = 0; t < w; ++t) y[t] = (j & w) ? y[t + w] : y[t];
-                if (i < n) {
-                    const int at = atomicAdd(&s_n, 1);
-                    if (at < kList) sm.c.list[at] = argmax_key(y[0] + 0.0f, i);  // -0 and 0 are one value
+                        for (int t = 0; t < w; ++t) y[t] = (j & w) ? y[t + w] : y[t];
+                    if (i < n) push(y[0], i);
                 }
             }
-        };
-
-        // the list is looked at every fourth block, so that the warps need not keep in step; where that lets it
-        // overflow (rising values), the piece is done again with a look after every block
-        for (bool careful = false;; careful = true) {
-            float floor = -INFINITY;
-            bool full = false;
-            load(v, 0);
-            m = -INFINITY;
-            s = 0.0f;
-            if (tid == 0) s_n = 0;
-            for (int it = 0, b0 = 0; b0 < n; ++it, b0 += kBlock) {
-                if (b0 + kBlock < n) load(next, b0 + kBlock);
-                const float top = take_block();
-                if (it == 0) {
-                    find_floor(top);
+            if (!full && ((b & 3) == 3 || b + 1 == blocks)) {
+                __syncthreads();
+                const int count = s_n;
+                __syncthreads();  // s_n has been read before anyone adds to it
+                full = count > kList;
+                if (!full && count > few) {
+                    cut_list(count);
                     floor = s_floor;
                 }
-                // a later value has to be above the bound, one of the first block at it
-                if (it == 0 ? top >= floor : top > floor) push_block(it == 0, floor, b0);
-                if (careful || (it & 3) == 3 || b0 + kBlock >= n) {
-                    __syncthreads();
-                    const int count = s_n;
-                    __syncthreads();  // s_n has been read before anyone adds to it
-                    if (count > kList) {
-                        full = true;
-                        break;
-                    }
-                    if (count > few) {
-                        cut_list(count);
-                        floor = s_floor;
-                    }
+            }
+#pragma unroll
+            for (int j = 0; j < IT; ++j) v[j] = next[j];
+        }
+        if (full) {  // 1024 values at a time, the list looked at after each
+            if (tid == 0) s_n = 0;
+            for (int i0 = tid; i0 - tid < n; i0 += 4 * kBeamThreads) {
+                float y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = i0 + k * kBeamThreads < n ? x[i0 + k * kBeamThreads] : -INFINITY;
+                if (i0 == tid) {
+                    const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                    find_floor(top == top ? top : -INFINITY);
+                    floor = s_floor;
                 }
 #pragma unroll
-                for (int j = 0; j < IT; ++j) v[j] = next[j];
+                for (int k = 0; k < 4; ++k)
+                    if (i0 + k * kBeamThreads < n && (i0 == tid ? y[k] >= floor : y[k] > floor))
+                        push(y[k], i0 + k * kBeamThreads);
+                __syncthreads();
+                const int count = s_n;
+                __syncthreads();
+                if (count > few) {
+                    cut_list(count);
+                    floor = s_floor;
+                }
             }
-            if (!full) break;  // the same in every thread
-        }
-        {
-            const float wm = warp_max(m);
-            const float ws = warp_sum(m > -INFINITY ? s * expf(m - wm) : s);
-            if (lane == 0) { red_m[warp] = wm; red_s[warp] = ws; }
-        }
-        __syncthreads();
-        if (warp == kBeamThreads / 32 - 1) {
-            const float wm0 = lane < kBeamThreads / 32 ? red_m[lane] : -INFINITY;
-            const float ws0 = lane < kBeamThreads / 32 ? red_s[lane] : 0.0f;
-            const float wm = warp_max(wm0);
-            const float ws = warp_sum(wm0 > -INFINITY ? ws0 * expf(wm0 - wm) : ws0);
-            if (lane == 0) a.stat[(int64_t)row * a.chunks + chunk] = ChunkStat{wm, ws};
         }
         ChunkCand* out = a.cand + ((int64_t)row * a.chunks + chunk) * a.n_out;
         const int nc = s_n;
@@ -559,7 +609,6 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(BeamArgs a
         __syncthreads();
         if (!s_last) continue;  // the same in every thread; what the next piece writes first is behind a barrier
         if (tid == 0) a.counters[group] = 0;
-
         choose(a, sm.g, group);
         __syncthreads();  // the shared memory is the next piece's
     }
@@ -578,7 +627,7 @@ static bool beam_sizes_ok(int32_t groups, int32_t beams, int32_t n_vocab, int32_
 static bool beam_sizes_supported(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out) {
     return beams <= kBeamMax && n_out <= kBeamMax && (int64_t)groups * beams < kMaxCounters && n_vocab <= kBeamVocab &&
            // blocks are counted in 32 bits
-           (int64_t)groups * beams * (n_vocab / (kBeamThreads * 8) + 1) < INT32_MAX - kBeamVocab;
+           (int64_t)groups * beams * (n_vocab / 2048 + 1) < INT32_MAX - kBeamVocab;
 }
 
 size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out) {
@@ -603,11 +652,14 @@ llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride,
     a.logits = logits, a.stride = logits_stride, a.scores = scores, a.beams = beams, a.n_vocab = n_vocab;
     a.n_out = n_out, a.out_scores = out_scores, a.out_parent = out_parent, a.out_token = out_token;
     const BeamCut cut = beam_cut((int64_t)groups * beams, n_vocab);
-    const dim3 grid((unsigned)cut.ctas);
+    const dim3 grid((unsigned)cut.ctas), block(kBeamThreads);
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool quad = ((uintptr_t)logits & 15) == 0 && logits_stride % 4 == 0;
     const cudaError_t e =
-        cut.items == 16
-            ? launch_ex(beam_select_kernel<16>, grid, dim3(kBeamThreads), 0, (cudaStream_t)stream, false, a)
-            : launch_ex(beam_select_kernel<8>, grid, dim3(kBeamThreads), 0, (cudaStream_t)stream, false, a);
+        cut.j == 4 ? (quad ? launch_ex(beam_select_kernel<4, true>, grid, block, 0, st, false, a)
+                           : launch_ex(beam_select_kernel<4, false>, grid, block, 0, st, false, a))
+                   : (quad ? launch_ex(beam_select_kernel<2, true>, grid, block, 0, st, false, a)
+                           : launch_ex(beam_select_kernel<2, false>, grid, block, 0, st, false, a));
     return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
 

@@ -585,6 +585,34 @@ def test_beam_select_sorted_rows(groups, beams):
         check_beam(B, row[None].repeat(groups * beams, 1).contiguous(), torch.zeros(groups * beams, device="cuda"), beams, 7)
 
 
+@pytest.mark.parametrize("groups,beams,vocab", [(1, 4, 5001), (3, 5, 70001), (40, 6, 30002), (130, 5, 8200), (7, 3, 100000)])
+def test_beam_select_equal_rows_tie(groups, beams, vocab):
+    """Beams with equal rows and scores have equal totals, wherever in memory their rows lie: the lowest beam first."""
+    B = binding()
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x = 3.0 * torch.randn((groups, 1, vocab), generator=g, device="cuda").expand(groups, beams, vocab)
+    check_beam(B, x.reshape(groups * beams, vocab).contiguous(), torch.zeros(groups * beams, device="cuda"), beams, 2 * beams + 1)
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+@pytest.mark.parametrize("vocab,rows", [(1, 4), (3, 4), (6, 4), (4099, 8), (70001, 8), (9001, 640)])
+def test_beam_select_unaligned_rows(offset, vocab, rows):
+    """Rows that start 0 to 12 bytes behind a 16-byte boundary, the best values and ties at both ends."""
+    B = binding()
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    big = torch.randn(rows * (vocab + 2) + 8, generator=g, device="cuda")
+    x = big[offset:offset + rows * (vocab + 2)].view(rows, vocab + 2)
+    x[:, 0], x[:, vocab - 1] = 9.0, 9.0
+    x[1::2, min(1, vocab - 1)] = 9.0
+    x[:, vocab:] = 1e30   # behind the row: not looked at
+    s = torch.zeros(rows, device="cuda")
+    n_out = min(5, 4 * vocab)
+    got = run_beam(B, x, s, 4, n_out, vocab=vocab, stride=vocab + 2)
+    want = P.beam_select(host(x)[:, :vocab], host(s), 4, n_out)
+    np.testing.assert_array_equal(got[1], want[1])
+    np.testing.assert_array_equal(got[2], want[2])
+
+
 def test_beam_select_strided_rows_and_repeated_calls():
     B = binding()
     x = torch.randn((8, 1003), device="cuda")
