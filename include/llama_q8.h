@@ -459,8 +459,8 @@ llama_q8_status llama_q8_attention_decode_noalloc(const float* q, const float* k
  *
  * Conventions, beside those of the device-level entry points above:
  *   - A row is one token. pos[row] is its position in its sequence (pos < 0: a
- *     padding row, for which nothing is read or written, except that attention
- *     writes the result of an empty mask), seq[row] the sequence; with seq ==
+ *     padding row, whose values are not used and for which nothing is written,
+ *     except that attention writes the result of an empty mask), seq[row] the sequence; with seq ==
  *     NULL row r belongs to sequence r (then rows <= n_seq, else LQ8_ERR_ARG).
  *   - table[n_seq][table_stride] holds the page of each block of `page`
  *     positions of a sequence: position p is slot p % page of page
@@ -549,7 +549,7 @@ typedef struct llama_q8_rope {
  * and sine taken in f32, so far positions keep f32 accuracy. n_head %
  * n_head_kv == 0. rows == 0 does nothing. Rows of one call name different
  * (sequence, position) pairs; of rows that name the same one, each written
- * value is one of theirs. A row whose sequence or position is out of range, or
+ * value is one of theirs. q_out does not overlap qkv. A row whose sequence or position is out of range, or
  * whose page is a hole or out of range, still gets its q_out (with the position
  * it names); its append is skipped and reported in err (may be NULL). qkv, q_out
  * 16-byte aligned. Enqueues one kernel. */

@@ -413,6 +413,8 @@ def _dev(a, dtype: str) -> int | None:
         raise TypeError(f"tensor must be {dtype}, got {kind}")
     if not a.is_contiguous():
         raise ValueError("tensor must be contiguous")
+    if not a.is_cuda:
+        raise ValueError("tensor must be on the GPU")
     return a.data_ptr()
 
 
@@ -424,6 +426,8 @@ def _dev_rows(a, dtype: str, stride: int) -> int | None:
         raise ValueError(f"tensor must be contiguous or have rows {stride} apart")
     if str(a.dtype) != dtype:
         raise TypeError(f"tensor must be {dtype}, got {a.dtype}")
+    if not a.is_cuda:
+        raise ValueError("tensor must be on the GPU")
     return a.data_ptr()
 
 
@@ -465,8 +469,8 @@ def make_rope(freq, style: int = 0, magnitude: float = 1.0) -> llama_q8_rope:
 def llama_q8_rope_append(pages: llama_q8_pages, layer: int, qkv, qkv_stride: int, rows: int, pos, seq, n_head: int,
                          rope: llama_q8_rope, table, n_seq: int, table_stride: int, q_out, err=None,
                          stream=0) -> None:
-    check(lib().llama_q8_rope_append(C.addressof(pages), layer, _dev_rows(qkv, _F32, qkv_stride), qkv_stride, rows, _dev(pos, _I32),
-                                     _dev(seq, _I32), n_head, C.addressof(rope), _dev(table, _I32), n_seq,
+    check(lib().llama_q8_rope_append(C.addressof(pages), layer, _dev_rows(qkv, _F32, qkv_stride), qkv_stride, rows,
+                                     _dev(pos, _I32), _dev(seq, _I32), n_head, C.addressof(rope), _dev(table, _I32), n_seq,
                                      table_stride, _dev(q_out, _F32), _dev(err, _I32), stream or None),
           "llama_q8_rope_append")
 
@@ -517,8 +521,8 @@ def llama_q8_beam_select_workspace_bytes(groups: int, beams: int, n_vocab: int, 
 
 def llama_q8_beam_select(logits, logits_stride: int, groups: int, beams: int, n_vocab: int, scores, n_out: int,
                          out_scores, out_parent, out_token, workspace, workspace_bytes: int, stream=0) -> None:
-    check(lib().llama_q8_beam_select(_dev_rows(logits, _F32, logits_stride), logits_stride, groups, beams, n_vocab, _dev(scores, _F32),
-                                     n_out, _dev(out_scores, _F32), _dev(out_parent, _I32), _dev(out_token, _I32),
+    check(lib().llama_q8_beam_select(_dev_rows(logits, _F32, logits_stride), logits_stride, groups, beams, n_vocab,
+                                     _dev(scores, _F32), n_out, _dev(out_scores, _F32), _dev(out_parent, _I32), _dev(out_token, _I32),
                                      _dev(workspace, _U8), workspace_bytes, stream or None), "llama_q8_beam_select")
 
 

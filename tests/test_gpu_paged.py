@@ -78,7 +78,8 @@ def test_rope_append(rows, heads, kv, dim, rot, style, page, kind, far, pad):
     q_out = torch.full((rows, heads, dim), 7.0, device="cuda")
     err = i32([0])
     rope = B.make_rope(torch.from_numpy(freq).cuda(), style, mag)
-    B.llama_q8_rope_append(B.make_pages(k, v), 1, qkv.data_ptr(), stride, rows, i32(pos), i32(seq), heads, rope,
+    rows_of = qkv[:, :(heads + 2 * kv) * dim]   # a view whose rows lie `stride` apart
+    B.llama_q8_rope_append(B.make_pages(k, v), 1, rows_of, stride, rows, i32(pos), i32(seq), heads, rope,
                            i32(table), n_seq, width, q_out, err)
     torch.cuda.synchronize()
     assert int(err[0]) == 0
@@ -827,6 +828,10 @@ def test_binding_refuses_other_types_and_layouts():
         call(args(q=q.half()))
     with pytest.raises(ValueError):
         call(args(q=q.transpose(1, 2).contiguous().transpose(1, 2)))
+    with pytest.raises(ValueError):
+        call(args(table=torch.zeros((1, table.shape[1]), dtype=torch.int32)))   # on the host
+    with pytest.raises(TypeError):
+        call(args(q=q.cpu().numpy()))
     with pytest.raises(TypeError):
         B.make_pages(k.double(), v.double())
     with pytest.raises(ValueError):
