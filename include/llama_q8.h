@@ -646,7 +646,7 @@ llama_q8_status llama_q8_pages_compact(const llama_q8_pages* pages, int32_t rows
  * or finished beam), or whose row has a NaN or +inf or nothing but -inf, has
  * totals -inf: it is chosen only where a group has fewer than n_out others.
  * groups, beams, n_vocab > 0, n_out in 1 .. beams * n_vocab (LQ8_ERR_ARG); beams
- * and n_out <= 64, groups * beams <= 65535, n_vocab <= 2^28 (LQ8_ERR_UNSUPPORTED). groups == 0
+ * and n_out <= 64, groups * beams <= 65535, n_vocab <= 2^24 (LQ8_ERR_UNSUPPORTED). groups == 0
  * does nothing. Enqueues one kernel. */
 size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out);
 llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride, int32_t groups, int32_t beams,

@@ -68,11 +68,11 @@ inline PageView<T> page_view(const llama_q8_pages* p, int layer) {
     return w;
 }
 
-// One arrival at a counter: the caller's CTA has written its part (and passed a
-// CTA barrier); the CTA that gets the last number sees every other's part.
-__device__ __forceinline__ unsigned take_ticket(unsigned int* counter) {
+// Arrival at a counter: the caller's CTA has written its part (and passed a CTA
+// barrier); the CTA that gets the last number sees every other's part.
+__device__ __forceinline__ unsigned take_ticket(unsigned int* counter, unsigned n = 1) {
     unsigned old;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(n) : "memory");
     return old;
 }
 

@@ -153,7 +153,7 @@ def _beam_call(B, **kw):
     (dict(beams=0), "ARG"), (dict(vocab=0), "ARG"), (dict(n_out=0), "ARG"), (dict(vocab=1, n_out=5), "ARG"),
     (dict(ws_bytes=10), "ARG"), (dict(ws=_off(W, 8)), "ARG"), (dict(logits=_off(A, 2)), "ARG"),
     (dict(beams=65), "UNSUPPORTED"), (dict(n_out=65), "UNSUPPORTED"), (dict(groups=20000), "UNSUPPORTED"),
-    (dict(vocab=(1 << 28) + 1, stride=1 << 30), "UNSUPPORTED"),
+    (dict(vocab=(1 << 24) + 1, stride=1 << 30), "UNSUPPORTED"),
     (dict(groups=0), "OK")])
 def test_beam_select_refuses(B, kw, status):
     assert _beam_call(B, **kw) == _status(B, status)
