@@ -19,8 +19,9 @@
 //
 // Bound: memory for large calls (each logit read once; about 6 issue slots per
 // value: load, maximum, subtract, scale, ex2, add, packed in pairs where there is
-// a packed form); for small ones the chain block -> counter -> sums -> blocks
-// again -> ranks. @@
+// a packed form) up to the end, where the last groups' choices, chains of a few
+// thousand cycles each (sums, blocks, values, ranks), pass alone: 8 of the 28 us
+// of 240 rows of 100003 (14 for the bytes), and most of a small call's 10.
 // Not kept: candidate lists with a rising bound during the one pass (34 to 46
 // us, most of it for the lists); a pass that looks up the values of the threads
 // whose maximum reaches a bound in every piece (53 us); a ring of 4-byte cp.async
@@ -36,8 +37,8 @@ namespace {
 constexpr int kBeamThreads = 256, kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamMax = 64;         // beams per group, results per group
 constexpr int kBeamVocab = 1 << 24;  // longest row: places of a group (64 rows of whole blocks) stay below 2^31
-constexpr int kBeamWave = 152 * 8;   // CTAs, twice as many as are resident at once
-constexpr int kPickItems = 4;        // blocks per thread and pass where there are many equal ones
+constexpr int kBeamWave = 152 * 4;   // CTAs resident at once
+constexpr int kPickItems = 4;        // blocks per thread that the final choice holds in registers
 
 struct BlockStat {
     float m, s;  // largest logit and sum of exp(logit - m); NaN s: a NaN or +inf among them
@@ -56,8 +57,8 @@ struct BeamArgs {
 };
 
 // A group's blocks of 512 values are dealt evenly to `ctas` CTAs of its own (a CTA
-// that chooses for its group keeps no other group waiting), together two waves of
-// them: the choices of the first wave's groups pass behind the second's loads.
+// that chooses for its group keeps no other group waiting), together one wave of
+// them (28 us for 240 rows of 100003; one and a half and two waves: 31 and 29).
 // Where blocks of 512 would leave warps idle, blocks of 256, one per warp: more
 // SMs take part, and less is read again.
 struct BeamCut {
@@ -301,12 +302,12 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
         float y[VPL];
 #pragma unroll
         for (int j = 0; j < VPL; ++j) y[j] = j * 32 < left ? x[j * 32] : 0.0f;
-        const float add = sm.add[b].hi;
+        // a total in one f32 addition is off by less than a millionth part of itself and of score - lse
+        const float add = sm.add[b].hi, sure = least_total - 1e-6f * (fabsf(least_total) + fabsf(add));
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            // in one f32 addition, off by less than a millionth part: clearly below
             const float t = y[j] + add;
-            if (j * 32 < left && !(t < least_total - 1e-6f * (fabsf(t) + fabsf(least_total)))) consider(y[j], b, block, j * 32 + lane);
+            if (j * 32 < left && !(t < sure - 1e-6f * fabsf(t))) consider(y[j], b, block, j * 32 + lane);
         }
     }
     __syncthreads();
@@ -372,10 +373,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_select_kernel(BeamArgs a
 #pragma unroll
             for (int j = 0; j < VPL; j += QUAD ? 4 : 1) {
                 if (QUAD) {
-                    const float4 y = __ldg(reinterpret_cast<const float4*>(x) + j * 8 + lane);
+                    const float4 y = __ldcs(reinterpret_cast<const float4*>(x) + j * 8 + lane);
                     v[j] = y.x; v[j + 1] = y.y; v[j + 2] = y.z; v[j + 3] = y.w;
                 } else {
-                    v[j] = __ldg(x + j * 32 + lane);
+                    v[j] = __ldcs(x + j * 32 + lane);
                 }
             }
         } else {

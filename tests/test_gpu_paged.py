@@ -595,6 +595,22 @@ def test_beam_select_equal_rows_tie(groups, beams, vocab):
     check_beam(B, x.reshape(groups * beams, vocab).contiguous(), torch.zeros(groups * beams, device="cuda"), beams, 2 * beams + 1)
 
 
+@pytest.mark.parametrize("shift", [1e3, -1e4, 3e4, 1e6])
+def test_beam_select_logits_far_from_zero(shift):
+    """Log sums far larger than the totals: what the f32 number nearest to score - lse leaves out decides."""
+    B = binding()
+    g = torch.Generator(device="cuda").manual_seed(int(abs(shift)))
+    for vocab, rows in ((3001, 8), (40009, 240)):
+        x = (4.0 * torch.randn((rows, vocab), generator=g, device="cuda")).round() + shift   # many equal logits
+        s = -3.0 * torch.rand(rows, generator=g, device="cuda")
+        got = run_beam(B, x, s, 4, 12)
+        want = P.beam_select(host(x), host(s), 4, 12)
+        np.testing.assert_array_equal(got[1], want[1])
+        np.testing.assert_array_equal(got[2], want[2])
+        # lse is off by 2^-20 of its own scale at most; one rounding
+        assert (np.abs(got[0] - want[0]) <= 2.0 ** -20 + U * np.abs(want[0])).all()
+
+
 @pytest.mark.parametrize("offset", [0, 1, 2, 3])
 @pytest.mark.parametrize("vocab,rows", [(1, 4), (3, 4), (6, 4), (4099, 8), (70001, 8), (9001, 640)])
 def test_beam_select_unaligned_rows(offset, vocab, rows):
