@@ -460,8 +460,9 @@ llama_q8_status llama_q8_attention_decode_noalloc(const float* q, const float* k
  * Conventions, beside those of the device-level entry points above:
  *   - A row is one token. pos[row] is its position in its sequence (pos < 0: a
  *     padding row, whose values are not used and for which nothing is written,
- *     except that attention writes the result of an empty mask), seq[row] the sequence; with seq ==
- *     NULL row r belongs to sequence r (then rows <= n_seq, else LQ8_ERR_ARG).
+ *     except that attention writes the result of an empty mask), seq[row] the
+ *     sequence; with seq == NULL row r belongs to sequence r (then rows <= n_seq,
+ *     else LQ8_ERR_ARG).
  *   - table[n_seq][table_stride] holds the page of each block of `page`
  *     positions of a sequence: position p is slot p % page of page
  *     table[seq][p / page]; entries < 0 are holes.
@@ -549,10 +550,10 @@ typedef struct llama_q8_rope {
  * and sine taken in f32, so far positions keep f32 accuracy. n_head %
  * n_head_kv == 0. rows == 0 does nothing. Rows of one call name different
  * (sequence, position) pairs; of rows that name the same one, each written
- * value is one of theirs. q_out does not overlap qkv. A row whose sequence or position is out of range, or
- * whose page is a hole or out of range, still gets its q_out (with the position
- * it names); its append is skipped and reported in err (may be NULL). qkv, q_out
- * 16-byte aligned. Enqueues one kernel. */
+ * value is one of theirs. q_out does not overlap qkv. A row whose sequence or
+ * position is out of range, or whose page is a hole or out of range, still gets
+ * its q_out (with the position it names); its append is skipped and reported in
+ * err (may be NULL). qkv, q_out 16-byte aligned. Enqueues one kernel. */
 llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer, const float* qkv,
                                      int64_t qkv_stride, int32_t rows, const int32_t* pos, const int32_t* seq,
                                      int32_t n_head, const llama_q8_rope* rope, const int32_t* table,
@@ -572,14 +573,16 @@ llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer,
  * does not matter; visible keys and values must be finite. Rows may share a
  * sequence (several new tokens of one sequence, each with its own pos).
  * Products with F16 / BF16 pages run on the tensor cores on q and the
- * probabilities split into parts that keep 22 bits or more, summed in f32; F32 pages are multiplied in f32. The visible
- * positions of all rows are dealt evenly to the GPU's blocks, whatever their
- * lengths; parts of one row meet through the workspace, always added in the
- * order of the positions, so equal calls give equal bits.
+ * probabilities split into parts that keep 22 bits or more, summed in f32; F32
+ * pages are multiplied in f32. The visible positions of all rows are dealt evenly
+ * to the GPU's SMs, whatever their lengths; parts of one row meet through the
+ * workspace, always added in the order of the positions, so equal calls give
+ * equal bits.
  * n_head / n_head_kv <= 8, rows * n_head_kv < 2^24, and rows * n_head_kv *
  * (the positions a table row holds, / 32 + 2) < 2^31 - 4096, which a chunk of
- * rows at a time meets (LQ8_ERR_UNSUPPORTED); window >= 0, scale finite and >= 0 (LQ8_ERR_ARG);
- * rows == 0 does nothing. q, out 16-byte aligned. Enqueues one kernel. */
+ * rows at a time meets (LQ8_ERR_UNSUPPORTED); window >= 0, scale finite and >= 0
+ * (LQ8_ERR_ARG); rows == 0 does nothing. q, out 16-byte aligned. Enqueues one
+ * kernel. */
 size_t llama_q8_attention_paged_workspace_bytes(int32_t rows, int32_t n_head, int32_t n_head_kv, int32_t head_dim);
 llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t layer, const float* q, int32_t rows,
                                          const int32_t* pos, const int32_t* seq, int32_t n_head, float scale,
@@ -641,13 +644,15 @@ llama_q8_status llama_q8_pages_compact(const llama_q8_pages* pages, int32_t rows
  * out_scores[groups][n_out], out_parent (the row, group * beams + beam: the
  * parent array of llama_q8_pages_fork when n_out == beams) and out_token.
  * With n_out == beams, out_scores may be scores; no other array may overlap.
- * Totals are formed in two f32 parts (48 bits) and rounded to f32 at the end. A logit of -inf
- * forbids its token (total -inf). A beam whose score is not finite (a padding
+ * Totals are formed in two f32 parts (48 bits) and rounded to f32 at the end; rows
+ * of equal logits get equal log sums. A logit of -inf forbids its token (total
+ * -inf). A beam whose score is not finite (a padding
  * or finished beam), or whose row has a NaN or +inf or nothing but -inf, has
  * totals -inf: it is chosen only where a group has fewer than n_out others.
  * groups, beams, n_vocab > 0, n_out in 1 .. beams * n_vocab (LQ8_ERR_ARG); beams
- * and n_out <= 64, groups * beams <= 65535, n_vocab <= 2^24 (LQ8_ERR_UNSUPPORTED). groups == 0
- * does nothing. Enqueues one kernel. */
+ * and n_out <= 64, groups * beams <= 65535, n_vocab <= 2^24, groups * beams *
+ * (n_vocab / 512 + 1) < 2^30 (LQ8_ERR_UNSUPPORTED). groups == 0 does nothing.
+ * Enqueues one kernel. */
 size_t llama_q8_beam_select_workspace_bytes(int32_t groups, int32_t beams, int32_t n_vocab, int32_t n_out);
 llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride, int32_t groups, int32_t beams,
                                      int32_t n_vocab, const float* scores, int32_t n_out, float* out_scores,
