@@ -1,5 +1,5 @@
 // The paged KV cache as the kernels see it: one layer of a pool, element types
-// and the checks shared by the entry points of paged.cu and pages.cu.
+// and the checks shared by the entry points.
 #pragma once
 
 #include <cmath>
