@@ -294,12 +294,13 @@ __device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, u
 #pragma unroll
             for (int j = 0; j < 4; ++j) s.o[d][j] *= f;
     }
-    // f16: probabilities times 2^15, so that the second part of a small one is not lost below f16's range
-    const float ref = St::kHalf ? m - 15.0f : m;
     uint32_t a[NT / 2][4], a3[NT / 2][4] = {};
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
-        x[j] = ex2(x[j] - ref);
+        x[j] = ex2(x[j] - m);
+        // f16: times 2^15, so that the second part of a small one is not lost below f16's range. Not as m - 15 in the
+        // exponent: far from zero that rounds, up to where the largest probability leaves f16's range.
+        if (St::kHalf) x[j] *= 32768.0f;
         s.l += x[j];
     }
 #pragma unroll
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             reinterpret_cast<float4*>(a.out + orow * HD)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             if (a.lse && e % (HD / 4) == 0)
-                a.lse[orow + g] = l > 0.0f ? (m - (kHalf ? 15.0f : 0.0f)) * 0.69314718055994531f + logf(l) : -INFINITY;
+                a.lse[orow + g] = l > 0.0f ? m * 0.69314718055994531f + logf(kHalf ? l * 0x1p-15f : l) : -INFINITY;
         };
         for (int e = tid; e < G * (HD / 4); e += kThreads) {
             const int g = e / (HD / 4);

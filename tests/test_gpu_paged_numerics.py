@@ -1,0 +1,68 @@
+"""Paged attention and beam selection where their arithmetic can go wrong:
+scores far from zero, long sums, parts that are joined, parts of split numbers.
+What is checked has a closed form, so that the bounds are a few roundings."""
+import numpy as np
+import pytest
+
+from tests.gpu_helpers import binding, require_gpu, torch
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24  # half a step of f32, relative
+LOG2E = 1.4426950408889634
+KINDS = ["f32", "f16", "bf16"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _dt(kind):
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[kind]
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def attend(B, k, v, q, pos, table, window=0, seq=None, scale=0.0):
+    """(out, lse) of rows over the pages k, v [pages][kv][page][dim]."""
+    rows, heads, dim = q.shape
+    n = B.llama_q8_attention_paged_workspace_bytes(rows, heads, k.shape[1], dim)
+    out, lse, err = torch.empty_like(q), torch.empty((rows, heads), device="cuda"), i32([0])
+    B.llama_q8_attention_paged(B.make_pages(k[None], v[None]), 0, q, rows, i32(pos), None if seq is None else i32(seq),
+                               heads, scale, window, i32(table), len(table), len(table[0]), out, lse,
+                               torch.zeros(n, dtype=torch.uint8, device="cuda"), n, err)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("m", [2.0 ** 20, 2.0 ** 24 + 64, 2.0 ** 25 + 64, 2.0 ** 27 + 64, 2.0 ** 29, 2.0 ** 100])
+def test_attention_paged_scores_far_from_zero(kind, sign, m):
+    """One key far above all others, its score (in units of log2) anywhere: its value is the answer."""
+    B = binding()
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for n, heads, kv, dim, page in [(8, 1, 1, 64, 8), (700, 6, 2, 128, 16), (9000, 8, 1, 64, 64)]:
+        blocks, best = -(-n // page), n * 2 // 3
+        k = torch.zeros((blocks, kv, page, dim), device="cuda", dtype=_dt(kind))
+        v = torch.randn(k.shape, generator=g, device="cuda").to(_dt(kind))
+        k[..., 0] = 1.0 if sign > 0 else -2.0
+        k[best // page, :, best % page, 0] = 2.0 if sign > 0 else -1.0
+        q = torch.zeros((1, heads, dim), device="cuda")
+        q[0, :, 0] = m / 2 / LOG2E if sign > 0 else m / LOG2E
+        out, lse = attend(B, k, v, q, [n - 1], [list(range(blocks))], scale=1.0)
+        # the others' probabilities are 2^-(2^19) at most: 0; the one is 1, and no sum rounds
+        want = v[best // page, :, best % page].float().repeat_interleave(heads // kv, 0)
+        assert torch.equal(out[0], want), (n, heads)
+        # lse: log2 e, q times it, ln 2 and the product with it round; f16: the second part of q ends 2^-23 below q,
+        # and the two parts' sum rounds
+        score = f64(q)[..., 0] * (2.0 if sign > 0 else -1.0)
+        assert (np.abs(f64(lse) - score) <= (7 if kind == "f16" else 4) * U * np.abs(score)).all(), (n, heads)
