@@ -31,16 +31,21 @@
 //  - bf16: q and the probabilities in three parts, 24 bits. Groups of up to 4
 //    heads have the three parts in rows 0-3, 4-7 and 8-11 of one product; larger
 //    ones the third in a second product.
+// Long sums are kept in two levels: o and l of up to kFold tiles, added to o_all
+// and l_all. In one chain a warp's share of 131071 positions was off by up to
+// 1.2e-4 (f32, equal probabilities, whose roundings all go one way), and by 3.5e-5
+// on average in the tensor cores, which cut digits off; in two levels 1.4e-6 and
+// less (64 rows 150 -> 151 us, one row of 131071 90.3 -> 91).
 // f32 pages: f32 products. Scores: a few lanes per key over the dimensions,
 // q from shared memory; output: a few dimensions per lane.
 //
 // Measured (bytes of the visible rows per time, of 6.7 TB/s that a copy reaches):
-// 64 rows up to 8191 positions, f16, 32/8 heads of 128: 150 us, 6.5 TB/s; one
-// row of 131071, bf16: 90 us, 6.0; 48 rows up to 4096, f32, 9/3 heads of 64: 31
-// us, 4.4. Where the bytes are few, the fixed chain is what takes the time:
+// 64 rows up to 8191 positions, f16, 32/8 heads of 128: 151 us, 6.4 TB/s; one
+// row of 131071, bf16: 91 us, 5.9; 48 rows up to 4096, f32, 9/3 heads of 64: 32
+// us, 4.3. Where the bytes are few, the fixed chain is what takes the time:
 // positions (1.3 us), page numbers, first tiles, join, ticket and parts, about 7
 // us in all. f32 groups of 5-8 heads are bound by their arithmetic instead (2900
-// cycles per tile and warp: 16/2 heads of 128, 32 rows: 44 us, 21 for the bytes).
+// cycles per tile and warp: 16/2 heads of 128, 32 rows: 45 us, 20 for the bytes).
 #include <algorithm>
 #include <type_traits>
 
@@ -93,6 +98,7 @@ struct Shape {
     static constexpr int kRowBytes = HD * (int)sizeof(T);
     static constexpr int kUnit = kWarps * kTile;                   // positions
     static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kFold = sizeof(T) == 4 ? 16 : 32;         // tiles per partial sum
 };
 constexpr int kTileBytes = 4096;                                   // of K or of V
 constexpr int kStages = kRingBytes / (2 * kTileBytes);
@@ -106,6 +112,16 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -181,8 +197,8 @@ struct State16 {
     static constexpr bool kTwo = !kHalf && GP == 8;  // the third part in a second product
     uint32_t q[HD / 16][4];
     uint32_t q3[kTwo ? HD / 16 : 1][2];
-    float o[HD / 8][4];
-    float m, l, q_inv;
+    uint64_t o[HD / 8], o_all[HD / 8];  // pairs of dimensions
+    float m, l, l_all, q_inv;
 };
 // (x, y) as the two words of an A operand for a row's parts: rows lane / 4 and lane / 4 + 8, and the third part apart.
 template <typename St, typename T>
@@ -198,8 +214,8 @@ __device__ __forceinline__ void split_parts(float x, float y, uint32_t& top, uin
 }
 template <int HD>
 struct State32 {
-    uint64_t o[kMaxG][HD / 64];  // pairs of dimensions
-    float m[kMaxG], l[kMaxG];  // m the same in every lane, l a part per lane
+    uint64_t o[kMaxG][HD / 64], o_all[kMaxG][HD / 64];  // pairs of dimensions
+    float m[kMaxG], l[kMaxG], l_all[kMaxG];  // m the same in every lane, l a part per lane
 };
 
 // q [G][HD] in shared memory
@@ -238,11 +254,9 @@ __device__ __forceinline__ void state_init(State16<T, HD, GP>& s, const float* q
         split_parts<St>(v[k][2] * up, v[k][3] * up, s.q[k][2], s.q[k][3], third[1], lane, tag);
     }
 #pragma unroll
-    for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s.o[d][j] = 0.0f;
+    for (int d = 0; d < HD / 8; ++d) s.o[d] = s.o_all[d] = 0;
     s.m = -INFINITY;
-    s.l = 0.0f;
+    s.l = s.l_all = 0.0f;
 }
 
 // A tile of 2048 / HD keys: K at ks, V at vs (shared addresses); key j of the tile counts if bit j of see is set.
@@ -289,10 +303,13 @@ __device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, u
         const float f = ex2(s.m - m);
         s.m = m;
         s.l *= f;
+        s.l_all *= f;
+        const uint64_t f2 = pack_f2(f, f);
 #pragma unroll
-        for (int d = 0; d < HD / 8; ++d)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s.o[d][j] *= f;
+        for (int d = 0; d < HD / 8; ++d) {
+            s.o[d] = mul_f2(s.o[d], f2);
+            s.o_all[d] = mul_f2(s.o_all[d], f2);
+        }
     }
     uint32_t a[NT / 2][4], a3[NT / 2][4] = {};
 #pragma unroll
@@ -301,7 +318,6 @@ __device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, u
         // f16: times 2^15, so that the second part of a small one is not lost below f16's range. Not as m - 15 in the
         // exponent: far from zero that rounds, up to where the largest probability leaves f16's range.
         if (St::kHalf) x[j] *= 32768.0f;
-        s.l += x[j];
     }
 #pragma unroll
     for (int h = 0; h < NT / 2; ++h) {
@@ -309,18 +325,39 @@ __device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, u
         split_parts<St>(x[4 * h + 2], x[4 * h + 3], a[h][2], a[h][3], a3[h][2], lane, tag);
     }
 #pragma unroll
-    for (int d = 0; d < HD / 16; ++d)
+    for (int w = NT; w > 0; w >>= 1)
+#pragma unroll
+        for (int j = 0; j < w; ++j) x[j] += x[j + w];
+    s.l += x[0];
+    // the tile's products in sums of their own, added to the running ones with rounding
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) {
+        float c[2][4] = {};
 #pragma unroll
         for (int h = 0; h < NT / 2; ++h) {
             uint32_t b[4];
             ldsm4_t(b, vs + (h * 16 + (mi & 1) * 8 + l8) * RB + (((2 * d + (mi >> 1)) ^ l8) << 4));
-            mma16(s.o[2 * d], a[h], b[0], b[1], tag);
-            mma16(s.o[2 * d + 1], a[h], b[2], b[3], tag);
+            mma16(c[0], a[h], b[0], b[1], tag);
+            mma16(c[1], a[h], b[2], b[3], tag);
             if constexpr (St::kTwo) {
-                mma16(s.o[2 * d], a3[h], b[0], b[1], tag);
-                mma16(s.o[2 * d + 1], a3[h], b[2], b[3], tag);
+                mma16(c[0], a3[h], b[0], b[1], tag);
+                mma16(c[1], a3[h], b[2], b[3], tag);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            s.o[2 * d + i] = add_f2(s.o[2 * d + i], add_f2(pack_f2(c[i][0], c[i][1]), pack_f2(c[i][2], c[i][3])));
+    }
+}
+template <typename T, int HD, int GP>
+__device__ __forceinline__ void state_fold(State16<T, HD, GP>& s) {
+#pragma unroll
+    for (int d = 0; d < HD / 8; ++d) {
+        s.o_all[d] = add_f2(s.o_all[d], s.o[d]);
+        s.o[d] = 0;
+    }
+    s.l_all += s.l;
+    s.l = 0.0f;
 }
 
 // The warp's part: output [8][HD] to ob, m and l of its heads to ml (l of f16 pages carries the factor 2^15).
@@ -328,13 +365,14 @@ template <typename T, int HD, int GP>
 __device__ __forceinline__ void state_store(State16<T, HD, GP>& s, float* ob, float2* ml, int lane) {
     constexpr bool kOne = State16<T, HD, GP>::kOne;
     const int g = lane >> 2, t = lane & 3;
-    float l = s.l;
+    float l = s.l_all + s.l;
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (t == 0) ml[g] = make_float2(s.m, l);
 #pragma unroll
     for (int d = 0; d < HD / 8; ++d) {
-        float x = s.o[d][0] + s.o[d][2], y = s.o[d][1] + s.o[d][3];
+        const uint64_t o = add_f2(s.o_all[d], s.o[d]);
+        float x = f2_lo(o), y = f2_hi(o);
         if (kOne) {
             x += __shfl_xor_sync(0xffffffffu, x, 16);
             y += __shfl_xor_sync(0xffffffffu, y, 16);
@@ -348,9 +386,9 @@ __device__ __forceinline__ void state_init(State32<HD>& s) {
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
 #pragma unroll
-        for (int d = 0; d < HD / 64; ++d) s.o[g][d] = 0;
+        for (int d = 0; d < HD / 64; ++d) s.o[g][d] = s.o_all[g][d] = 0;
         s.m[g] = -INFINITY;
-        s.l[g] = 0.0f;
+        s.l[g] = s.l_all[g] = 0.0f;
     }
 }
 
@@ -394,8 +432,13 @@ __device__ __forceinline__ void state_tile(State32<HD>& s, const uint8_t* ks, co
             const float f = ex2(s.m[g] - m[g]);
             s.m[g] = m[g];
             s.l[g] *= f;
+            s.l_all[g] *= f;
+            const uint64_t f2 = pack_f2(f, f);
 #pragma unroll
-            for (int d = 0; d < HD / 64; ++d) s.o[g][d] = pack_f2(f2_lo(s.o[g][d]) * f, f2_hi(s.o[g][d]) * f);
+            for (int d = 0; d < HD / 64; ++d) {
+                s.o[g][d] = mul_f2(s.o[g][d], f2);
+                s.o_all[g][d] = mul_f2(s.o_all[g][d], f2);
+            }
         }
     }
     __syncwarp();  // the last tile's probabilities have been read
@@ -430,14 +473,28 @@ __device__ __forceinline__ void state_tile(State32<HD>& s, const uint8_t* ks, co
 }
 
 template <int HD, int GP>
+__device__ __forceinline__ void state_fold(State32<HD>& s) {
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+#pragma unroll
+        for (int d = 0; d < HD / 64; ++d) {
+            s.o_all[g][d] = add_f2(s.o_all[g][d], s.o[g][d]);
+            s.o[g][d] = 0;
+        }
+        s.l_all[g] += s.l[g];
+        s.l[g] = 0.0f;
+    }
+}
+
+template <int HD, int GP>
 __device__ __forceinline__ void state_store(State32<HD>& s, float* ob, float2* ml, int lane) {
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
-        const float l = warp_sum(s.l[g]);
+        const float l = warp_sum(s.l_all[g] + s.l[g]);
         if (lane == 0) ml[g] = make_float2(s.m[g], l);
 #pragma unroll
         for (int d = 0; d < HD / 64; ++d)
-            *reinterpret_cast<uint64_t*>(ob + g * HD + lane * (HD / 32) + 2 * d) = s.o[g][d];
+            *reinterpret_cast<uint64_t*>(ob + g * HD + lane * (HD / 32) + 2 * d) = add_f2(s.o_all[g][d], s.o[g][d]);
     }
 }
 
@@ -637,6 +694,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
                     state_tile<HD, GP>(state, t, t + kTileBytes, qs, pb, a.scale_log2, bits, lane);
                 else
                     state_tile(state, smem_u32(t), smem_u32(t + kTileBytes), bits, lane);
+            }
+            if (j % S::kFold == S::kFold - 1) {
+                if constexpr (kF32)
+                    state_fold<HD, GP>(state);
+                else
+                    state_fold(state);
             }
             st = st == kStages - 1 ? 0 : st + 1;
         }

@@ -66,3 +66,47 @@ def test_attention_paged_scores_far_from_zero(kind, sign, m):
         # and the two parts' sum rounds
         score = f64(q)[..., 0] * (2.0 if sign > 0 else -1.0)
         assert (np.abs(f64(lse) - score) <= (7 if kind == "f16" else 4) * U * np.abs(score)).all(), (n, heads)
+
+
+def chain_bounds(kind, dim, n):
+    """Relative bounds, in half steps of f32, of the sum of a row's weighted values and of the sum of its weights, for
+    n positions that one CTA's four warps take: tiles of 4 KB of keys, 16 (f32) or 32 tiles per partial sum. The i-th of
+    N additions of terms of about one size errs by at most half a step of i / N of the sum: N / 2 half steps in all."""
+    size = 4 if kind == "f32" else 2
+    tile = 4096 // (dim * size)
+    fold = 16 if kind == "f32" else 32
+    tiles = -(-n // (4 * tile))
+    weights = (fold + tiles / fold) / 2
+    # f32: a multiply-add per position. 16-bit: four products per tile at most in the tensor cores, which cut what lies
+    # below a step of the sum (2 half steps each), and the probabilities to 22 bits (4 half steps)
+    values = (fold * tile + tiles / fold) / 2 if kind == "f32" else weights + 4 * 2 + 4
+    # a tile's own tree or the parts' sum, the joins of lanes and warps, the factors as the maximum grows
+    return values + 32, weights + 32
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,dim", [(2, 64), (2, 128), (10, 64), (16, 128)])
+def test_attention_paged_long_sums(kind, heads, dim):
+    """Rows enough that a CTA has whole rows, 131071 positions each, and values that are all 1: the answer is 1. With
+    random keys, and with equal keys but one, where every addition to a sum rounds the same way."""
+    B = binding()
+    n, kv, rows, page = 131071, 2, 256, 64
+    blocks = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(heads + dim)
+    k = torch.randn((blocks, kv, page, dim), generator=g, device="cuda").to(_dt(kind))
+    v = torch.ones_like(k)
+    q = 0.5 * torch.randn((rows, heads, dim), generator=g, device="cuda")
+    values, weights = chain_bounds(kind, dim, n)
+    table, pos, seq = [list(range(blocks))], [n - 1] * rows, [0] * rows
+    out, _ = attend(B, k, v, q, pos, table, seq=seq)
+    err = f64(out) - 1.0
+    assert np.abs(err).max() <= (values + weights) * U
+    k.zero_()
+    k[0, :, 0] = 1.0
+    q = 0.02 * torch.rand((rows, heads, dim), generator=g, device="cuda")
+    out, lse = attend(B, k, v, q, pos, table, seq=seq)
+    assert np.abs(f64(out) - 1.0).max() <= (values + weights) * U
+    s = f64(q).sum(-1) * dim ** -0.5
+    # and the score's products and sums, and the logarithm of about 11.8 (a step and its own rounding)
+    tol = (weights + (dim + 8) * s + 4 * 12) * U
+    assert (np.abs(f64(lse) - np.log(np.exp(s) + n - 1)) <= tol).all()
