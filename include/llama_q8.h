@@ -644,8 +644,11 @@ llama_q8_status llama_q8_pages_compact(const llama_q8_pages* pages, int32_t rows
  * out_scores[groups][n_out], out_parent (the row, group * beams + beam: the
  * parent array of llama_q8_pages_fork when n_out == beams) and out_token.
  * With n_out == beams, out_scores may be scores; no other array may overlap.
- * Totals are formed in two f32 parts (48 bits) and rounded to f32 at the end; rows
- * of equal logits get equal log sums. A logit of -inf forbids its token (total
+ * score + logit - log sum is added in two f32 parts (48 bits) and rounded to f32 at
+ * the end. The log sum itself comes from exponentials and block sums in f32 and is
+ * off by 2^-19 at most, by a few 2^-24 as a rule: continuations of different beams
+ * whose totals lie closer than that may change places, those of one beam do not.
+ * Rows of equal logits get equal log sums. A logit of -inf forbids its token (total
  * -inf). A beam whose score is not finite (a padding
  * or finished beam), or whose row has a NaN or +inf or nothing but -inf, has
  * totals -inf: it is chosen only where a group has fewer than n_out others.

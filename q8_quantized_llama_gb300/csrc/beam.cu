@@ -93,8 +93,10 @@ __device__ __forceinline__ bool above(const Pick& a, const Pick& b) {
     // no short circuits: as branches they made the counting loops wait 100 cycles and more per entry
     return (a.key > b.key) | ((a.key == b.key) & (a.place < b.place));
 }
-// Totals and log sums are unevaluated sums hi + lo of two f32 numbers (about 48
-// bits): double arithmetic runs at a small fraction of f32's rate here.
+// Totals are unevaluated sums hi + lo of two f32 numbers (about 48 bits): double
+// arithmetic runs at a small fraction of f32's rate here. So are the sums of a
+// row's blocks; the exponentials and a block's sum of them are f32, and the log
+// sum is as good as those (2^-19 at most, a few 2^-24 as a rule).
 struct Sum2 {
     float hi, lo;
 };
@@ -168,10 +170,14 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
     for (int b = warp; b < a.beams; b += kBeamWarps) {
         const BlockStat* st = stat + (int64_t)b * a.blocks;
         const float sc = a.scores[row0 + b];
-        float top = -INFINITY, part = 0.0f;  // the lane's blocks, eight at a time
+        // The lane's blocks, eight at a time: eight in f32, those of a lane in two parts (in one f32 sum the 1024 blocks
+        // per lane of a row of 2^24 were off by 1e-5). The exponentials' reference follows the maximum only in steps of
+        // 8 or more, as every change of it rounds.
+        float top = -INFINITY;
+        Sum2 sum{0.0f, 0.0f};
         for (int c0 = lane; c0 < a.blocks; c0 += 256) {
             float2 x[8];
-            float m1 = top;
+            float m1 = -INFINITY, y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[j] = c0 + j * 32 < a.blocks ? __ldcg(reinterpret_cast<const float2*>(st + c0 + j * 32))
@@ -179,15 +185,20 @@ __device__ __noinline__ void choose(const BeamArgs& a, ChooseShared& sm, int gro
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) m1 = fmaxf(m1, x[j].x);
-            const float ref = m1 > -INFINITY ? m1 : 0.0f;
-            part *= ex2((top - ref) * 1.4426950408889634f);
+            if (m1 > top + 8.0f) {
+                const float f = top > -INFINITY ? expf(top - m1) : 1.0f;
+                sum = Sum2{sum.hi * f, sum.lo * f};
+                top = m1;
+            }
+            const float ref = top > -INFINITY ? top : 0.0f;
             // a block of -inf alone adds 0, one with NaN NaN
 #pragma unroll
-            for (int j = 0; j < 8; ++j) part += x[j].y * (x[j].x > -INFINITY ? expf(x[j].x - ref) : 1.0f);
-            top = m1;
+            for (int j = 0; j < 8; ++j) y[j] = x[j].y * (x[j].x > -INFINITY ? expf(x[j].x - ref) : 1.0f);
+            sum = add2(sum, ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7])));
         }
         const float all_top = warp_max(top);
-        Sum2 sum{top > -INFINITY ? part * expf(top - all_top) : part, 0.0f};
+        const float f1 = top > -INFINITY ? expf(top - all_top) : 1.0f;
+        sum = Sum2{sum.hi * f1, sum.lo * f1};
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const float y = __shfl_xor_sync(0xffffffffu, sum.hi, o), z = __shfl_xor_sync(0xffffffffu, sum.lo, o);

@@ -110,3 +110,24 @@ def test_attention_paged_long_sums(kind, heads, dim):
     # and the score's products and sums, and the logarithm of about 11.8 (a step and its own rounding)
     tol = (weights + (dim + 8) * s + 4 * 12) * U
     assert (np.abs(f64(lse) - np.log(np.exp(s) + n - 1)) <= tol).all()
+
+
+@pytest.mark.parametrize("vocab", [100003, 1 << 20, (1 << 22) + 5, 1 << 24])
+def test_beam_select_long_vocabulary_sums(vocab):
+    """Log sums of up to 2^24 logits: rows of two values, whose block sums are all equal, and rising rows, whose maximum
+    grows with every block."""
+    B = binding()
+    i = torch.arange(vocab, device="cuda", dtype=torch.float64)
+    rows = [torch.where(i % 2 == 0, -a, 0.0 * i) for a in (0.3, 0.7, 1.1, 1.9, 2.3, 3.1)] + [i * (8.0 / vocab), i * (1.0 / vocab)]
+    x = torch.stack([r.float() for r in rows])
+    n, g = B.llama_q8_beam_select_workspace_bytes(len(rows), 1, vocab, 1), len(rows)
+    s, p, t = torch.empty(g, device="cuda"), i32([0] * g), i32([0] * g)
+    B.llama_q8_beam_select(x, vocab, g, 1, vocab, torch.zeros(g, device="cuda"), 1, s, p, t,
+                           torch.zeros(n, dtype=torch.uint8, device="cuda"), n)
+    y = x.double()
+    top = y.max(1).values
+    want = f64(-torch.log(torch.exp(y - top[:, None]).sum(1)))  # top - lse
+    # In half steps of f32: a block's sum 10 (eight additions of growing sums: 4; the lanes' six), ex2 4 and its argument
+    # of 1.9 on average, times ln 2, 3; a block's factor 2 and product 1, the sums of eight 3, the row's none; a change of
+    # the reference, for a lane's blocks and for the row, 3 each; the logarithm 2. And the rounding of the total.
+    np.testing.assert_allclose(f64(s), want, rtol=U, atol=31 * U)
