@@ -131,3 +131,111 @@ def test_beam_select_long_vocabulary_sums(vocab):
     # of 1.9 on average, times ln 2, 3; a block's factor 2 and product 1, the sums of eight 3, the row's none; a change of
     # the reference, for a lane's blocks and for the row, 3 each; the logarithm 2. And the rounding of the total.
     np.testing.assert_allclose(f64(s), want, rtol=U, atol=31 * U)
+
+
+# lens, heads, kv, dim, page, window, share of holes among the pages, rows of one sequence
+JOINED = [([131071], 7, 1, 128, 16, 0, 0.0, False), ([131071], 8, 1, 64, 64, 0, 0.1, False),
+          ([70000, 1, 40000], 3, 1, 64, 8, 0, 0.0, False), ([50000, 50000], 9, 3, 64, 32, 20001, 0.0, False),
+          ([30000, 0, 63, 64, 65, 29999], 32, 8, 128, 256, 0, 0.2, False), ([9000] * 5, 4, 2, 64, 16, 0, 0.0, True),
+          ([0, 1, 7, 8, 9, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257], 6, 3, 128, 8, 0, 0.0, False),
+          ([int(300 ** (i / 400)) for i in range(400)], 8, 8, 64, 16, 0, 0.1, False),
+          ([1 + 37 * i % 2500 for i in range(101)], 10, 2, 64, 16, 333, 0.0, True)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,heads,kv,dim,page,window,holes,shared", JOINED)
+@pytest.mark.parametrize("steps", [0, 3])
+def test_attention_paged_counts_every_position_once(kind, lens, heads, kv, dim, page, window, holes, shared, steps):
+    """Values that are 1 in one dimension, drawn per position: the answer counts the positions of each dimension, so one
+    that is lost or counted twice shows, wherever it lies among units, pages, warps, CTAs and joined parts. All scores
+    0, or (steps) scores that fall and rise by powers of two along the sequence and differ between the heads."""
+    B = binding()
+    rng = np.random.default_rng(len(lens) * 7 + dim + heads + steps)
+    n_seq = 1 if shared else len(lens)
+    longest = [max(lens)] if shared else lens
+    blocks = [-(-n // page) for n in longest]
+    table, at, ids = np.full((n_seq, max(blocks) + 1), -1), 0, rng.permutation(sum(blocks) + 2)
+    for r, b in enumerate(blocks):
+        table[r, :b] = ids[at:at + b]
+        at += b
+    where = rng.integers(0, dim, (len(ids), kv, page))      # of a slot: its value's dimension,
+    level = rng.integers(0, 3, (len(ids), kv, page))        # its score in units of log2, with the steps below
+    for r in range(n_seq):
+        for b in range(blocks[r]):
+            level[table[r, b]] += 3 * (abs(b * 8 // blocks[r] - 3) % 4)
+    v = torch.zeros((len(ids), kv, page, dim), device="cuda", dtype=_dt(kind))
+    v.scatter_(3, torch.as_tensor(where, device="cuda")[..., None], 1.0)
+    k = torch.zeros_like(v)
+    k[..., 5] = torch.as_tensor(level, device="cuda").to(_dt(kind))
+    table[rng.random(table.shape) < holes] = -1
+    group = heads // kv
+    size = np.array([[0.0, 1.0, -1.0, 0.5, 0.25, -0.5, 0.75, 2.0][g % group] for g in range(heads)]) * (steps > 0)
+    q = torch.zeros((len(lens), heads, dim), device="cuda")
+    q[:, :, 5] = torch.as_tensor(size / LOG2E, device="cuda").float()
+    pos, seq = np.array(lens) - 1, [0] * len(lens) if shared else list(range(len(lens)))
+    out, lse = (f64(x) for x in attend(B, k, v, q, pos, table.tolist(), window, seq, scale=1.0))
+    step = f64(q)[0, :, 5]
+    for r, p in enumerate(pos):
+        j = np.arange(max(0, p + 1 - window) if window else 0, p + 1)
+        pg = table[seq[r], j // page] if len(j) else j
+        j, pg = j[pg >= 0], pg[pg >= 0]
+        if not len(j):
+            assert (out[r] == 0).all() and (lse[r] == -np.inf).all()
+            continue
+        values, weights = chain_bounds(kind, dim, len(j))
+        for h in range(heads):
+            s = step[h] * level[pg, h // group, j % page]
+            top = s.max()
+            w = np.exp(s - top)
+            want = np.bincount(where[pg, h // group, j % page], w, dim) / w.sum()
+            # scores 0: whole numbers up to 2^17, times 2^15 for f16, which no sum rounds: the reciprocal and the product
+            # do. Steps: a weight's exponent of 22 at most rounds four times (log2 e, q times it, the score, less the
+            # maximum), f16's parts of q twice, times ln 2: 92; the exponential 4; in the weights and in their sum.
+            tol = 2 if steps == 0 else values + weights + 2 * (92 + 4)
+            assert (np.abs(out[r, h] - want) <= tol * U * want).all(), (r, h)
+            # the logarithm is off by a step at most and rounded
+            wl = top + np.log(w.sum())
+            tol = 4 * abs(wl) if steps == 0 else 4 * (abs(top) + np.log(w.sum())) + weights + 92 + 4
+            assert abs(lse[r, h] - wl) <= tol * U, (r, h)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,dim", [(4, 64), (8, 64), (3, 128), (7, 128)])
+def test_attention_paged_keeps_the_digits_of_probabilities(kind, heads, dim):
+    """Two keys: the second's weight c against 1 is c / (1 + c), for weights with all their 24 bits."""
+    B = binding()
+    g = torch.Generator(device="cuda").manual_seed(heads * dim)
+    q = torch.zeros((500, heads, dim), device="cuda")
+    q[..., 0] = -0.05 - 0.95 * torch.rand((500, heads), generator=g, device="cuda")
+    k = torch.zeros((1, 1, 8, dim), device="cuda", dtype=_dt(kind))
+    v = torch.zeros_like(k)
+    k[0, 0, 1, 0] = v[0, 0, 1, 1] = v[0, 0, 0, 2] = 1.0
+    out, _ = attend(B, k, v, q, [1] * 500, [[0]], seq=[0] * 500, scale=1.0)
+    c = np.exp(f64(q)[..., 0])
+    # half steps: the exponent (1.45 at most) by log2 e, the product, f16's parts of q (2) and the parts' sum, times ln 2:
+    # 5; the exponential 4; f16's parts of the weight 2; the sum, its reciprocal and the product 3
+    want = np.stack([c / (1 + c), 1 / (1 + c)], -1)
+    assert (np.abs(f64(out)[..., 1:3] - want) <= 14 * U * want).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,dim", [(4, 64), (8, 64), (3, 128), (7, 128)])
+def test_attention_paged_keeps_the_digits_of_queries(kind, heads, dim):
+    """Scores 128 (q0 + q1) with q1 the negative of q0 rounded to the digits that the parts of q but the last hold: only
+    the last part is left of them."""
+    B = binding()
+    g = torch.Generator(device="cuda").manual_seed(heads + dim)
+    q0 = 1.0 + torch.rand((500, heads), generator=g, device="cuda")
+    bits = {"f32": 12, "f16": 11, "bf16": 16}[kind]
+    q = torch.zeros((500, heads, dim), device="cuda")
+    q[..., 0], q[..., dim // 2 + 1] = q0, -torch.round(q0 * 2.0 ** (bits - 1)) / 2.0 ** (bits - 1)
+    k = torch.zeros((1, 1, 8, dim), device="cuda", dtype=_dt(kind))
+    v = torch.zeros_like(k)
+    k[0, 0, 1, 0] = k[0, 0, 1, dim // 2 + 1] = 128.0
+    v[0, 0, 1, 1] = 1.0
+    out, _ = attend(B, k, v, q, [1] * 500, [[0]], seq=[0] * 500, scale=1.0)
+    s = 128.0 * f64(q).sum(-1)
+    # a score's two products of at most 370 (in units of log2): each q rounds as it is multiplied (1), f16 drops 2 of its
+    # parts, the sums of up to four products round or cut (2 each) and the sums' sums round (2): 2 (1 + 2) + 10 half steps
+    # of 370, times ln 2: 4110; a weight's derivative is 1 / 4 at most
+    assert np.abs(f64(out)[..., 1] - 1 / (1 + np.exp(-s))).max() <= (4110 / 4 + 14) * U
