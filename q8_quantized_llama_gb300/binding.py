@@ -393,57 +393,68 @@ def llama_q8_attention_decode_noalloc(q, k_cache, v_cache, kv_len: int, n_head: 
 
 
 # ---- batched decoding over a paged KV cache ---------------------------------------
+# Tensors are checked for type, layout, place and length before the call (a workspace
+# for all but its length, which workspace_bytes states); raw addresses are taken as they are.
 
 LQ8_ROPE_NONE, LQ8_ROPE_LINEAR, LQ8_ROPE_BASE, LQ8_ROPE_RAMP, LQ8_ROPE_RAMP_M = 0, 1, 2, 3, 4
 
 
-_dtype_names: dict = {}
+class _Type:
+    """An element type by torch's name for it, and torch's object once it has been met."""
+    __slots__ = ("name", "met")
+
+    def __init__(self, name: str):
+        self.name, self.met = name, None
 
 
-def _dev(a, dtype: str) -> int | None:
-    """Address of a contiguous device array of the given element type (a torch
-    tensor), of a raw address, or None."""
+def _dev(a, dtype: _Type, n: int = 0) -> int | None:
+    """Address of a contiguous device array of the given element type and at
+    least n values (a torch tensor), of a raw address, or None."""
     if a is None or type(a) is int:
         return a
-    kind = a.dtype
-    name = _dtype_names.get(kind)
-    if name is None:
-        name = _dtype_names[kind] = str(kind)
-    if name != dtype:
-        raise TypeError(f"tensor must be {dtype}, got {kind}")
+    if a.dtype is not dtype.met:
+        if str(a.dtype) != dtype.name:
+            raise TypeError(f"tensor must be {dtype.name}, got {a.dtype}")
+        dtype.met = a.dtype
     if not a.is_contiguous():
         raise ValueError("tensor must be contiguous")
     if not a.is_cuda:
         raise ValueError("tensor must be on the GPU")
+    if n and a.numel() < n:
+        raise ValueError(f"tensor must have {n} values, got {a.numel()}")
     return a.data_ptr()
 
 
-def _dev_rows(a, dtype: str, stride: int) -> int | None:
-    """As _dev, for rows `stride` values apart: a contiguous tensor, or one whose rows are that far apart."""
+def _dev_rows(a, dtype: _Type, stride: int, rows: int, width: int) -> int | None:
+    """As _dev, for `rows` rows of `width` values, `stride` apart: a contiguous tensor, or one whose rows are that far
+    apart."""
     if a is None or type(a) is int or a.is_contiguous():
-        return _dev(a, dtype)
+        return _dev(a, dtype, (rows - 1) * stride + width if rows > 0 else 0)
     if a.dim() != 2 or a.stride(1) != 1 or a.stride(0) != stride:
         raise ValueError(f"tensor must be contiguous or have rows {stride} apart")
-    if str(a.dtype) != dtype:
-        raise TypeError(f"tensor must be {dtype}, got {a.dtype}")
+    if a.shape[0] < rows or a.shape[1] < width:
+        raise ValueError(f"tensor must have {rows} rows of {width} values, got {tuple(a.shape)}")
+    if str(a.dtype) != dtype.name:
+        raise TypeError(f"tensor must be {dtype.name}, got {a.dtype}")
     if not a.is_cuda:
         raise ValueError("tensor must be on the GPU")
     return a.data_ptr()
 
 
-_F32, _I32, _F64, _U8 = "torch.float32", "torch.int32", "torch.float64", "torch.uint8"
-_PAGE_TYPES = {"torch.float32": GGUF_F32, "torch.float16": GGUF_F16, "torch.bfloat16": GGUF_BF16}
+_F32, _I32, _F64, _U8 = (_Type("torch." + t) for t in ("float32", "int32", "float64", "uint8"))
+_PAGE_TYPES = {t.name: (gguf, t) for t, gguf in ((_F32, GGUF_F32), (_Type("torch.float16"), GGUF_F16),
+                                                 (_Type("torch.bfloat16"), GGUF_BF16))}
 
 
 def make_pages(k, v) -> llama_q8_pages:
     """The pool of K and V page tensors, each [n_layer][n_pages][n_head_kv][page][head_dim]."""
     if tuple(k.shape) != tuple(v.shape) or len(k.shape) != 5 or k.dtype != v.dtype:
         raise ValueError("k and v must be 5-dimensional, of one shape and type")
-    kind = _PAGE_TYPES.get(str(k.dtype))
-    if kind is None:
+    if str(k.dtype) not in _PAGE_TYPES:
         raise TypeError(f"pages must be float32, float16 or bfloat16, got {k.dtype}")
+    gguf, t = _PAGE_TYPES[str(k.dtype)]
     n_layer, n_pages, n_head_kv, page, head_dim = k.shape
-    p = llama_q8_pages(_dev(k, str(k.dtype)), _dev(v, str(k.dtype)), kind, n_layer, n_pages, page, n_head_kv, head_dim)
+    p = llama_q8_pages(_dev(k, t), _dev(v, t), gguf, n_layer, n_pages, page, n_head_kv, head_dim)
     p.keep = (k, v)
     return p
 
@@ -469,9 +480,12 @@ def make_rope(freq, style: int = 0, magnitude: float = 1.0) -> llama_q8_rope:
 def llama_q8_rope_append(pages: llama_q8_pages, layer: int, qkv, qkv_stride: int, rows: int, pos, seq, n_head: int,
                          rope: llama_q8_rope, table, n_seq: int, table_stride: int, q_out, err=None,
                          stream=0) -> None:
-    check(lib().llama_q8_rope_append(C.addressof(pages), layer, _dev_rows(qkv, _F32, qkv_stride), qkv_stride, rows,
-                                     _dev(pos, _I32), _dev(seq, _I32), n_head, C.addressof(rope), _dev(table, _I32), n_seq,
-                                     table_stride, _dev(q_out, _F32), _dev(err, _I32), stream or None),
+    dim = pages.head_dim
+    check(lib().llama_q8_rope_append(C.addressof(pages), layer,
+                                     _dev_rows(qkv, _F32, qkv_stride, rows, (n_head + 2 * pages.n_head_kv) * dim),
+                                     qkv_stride, rows, _dev(pos, _I32, rows), _dev(seq, _I32, rows), n_head,
+                                     C.addressof(rope), _dev(table, _I32, n_seq * table_stride), n_seq, table_stride,
+                                     _dev(q_out, _F32, rows * n_head * dim), _dev(err, _I32), stream or None),
           "llama_q8_rope_append")
 
 
@@ -482,10 +496,14 @@ def llama_q8_attention_paged_workspace_bytes(rows: int, n_head: int, n_head_kv: 
 def llama_q8_attention_paged(pages: llama_q8_pages, layer: int, q, rows: int, pos, seq, n_head: int, scale: float,
                              window: int, table, n_seq: int, table_stride: int, out, lse, workspace,
                              workspace_bytes: int, err=None, stream=0) -> None:
-    check(lib().llama_q8_attention_paged(C.addressof(pages), layer, _dev(q, _F32), rows, _dev(pos, _I32),
-                                         _dev(seq, _I32), n_head, scale, window, _dev(table, _I32), n_seq,
-                                         table_stride, _dev(out, _F32), _dev(lse, _F32), _dev(workspace, _U8),
-                                         workspace_bytes, _dev(err, _I32), stream or None),
+    heads = rows * n_head
+    n = heads * pages.head_dim
+    check(lib().llama_q8_attention_paged(C.addressof(pages), layer, _dev(q, _F32, n), rows, _dev(pos, _I32, rows),
+                                         _dev(seq, _I32, rows), n_head, scale, window,
+                                         _dev(table, _I32, n_seq * table_stride), n_seq, table_stride,
+                                         _dev(out, _F32, n), _dev(lse, _F32, heads),
+                                         _dev(workspace, _U8), workspace_bytes, _dev(err, _I32),
+                                         stream or None),
           "llama_q8_attention_paged")
 
 
@@ -496,10 +514,13 @@ def llama_q8_pages_fork_workspace_bytes(rows_in: int, rows_out: int, table_strid
 def llama_q8_pages_fork(pages: llama_q8_pages, rows_in: int, len_in, table_in, table_stride: int, refs_in,
                         rows_out: int, parent, reserve: int, len_out, table_out, refs_out, workspace,
                         workspace_bytes: int, err, stream=0) -> None:
-    check(lib().llama_q8_pages_fork(C.addressof(pages), rows_in, _dev(len_in, _I32), _dev(table_in, _I32),
-                                    table_stride, _dev(refs_in, _I32), rows_out, _dev(parent, _I32), reserve,
-                                    _dev(len_out, _I32), _dev(table_out, _I32), _dev(refs_out, _I32),
-                                    _dev(workspace, _U8), workspace_bytes, _dev(err, _I32), stream or None),
+    n = pages.n_pages
+    check(lib().llama_q8_pages_fork(C.addressof(pages), rows_in, _dev(len_in, _I32, rows_in),
+                                    _dev(table_in, _I32, rows_in * table_stride), table_stride, _dev(refs_in, _I32, n),
+                                    rows_out, _dev(parent, _I32, rows_out), reserve, _dev(len_out, _I32, rows_out),
+                                    _dev(table_out, _I32, rows_out * table_stride), _dev(refs_out, _I32, n),
+                                    _dev(workspace, _U8), workspace_bytes, _dev(err, _I32),
+                                    stream or None),
           "llama_q8_pages_fork")
 
 
@@ -509,9 +530,11 @@ def llama_q8_pages_compact_workspace_bytes(n_pages: int) -> int:
 
 def llama_q8_pages_compact(pages: llama_q8_pages, rows: int, table_in, table_stride: int, refs_in, table_out,
                            refs_out, n_used, workspace, workspace_bytes: int, err, stream=0) -> None:
-    check(lib().llama_q8_pages_compact(C.addressof(pages), rows, _dev(table_in, _I32), table_stride,
-                                       _dev(refs_in, _I32), _dev(table_out, _I32), _dev(refs_out, _I32),
-                                       _dev(n_used, _I32), _dev(workspace, _U8), workspace_bytes, _dev(err, _I32),
+    n, entries = pages.n_pages, rows * table_stride
+    check(lib().llama_q8_pages_compact(C.addressof(pages), rows, _dev(table_in, _I32, entries), table_stride,
+                                       _dev(refs_in, _I32, n), _dev(table_out, _I32, entries),
+                                       _dev(refs_out, _I32, n), _dev(n_used, _I32, 1),
+                                       _dev(workspace, _U8), workspace_bytes, _dev(err, _I32),
                                        stream or None), "llama_q8_pages_compact")
 
 
@@ -521,9 +544,12 @@ def llama_q8_beam_select_workspace_bytes(groups: int, beams: int, n_vocab: int, 
 
 def llama_q8_beam_select(logits, logits_stride: int, groups: int, beams: int, n_vocab: int, scores, n_out: int,
                          out_scores, out_parent, out_token, workspace, workspace_bytes: int, stream=0) -> None:
-    check(lib().llama_q8_beam_select(_dev_rows(logits, _F32, logits_stride), logits_stride, groups, beams, n_vocab,
-                                     _dev(scores, _F32), n_out, _dev(out_scores, _F32), _dev(out_parent, _I32), _dev(out_token, _I32),
-                                     _dev(workspace, _U8), workspace_bytes, stream or None), "llama_q8_beam_select")
+    rows, n = groups * beams, groups * n_out
+    check(lib().llama_q8_beam_select(_dev_rows(logits, _F32, logits_stride, rows, n_vocab), logits_stride, groups,
+                                     beams, n_vocab, _dev(scores, _F32, rows), n_out, _dev(out_scores, _F32, n),
+                                     _dev(out_parent, _I32, n), _dev(out_token, _I32, n),
+                                     _dev(workspace, _U8), workspace_bytes, stream or None),
+          "llama_q8_beam_select")
 
 
 def status_str(s: int) -> str:
