@@ -510,7 +510,9 @@ typedef struct llama_q8_pages {
  *   LQ8_ROPE_RAMP    by parts: with r = trained_ctx * freq / 2 pi rotations in
  *                    the trained context, freq / factor where r <= low, freq
  *                    where r >= high, and between them the mixture with weight
- *                    (r - low) / (high - low) on freq
+ *                    (r - low) / (high - low) on freq (the ramp runs over r; one
+ *                    over the pair's index between the indices of low and high
+ *                    gives other frequencies)
  *   LQ8_ROPE_RAMP_M  the same, and *magnitude = 0.1 ln(factor) + 1
  * freq: host double[rot_dim / 2]; *magnitude, the factor on cos and sin, is 1
  * otherwise. rot_dim even and >= 2 (> 2 for BASE), theta > 0, factor >= 1,
@@ -550,7 +552,8 @@ typedef struct llama_q8_rope {
  * and sine taken in f32, so far positions keep f32 accuracy. n_head %
  * n_head_kv == 0. rows == 0 does nothing. Rows of one call name different
  * (sequence, position) pairs; of rows that name the same one, each written
- * value is one of theirs. q_out does not overlap qkv. A row whose sequence or
+ * value is one of theirs. (n_head + 2 n_head_kv) * head_dim < 2^31
+ * (LQ8_ERR_UNSUPPORTED). q_out does not overlap qkv. A row whose sequence or
  * position is out of range, or whose page is a hole or out of range, still gets
  * its q_out (with the position it names); its append is skipped and reported in
  * err (may be NULL). qkv, q_out 16-byte aligned. Enqueues one kernel. */
@@ -593,8 +596,8 @@ llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t la
 /* Fork, extend and free: rows_out sequences that continue rows_in ones, as
  * after a beam search step, in bookkeeping that goes from the _in arrays to the
  * _out arrays (which must not overlap; a program swaps two sets). refs_in
- * [n_pages] counts the table entries that name each page (0: free); a caller
- * may hold counts of its own on pages it wants kept. Child i continues sequence
+ * [n_pages] counts the table entries that name each page (0: free, never
+ * negative); a caller may hold counts of its own on pages it wants kept. Child i continues sequence
  * parent[i] (-1: empty, length 0) with len_out[i] = len_in[parent[i]] = n:
  *   - pages filled entirely (blocks below n / page) are shared, holes stay;
  *   - the blocks from there on are written next, so they belong to one sequence:
@@ -612,7 +615,9 @@ llama_q8_status llama_q8_attention_paged(const llama_q8_pages* pages, int32_t la
  * pages), LQ8_ERR_CTX (n < 0, or n + reserve past the table), LQ8_ERR_ARG (a
  * parent outside [-1, rows_in)). A page number >= n_pages in a row that is
  * continued or freed counts as a hole and is reported as LQ8_ERR_ARG. rows_in,
- * rows_out in 1 .. 65536, reserve >= 0. Enqueues two kernels. */
+ * rows_out >= 1, reserve >= 0 (LQ8_ERR_ARG); rows_in, rows_out <= 65536, each times
+ * table_stride < 2^31, n_pages <= 2^30, n_layer * n_head_kv <= 2^24, n_head_kv *
+ * page * head_dim <= 2^34 (LQ8_ERR_UNSUPPORTED). Enqueues two kernels. */
 size_t llama_q8_pages_fork_workspace_bytes(int32_t rows_in, int32_t rows_out, int32_t table_stride);
 llama_q8_status llama_q8_pages_fork(const llama_q8_pages* pages, int32_t rows_in, const int32_t* len_in,
                                     const int32_t* table_in, int32_t table_stride, const int32_t* refs_in,
@@ -628,7 +633,8 @@ llama_q8_status llama_q8_pages_fork(const llama_q8_pages* pages, int32_t rows_in
  * counts, *n_used (device) is U. Every table that names pages of the pool has to
  * be in table_in. The _out arrays do not overlap the _in arrays; the moved
  * pages' old contents stay until they are written again. rows == 0 (no tables)
- * is allowed. err is not NULL. Enqueues two kernels. */
+ * is allowed. The pool's limits are those of llama_q8_pages_fork. err is not NULL.
+ * Enqueues two kernels. */
 size_t llama_q8_pages_compact_workspace_bytes(int32_t n_pages);
 llama_q8_status llama_q8_pages_compact(const llama_q8_pages* pages, int32_t rows, const int32_t* table_in,
                                        int32_t table_stride, const int32_t* refs_in, int32_t* table_out,

@@ -461,9 +461,10 @@ PoolBytes pool_bytes(const llama_q8_pages* p) {
 
 bool misaligned(const void* p) { return ((uintptr_t)p & 3) != 0; }
 
-// Units of copy work are counted in 32 bits per page: layers * 2 * heads (or pieces).
+// Units of copy work are counted in 32 bits per page: layers * 2 * heads (or pieces). The plans' passes over the counts
+// step past n_pages in 32 bits.
 bool pool_too_large(const llama_q8_pages* p) {
-    return (int64_t)p->n_layer * p->n_head_kv > (1 << 24) ||
+    return p->n_pages > (1 << 30) || (int64_t)p->n_layer * p->n_head_kv > (1 << 24) ||
            (int64_t)p->n_head_kv * p->page * p->head_dim * 4 > (int64_t)1 << 36;
 }
 
