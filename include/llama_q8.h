@@ -573,7 +573,9 @@ llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer,
  * out of range are masked (the latter reported in err, as is a position past
  * the table, of which the part inside counts); a row that sees nothing gets
  * zeros and lse -infinity. What lies in masked slots, also infinities and NaN,
- * does not matter; visible keys and values must be finite. Rows may share a
+ * does not matter; visible keys and values, queries times scale, and scores must
+ * be finite in f32 (a head's query that is not makes that head's out and lse NaN
+ * and no other's). Rows may share a
  * sequence (several new tokens of one sequence, each with its own pos).
  * Products with F16 / BF16 pages run on the tensor cores on q and the
  * probabilities split into parts that keep 22 bits or more, summed in f32; F32

@@ -730,10 +730,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
         const uint8_t* parts_of_warps = smem + stl * 2 * kTileBytes;
         auto finish = [&](int e, float4 o, float m, float l) {  // value e of the pair from its sums
             const int g = e / (HD / 4);
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             reinterpret_cast<float4*>(a.out + orow * HD)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             if (a.lse && e % (HD / 4) == 0)
-                a.lse[orow + g] = l > 0.0f ? m * 0.69314718055994531f + logf(kHalf ? l * 0x1p-15f : l) : -INFINITY;
+                a.lse[orow + g] = l == 0.0f ? -INFINITY : m * 0.69314718055994531f + logf(kHalf ? l * 0x1p-15f : l);
         };
         for (int e = tid; e < G * (HD / 4); e += kThreads) {
             const int g = e / (HD / 4);

@@ -239,3 +239,22 @@ def test_attention_paged_keeps_the_digits_of_queries(kind, heads, dim):
     # parts, the sums of up to four products round or cut (2 each) and the sums' sums round (2): 2 (1 + 2) + 10 half steps
     # of 370, times ln 2: 4110; a weight's derivative is 1 / 4 at most
     assert np.abs(f64(out)[..., 1] - 1 / (1 + np.exp(-s))).max() <= (4110 / 4 + 14) * U
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [5, 90, 20000])
+def test_attention_paged_nan_query_spoils_its_head_alone(kind, n):
+    """NaN in one head's query: that head's out and lse are NaN (not an empty row's), all others as without it."""
+    B = binding()
+    heads, kv, dim, page = 12, 2, 64, 16
+    blocks = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = (torch.randn((blocks, kv, page, dim), generator=g, device="cuda").to(_dt(kind)) for _ in range(2))
+    q = torch.randn((3, heads, dim), generator=g, device="cuda")
+    args = [n - 1] * 3, [list(range(blocks))]
+    want, wl = attend(B, k, v, q, *args, seq=[0] * 3)
+    q[1, 7, 3] = float("nan")
+    out, lse = attend(B, k, v, q, *args, seq=[0] * 3)
+    assert out[1, 7].isnan().all() and lse[1, 7].isnan()
+    out[1, 7], lse[1, 7] = want[1, 7], wl[1, 7]
+    assert torch.equal(out, want) and torch.equal(lse, wl)
