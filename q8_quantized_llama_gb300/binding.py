@@ -407,16 +407,16 @@ class _Type:
         self.name, self.met = name, None
 
 
-def _dev(a, dtype: _Type, n: int = 0) -> int | None:
-    """Address of a contiguous device array of the given element type and at
-    least n values (a torch tensor), of a raw address, or None."""
+def _dev(a, dtype: _Type, n: int = 0, flat: bool = True) -> int | None:
+    """Address of a device array of the given element type and at least n values
+    (a torch tensor, contiguous if flat), of a raw address, or None."""
     if a is None or type(a) is int:
         return a
     if a.dtype is not dtype.met:
         if str(a.dtype) != dtype.name:
             raise TypeError(f"tensor must be {dtype.name}, got {a.dtype}")
         dtype.met = a.dtype
-    if not a.is_contiguous():
+    if flat and not a.is_contiguous():
         raise ValueError("tensor must be contiguous")
     if not a.is_cuda:
         raise ValueError("tensor must be on the GPU")
@@ -428,17 +428,15 @@ def _dev(a, dtype: _Type, n: int = 0) -> int | None:
 def _dev_rows(a, dtype: _Type, stride: int, rows: int, width: int) -> int | None:
     """As _dev, for `rows` rows of `width` values, `stride` apart: a contiguous tensor, or one whose rows are that far
     apart."""
-    if a is None or type(a) is int or a.is_contiguous():
-        return _dev(a, dtype, (rows - 1) * stride + width if rows > 0 else 0)
+    if a is None or type(a) is int:
+        return a
+    if a.is_contiguous():
+        return _dev(a, dtype, (rows - 1) * stride + width if rows > 0 else 0, False)
     if a.dim() != 2 or a.stride(1) != 1 or a.stride(0) != stride:
         raise ValueError(f"tensor must be contiguous or have rows {stride} apart")
     if a.shape[0] < rows or a.shape[1] < width:
         raise ValueError(f"tensor must have {rows} rows of {width} values, got {tuple(a.shape)}")
-    if str(a.dtype) != dtype.name:
-        raise TypeError(f"tensor must be {dtype.name}, got {a.dtype}")
-    if not a.is_cuda:
-        raise ValueError("tensor must be on the GPU")
-    return a.data_ptr()
+    return _dev(a, dtype, 0, False)
 
 
 _F32, _I32, _F64, _U8 = (_Type("torch." + t) for t in ("float32", "int32", "float64", "uint8"))
