@@ -37,7 +37,7 @@ namespace {
 constexpr int kBeamThreads = 256, kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamMax = 64;         // beams per group, results per group
 constexpr int kBeamVocab = 1 << 24;  // longest row: places of a group (64 rows of whole blocks) stay below 2^31
-constexpr int kBeamWave = 152 * 4;   // CTAs resident at once
+constexpr int kBeamWave = 152 * 4;   // CTAs resident at once on a GB300's 152 SMs
 constexpr int kPickItems = 4;        // blocks per thread that the final choice holds in registers
 
 struct BlockStat {

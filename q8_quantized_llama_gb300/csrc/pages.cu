@@ -10,8 +10,14 @@
 // does what is independent per entry: table rows, counts and the page copies,
 // spread over the GPU by warps.
 //
-// Bound: the copies (read + write once at HBM rate) where pages are copied;
-// the two launches and the plan's chain of dependent loads where few are.
+// Bound: the plan's chain of dependent loads and the hand-over (about 8 us), then
+// the copies at the memory's rate; where few pages are copied, the first alone.
+// 36 rows of a pool of 8x128, 32 layers, compacted: 120 us (721 MB, 6.0 TB/s); 24
+// rows of 3x64, 30 layers: 26 us (108 MB). Fork of 16 groups of 4 beams on the
+// first pool: 51 us, its copies 42 (children of one parent read their page from
+// L2); of 4 x 4 on the second: 10 us, 7.8 of them on the GPU.
+// Not built: small pools in one launch, each CTA making the plan for itself (the
+// plan depends only on arrays that the call does not write).
 #include <algorithm>
 
 #include "kernels.cuh"

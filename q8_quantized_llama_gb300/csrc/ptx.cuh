@@ -85,9 +85,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // ---- programmatic dependent launch ---------------------------------------------
 // wait: block until the preceding grid in the stream has completed and its
 // memory is visible. launch_dependents: allow the next grid to start its
-// CTAs (which run until their own wait). Every kernel here calls
-// launch_dependents only after its own wait, so when a kernel starts, every
-// grid two or more launches back has completed.
+// CTAs (which run until their own wait). A kernel that is launched as a
+// dependent calls launch_dependents only after its own wait, and one that calls
+// it without a wait (the plans of pages.cu) is launched plainly, so that it
+// starts when its predecessor has completed: either way, when a kernel starts,
+// every grid two or more launches back has completed.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

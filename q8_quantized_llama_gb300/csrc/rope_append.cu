@@ -13,8 +13,11 @@
 // two stores): the two halves of 4 pairs for the half layout, so that no value
 // is read twice; the loads are issued before the angles are computed, whose
 // latency (double multiply, sincospif) they cover. One CTA per row or per eight
-// narrow rows: 8 or more resident per SM, enough bytes in flight without a
-// pipeline (8195 rows of 32/8 heads of 128 into bf16: 59.6 us, 6.2 TB/s; with 3, 4, 6 items ahead 60.6, 61.5, 83.6).
+// narrow rows, 6 or 5 of them resident per SM (registers). Wide rows of a prompt:
+// 8195 of 32/8 heads of 128 into bf16 59.5 us, 6.2 TB/s (with 3, 4, 6 items ahead
+// 60.6, 61.5, 83.6). Narrow ones wait for memory twice, as only two of a thread's
+// four items are asked for before the barrier, and 1025 CTAs are 1.35 waves: 8195
+// of 9/3 heads of 64 into f32 16.1 us in a captured graph, 9.4 for the bytes.
 #include <algorithm>
 
 #include "kernels.cuh"
