@@ -15,9 +15,10 @@
 // latency (double multiply, sincospif) they cover. One CTA per row or per eight
 // narrow rows, 6 or 5 of them resident per SM (registers). Wide rows of a prompt:
 // 8195 of 32/8 heads of 128 into bf16 59.5 us, 6.2 TB/s (with 3, 4, 6 items ahead
-// 60.6, 61.5, 83.6). Narrow ones wait for memory twice, as only two of a thread's
-// four items are asked for before the barrier, and 1025 CTAs are 1.35 waves: 8195
-// of 9/3 heads of 64 into f32 16.1 us in a captured graph, 9.4 for the bytes.
+// 60.6, 61.5, 83.6). Narrow rows are CTAs of 128 threads or fewer that live for one
+// memory latency and a few KB, or, eight in a CTA, for two, as only two of a
+// thread's four items are asked for before the barrier: 8195 of 9/3 heads of 64
+// into f32 15.4 us in a captured graph, 9.4 for the bytes.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -168,9 +169,12 @@ cudaError_t launch_rope_hd(const RopeArgs& a, const llama_q8_pages* p, int layer
     const int items = (a.n_head + 2 * p->n_head_kv) * (HD / 8);
     const PageView<T> pg = page_view<T>(p, layer);
     // One row per CTA, as many warps as one pass over its items needs (at least those that compute the angles): the
-    // shortest call. Narrow rows of a prompt, once there are enough to fill the GPU either way: several per CTA
-    // (8195 rows of 9/3 heads of 64: 20.6 us with one, 17.0 with eight).
-    if (items <= kRopeThreads / 2 && a.rows >= 152 * 8 * kRopeRows / 2)
+    // shortest call, and the better one while its CTAs are few waves. Rows too narrow to fill a CTA, in longer calls:
+    // eight per CTA, from where that is three waves of CTAs (six for heads of 128, whose angles cost more). One
+    // and eight, into f32: 14000 rows of 9/3 heads of 64 23.0 and 23.0 us, 8195 15.4 and 16.0, 27000 41.7 and 38.9;
+    // 40000 of 4/1 heads of 128 47.6 and 47.8, 20000 25.9 and 27.3, 100000 113 and 110. Rows of 64 items and less fill
+    // neither: 100000 of 6/1 heads of 64 77 and 81.
+    if (items <= kRopeThreads / 2 && items > kRopeThreads / 4 && a.rows >= 152 * 16 * kRopeRows * (HD / 64))
         return launch_ex(rope_append_kernel<T, HD, kRopeRows>, dim3((a.rows + kRopeRows - 1) / kRopeRows),
                          dim3(kRopeThreads), 0, s, false, a, pg, tb);
     const int threads = std::min(kRopeThreads, std::max((items + 31) / 32 * 32, HD / 2));

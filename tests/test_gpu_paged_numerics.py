@@ -4,6 +4,7 @@ What is checked has a closed form, so that the bounds are a few roundings."""
 import numpy as np
 import pytest
 
+from tests import test_gpu_paged
 from tests.gpu_helpers import binding, require_gpu, torch
 
 pytestmark = pytest.mark.gpu
@@ -258,3 +259,14 @@ def test_attention_paged_nan_query_spoils_its_head_alone(kind, n):
     assert out[1, 7].isnan().all() and lse[1, 7].isnan()
     out[1, 7], lse[1, 7] = want[1, 7], wl[1, 7]
     assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+# rows, heads, kv, dim, rot, style, page, kind: the sizes at which narrow rows go eight to a CTA (from 19456 rows of more
+# than 64 and at most 128 items of 8 values, twice as many for heads of 128), on both sides of each border
+@pytest.mark.parametrize("rows,heads,kv,dim,rot,style,page,kind", [
+    (19455, 9, 3, 64, 64, 0, 16, "f32"), (19459, 9, 3, 64, 32, 1, 16, "f16"), (19457, 6, 1, 64, 64, 0, 32, "bf16"),
+    (19461, 7, 1, 64, 64, 1, 64, "bf16"), (19463, 14, 1, 64, 64, 0, 16, "bf16"),
+    (19470, 15, 1, 64, 48, 0, 16, "f16"), (38911, 3, 1, 128, 96, 1, 64, "f32"),
+    (38917, 3, 1, 128, 128, 0, 64, "f16"), (38913, 2, 1, 128, 64, 1, 16, "f32")])
+def test_rope_append_long_prompts_of_narrow_rows(rows, heads, kv, dim, rot, style, page, kind):
+    test_gpu_paged.test_rope_append(rows, heads, kv, dim, rot, style, page, kind, 50, True)
