@@ -27,7 +27,7 @@
 // one thread. tcgen05 (128 rows) would idle 15/16 of its rows and pass the
 // probabilities through tensor memory; the kernel is bound by memory without.
 //  - f16: q is scaled per head by a power of two (largest value into [2^14,
-//    2^15)) and split in two: 22 bits; the probabilities by 2^15.
+//    2^15)) and split in two: 22 bits; the probabilities by 2^14.
 //  - bf16: q and the probabilities in three parts, 24 bits. Groups of up to 4
 //    heads have the three parts in rows 0-3, 4-7 and 8-11 of one product; larger
 //    ones the third in a second product.
@@ -62,6 +62,12 @@ constexpr int kRingBytes = 24 * 1024;  // per warp
 constexpr int kMinShare = 2;           // units a CTA takes at least
 constexpr int kJoin = 16;              // parts joined at once where a pair has more than twice as many
 static_assert((kMaxCtas + kJoin - 1) / kJoin <= 32, "one lane per part or group");
+
+// The running reference m of the exponentials follows the maximum when that is more than kLag (units of log2) above it:
+// every change rounds all sums so far, and one per tile, as under rising scores, put 1.2e-4 on lse over 131071
+// positions; this way what a change rounds counts half after the next. Probabilities are 2^kLag at most, which times
+// kUpF16 f16 holds.
+constexpr float kLag = 1.0f, kUpF16 = 16384.0f;
 
 struct AttnArgs {
     const float* q;
@@ -298,7 +304,8 @@ __device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, u
     for (int j = 1; j < 2 * NT; ++j) mx = fmaxf(mx, x[j]);
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const float m = fmaxf(s.m, mx);  // finite: a tile in which nothing counts is not given to this function
+    // finite: a tile in which nothing counts is not given to this function
+    const float m = mx - s.m > kLag ? mx : s.m;
     if (__any_sync(0xffffffffu, m > s.m)) {
         const float f = ex2(s.m - m);
         s.m = m;
@@ -315,9 +322,9 @@ __device__ __forceinline__ void state_tile(State16<T, HD, GP>& s, uint32_t ks, u
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j) {
         x[j] = ex2(x[j] - m);
-        // f16: times 2^15, so that the second part of a small one is not lost below f16's range. Not as m - 15 in the
+        // f16: times 2^14, so that the second part of a small one is not lost below f16's range. Not as m - 14 in the
         // exponent: far from zero that rounds, up to where the largest probability leaves f16's range.
-        if (St::kHalf) x[j] *= 32768.0f;
+        if (St::kHalf) x[j] *= kUpF16;
     }
 #pragma unroll
     for (int h = 0; h < NT / 2; ++h) {
@@ -360,7 +367,7 @@ __device__ __forceinline__ void state_fold(State16<T, HD, GP>& s) {
     s.l = 0.0f;
 }
 
-// The warp's part: output [8][HD] to ob, m and l of its heads to ml (l of f16 pages carries the factor 2^15).
+// The warp's part: output [8][HD] to ob, m and l of its heads to ml (l of f16 pages carries kUpF16).
 template <typename T, int HD, int GP>
 __device__ __forceinline__ void state_store(State16<T, HD, GP>& s, float* ob, float2* ml, int lane) {
     constexpr bool kOne = State16<T, HD, GP>::kOne;
@@ -422,7 +429,8 @@ __device__ __forceinline__ void state_tile(State32<HD>& s, const uint8_t* ks, co
 #pragma unroll
         for (int o = TK; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (!in) x = -INFINITY;
-        m[g] = fmaxf(s.m[g], order_float(__reduce_max_sync(0xffffffffu, order_int(x))));
+        const float mx = order_float(__reduce_max_sync(0xffffffffu, order_int(x)));
+        m[g] = mx - s.m[g] > kLag ? mx : s.m[g];
         grew |= m[g] > s.m[g];
         p[g] = ex2(x - m[g]);
     }
@@ -733,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_paged_kernel(AttnArgs a
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             reinterpret_cast<float4*>(a.out + orow * HD)[e] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             if (a.lse && e % (HD / 4) == 0)
-                a.lse[orow + g] = l == 0.0f ? -INFINITY : m * 0.69314718055994531f + logf(kHalf ? l * 0x1p-15f : l);
+                a.lse[orow + g] = l == 0.0f ? -INFINITY : m * 0.69314718055994531f + logf(kHalf ? l * (1.0f / kUpF16) : l);
         };
         for (int e = tid; e < G * (HD / 4); e += kThreads) {
             const int g = e / (HD / 4);

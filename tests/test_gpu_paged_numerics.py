@@ -270,3 +270,37 @@ def test_attention_paged_nan_query_spoils_its_head_alone(kind, n):
     (38917, 3, 1, 128, 128, 0, 64, "f16"), (38913, 2, 1, 128, 64, 1, 16, "f32")])
 def test_rope_append_long_prompts_of_narrow_rows(rows, heads, kv, dim, rot, style, page, kind):
     test_gpu_paged.test_rope_append(rows, heads, kv, dim, rot, style, page, kind, 50, True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,dim", [(2, 64), (8, 128), (16, 64)])
+@pytest.mark.parametrize("rise", [0.1, 1.0, 10.0])
+def test_attention_paged_rising_scores(kind, heads, dim, rise):
+    """Scores that rise along 131071 positions of one CTA's share, so that every tile has a new maximum."""
+    B = binding()
+    n, kv, rows, page = 131071, 2, 256, 64
+    blocks = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    k = torch.zeros((blocks, kv, page, dim), device="cuda", dtype=_dt(kind))
+    left = torch.arange(blocks * page, device="cuda", dtype=torch.float64) / n
+    for c in range(3):  # position / n in as many values of the pages' type as hold it
+        k[..., c] = left.to(_dt(kind)).view(blocks, 1, page)
+        left = left - k[:, 0, :, c].reshape(-1).double()
+    v = (1 + torch.randn(k.shape, generator=g, device="cuda")).to(_dt(kind))
+    q = torch.zeros((rows, heads, dim), device="cuda")
+    q[..., :3] = rise * (1 - 0.1 * torch.rand((rows, heads, 1), generator=g, device="cuda"))
+    out, lse = attend(B, k, v, q, [n - 1] * rows, [list(range(blocks))], seq=[0] * rows, scale=1.0)
+    values, weights = chain_bounds(kind, dim, n)
+    # half steps: a score's log2 e, its product, sums, f16's parts: 8 of it; the exponential 4; changes of the reference,
+    # of which each rounds (5) what counts half after the next: 10
+    weight = 8 * rise + 4 + 10
+    at = k[:, 0, :, :3].double().sum(-1).view(-1)[:n]
+    for r in (0, 100, 255):
+        s = q[r, :, 0].double()[:, None] * at
+        z = torch.logsumexp(s, 1)
+        p = torch.exp(s - z[:, None]).view(kv, heads // kv, n)
+        w = v.double().transpose(0, 1).reshape(kv, -1, dim)[:, :n]
+        err, size = (out[r].double() - (p @ w).view(heads, dim)).abs(), (p @ w.abs()).view(heads, dim)
+        assert (err <= (values + weights + 2 * weight) * U * size).all()
+        # and the logarithm of up to 11.8 and the reference, a step and a rounding each
+        assert ((lse[r].double() - z).abs() <= (weights + weight + 4 * (12 + 2 * rise)) * U).all()
