@@ -578,7 +578,8 @@ llama_q8_status llama_q8_rope_append(const llama_q8_pages* pages, int32_t layer,
  * and no other's). Rows may share a
  * sequence (several new tokens of one sequence, each with its own pos).
  * Products with F16 / BF16 pages run on the tensor cores on q and the
- * probabilities split into parts that keep 22 bits or more, summed in f32; F32
+ * probabilities split into parts that keep 22 bits or more (F16 pages: or 2^-37 of
+ * the head's largest, where that is more), summed in f32; F32
  * pages are multiplied in f32. The visible positions of all rows are dealt evenly
  * to the GPU's SMs, whatever their lengths; parts of one row meet through the
  * workspace, always added in the order of the positions, so equal calls give
