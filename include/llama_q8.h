@@ -671,6 +671,87 @@ llama_q8_status llama_q8_beam_select(const float* logits, int64_t logits_stride,
                                      int32_t* out_parent, int32_t* out_token, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit integers. No counterpart on the pages (their activations are
+ * f32 throughout): the operators of a program that runs prompts and batches with
+ * both operands in 8 bits, a scale per token and a scale per output channel. Such a
+ * layer, every call on one stream:
+ *   norm_quant -> i8_matmul (Q/K/V) -> attention -> rows_quant -> i8_matmul (output)
+ *   -> norm_quant -> i8_matmul (gate | up) -> silu_quant -> i8_matmul (down)
+ * where each norm_quant adds the preceding product to the residual stream.
+ *
+ * Conventions, beside those of the device-level entry points above:
+ *   - codes[rows][llama_q8_i8_row_bytes(k)]: int8, rows of k codes padded with zeros
+ *     to a multiple of 16 bytes, 16-byte aligned; scale[rows] f32. A value is code *
+ *     scale.
+ *   - `type` names the element type of activations: LLAMA_Q8_GGUF_F32, _F16 or _BF16.
+ *     Strides count elements; rows may lie on any element boundary (16-byte aligned
+ *     rows of a multiple of 16 bytes are read and written in 16-byte pieces).
+ *   - k is at most LLAMA_Q8_I8_MAX_K, for which sums of products stay within 32 bits
+ *     (LQ8_ERR_UNSUPPORTED).
+ *   - rows == 0 (m == 0) does nothing. Every call runs on the calling thread's current
+ *     device, keeps nothing between calls and may be captured in a CUDA graph.
+ * ------------------------------------------------------------------------- */
+#define LLAMA_Q8_I8_MAX_K 131056
+
+/* Bytes of a row of k codes: k rounded up to a multiple of 16 (0 for k <= 0). */
+int64_t llama_q8_i8_row_bytes(int64_t k);
+
+/* Codes and a scale for each row of x: with M the row's largest magnitude, code_i =
+ * 127 x_i / M rounded to the nearest integer, ties away from zero, and scale = M / 127
+ * rounded to f32; a row of zeros has codes and scale 0, a row with a NaN or an infinity
+ * codes 0 and scale NaN. The codes are those of exact arithmetic on the stored numbers.
+ * x: f32, f16 or bf16 rows x_stride elements apart, or LLAMA_Q8_GGUF_Q8_0 blocks (as in a
+ * GGUF file; k and x_stride multiples of 32, rows x_stride / 32 * 34 bytes apart, on
+ * 2-byte boundaries), whose values are d * q. Rows are the tokens of an activation or the
+ * output channels of a weight matrix. x_stride >= k; codes does not overlap x. Enqueues
+ * one kernel. */
+llama_q8_status llama_q8_rows_quant(int32_t type, const void* x, int64_t x_stride, int32_t rows, int32_t k,
+                                    int8_t* codes, float* scale, void* stream);
+
+/* The residual's addition, RMSNorm, and codes with a scale for each row: h = x + delta
+ * (added in f32, rounded to the type; delta NULL: h = x), stored to x_out unless that is
+ * NULL, y = h g / sqrt(mean(h^2) + eps) with f32 g[k], and codes and scale of y by the
+ * rule of llama_q8_rows_quant (y itself is not rounded: the codes depend on h g alone, and
+ * the scale is rounded to f32 at the end; the sum of squares is kept in f32, in double where
+ * that would leave the range of f32). x_out may be x or delta (with the same stride); no
+ * other arrays overlap. A row whose h or h g is not finite has codes 0 and scale NaN; eps >=
+ * 0 and finite. Enqueues one kernel. */
+llama_q8_status llama_q8_norm_quant(int32_t type, const void* x, int64_t x_stride, const void* delta,
+                                    int64_t delta_stride, void* x_out, int64_t out_stride, const float* g, float eps,
+                                    int32_t rows, int32_t k, int8_t* codes, float* scale, void* stream);
+
+/* Codes and a scale for each row of silu(gate) * up, silu(z) = z / (1 + exp(-z)), by the
+ * rule of llama_q8_rows_quant. gate and up have the same row stride: columns 0 .. k - 1 and
+ * k .. 2k - 1 of one product, or two arrays. A row with a NaN or an infinity in gate or up
+ * has codes 0 and scale NaN. Enqueues one kernel. */
+llama_q8_status llama_q8_silu_quant(int32_t type, const void* gate, const void* up, int64_t stride, int32_t rows,
+                                    int32_t k, int8_t* codes, float* scale, void* stream);
+
+/* The layout that llama_q8_i8_matmul reads a weight matrix in: codes and scales of
+ * llama_q8_rows_quant (or int8 codes of any origin, -128 included) regrouped by tiles of 32
+ * rows. packed: llama_q8_i8_packed_bytes(rows, k) bytes (0 for sizes out of range), 16-byte
+ * aligned, caller-owned. rows <= 2^30. Enqueues one kernel. */
+size_t llama_q8_i8_packed_bytes(int64_t rows, int64_t k);
+llama_q8_status llama_q8_i8_pack(const int8_t* codes, const float* scale, int64_t rows, int64_t k, void* packed,
+                                 void* stream);
+
+/* y[t][n] = (sum_k codes[t][k] W[n][k]) * scale[t] * wscale[n] for t < m, n < rows, with W
+ * and wscale packed by llama_q8_i8_pack. The sum is exact; it is turned into f32 and
+ * multiplied by the token's and the channel's scale in f32, then rounded to `type`. y rows
+ * are y_stride >= rows elements apart; what lies between them is not written. m <= 2^30.
+ * workspace: llama_q8_i8_matmul_workspace_bytes(rows, k, m) bytes (may be 0; 0 also for sizes
+ * out of range), 16-byte aligned, zeroed before its first use; it can be used by calls of any
+ * sizes that it is large enough for, in turn, and by other operators' calls whose workspaces
+ * are kept the same way. Calls that share one (or graphs that captured such calls) must not
+ * overlap on the GPU. y overlaps nothing else. err (device int32, may be NULL, zeroed by the
+ * caller) receives LQ8_ERR_CUDA if a wait inside the kernel ran out, which leaves y
+ * undefined. */
+size_t llama_q8_i8_matmul_workspace_bytes(int64_t rows, int64_t k, int64_t m);
+llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, const int8_t* codes,
+                                   const float* scale, int64_t m, int32_t type, void* y, int64_t y_stride,
+                                   void* workspace, size_t workspace_bytes, int32_t* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

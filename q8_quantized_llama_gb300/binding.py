@@ -36,7 +36,9 @@ EXPORTS = ("llama_q8_load", "llama_q8_forward", "llama_q8_forward_argmax", "llam
            "llama_q8_rope_frequencies", "llama_q8_rope_append", "llama_q8_attention_paged_workspace_bytes",
            "llama_q8_attention_paged", "llama_q8_pages_fork_workspace_bytes", "llama_q8_pages_fork",
            "llama_q8_pages_compact_workspace_bytes", "llama_q8_pages_compact",
-           "llama_q8_beam_select_workspace_bytes", "llama_q8_beam_select")
+           "llama_q8_beam_select_workspace_bytes", "llama_q8_beam_select",
+           "llama_q8_i8_row_bytes", "llama_q8_rows_quant", "llama_q8_norm_quant", "llama_q8_silu_quant",
+           "llama_q8_i8_packed_bytes", "llama_q8_i8_pack", "llama_q8_i8_matmul_workspace_bytes", "llama_q8_i8_matmul")
 GGUF_Q5_0, GGUF_Q8_0, GGUF_Q4_K, GGUF_Q6_K = 6, 8, 12, 14
 GGUF_F32, GGUF_F16, GGUF_BF16 = 0, 1, 30
 
@@ -140,6 +142,14 @@ def lib() -> C.CDLL:
         "llama_q8_pages_compact": (i32, [vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp]),
         "llama_q8_beam_select_workspace_bytes": (sz, [i32, i32, i32, i32]),
         "llama_q8_beam_select": (i32, [vp, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
+        "llama_q8_i8_row_bytes": (i64, [i64]),
+        "llama_q8_rows_quant": (i32, [i32, vp, i64, i32, i32, vp, vp, vp]),
+        "llama_q8_norm_quant": (i32, [i32, vp, i64, vp, i64, vp, i64, vp, C.c_float, i32, i32, vp, vp, vp]),
+        "llama_q8_silu_quant": (i32, [i32, vp, vp, i64, i32, i32, vp, vp, vp]),
+        "llama_q8_i8_packed_bytes": (sz, [i64, i64]),
+        "llama_q8_i8_pack": (i32, [vp, vp, i64, i64, vp, vp]),
+        "llama_q8_i8_matmul_workspace_bytes": (sz, [i64, i64, i64]),
+        "llama_q8_i8_matmul": (i32, [vp, i64, i64, vp, vp, i64, i32, vp, i64, vp, sz, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -439,9 +449,10 @@ def _dev_rows(a, dtype: _Type, stride: int, rows: int, width: int) -> int | None
     return _dev(a, dtype, 0, False)
 
 
-_F32, _I32, _F64, _U8 = (_Type("torch." + t) for t in ("float32", "int32", "float64", "uint8"))
-_PAGE_TYPES = {t.name: (gguf, t) for t, gguf in ((_F32, GGUF_F32), (_Type("torch.float16"), GGUF_F16),
-                                                 (_Type("torch.bfloat16"), GGUF_BF16))}
+_F32, _I32, _F64, _U8, _I8, _F16, _BF16 = (_Type("torch." + t) for t in ("float32", "int32", "float64", "uint8",
+                                                                       "int8", "float16", "bfloat16"))
+_PAGE_TYPES = {t.name: (gguf, t) for t, gguf in ((_F32, GGUF_F32), (_F16, GGUF_F16), (_BF16, GGUF_BF16))}
+_GGUF_TYPES = {GGUF_F32: _F32, GGUF_F16: _F16, GGUF_BF16: _BF16}
 
 
 def make_pages(k, v) -> llama_q8_pages:
@@ -548,6 +559,73 @@ def llama_q8_beam_select(logits, logits_stride: int, groups: int, beams: int, n_
                                      _dev(out_parent, _I32, n), _dev(out_token, _I32, n),
                                      _dev(workspace, _U8), workspace_bytes, stream or None),
           "llama_q8_beam_select")
+
+
+# ---- products in 8-bit integers -----------------------------------------------------
+# Tensors are checked as above; `type` (GGUF_F32, GGUF_F16 or GGUF_BF16) names the
+# activations' element type, which the library refuses when it is none of these.
+
+def _row_bytes(k: int) -> int:
+    return (k + 15) // 16 * 16
+
+
+def _packed_bytes(rows: int, k: int) -> int:
+    """llama_q8_i8_packed_bytes of sizes in range, without the call: codes to a multiple of 256 bytes, then scales."""
+    tiles = (rows + 31) // 32
+    return (tiles * 32 * _row_bytes(k) + 255) // 256 * 256 + tiles * 128
+
+
+def llama_q8_i8_row_bytes(k: int) -> int:
+    return int(lib().llama_q8_i8_row_bytes(k))
+
+
+def llama_q8_rows_quant(type: int, x, x_stride: int, rows: int, k: int, codes, scale, stream=0) -> None:
+    if type == GGUF_Q8_0:
+        at = _dev_rows(x, _U8, x_stride // 32 * 34, rows, k // 32 * 34)
+    else:
+        at = _dev_rows(x, _GGUF_TYPES.get(type, _F32), x_stride, rows, k)
+    check(lib().llama_q8_rows_quant(type, at, x_stride, rows, k, _dev(codes, _I8, rows * _row_bytes(k)),
+                                    _dev(scale, _F32, rows), stream or None), "llama_q8_rows_quant")
+
+
+def llama_q8_norm_quant(type: int, x, x_stride: int, delta, delta_stride: int, x_out, out_stride: int, g, eps: float,
+                        rows: int, k: int, codes, scale, stream=0) -> None:
+    t = _GGUF_TYPES.get(type, _F32)
+    check(lib().llama_q8_norm_quant(type, _dev_rows(x, t, x_stride, rows, k), x_stride,
+                                    _dev_rows(delta, t, delta_stride, rows, k), delta_stride,
+                                    _dev_rows(x_out, t, out_stride, rows, k), out_stride, _dev(g, _F32, k), eps, rows,
+                                    k, _dev(codes, _I8, rows * _row_bytes(k)), _dev(scale, _F32, rows),
+                                    stream or None), "llama_q8_norm_quant")
+
+
+def llama_q8_silu_quant(type: int, gate, up, stride: int, rows: int, k: int, codes, scale, stream=0) -> None:
+    t = _GGUF_TYPES.get(type, _F32)
+    check(lib().llama_q8_silu_quant(type, _dev_rows(gate, t, stride, rows, k), _dev_rows(up, t, stride, rows, k),
+                                    stride, rows, k, _dev(codes, _I8, rows * _row_bytes(k)), _dev(scale, _F32, rows),
+                                    stream or None), "llama_q8_silu_quant")
+
+
+def llama_q8_i8_packed_bytes(rows: int, k: int) -> int:
+    return int(lib().llama_q8_i8_packed_bytes(rows, k))
+
+
+def llama_q8_i8_pack(codes, scale, rows: int, k: int, packed, stream=0) -> None:
+    check(lib().llama_q8_i8_pack(_dev(codes, _I8, rows * _row_bytes(k)), _dev(scale, _F32, rows), rows, k,
+                                 _dev(packed, _U8, _packed_bytes(rows, k)), stream or None),
+          "llama_q8_i8_pack")
+
+
+def llama_q8_i8_matmul_workspace_bytes(rows: int, k: int, m: int) -> int:
+    return int(lib().llama_q8_i8_matmul_workspace_bytes(rows, k, m))
+
+
+def llama_q8_i8_matmul(packed, rows: int, k: int, codes, scale, m: int, type: int, y, y_stride: int, workspace,
+                       workspace_bytes: int, err=None, stream=0) -> None:
+    check(lib().llama_q8_i8_matmul(_dev(packed, _U8, _packed_bytes(rows, k)), rows, k, _dev(codes, _I8, m * _row_bytes(k)),
+                                   _dev(scale, _F32, m), m, type,
+                                   _dev_rows(y, _GGUF_TYPES.get(type, _F32), y_stride, m, rows), y_stride,
+                                   _dev(workspace, _U8), workspace_bytes, _dev(err, _I32), stream or None),
+          "llama_q8_i8_matmul")
 
 
 def status_str(s: int) -> str:

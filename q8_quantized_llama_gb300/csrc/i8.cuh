@@ -1,0 +1,52 @@
+// The packed layout of an int8 weight matrix with a scale per output channel, and
+// the last step of its product.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+namespace lq8 {
+
+// Rows in tiles of 32 (padded with zero rows), k in chunks of 16 (padded with
+// zero codes): the 32 rows' 16-byte pieces of a chunk lie next to each other, so a
+// warp-wide 16-byte load (lane = row) reads 512 contiguous bytes and the chunks of
+// a tile are one contiguous run:
+//   byte offset(n, kk) = ((n / 32) * chunks + kk / 16) * 512 + (n % 32) * 16 + kk % 16
+// The f32 scales of all padded rows follow, 256-byte aligned.
+struct I8Weights {
+    const int8_t* codes;
+    const float* scale;
+    int64_t rows, rows_pad;
+    int64_t chunks;  // k / 16, rounded up
+};
+
+__host__ __device__ inline int64_t i8_codes_bytes(int64_t rows, int64_t k) {
+    return (rows + 31) / 32 * 32 * ((k + 15) / 16 * 16);
+}
+__host__ __device__ inline int64_t i8_scale_offset(int64_t rows, int64_t k) {
+    return (i8_codes_bytes(rows, k) + 255) / 256 * 256;
+}
+__host__ __device__ inline int64_t i8_packed_total(int64_t rows, int64_t k) {
+    return i8_scale_offset(rows, k) + (rows + 31) / 32 * 32 * 4;
+}
+inline I8Weights i8_view(const void* packed, int64_t rows, int64_t k) {
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(packed);
+    return {reinterpret_cast<const int8_t*>(base), reinterpret_cast<const float*>(base + i8_scale_offset(rows, k)),
+            rows, (rows + 31) / 32 * 32, (k + 15) / 16};
+}
+
+// An exact sum times the token's and the channel's scale, rounded to the output type.
+template <typename T> __device__ __forceinline__ T i8_scaled(int sum, float sa, float sw);
+template <> __device__ __forceinline__ float i8_scaled<float>(int sum, float sa, float sw) {
+    return (float)sum * sa * sw;
+}
+template <> __device__ __forceinline__ __half i8_scaled<__half>(int sum, float sa, float sw) {
+    return __float2half_rn((float)sum * sa * sw);
+}
+template <> __device__ __forceinline__ __nv_bfloat16 i8_scaled<__nv_bfloat16>(int sum, float sa, float sw) {
+    return __float2bfloat16_rn((float)sum * sa * sw);
+}
+
+}  // namespace lq8
