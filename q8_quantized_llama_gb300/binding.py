@@ -570,9 +570,9 @@ def _row_bytes(k: int) -> int:
 
 
 def _packed_bytes(rows: int, k: int) -> int:
-    """llama_q8_i8_packed_bytes of sizes in range, without the call: codes to a multiple of 256 bytes, then scales."""
+    """llama_q8_i8_packed_bytes of sizes in range, without the call: codes to a multiple of 256 bytes, then scales, norms."""
     tiles = (rows + 31) // 32
-    return (tiles * 32 * _row_bytes(k) + 255) // 256 * 256 + tiles * 128
+    return (tiles * 32 * _row_bytes(k) + 255) // 256 * 256 + tiles * 132
 
 
 def llama_q8_i8_row_bytes(k: int) -> int:

@@ -42,11 +42,9 @@
 // tile run at the same time and read it from DRAM once. At the end the
 // accumulators return the tile to tensor memory and all 16 converter and
 // accumulator warps apply the epilogue, 32 token columns each.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "epilogue.cuh"
 #include "ptx.cuh"
+#include "tc.cuh"
 
 namespace lq8 {
 
@@ -87,103 +85,8 @@ constexpr int kTmemA = 2 * kTcBN;
 constexpr int kTmemACols = 16;  // columns of one stage's A
 static_assert(kTmemA + kTcStagesMax * kTmemACols <= kTmemCols, "tensor memory columns");
 
-// ---- tcgen05 wrappers ---------------------------------------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t* holder, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor: K-major operand, 128-byte swizzle (16-byte
-// chunk c of row r stored at chunk c ^ (r % 8)), 8-row groups 1024 bytes
-// apart. A start address 32 or 64 bytes into the row selects the next 16
-// k-values or the lo half.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFF) >> 4);         // start address
-    d |= (uint64_t)(16 >> 4) << 16;                   // leading byte offset (unused for swizzled K-major)
-    d |= (uint64_t)(1024 >> 4) << 32;                 // stride byte offset
-    d |= (uint64_t)1 << 46;                           // descriptor version
-    d |= (uint64_t)2 << 61;                           // 128-byte swizzle
-    return d;
-}
-
 // Instruction descriptor: D f32, A and B f16, both K-major, M = 128, N = 128.
-constexpr uint32_t kIdescF16 = (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)(kTcBN >> 3) << 17) |
-                               ((uint32_t)(kTcBM >> 4) << 24);
-
-// D (tensor memory) += A (tensor memory, row i in lane i, k along columns) * B (shared memory)
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(kIdescF16), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 16 consecutive columns of this thread's lane (the warp's 32 lanes at taddr).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 3-D tensor copy global -> shared, completing on an mbarrier.
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// 2-D tensor copy global -> shared, completing on an mbarrier; coordinates in
-// elements (x innermost).
-__device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
-// Four codes (one word) as two f16 pairs, exactly: each byte u = q + 128
-// becomes the f16 1024 + u (exponent 10, u in the mantissa), minus 1152.
-__device__ __forceinline__ void codes_to_f16x2(uint32_t q, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = q ^ 0x80808080u;
-    const __half2 bias = __halves2half2(__ushort_as_half((unsigned short)0x6480u), __ushort_as_half((unsigned short)0x6480u));
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
-    const __half2 hb = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
-    lo = *reinterpret_cast<const uint32_t*>(&ha);
-    hi = *reinterpret_cast<const uint32_t*>(&hb);
-}
+constexpr uint32_t kIdescF16 = idesc_f16(kTcBM, kTcBN);
 
 // Epilogue of one output element pair/element (row r of W, token t).
 template <int EPI>
@@ -316,8 +219,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {  // two 16-wide k-steps, 32 bytes apart in the rows
                     const uint64_t b_hi = sw128_desc(xs + kStHiLo + kk * 32), b_lo = sw128_desc(xs + kStHiLo + 64 + kk * 32);
-                    mma_f16_ts(d, a + kk * 8, b_hi, kk != 0);
-                    mma_f16_ts(d, a + kk * 8, b_lo, 1u);
+                    mma_f16_ts(d, a + kk * 8, b_hi, kIdescF16, kk != 0);
+                    mma_f16_ts(d, a + kk * 8, b_lo, kIdescF16, 1u);
                 }
                 mma_commit(&done_bar[s]);
                 mma_commit(&part_full[p]);
@@ -573,23 +476,6 @@ static int gemm_tc_splits(int tiles, int nb) {
         }
     }
     return best;
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// dependency on the driver library).
-static PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
-
-static cudaError_t get_encode_tiled() {
-    if (!g_encode_tiled) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess || !fn)
-            return cudaErrorNotSupported;
-        g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
-    return cudaSuccess;
 }
 
 // Tensor map of the split activations hl[m][2k] (f16): boxes of one k-block

@@ -13,11 +13,29 @@ namespace lq8 {
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) i8_pack_kernel(const uint4* __restrict__ codes, const float* __restrict__ scale,
                                                       int64_t rows, int64_t chunks, uint4* __restrict__ out,
-                                                      float* __restrict__ out_scale) {
-    const int64_t tile = blockIdx.x, n = tile * 32 + (threadIdx.x & 31);
-    for (int64_t c = threadIdx.x >> 5; c < chunks; c += 8)
-        out[(tile * chunks + c) * 32 + (threadIdx.x & 31)] = n < rows ? codes[n * chunks + c] : make_uint4(0, 0, 0, 0);
-    if (threadIdx.x < 32) out_scale[n] = n < rows ? scale[n] : 0.0f;
+                                                      float* __restrict__ out_scale, float* __restrict__ out_norm) {
+    __shared__ uint32_t part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t tile = blockIdx.x, n = tile * 32 + lane;
+    int sum = 0;
+    for (int64_t c = warp; c < chunks; c += 8) {
+        const uint4 q = n < rows ? codes[n * chunks + c] : make_uint4(0, 0, 0, 0);
+        out[(tile * chunks + c) * 32 + lane] = q;
+        sum = __dp4a((int)q.x, (int)q.x, sum);
+        sum = __dp4a((int)q.y, (int)q.y, sum);
+        sum = __dp4a((int)q.z, (int)q.z, sum);
+        sum = __dp4a((int)q.w, (int)q.w, sum);
+    }
+    part[warp][lane] = (uint32_t)sum;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t all = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) all += part[w][lane];  // at most 131056 * 2^14 < 2^31
+        out_scale[n] = n < rows ? scale[n] : 0.0f;
+        const float norm = warp_max(__fsqrt_ru(__uint2float_ru(all)));
+        if (lane == 0) out_norm[tile] = norm;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -62,18 +80,15 @@ __global__ void __launch_bounds__(256) i8_rows_kernel(const I8Weights W, const i
 }
 
 template <typename T>
-static cudaError_t launch_i8_matmul(const I8Weights& W, const int8_t* a, const float* sa, int64_t m, T* y,
-                                    int64_t y_stride, cudaStream_t s) {
+static cudaError_t launch_i8_matmul(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
+                                    int64_t y_stride, void* workspace, int32_t* err, cudaStream_t s) {
+    if (m >= kI8GemmMin) {
+        const cudaError_t e = ensure_kernel_attributes();
+        return e != cudaSuccess ? e : launch_i8_gemm<T>(W, k, a, sa, m, y, y_stride, workspace, err, s);
+    }
     const unsigned tiles = (unsigned)(W.rows_pad / 32);
     auto go = [&](auto kernel, int mt) {
-        // the grid's second dimension holds 65535
-        for (int64_t t = 0; t < m; t += 65535ll * mt) {
-            const int64_t part = m - t < 65535ll * mt ? m - t : 65535ll * mt;
-            const cudaError_t e = launch_ex(kernel, dim3(tiles, (unsigned)((part + mt - 1) / mt)), dim3(256), 0, s, false,
-                                            W, a + t * W.chunks * 16, sa + t, part, y + t * y_stride, y_stride);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
+        return launch_ex(kernel, dim3(tiles, (unsigned)((m + mt - 1) / mt)), dim3(256), 0, s, false, W, a, sa, m, y, y_stride);
     };
     if (m == 1) return go(i8_rows_kernel<1, T>, 1);
     if (m == 2) return go(i8_rows_kernel<2, T>, 2);
@@ -105,13 +120,13 @@ llama_q8_status llama_q8_i8_pack(const int8_t* codes, const float* scale, int64_
     const cudaError_t e =
         launch_ex(i8_pack_kernel, dim3((unsigned)(w.rows_pad / 32)), dim3(256), 0, (cudaStream_t)stream, false,
                   reinterpret_cast<const uint4*>(codes), scale, rows, w.chunks,
-                  reinterpret_cast<uint4*>(const_cast<int8_t*>(w.codes)), const_cast<float*>(w.scale));
+                  reinterpret_cast<uint4*>(const_cast<int8_t*>(w.codes)), const_cast<float*>(w.scale),
+                  const_cast<float*>(w.norm));
     return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
 
 size_t llama_q8_i8_matmul_workspace_bytes(int64_t rows, int64_t k, int64_t m) {
-    (void)rows, (void)k, (void)m;
-    return 0;
+    return !i8_sizes_ok(rows, k) || m < kI8GemmMin || m > (1ll << 30) ? 0 : i8_gemm_workspace(rows, k, m);
 }
 
 llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, const int8_t* codes,
@@ -130,9 +145,9 @@ llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, 
     const I8Weights w = i8_view(packed, rows, k);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (type == LLAMA_Q8_GGUF_F32) e = launch_i8_matmul(w, codes, scale, m, (float*)y, y_stride, s);
-    else if (type == LLAMA_Q8_GGUF_F16) e = launch_i8_matmul(w, codes, scale, m, (__half*)y, y_stride, s);
-    else e = launch_i8_matmul(w, codes, scale, m, (__nv_bfloat16*)y, y_stride, s);
+    if (type == LLAMA_Q8_GGUF_F32) e = launch_i8_matmul(w, k, codes, scale, m, (float*)y, y_stride, workspace, err, s);
+    else if (type == LLAMA_Q8_GGUF_F16) e = launch_i8_matmul(w, k, codes, scale, m, (__half*)y, y_stride, workspace, err, s);
+    else e = launch_i8_matmul(w, k, codes, scale, m, (__nv_bfloat16*)y, y_stride, workspace, err, s);
     return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
 

@@ -112,10 +112,10 @@ def test_matmul_refuses_a_short_workspace(B, rows, k, m):
 
 def test_sizes(B):
     assert [B.llama_q8_i8_row_bytes(k) for k in (-1, 0, 1, 16, 17, 4096)] == [0, 0, 16, 16, 32, 4096]
-    assert B.llama_q8_i8_packed_bytes(32, 16) == 512 + 128
+    assert B.llama_q8_i8_packed_bytes(32, 16) == 512 + 132
     for rows, k in ((1, 1), (70, 70), (96, 4096), (28672, 4096), (100, 14336)):
         assert B._packed_bytes(rows, k) == B.llama_q8_i8_packed_bytes(rows, k)
-    assert B.llama_q8_i8_packed_bytes(33, 17) == 64 * 32 + 64 * 4
+    assert B.llama_q8_i8_packed_bytes(33, 17) == 64 * 32 + 66 * 4
     for rows, k in ((0, 16), (16, 0), (1 << 31, 16), (16, MAX_K + 1)):
         assert B.llama_q8_i8_packed_bytes(rows, k) == 0
         assert B.llama_q8_i8_matmul_workspace_bytes(rows, k, 64) == 0
@@ -137,7 +137,7 @@ def S(B, monkeypatch):
 def _tensors(**kw):
     f32 = lambda *s, **o: Tensor("float32", *s, **o)  # noqa: E731
     t = dict(x=f32(ROWS, WIDTH), delta=f32(ROWS, WIDTH), out=f32(ROWS, WIDTH), g=f32(K), codes=Tensor("int8", ROWS, 80),
-             scale=f32(ROWS), packed=Tensor("uint8", 8064), y=f32(ROWS, WIDTH), ws=Tensor("uint8", 64),
+             scale=f32(ROWS), packed=Tensor("uint8", 8076), y=f32(ROWS, WIDTH), ws=Tensor("uint8", 64),
              err=Tensor("int32", 1))
     t.update(kw)
     return t
@@ -172,9 +172,9 @@ BAD_X = [("x", Tensor("float16", ROWS, WIDTH)), ("x", Tensor("float32", ROWS * W
     ("norm", *b) for b in BAD_X + BAD_CODES] + [("silu", *b) for b in BAD_X + BAD_CODES] + [
     ("norm", "delta", Tensor("float32", ROWS, WIDTH - 10)), ("norm", "out", Tensor("bfloat16", ROWS, WIDTH)),
     ("norm", "g", Tensor("float32", K - 1)), ("silu", "delta", Tensor("float32", ROWS, WIDTH - 10)),
-    ("pack", "codes", Tensor("int8", ROWS, 79)), ("pack", "packed", Tensor("uint8", 2687)),
+    ("pack", "codes", Tensor("int8", ROWS, 79)), ("pack", "packed", Tensor("uint8", 2691)),
     ("matmul", "y", Tensor("float32", ROWS, WIDTH - 10)), ("matmul", "y", Tensor("float16", ROWS, WIDTH)),
-    ("matmul", "codes", Tensor("int8", ROWS, 79)), ("matmul", "packed", Tensor("uint8", 8063)),
+    ("matmul", "codes", Tensor("int8", ROWS, 79)), ("matmul", "packed", Tensor("uint8", 8075)),
     ("matmul", "scale", Tensor("float32", ROWS - 1)), ("matmul", "err", Tensor("float32", 1))])
 def test_binding_refuses(S, name, key, bad):
     with pytest.raises((TypeError, ValueError)):
