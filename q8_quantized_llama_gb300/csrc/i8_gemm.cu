@@ -85,6 +85,17 @@ struct I8Segments {
     __device__ int token0() const { return (int)(tile % g.token_tiles) * g.bn; }
 };
 
+// A position in a ring of buffers and the parity of its pass (no divisions: a quotient by a number that is not known
+// when compiling takes longer than a stage's products).
+struct I8Ring {
+    int n, at = 0;
+    uint32_t parity = 0;
+    __device__ explicit I8Ring(int count) : n(count) {}
+    __device__ __forceinline__ void next() {
+        if (++at == n) at = 0, parity ^= 1u;
+    }
+};
+
 // Whether no sum of the tile can pass 2^24 (one warp; the same answer in every warp).
 __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int token0, int lane) {
     float w = 0.0f, a = 0.0f;
@@ -152,72 +163,88 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         int ahead = 0;
         {
             I8Segments seg(g);
-            while (ahead < stages && seg.next())
-                for (int kb = seg.k0; kb < seg.k1 && ahead < stages; ++kb) issue_codes(seg.channel0(), kb, ahead++);
+            while (ahead < stages && seg.next()) {
+                const int channel0 = seg.channel0();
+                for (int kb = seg.k0; kb < seg.k1 && ahead < stages; ++kb) issue_codes(channel0, kb, ahead++);
+            }
         }
         pdl_wait();
         I8Segments seg(g);
-        int it = 0;
-        while (alive && seg.next())
-            for (int kb = seg.k0; kb < seg.k1; ++kb, ++it) {
-                const int s = it % stages;
-                if (it >= ahead) {
-                    if (lane == 0) alive = mbar_wait_bounded(&done_bar[s], ((it / stages) - 1) & 1, g.err, LQ8_ERR_CUDA);
+        I8Ring ring(stages);
+        bool again = false;  // past the first pass over the stages
+        while (alive && seg.next()) {
+            const int channel0 = seg.channel0(), token0 = seg.token0();
+            for (int kb = seg.k0; kb < seg.k1; ++kb) {
+                const int s = ring.at;
+                if (again) {
+                    if (lane == 0) alive = mbar_wait_bounded(&done_bar[s], ring.parity ^ 1u, g.err, LQ8_ERR_CUDA);
                     alive = __shfl_sync(0xffffffffu, alive, 0);
                     if (!alive) break;
-                    issue_codes(seg.channel0(), kb, s);
+                    issue_codes(channel0, kb, s);
                 }
-                issue_tokens(seg.token0(), kb, s);
+                issue_tokens(token0, kb, s);
+                ring.next();
+                again |= ring.at == 0;
             }
-        // every copy has landed before the CTA may exit (stages whose token tile was not asked for excepted)
+        }
+        // every copy has landed before the CTA may exit: the last of each stage
         if (lane == 0)
-            for (int i = it > stages ? it - stages : 0; i < it; ++i)
-                mbar_wait_bounded(&full_bar[i % stages], (i / stages) & 1, g.err, LQ8_ERR_CUDA);
+            for (int i = 0; i < stages; ++i) {
+                if (i >= ring.at && !again) break;
+                mbar_wait_bounded(&full_bar[i], i < ring.at ? ring.parity : ring.parity ^ 1u, g.err, LQ8_ERR_CUDA);
+            }
         __syncwarp();
     } else if (warp == kI8MmaWarp) {
         pdl_wait();
         const uint32_t idesc = idesc_f16(kI8BM, (uint32_t)g.bn);
         I8Segments seg(g);
-        int it = 0, sum = 0;  // stages and chunks so far
+        I8Ring ring(stages), sums(g.buffers);
+        bool again = false;  // past the first pass over the sum buffers
+        uint64_t* last = nullptr;
+        uint32_t last_parity = 0;
         while (alive && seg.next()) {
             const int n = seg.k1 - seg.k0;
             const bool one = n <= kI8Exact || i8_one_sum(g, seg.channel0(), seg.token0(), lane);
             if (lane == 0) {
-                for (int j = 0; j < n && alive; ++j, ++it) {
-                    const int s = it % stages, p = sum % g.buffers;
-                    const bool first = j == 0 || (!one && j % kI8Exact == 0);
-                    if (first && sum >= g.buffers)
-                        alive = mbar_wait_bounded(&sum_empty[p], ((sum / g.buffers) - 1) & 1, g.err, LQ8_ERR_CUDA);
-                    if (alive) alive = mbar_wait_bounded(&full_bar[s], (it / stages) & 1, g.err, LQ8_ERR_CUDA);
-                    if (alive) alive = mbar_wait_bounded(&conv_bar[s], (it / stages) & 1, g.err, LQ8_ERR_CUDA);
+                bool first = true;
+                for (int j = 0; j < n; ++j) {
+                    const int s = ring.at;
+                    if (first && again)
+                        alive = mbar_wait_bounded(&sum_empty[sums.at], sums.parity ^ 1u, g.err, LQ8_ERR_CUDA);
+                    // both: the token tile by tensor copy, A by the converters
+                    if (alive) alive = mbar_wait_bounded(&full_bar[s], ring.parity, g.err, LQ8_ERR_CUDA);
+                    if (alive) alive = mbar_wait_bounded(&conv_bar[s], ring.parity, g.err, LQ8_ERR_CUDA);
                     if (!alive) break;
                     tc_fence_after();
-                    const uint32_t b = smem_u32(smem + s * stage_bytes), a = tmem_a + (uint32_t)(s * kI8ACols);
+                    const uint64_t b = sw128_desc(smem_u32(smem + s * stage_bytes));
+                    const uint32_t a = tmem_a + (uint32_t)(s * kI8ACols), d = tmem + (uint32_t)(sums.at * g.bn);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_ts(tmem + (uint32_t)(p * g.bn), a + kk * 8, sw128_desc(b + kk * 32), idesc,
-                                   !(first && kk == 0));
+                    for (int kk = 0; kk < 4; ++kk)  // 16 k: 8 columns of A, 32 bytes of B's rows
+                        mma_f16_ts(d, a + kk * 8, b + kk * 2, idesc, !(first && kk == 0));
                     mma_commit(&done_bar[s]);
-                    if (j == n - 1 || (!one && j % kI8Exact == kI8Exact - 1)) {
-                        mma_commit(&sum_full[p]);
-                        ++sum;
+                    last = &done_bar[s], last_parity = ring.parity;
+                    ring.next();
+                    first = j == n - 1 || (!one && j % kI8Exact == kI8Exact - 1);
+                    if (first) {
+                        mma_commit(&sum_full[sums.at]);
+                        sums.next();
+                        again |= sums.at == 0;
                     }
                 }
             }
             alive = __shfl_sync(0xffffffffu, alive, 0);
         }
-        // products in flight read shared memory and write tensor memory: the last must be complete before the CTA exits
-        if (lane == 0 && it > 0)
-            mbar_wait_bounded(&done_bar[(it - 1) % stages], ((it - 1) / stages) & 1, g.err, LQ8_ERR_CUDA);
+        // products in flight read shared memory and write tensor memory: the last is complete before the CTA exits
+        if (lane == 0 && last) mbar_wait_bounded(last, last_parity, g.err, LQ8_ERR_CUDA);
         __syncwarp();
     } else if (warp < kI8ConvWarps) {
         const uint32_t base = tmem_a + ((uint32_t)(warp * 32) << 16);
         I8Segments seg(g);
-        int it = 0;
+        I8Ring ring(stages);
         while (alive && seg.next())
-            for (int kb = seg.k0; kb < seg.k1; ++kb, ++it) {
-                const int s = it % stages;
-                alive = mbar_wait_bounded(&full_bar[s], (it / stages) & 1, g.err, LQ8_ERR_CUDA);
+            for (int kb = seg.k0; kb < seg.k1; ++kb, ring.next()) {
+                const int s = ring.at;
+                alive = mbar_wait_bounded(&full_bar[s], ring.parity, g.err, LQ8_ERR_CUDA);
                 if (!__all_sync(0xffffffffu, alive)) {
                     alive = false;
                     break;
@@ -249,7 +276,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
         // a warp whose wait ran out still meets the others at their barriers
         I8Segments seg(g);
-        int sum = 0;
+        I8Ring sums(g.buffers);
         while (seg.next()) {
             const int n = seg.k1 - seg.k0, channel0 = seg.channel0(), token0 = seg.token0();
             const bool one = n <= kI8Exact || i8_one_sum(g, channel0, token0, lane);
@@ -265,9 +292,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 if (mine && t < g.m) y[(int64_t)t * g.y_stride + channel] = i8_scaled<T>(v, g.sa[t], sw);
             };
             const int chunks = one ? 1 : (n + kI8Exact - 1) / kI8Exact;
-            for (int ch = 0; ch < chunks; ++ch, ++sum) {
-                const int p = sum % g.buffers;
-                if (alive) alive = mbar_wait_bounded(&sum_full[p], (sum / g.buffers) & 1, g.err, LQ8_ERR_CUDA);
+            for (int ch = 0; ch < chunks; ++ch, sums.next()) {
+                const int p = sums.at;
+                if (alive) alive = mbar_wait_bounded(&sum_full[p], sums.parity, g.err, LQ8_ERR_CUDA);
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
                 tc_fence_after();
