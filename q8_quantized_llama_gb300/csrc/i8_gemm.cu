@@ -12,9 +12,9 @@
 // i8_widen_kernel turns the token rows into f16 once per call and notes their
 // norms. i8_gemm_kernel: CTA tile 128 channels (M) x bn tokens (N, a multiple of
 // 16 up to 256), 64 codes of k per stage, one CTA per SM, persistent. Warp roles:
-//  - producer: per stage the f16 token tile by one tensor copy (128-byte rows of 64
+//  - producer: per stage two tensor copies, the f16 token tile (128-byte rows of 64
 //    values, 128-byte swizzle: the K-major B operand, used in place) and the codes
-//    of the four 32-row tiles by bulk copies;
+//    of the four 32-row tiles;
 //  - 4 converter warps: row r's 64 codes as f16 into lane r of tensor memory (the A
 //    operand), one stage's columns next to the other's;
 //  - MMA warp: one thread issues four 128 x bn x 16 products per stage;
@@ -60,6 +60,32 @@ struct I8Gemm {
     int32_t* err;
 };
 
+__device__ __forceinline__ bool i8_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void i8_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void i8_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// a tensor copy of a box at (x, y), completing on the barrier
+__device__ __forceinline__ void i8_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
 // The segments of tiles that a CTA works on, the same for all its warps.
 struct I8Segments {
     const I8Gemm& g;
@@ -85,8 +111,10 @@ struct I8Segments {
     __device__ int token0() const { return (int)(tile % g.token_tiles) * g.bn; }
 };
 
-// A position in a ring of buffers and the parity of its pass (no divisions: a quotient by a number that is not known
-// when compiling takes longer than a stage's products).
+// A position in a ring of buffers and the parity of its pass. What a role does for each stage is a chain of
+// dependent instructions that one thread or warp issues alone, so it is kept short: positions are counted up (a
+// quotient by a number that is not known when compiling takes longer than a stage's products) and barriers are
+// addressed in shared memory.
 struct I8Ring {
     int n, at = 0;
     uint32_t parity = 0;
@@ -95,6 +123,20 @@ struct I8Ring {
         if (++at == n) at = 0, parity ^= 1u;
     }
 };
+
+// The bounded wait of mbar_wait_bounded with its timer out of the way.
+__device__ __noinline__ bool i8_wait_long(uint32_t bar, uint32_t parity, int32_t* err) {
+    const uint64_t t0 = global_timer_ns();
+    while (!i8_try(bar, parity))
+        if (global_timer_ns() - t0 > 1000000000ull) {
+            report(err, LQ8_ERR_CUDA);
+            return false;
+        }
+    return true;
+}
+__device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, int32_t* err) {
+    return i8_try(bar, parity) || i8_try(bar, parity) || i8_try(bar, parity) || i8_wait_long(bar, parity, err);
+}
 
 // Whether no sum of the tile can pass 2^24 (one warp; the same answer in every warp).
 __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int token0, int lane) {
@@ -108,7 +150,8 @@ __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int to
 
 template <typename T>
 __global__ void __launch_bounds__(kI8Threads, 1)
-    i8_gemm_kernel(const I8Gemm g, const __grid_constant__ CUtensorMap amap, T* __restrict__ y) {
+    i8_gemm_kernel(const I8Gemm g, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+                   T* __restrict__ y) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full_bar[kI8StagesMax];  // copies landed
@@ -120,7 +163,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __shared__ unsigned ticket;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int stages = g.stages, stage_bytes = g.bn * 128 + kI8CodeBytes;
+    const int stages = g.stages, token_bytes = g.bn * 128, stage_bytes = token_bytes + kI8CodeBytes;
     if (tid == 0) {
         for (int s = 0; s < kI8StagesMax; ++s) {
             mbar_init(&full_bar[s], 1);
@@ -138,104 +181,101 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_holder, tmem_a = tmem + (uint32_t)(g.buffers * g.bn);
+    const uint32_t data = smem_u32(smem), full = smem_u32(full_bar), conv = smem_u32(conv_bar), done = smem_u32(done_bar),
+                   sfull = smem_u32(sum_full), sempty = smem_u32(sum_empty);
     bool alive = true;  // cleared by a wait that ran out; the role then ends
 
     if (warp == kI8ProducerWarp) {
-        const int64_t tile_bytes = g.W.chunks * 512;
-        const int n_tiles = (int)(g.W.rows_pad / 32);
-        auto issue_codes = [&](int channel0, int kb, int s) {
-            // the stage's chunks (fewer in the last block) of the tiles there are; what is not copied is multiplied
-            // with zeros, or belongs to channels past the last
-            const int chunks = (int)(g.W.chunks - 4 * kb < 4 ? g.W.chunks - 4 * kb : 4);
-            const int valid = min(4, n_tiles - channel0 / 32);
-            if (lane == 0)
-                mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(g.bn * 128 + valid * chunks * 512));
-            __syncwarp();
-            if (lane < valid)
-                bulk_g2s(smem + s * stage_bytes + g.bn * 128 + lane * 2048,
-                         g.W.codes + (int64_t)(channel0 / 32 + lane) * tile_bytes + (int64_t)kb * 2048,
-                         (uint32_t)(chunks * 512), &full_bar[s]);
-        };
-        auto issue_tokens = [&](int token0, int kb, int s) {
-            if (lane == 0) tma_load_2d(smem + s * stage_bytes, &amap, kb * 64, token0, &full_bar[s]);
-        };
-        // the first stages' codes do not depend on the kernel before
-        int ahead = 0;
-        {
-            I8Segments seg(g);
-            while (ahead < stages && seg.next()) {
-                const int channel0 = seg.channel0();
-                for (int kb = seg.k0; kb < seg.k1 && ahead < stages; ++kb) issue_codes(channel0, kb, ahead++);
-            }
-        }
-        pdl_wait();
-        I8Segments seg(g);
-        I8Ring ring(stages);
-        bool again = false;  // past the first pass over the stages
-        while (alive && seg.next()) {
-            const int channel0 = seg.channel0(), token0 = seg.token0();
-            for (int kb = seg.k0; kb < seg.k1; ++kb) {
-                const int s = ring.at;
-                if (again) {
-                    if (lane == 0) alive = mbar_wait_bounded(&done_bar[s], ring.parity ^ 1u, g.err, LQ8_ERR_CUDA);
-                    alive = __shfl_sync(0xffffffffu, alive, 0);
-                    if (!alive) break;
-                    issue_codes(channel0, kb, s);
+        if (lane == 0) {
+            // boxes are whole: codes past the last chunk or tile and tokens past the last arrive as zeros
+            auto issue_codes = [&](int channel0, int kb, int s) {
+                const uint32_t bar = full + s * 8;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(stage_bytes)
+                             : "memory");
+                i8_box(data + s * stage_bytes + token_bytes, &wmap, kb * 256, channel0 / 32, bar);
+            };
+            auto issue_tokens = [&](int token0, int kb, int s) {
+                i8_box(data + s * stage_bytes, &amap, kb * 64, token0, full + s * 8);
+            };
+            // the first stages' codes do not depend on the kernel before
+            int ahead = 0;
+            {
+                I8Segments seg(g);
+                while (ahead < stages && seg.next()) {
+                    const int channel0 = seg.channel0();
+                    for (int kb = seg.k0; kb < seg.k1 && ahead < stages; ++kb) issue_codes(channel0, kb, ahead++);
                 }
-                issue_tokens(token0, kb, s);
-                ring.next();
-                again |= ring.at == 0;
             }
-        }
-        // every copy has landed before the CTA may exit: the last of each stage
-        if (lane == 0)
+            pdl_wait();
+            I8Segments seg(g);
+            I8Ring ring(stages);
+            bool again = false;  // past the first pass over the stages
+            while (alive && seg.next()) {
+                const int channel0 = seg.channel0(), token0 = seg.token0();
+                for (int kb = seg.k0; kb < seg.k1; ++kb) {
+                    const int s = ring.at;
+                    if (again) {
+                        alive = i8_wait(done + s * 8, ring.parity ^ 1u, g.err);
+                        if (!alive) break;
+                        issue_codes(channel0, kb, s);
+                    }
+                    issue_tokens(token0, kb, s);
+                    ring.next();
+                    again |= ring.at == 0;
+                }
+            }
+            // every copy has landed before the CTA may exit: the last of each stage
             for (int i = 0; i < stages; ++i) {
                 if (i >= ring.at && !again) break;
-                mbar_wait_bounded(&full_bar[i], i < ring.at ? ring.parity : ring.parity ^ 1u, g.err, LQ8_ERR_CUDA);
+                i8_wait(full + i * 8, i < ring.at ? ring.parity : ring.parity ^ 1u, g.err);
             }
+        }
         __syncwarp();
     } else if (warp == kI8MmaWarp) {
         pdl_wait();
         const uint32_t idesc = idesc_f16(kI8BM, (uint32_t)g.bn);
+        const uint64_t desc0 = sw128_desc(data);
         I8Segments seg(g);
         I8Ring ring(stages), sums(g.buffers);
         bool again = false;  // past the first pass over the sum buffers
-        uint64_t* last = nullptr;
-        uint32_t last_parity = 0;
+        uint32_t last = 0, last_parity = 0;
         while (alive && seg.next()) {
             const int n = seg.k1 - seg.k0;
             const bool one = n <= kI8Exact || i8_one_sum(g, seg.channel0(), seg.token0(), lane);
             if (lane == 0) {
-                bool first = true;
-                for (int j = 0; j < n; ++j) {
-                    const int s = ring.at;
-                    if (first && again)
-                        alive = mbar_wait_bounded(&sum_empty[sums.at], sums.parity ^ 1u, g.err, LQ8_ERR_CUDA);
-                    // both: the token tile by tensor copy, A by the converters
-                    if (alive) alive = mbar_wait_bounded(&full_bar[s], ring.parity, g.err, LQ8_ERR_CUDA);
-                    if (alive) alive = mbar_wait_bounded(&conv_bar[s], ring.parity, g.err, LQ8_ERR_CUDA);
-                    if (!alive) break;
-                    tc_fence_after();
-                    const uint64_t b = sw128_desc(smem_u32(smem + s * stage_bytes));
-                    const uint32_t a = tmem_a + (uint32_t)(s * kI8ACols), d = tmem + (uint32_t)(sums.at * g.bn);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // 16 k: 8 columns of A, 32 bytes of B's rows
-                        mma_f16_ts(d, a + kk * 8, b + kk * 2, idesc, !(first && kk == 0));
-                    mma_commit(&done_bar[s]);
-                    last = &done_bar[s], last_parity = ring.parity;
-                    ring.next();
-                    first = j == n - 1 || (!one && j % kI8Exact == kI8Exact - 1);
-                    if (first) {
-                        mma_commit(&sum_full[sums.at]);
-                        sums.next();
-                        again |= sums.at == 0;
+                for (int left = n; left > 0 && alive;) {
+                    int blocks = one ? left : min(left, kI8Exact);
+                    left -= blocks;
+                    if (again) alive = i8_wait(sempty + sums.at * 8, sums.parity ^ 1u, g.err);
+                    const uint32_t d = tmem + (uint32_t)(sums.at * g.bn);
+                    uint32_t accumulate = 0;
+                    for (; blocks > 0 && alive; --blocks) {
+                        const int s = ring.at;
+                        // the converters arrive after the stage's copies: the token tile has landed too
+                        alive = i8_wait(conv + s * 8, ring.parity, g.err);
+                        if (!alive) break;
+                        tc_fence_after();
+                        const uint64_t b = desc0 + (uint32_t)(s * stage_bytes >> 4);
+                        const uint32_t a = tmem_a + (uint32_t)(s * kI8ACols);
+                        mma_f16_ts(d, a, b, idesc, accumulate);  // 16 k: 8 columns of A, 32 bytes of B's rows
+                        mma_f16_ts(d, a + 8, b + 2, idesc, 1u);
+                        mma_f16_ts(d, a + 16, b + 4, idesc, 1u);
+                        mma_f16_ts(d, a + 24, b + 6, idesc, 1u);
+                        i8_commit(done + s * 8);
+                        accumulate = 1u;
+                        last = done + s * 8, last_parity = ring.parity;
+                        ring.next();
                     }
+                    if (!alive) break;
+                    i8_commit(sfull + sums.at * 8);
+                    sums.next();
+                    again |= sums.at == 0;
                 }
             }
             alive = __shfl_sync(0xffffffffu, alive, 0);
         }
         // products in flight read shared memory and write tensor memory: the last is complete before the CTA exits
-        if (lane == 0 && last) mbar_wait_bounded(last, last_parity, g.err, LQ8_ERR_CUDA);
+        if (lane == 0 && last) i8_wait(last, last_parity, g.err);
         __syncwarp();
     } else if (warp < kI8ConvWarps) {
         const uint32_t base = tmem_a + ((uint32_t)(warp * 32) << 16);
@@ -244,13 +284,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         while (alive && seg.next())
             for (int kb = seg.k0; kb < seg.k1; ++kb, ring.next()) {
                 const int s = ring.at;
-                alive = mbar_wait_bounded(&full_bar[s], ring.parity, g.err, LQ8_ERR_CUDA);
+                alive = i8_wait(full + s * 8, ring.parity, g.err);
                 if (!__all_sync(0xffffffffu, alive)) {
                     alive = false;
                     break;
                 }
                 tc_fence_after();
-                const uint4* q = reinterpret_cast<const uint4*>(smem + s * stage_bytes + g.bn * 128 + warp * 2048) + lane;
+                const uint4* q = reinterpret_cast<const uint4*>(smem + s * stage_bytes + token_bytes + warp * 2048) + lane;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t u[16];
@@ -267,7 +307,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&conv_bar[s]);
+                if (lane == 0) i8_arrive(conv + s * 8);
             }
     } else {
         pdl_wait();
@@ -294,7 +334,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             const int chunks = one ? 1 : (n + kI8Exact - 1) / kI8Exact;
             for (int ch = 0; ch < chunks; ++ch, sums.next()) {
                 const int p = sums.at;
-                if (alive) alive = mbar_wait_bounded(&sum_full[p], sums.parity, g.err, LQ8_ERR_CUDA);
+                if (alive) alive = i8_wait(sfull + p * 8, sums.parity, g.err);
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
                 tc_fence_after();
@@ -320,7 +360,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sum_empty[p]);
+                if (lane == 0) i8_arrive(sempty + p * 8);
             }
             if (!whole) {
                 // the part is in the workspace; the CTA that brings the tile's last one adds them all
@@ -450,6 +490,17 @@ cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const
     cudaError_t e = get_encode_tiled();
     if (e != cudaSuccess) return e;
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    // the packed codes as rows of 8-byte words, a row per 32-row tile: boxes of 4 tiles x 64 k (2 KB of a row)
+    CUtensorMap wmap;
+    {
+        const cuuint64_t dims[2] = {(cuuint64_t)W.chunks * 64, (cuuint64_t)W.rows_pad / 32};
+        const cuuint64_t strides[1] = {(cuuint64_t)W.chunks * 512};
+        const cuuint32_t box[2] = {256, 4}, elem[2] = {1, 1};
+        if (g_encode_tiled(&wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<int8_t*>(W.codes), dims, strides, box, elem,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     const int64_t k16 = W.chunks * 16;
     for (int64_t t = 0; t < m; t += full.tokens) {
         const int64_t part = m - t < full.tokens ? m - t : full.tokens;
@@ -475,7 +526,7 @@ cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const
         g.counters = reinterpret_cast<unsigned*>(ws), g.cut = p.cut, g.err = err;
         const int64_t units = p.tiles * p.kb;
         const int64_t ctas = p.cut ? (units < kI8Ctas ? units : kI8Ctas) : (p.tiles < kI8Ctas ? p.tiles : kI8Ctas);
-        e = launch_ex(i8_gemm_kernel<T>, dim3((unsigned)ctas), dim3(kI8Threads), (size_t)kI8Smem + 1024, s, true, g, map,
+        e = launch_ex(i8_gemm_kernel<T>, dim3((unsigned)ctas), dim3(kI8Threads), (size_t)kI8Smem + 1024, s, true, g, map, wmap,
                       y + t * y_stride);
         if (e != cudaSuccess) return e;
     }
