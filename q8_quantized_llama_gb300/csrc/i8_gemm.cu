@@ -71,6 +71,17 @@ __device__ __forceinline__ bool i8_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// One thread of the warp, the same at every call (the single-thread instructions of the tensor cores take uniform
+// operands: behind a comparison with the lane's number each of them took 65 cycles to issue).
+__device__ __forceinline__ bool i8_elect() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void i8_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -242,40 +253,38 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         while (alive && seg.next()) {
             const int n = seg.k1 - seg.k0;
             const bool one = n <= kI8Exact || i8_one_sum(g, seg.channel0(), seg.token0(), lane);
-            if (lane == 0) {
-                for (int left = n; left > 0 && alive;) {
-                    int blocks = one ? left : min(left, kI8Exact);
-                    left -= blocks;
-                    if (again) alive = i8_wait(sempty + sums.at * 8, sums.parity ^ 1u, g.err);
-                    const uint32_t d = tmem + (uint32_t)(sums.at * g.bn);
-                    uint32_t accumulate = 0;
-                    for (; blocks > 0 && alive; --blocks) {
-                        const int s = ring.at;
-                        // the converters arrive after the stage's copies: the token tile has landed too
-                        alive = i8_wait(conv + s * 8, ring.parity, g.err);
-                        if (!alive) break;
-                        tc_fence_after();
-                        const uint64_t b = desc0 + (uint32_t)(s * stage_bytes >> 4);
-                        const uint32_t a = tmem_a + (uint32_t)(s * kI8ACols);
+            for (int left = n; left > 0 && alive;) {
+                int blocks = one ? left : min(left, kI8Exact);
+                left -= blocks;
+                if (again) alive = __all_sync(0xffffffffu, i8_wait(sempty + sums.at * 8, sums.parity ^ 1u, g.err));
+                const uint32_t d = tmem + (uint32_t)(sums.at * g.bn);
+                uint32_t accumulate = 0;
+                for (; blocks > 0 && alive; --blocks) {
+                    const int s = ring.at;
+                    // the converters arrive after the stage's copies: the token tile has landed too
+                    alive = __all_sync(0xffffffffu, i8_wait(conv + s * 8, ring.parity, g.err));
+                    if (!alive) break;
+                    tc_fence_after();
+                    const uint64_t b = desc0 + (uint32_t)(s * stage_bytes >> 4);
+                    const uint32_t a = tmem_a + (uint32_t)(s * kI8ACols);
+                    if (i8_elect()) {
                         mma_f16_ts(d, a, b, idesc, accumulate);  // 16 k: 8 columns of A, 32 bytes of B's rows
                         mma_f16_ts(d, a + 8, b + 2, idesc, 1u);
                         mma_f16_ts(d, a + 16, b + 4, idesc, 1u);
                         mma_f16_ts(d, a + 24, b + 6, idesc, 1u);
                         i8_commit(done + s * 8);
-                        accumulate = 1u;
-                        last = done + s * 8, last_parity = ring.parity;
-                        ring.next();
+                        if (blocks == 1) i8_commit(sfull + sums.at * 8);
                     }
-                    if (!alive) break;
-                    i8_commit(sfull + sums.at * 8);
-                    sums.next();
-                    again |= sums.at == 0;
+                    accumulate = 1u;
+                    last = done + s * 8, last_parity = ring.parity;
+                    ring.next();
                 }
+                sums.next();
+                again |= sums.at == 0;
             }
-            alive = __shfl_sync(0xffffffffu, alive, 0);
         }
         // products in flight read shared memory and write tensor memory: the last is complete before the CTA exits
-        if (lane == 0 && last) i8_wait(last, last_parity, g.err);
+        if (last) i8_wait(last, last_parity, g.err);
         __syncwarp();
     } else if (warp < kI8ConvWarps) {
         const uint32_t base = tmem_a + ((uint32_t)(warp * 32) << 16);
