@@ -11,21 +11,25 @@
 //
 // i8_widen_kernel turns the token rows into f16 once per call and notes their
 // norms. i8_gemm_kernel: CTA tile 128 channels (M) x bn tokens (N, a multiple of
-// 16 up to 256), 64 codes of k per stage, one CTA per SM, persistent. Warp roles:
-//  - producer: per stage two tensor copies, the f16 token tile (128-byte rows of 64
-//    values, 128-byte swizzle: the K-major B operand, used in place) and the codes
-//    of the four 32-row tiles;
-//  - 4 converter warps: row r's 64 codes as f16 into lane r of tensor memory (the A
-//    operand), one stage's columns next to the other's;
-//  - MMA warp: one thread issues four 128 x bn x 16 products per stage;
+// 16 up to 256), one CTA per SM, persistent; a stage holds KS blocks of 64 codes of
+// k (two up to 128 tokens, where the products are shorter than what surrounds
+// them). Warp roles:
+//  - two producers: the f16 token tile (128-byte rows of 64 values, 128-byte swizzle:
+//    the K-major B operand, used in place) and the codes of the four 32-row tiles,
+//    each by one tensor copy per block;
+//  - two groups of 4 converter warps, one for the even and one for the odd stages: row
+//    r's codes as f16 into lane r of tensor memory (the A operand), one stage's columns
+//    next to the other's;
+//  - MMA warp: one thread issues four 128 x bn x 16 products per block;
 //  - 8 accumulator warps read the finished sums (every second group of 16 columns
 //    each), apply the scales and store: a warp's 32 lanes hold 32 neighbouring
 //    channels of a token, 128 bytes of y.
 //
 // Work is dealt in whole tiles (tokens fastest, so that the CTAs that share a weight
-// tile run together), or, where whole tiles would leave SMs idle, in equal runs of
-// k-blocks: tiles that are cut meet as integers in the workspace, where the last CTA
-// to finish its part adds them (integers: in any order the same).
+// tile run together). The tiles that do not fill a wave are cut into equal runs of
+// k-blocks, one per CTA, where that is shorter: their parts are added to sums in the
+// workspace (integers: in any order the same), and the CTA that brings the last part
+// of a tile stores it.
 #include "i8.cuh"
 #include "kernels.cuh"
 #include "llama_q8.h"
@@ -36,15 +40,15 @@ namespace lq8 {
 
 constexpr int kI8BM = 128;
 constexpr int kI8Ctas = 152;       // SMs of a GB300; the plan does not depend on the device at hand
-constexpr int kI8ConvWarps = 4, kI8AccWarps = 8;
-constexpr int kI8AccWarp0 = kI8ConvWarps, kI8ProducerWarp = kI8ConvWarps + kI8AccWarps, kI8MmaWarp = kI8ProducerWarp + 1;
+constexpr int kI8ConvWarps = 8, kI8AccWarps = 8;
+constexpr int kI8AccWarp0 = kI8ConvWarps, kI8TokenWarp = kI8AccWarp0 + kI8AccWarps, kI8CodeWarp = kI8TokenWarp + 1,
+              kI8MmaWarp = kI8CodeWarp + 1;
 constexpr int kI8Threads = (kI8MmaWarp + 1) * 32;
 constexpr int kI8StagesMax = 8;
-constexpr int kI8CodeBytes = kI8BM * 64;  // a stage's codes
+constexpr int kI8CodeBytes = kI8BM * 64;  // a block's codes
 constexpr int kI8Smem = 220 * 1024;       // stages, in units of what a tile's width needs
-constexpr int kI8Exact = 16;              // k-blocks whose products cannot pass 2^24
-constexpr int kI8ACols = 32;              // tensor-memory columns of a stage's A
-constexpr int kI8Slots = 3;               // parts a CTA can hold: the tile it begins in, the one it ends in, one between
+constexpr int kI8Exact = 16;              // blocks whose products cannot pass 2^24
+constexpr int kI8ACols = 32;              // tensor-memory columns of a block's A
 
 struct I8Gemm {
     I8Weights W;
@@ -52,11 +56,12 @@ struct I8Gemm {
     const float* sa;
     int m, bn, token_tiles, kb;
     int stages, buffers;
-    int64_t tiles;
+    int64_t tiles, cut0;  // tiles from cut0 on are cut into runs for the first `cutters` CTAs
+    int cutters;
     int64_t y_stride;
-    int32_t* slots;      // [CTA][kI8Slots][bn][128]
-    unsigned* counters;  // per CTA: parts of the tile it ends in
-    bool cut;            // equal runs of k-blocks instead of whole tiles
+    int32_t* sums;       // of the cut tiles, [tile][bn][128], zero at the start
+    int32_t* spare;      // [CTA][bn][128]: sums so far of a whole tile that is read out more than once
+    unsigned* counters;  // per cut tile: blocks that have arrived
     int32_t* err;
 };
 
@@ -82,6 +87,21 @@ __device__ __forceinline__ bool i8_elect() {
         : "=r"(one));
     return one != 0;
 }
+// whether the phase is complete now
+__device__ __forceinline__ bool i8_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void i8_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void i8_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -97,25 +117,27 @@ __device__ __forceinline__ void i8_box(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
-// The segments of tiles that a CTA works on, the same for all its warps.
+// The segments of tiles that a CTA works on, the same for all its warps: its run of the cut tiles, then whole tiles.
 struct I8Segments {
     const I8Gemm& g;
-    int64_t at, end, tile;
+    int64_t at, end, whole, tile;
     int k0, k1;
-    __device__ I8Segments(const I8Gemm& args) : g(args) {
-        const int64_t units = g.tiles * g.kb, c = blockIdx.x, n = gridDim.x;
-        at = g.cut ? units * c / n : c, end = g.cut ? units * (c + 1) / n : g.tiles;
+    __device__ I8Segments(const I8Gemm& args) : g(args), at(0), end(0), whole(blockIdx.x) {
+        const int64_t units = (g.tiles - g.cut0) * g.kb;
+        if ((int)blockIdx.x < g.cutters)
+            at = units * blockIdx.x / g.cutters, end = units * (blockIdx.x + 1) / g.cutters;
     }
     __device__ bool next() {
-        if (at >= end) return false;
-        if (g.cut) {
+        if (at < end) {
             tile = at / g.kb, k0 = (int)(at % g.kb);
             k1 = (int)(end - at < g.kb - k0 ? k0 + (end - at) : g.kb);
             at += k1 - k0;
-        } else {
-            tile = at, k0 = 0, k1 = g.kb;
-            at += gridDim.x;
+            tile += g.cut0;
+            return true;
         }
+        if (whole >= g.cut0) return false;
+        tile = whole, k0 = 0, k1 = g.kb;
+        whole += gridDim.x;
         return true;
     }
     __device__ int channel0() const { return (int)(tile / g.token_tiles) * kI8BM; }
@@ -159,7 +181,7 @@ __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int to
     return warp_max(w) * warp_max(a) <= 16777216.0f;
 }
 
-template <typename T>
+template <typename T, int KS>
 __global__ void __launch_bounds__(kI8Threads, 1)
     i8_gemm_kernel(const I8Gemm g, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                    T* __restrict__ y) {
@@ -171,14 +193,15 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __shared__ __align__(8) uint64_t sum_full[2];             // a chunk's sums complete
     __shared__ __align__(8) uint64_t sum_empty[2];            // and read
     __shared__ uint32_t tmem_holder;
-    __shared__ unsigned ticket;
+    __shared__ unsigned arrived;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int stages = g.stages, token_bytes = g.bn * 128, stage_bytes = token_bytes + kI8CodeBytes;
+    // a stage: KS token tiles, then KS blocks of codes
+    const int stages = g.stages, token_bytes = g.bn * 128, stage_bytes = KS * (token_bytes + kI8CodeBytes);
     if (tid == 0) {
         for (int s = 0; s < kI8StagesMax; ++s) {
-            mbar_init(&full_bar[s], 1);
-            mbar_init(&conv_bar[s], kI8ConvWarps);
+            mbar_init(&full_bar[s], 2);
+            mbar_init(&conv_bar[s], 4);
             mbar_init(&done_bar[s], 1);
         }
         for (int p = 0; p < 2; ++p) {
@@ -196,50 +219,40 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                    sfull = smem_u32(sum_full), sempty = smem_u32(sum_empty);
     bool alive = true;  // cleared by a wait that ran out; the role then ends
 
-    if (warp == kI8ProducerWarp) {
-        if (lane == 0) {
-            // boxes are whole: codes past the last chunk or tile and tokens past the last arrive as zeros
-            auto issue_codes = [&](int channel0, int kb, int s) {
-                const uint32_t bar = full + s * 8;
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(stage_bytes)
-                             : "memory");
-                i8_box(data + s * stage_bytes + token_bytes, &wmap, kb * 256, channel0 / 32, bar);
-            };
-            auto issue_tokens = [&](int token0, int kb, int s) {
-                i8_box(data + s * stage_bytes, &amap, kb * 64, token0, full + s * 8);
-            };
-            // the first stages' codes do not depend on the kernel before
-            int ahead = 0;
-            {
-                I8Segments seg(g);
-                while (ahead < stages && seg.next()) {
-                    const int channel0 = seg.channel0();
-                    for (int kb = seg.k0; kb < seg.k1 && ahead < stages; ++kb) issue_codes(channel0, kb, ahead++);
+    if (warp == kI8TokenWarp || warp == kI8CodeWarp) {
+        // boxes are whole: codes past the last chunk or tile and tokens past the last arrive as zeros
+        const bool codes = warp == kI8CodeWarp;
+        const CUtensorMap* map = codes ? &wmap : &amap;
+        const uint32_t to = data + (codes ? KS * token_bytes : 0), size = codes ? kI8CodeBytes : token_bytes;
+        const int step = codes ? 256 : 64;  // a block in the map's elements
+        if (!codes) pdl_wait();  // the codes do not depend on the kernel before
+        I8Segments seg(g);
+        I8Ring ring(stages);
+        bool again = false;  // past the first pass over the stages
+        while (alive && seg.next()) {
+            const int row = codes ? seg.channel0() / 32 : seg.token0();
+            for (int kb = seg.k0; kb < seg.k1; kb += KS) {
+                const int s = ring.at;
+                if (again) {
+                    alive = __all_sync(0xffffffffu, i8_wait(done + s * 8, ring.parity ^ 1u, g.err));
+                    if (!alive) break;
                 }
-            }
-            pdl_wait();
-            I8Segments seg(g);
-            I8Ring ring(stages);
-            bool again = false;  // past the first pass over the stages
-            while (alive && seg.next()) {
-                const int channel0 = seg.channel0(), token0 = seg.token0();
-                for (int kb = seg.k0; kb < seg.k1; ++kb) {
-                    const int s = ring.at;
-                    if (again) {
-                        alive = i8_wait(done + s * 8, ring.parity ^ 1u, g.err);
-                        if (!alive) break;
-                        issue_codes(channel0, kb, s);
-                    }
-                    issue_tokens(token0, kb, s);
-                    ring.next();
-                    again |= ring.at == 0;
+                if (i8_elect()) {
+                    const uint32_t bar = full + s * 8, at = to + s * stage_bytes;
+                    const bool two = KS == 2 && kb + 1 < seg.k1;
+                    i8_expect(bar, two ? 2 * size : size);
+                    i8_box(at, map, kb * step, row, bar);
+                    if (two) i8_box(at + size, map, (kb + 1) * step, row, bar);
                 }
+                ring.next();
+                again |= ring.at == 0;
             }
-            // every copy has landed before the CTA may exit: the last of each stage
-            for (int i = 0; i < stages; ++i) {
-                if (i >= ring.at && !again) break;
-                i8_wait(full + i * 8, i < ring.at ? ring.parity : ring.parity ^ 1u, g.err);
-            }
+        }
+        // every copy has landed before the CTA may exit: the last of each stage
+        if (codes) pdl_wait();
+        for (int i = 0; i < stages; ++i) {
+            if (i >= ring.at && !again) break;
+            i8_wait(full + i * 8, i < ring.at ? ring.parity : ring.parity ^ 1u, g.err);
         }
         __syncwarp();
     } else if (warp == kI8MmaWarp) {
@@ -259,21 +272,28 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 if (again) alive = __all_sync(0xffffffffu, i8_wait(sempty + sums.at * 8, sums.parity ^ 1u, g.err));
                 const uint32_t d = tmem + (uint32_t)(sums.at * g.bn);
                 uint32_t accumulate = 0;
-                for (; blocks > 0 && alive; --blocks) {
+                for (; blocks > 0 && alive; blocks -= KS) {
                     const int s = ring.at;
                     // the converters arrive after the stage's copies: the token tile has landed too
                     alive = __all_sync(0xffffffffu, i8_wait(conv + s * 8, ring.parity, g.err));
                     if (!alive) break;
                     tc_fence_after();
                     const uint64_t b = desc0 + (uint32_t)(s * stage_bytes >> 4);
-                    const uint32_t a = tmem_a + (uint32_t)(s * kI8ACols);
+                    const uint32_t a = tmem_a + (uint32_t)(s * KS * kI8ACols);
                     if (i8_elect()) {
                         mma_f16_ts(d, a, b, idesc, accumulate);  // 16 k: 8 columns of A, 32 bytes of B's rows
                         mma_f16_ts(d, a + 8, b + 2, idesc, 1u);
                         mma_f16_ts(d, a + 16, b + 4, idesc, 1u);
                         mma_f16_ts(d, a + 24, b + 6, idesc, 1u);
+                        if (KS == 2 && blocks > 1) {
+                            const uint64_t b1 = b + (uint32_t)(token_bytes >> 4);
+                            mma_f16_ts(d, a + 32, b1, idesc, 1u);
+                            mma_f16_ts(d, a + 40, b1 + 2, idesc, 1u);
+                            mma_f16_ts(d, a + 48, b1 + 4, idesc, 1u);
+                            mma_f16_ts(d, a + 56, b1 + 6, idesc, 1u);
+                        }
                         i8_commit(done + s * 8);
-                        if (blocks == 1) i8_commit(sfull + sums.at * 8);
+                        if (blocks <= KS) i8_commit(sfull + sums.at * 8);
                     }
                     accumulate = 1u;
                     last = done + s * 8, last_parity = ring.parity;
@@ -287,31 +307,35 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         if (last) i8_wait(last, last_parity, g.err);
         __syncwarp();
     } else if (warp < kI8ConvWarps) {
-        const uint32_t base = tmem_a + ((uint32_t)(warp * 32) << 16);
+        // a stage is always converted by the same group, so that a wait never meets a barrier two phases behind
+        const int quarter = warp & 3, group = warp >> 2;
+        const uint32_t base = tmem_a + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t from = data + KS * token_bytes + quarter * 2048 + lane * 16;
         I8Segments seg(g);
         I8Ring ring(stages);
         while (alive && seg.next())
-            for (int kb = seg.k0; kb < seg.k1; ++kb, ring.next()) {
+            for (int n = seg.k1 - seg.k0; n > 0; n -= KS, ring.next()) {
                 const int s = ring.at;
-                alive = i8_wait(full + s * 8, ring.parity, g.err);
-                if (!__all_sync(0xffffffffu, alive)) {
-                    alive = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint4* q = reinterpret_cast<const uint4*>(smem + s * stage_bytes + token_bytes + warp * 2048) + lane;
+                if ((s & 1) != group) continue;
+                alive = __all_sync(0xffffffffu, i8_wait(full + s * 8, ring.parity, g.err));
+                if (!alive) break;
+                tc_fence_after();  // the products that read the stage's columns before are complete: its copies followed them
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2 * KS; ++h) {
+                    if (KS == 2 && h == 2 && n == 1) break;
                     uint32_t u[16];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const uint4 v = q[(2 * h + c) * 32];
-                        codes_to_f16x2(v.x, u[8 * c + 0], u[8 * c + 1]);
-                        codes_to_f16x2(v.y, u[8 * c + 2], u[8 * c + 3]);
-                        codes_to_f16x2(v.z, u[8 * c + 4], u[8 * c + 5]);
-                        codes_to_f16x2(v.w, u[8 * c + 6], u[8 * c + 7]);
+                        uint4 q;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                     : "r"(from + s * stage_bytes + (h >> 1) * kI8CodeBytes + (h & 1) * 1024 + c * 512));
+                        codes_to_f16x2(q.x, u[8 * c + 0], u[8 * c + 1]);
+                        codes_to_f16x2(q.y, u[8 * c + 2], u[8 * c + 3]);
+                        codes_to_f16x2(q.z, u[8 * c + 4], u[8 * c + 5]);
+                        codes_to_f16x2(q.w, u[8 * c + 6], u[8 * c + 7]);
                     }
-                    tmem_st16(base + (uint32_t)(s * kI8ACols + h * 16), u);
+                    tmem_st16(base + (uint32_t)(s * KS * kI8ACols + h * 16), u);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -320,8 +344,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
     } else {
         pdl_wait();
-        const int aw = warp - kI8AccWarp0, quarter = warp & 3, half = aw >> 2;
-        const int groups = g.bn / 16;
+        const int quarter = warp & 3, half = (warp - kI8AccWarp0) >> 2, groups = g.bn / 16;
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
         // a warp whose wait ran out still meets the others at their barriers
         I8Segments seg(g);
@@ -333,13 +356,24 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             const int channel = channel0 + quarter * 32 + lane;
             const bool mine = channel < g.W.rows;
             const float sw = mine ? g.W.scale[channel] : 0.0f;
-            // parts: 0 the tile the CTA begins in, 1 the one it ends in, 2 a whole tile in more than one chunk
-            int32_t* slot = g.slots + ((int64_t)blockIdx.x * kI8Slots + (whole ? 2 : seg.k0 > 0 ? 0 : 1)) * g.bn * kI8BM +
-                            quarter * 32 + lane;
-            auto store = [&](int c, auto v) {  // an exact sum, as an integer or as f32
-                const int t = token0 + c;
-                if (mine && t < g.m) y[(int64_t)t * g.y_stride + channel] = i8_scaled<T>(v, g.sa[t], sw);
+            // 16 tokens' exact sums, as integers or as f32
+            auto store = [&](int gr, const auto* v) {
+                const int t0 = token0 + gr * 16;
+                T* at = y + (int64_t)t0 * g.y_stride + channel;
+                const float* sa = g.sa + t0;
+                if (t0 + 16 <= g.m) {
+                    if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j, at += g.y_stride) *at = i8_scaled<T>(v[j], __ldg(sa + j), sw);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, at += g.y_stride)
+                        if (mine && t0 + j < g.m) *at = i8_scaled<T>(v[j], __ldg(sa + j), sw);
+                }
             };
+            const int64_t part = (int64_t)g.bn * kI8BM, off = quarter * 32 + lane;
+            int32_t* sum = whole ? g.spare + blockIdx.x * part + off : g.sums + (seg.tile - g.cut0) * part + off;
             const int chunks = one ? 1 : (n + kI8Exact - 1) / kI8Exact;
             for (int ch = 0; ch < chunks; ++ch, sums.next()) {
                 const int p = sums.at;
@@ -350,17 +384,18 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 for (int gr = half; gr < groups; gr += 2) {
                     float v[16];
                     tmem_ld16(base + (uint32_t)(p * g.bn + gr * 16), v);
-                    int32_t* at = slot + (int64_t)gr * 16 * kI8BM;
+                    int32_t* at = sum + gr * 16 * kI8BM;
                     if (whole && chunks == 1) {
+                        store(gr, v);
+                    } else if (!whole) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) store(gr * 16 + j, v[j]);
+                        for (int j = 0; j < 16; ++j) atomicAdd(at + j * kI8BM, __float2int_rn(v[j]));
                     } else {
                         int i[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) i[j] = __float2int_rn(v[j]) + (ch > 0 ? at[j * kI8BM] : 0);
-                        if (whole && ch == chunks - 1) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) store(gr * 16 + j, i[j]);
+                        if (ch == chunks - 1) {
+                            store(gr, i);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) at[j * kI8BM] = i[j];
@@ -372,36 +407,20 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 if (lane == 0) i8_arrive(sempty + p * 8);
             }
             if (!whole) {
-                // the part is in the workspace; the CTA that brings the tile's last one adds them all
-                const int64_t units = g.tiles * g.kb, u0 = seg.tile * g.kb, u1 = u0 + g.kb;
-                const int G = gridDim.x;
-                // the CTAs whose runs hold the tile's first and last unit: unit u is in run c with
-                // units * c / G <= u < units * (c + 1) / G, rounded down
-                auto owner = [&](int64_t u) { return (int)(((u + 1) * G - 1) / units); };
-                const int c0 = owner(u0), c1 = owner(u1 - 1);
+                // the part has been added; the CTA that brings the tile's last blocks stores it
                 named_bar_sync(1, kI8AccWarps * 32);
-                if (tid == kI8AccWarp0 * 32) ticket = take_ticket(&g.counters[c0]);
+                if (tid == kI8AccWarp0 * 32) arrived = take_ticket(&g.counters[seg.tile - g.cut0], (unsigned)n) + n;
                 named_bar_sync(1, kI8AccWarps * 32);
-                if (alive && ticket == (unsigned)(c1 - c0)) {
-                    if (tid == kI8AccWarp0 * 32) g.counters[c0] = 0u;
-                    const int64_t part = (int64_t)g.bn * kI8BM;
-                    const int32_t* first = g.slots + ((int64_t)c0 * kI8Slots + 1) * part + quarter * 32 + lane;
+                if (alive && arrived == (unsigned)g.kb) {
+                    if (tid == kI8AccWarp0 * 32) g.counters[seg.tile - g.cut0] = 0u;
                     for (int gr = half; gr < groups; gr += 2) {
                         int i[16];
-                        const int64_t off = (int64_t)gr * 16 * kI8BM;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) i[j] = __ldcg(first + off + j * kI8BM);
-                        for (int c = c0 + 1; c <= c1; ++c) {
-                            const int32_t* other =
-                                g.slots + (int64_t)c * kI8Slots * part + off + quarter * 32 + lane;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) i[j] += __ldcg(other + j * kI8BM);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) store(gr * 16 + j, i[j]);
+                        for (int j = 0; j < 16; ++j) i[j] = __ldcg(sum + gr * 16 * kI8BM + j * kI8BM);
+                        store(gr, i);
                     }
                 }
-                named_bar_sync(1, kI8AccWarps * 32);  // `ticket` has been read
+                named_bar_sync(1, kI8AccWarps * 32);  // `arrived` has been read
             }
         }
     }
@@ -410,12 +429,20 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     if (warp == kI8MmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The token rows as f16 and their norms, rounded up: one CTA per row.
-__global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__ codes, int64_t chunks,
-                                                       uint4* __restrict__ wide, float* __restrict__ norm) {
+// The token rows as f16 and their norms, rounded up: one CTA per row. Further CTAs clear the sums of the cut tiles
+// (kI8Clear of 16 bytes each).
+constexpr int kI8Clear = 2048;
+__global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__ codes, int64_t rows, int64_t chunks,
+                                                       uint4* __restrict__ wide, float* __restrict__ norm,
+                                                       uint4* __restrict__ sums, int64_t n_sums) {
     __shared__ uint32_t part[8];
     pdl_launch_dependents();
     const int64_t row = blockIdx.x;
+    if (row >= rows) {
+        const int64_t at = (row - rows) * kI8Clear, end = n_sums - at < kI8Clear ? n_sums - at : kI8Clear;
+        for (int64_t i = threadIdx.x; i < end; i += 256) sums[at + i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     int sum = 0;
     for (int64_t c = threadIdx.x; c < chunks; c += 256) {
         const uint4 q = codes[row * chunks + c];
@@ -444,10 +471,10 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__
 // ---- the plan of a call, from its sizes alone ------------------------------------------
 struct I8Plan {
     int64_t tokens;  // of one launch
-    int bn, token_tiles, kb, stages, buffers;
-    int64_t tiles;
-    bool cut;
-    size_t wide, norms, slots, total;  // byte offsets in the workspace
+    int bn, ks, token_tiles, kb, stages, buffers, cutters;
+    int64_t tiles, cut0;
+    int64_t sums;  // 16-byte pieces
+    size_t at_wide, at_norms, at_sums, at_spare, total;  // byte offsets in the workspace
 };
 
 static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
@@ -460,83 +487,98 @@ static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
     p.token_tiles = (int)((p.tokens + 255) / 256);
     p.bn = (int)(((p.tokens + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16);
     if (p.bn < 32) p.bn = 32;
-    const int64_t tiles = (rows + kI8BM - 1) / kI8BM * p.token_tiles;
-    p.tiles = tiles;
+    p.tiles = (rows + kI8BM - 1) / kI8BM * p.token_tiles;
     p.kb = (int)((k16 + 63) / 64);
-    p.stages = kI8Smem / (p.bn * 128 + kI8CodeBytes);
+    p.ks = p.bn <= 128 ? 2 : 1;
+    p.stages = kI8Smem / (p.ks * (p.bn * 128 + kI8CodeBytes));
     if (p.stages > kI8StagesMax) p.stages = kI8StagesMax;
     // two buffers of sums where four stages still fit beside them
-    p.buffers = (512 - 2 * p.bn) / kI8ACols >= 4 ? 2 : 1;
-    const int room = (512 - p.buffers * p.bn) / kI8ACols;
+    const int cols = p.ks * kI8ACols;
+    p.buffers = (512 - 2 * p.bn) / cols >= 4 ? 2 : 1;
+    const int room = (512 - p.buffers * p.bn) / cols;
     if (p.stages > room) p.stages = room;
-    // whole tiles take waves * kb blocks of time, equal runs their share and the exchange of parts (about 8 blocks)
-    const int64_t waves = (tiles + kI8Ctas - 1) / kI8Ctas;
-    p.cut = waves * p.kb > (tiles * p.kb + kI8Ctas - 1) / kI8Ctas + 8;
+    // The tiles past the last full wave, whole: kb blocks of time. Cut: their share and about 8 blocks for adding the
+    // parts up (runs of at least 4 blocks: each part costs as much as those).
+    const int64_t rest = p.tiles % kI8Ctas, units = rest * p.kb;
+    p.cut0 = p.tiles;
+    if (rest) {
+        int64_t runs = units / 4 < kI8Ctas ? units / 4 : kI8Ctas;
+        if (runs > rest && p.kb > (units + runs - 1) / runs + 8) p.cut0 = p.tiles - rest, p.cutters = (int)runs;
+    }
+    p.sums = (p.tiles - p.cut0) * p.bn * kI8BM / 4;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    p.wide = kCounterBytes;
-    p.norms = up(p.wide + (size_t)p.tokens * k16 * 2);
-    p.slots = up(p.norms + (size_t)p.tokens * 4);
-    p.total = up(p.slots + (size_t)kI8Ctas * kI8Slots * p.bn * kI8BM * 4);
+    p.at_wide = kCounterBytes;
+    p.at_norms = up(p.at_wide + (size_t)p.tokens * k16 * 2);
+    p.at_sums = up(p.at_norms + (size_t)p.tokens * 4);
+    p.at_spare = up(p.at_sums + (size_t)p.sums * 16);
+    p.total = up(p.at_spare + (p.kb > kI8Exact ? (size_t)kI8Ctas * p.bn * kI8BM * 4 : 0));
     return p;
 }
 
-size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m) { return i8_plan(rows, k, m).total; }
+// The largest of the workspaces of a call's launches (the last may have fewer tokens and another plan).
+static size_t i8_workspace(int64_t rows, int64_t k, int64_t m, const I8Plan& first) {
+    const int64_t tail = m % first.tokens;
+    const size_t last = tail ? i8_plan(rows, k, tail).total : 0;
+    return last > first.total ? last : first.total;
+}
+size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m) { return i8_workspace(rows, k, m, i8_plan(rows, k, m)); }
 
+template <typename T> static cudaError_t i8_gemm_attributes() {
+    cudaError_t e =
+        cudaFuncSetAttribute(i8_gemm_kernel<T, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(i8_gemm_kernel<T, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
+    return e;
+}
 cudaError_t init_i8_gemm_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(i8_gemm_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(i8_gemm_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(i8_gemm_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kI8Smem + 1024);
+    cudaError_t e = i8_gemm_attributes<float>();
+    if (e == cudaSuccess) e = i8_gemm_attributes<__half>();
+    if (e == cudaSuccess) e = i8_gemm_attributes<__nv_bfloat16>();
     return e;
 }
 
 template <typename T>
-cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m,
-                           T* y, int64_t y_stride, void* workspace, int32_t* err, cudaStream_t s) {
-    const I8Plan full = i8_plan(W.rows, k, m);
+cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
+                           int64_t y_stride, void* workspace, int32_t* err, cudaStream_t s) {
+    const int64_t most = i8_plan(W.rows, k, m).tokens;
     cudaError_t e = get_encode_tiled();
     if (e != cudaSuccess) return e;
     uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+    auto encode = [](CUtensorMap* map, CUtensorMapDataType type, const void* base, cuuint64_t width, cuuint64_t rows,
+                     cuuint64_t row_bytes, cuuint32_t box_x, cuuint32_t box_y, CUtensorMapSwizzle swizzle) {
+        const cuuint64_t dims[2] = {width, rows}, strides[1] = {row_bytes};
+        const cuuint32_t box[2] = {box_x, box_y}, elem[2] = {1, 1};
+        return g_encode_tiled(map, type, 2, const_cast<void*>(base), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
     // the packed codes as rows of 8-byte words, a row per 32-row tile: boxes of 4 tiles x 64 k (2 KB of a row)
-    CUtensorMap wmap;
-    {
-        const cuuint64_t dims[2] = {(cuuint64_t)W.chunks * 64, (cuuint64_t)W.rows_pad / 32};
-        const cuuint64_t strides[1] = {(cuuint64_t)W.chunks * 512};
-        const cuuint32_t box[2] = {256, 4}, elem[2] = {1, 1};
-        if (g_encode_tiled(&wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<int8_t*>(W.codes), dims, strides, box, elem,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-    }
     const int64_t k16 = W.chunks * 16;
-    for (int64_t t = 0; t < m; t += full.tokens) {
-        const int64_t part = m - t < full.tokens ? m - t : full.tokens;
-        I8Plan p = i8_plan(W.rows, k, part);
-        __half* wide = reinterpret_cast<__half*>(ws + full.wide);
-        float* norms = reinterpret_cast<float*>(ws + full.norms);
-        e = launch_ex(i8_widen_kernel, dim3((unsigned)part), dim3(256), 0, s, false,
-                      reinterpret_cast<const uint4*>(a + t * k16), W.chunks, reinterpret_cast<uint4*>(wide), norms);
+    CUtensorMap wmap, amap;
+    if (!encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, W.codes, (cuuint64_t)W.chunks * 64, (cuuint64_t)W.rows_pad / 32,
+                (cuuint64_t)W.chunks * 512, 256, 4, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    for (int64_t t = 0; t < m; t += most) {
+        const int64_t part = m - t < most ? m - t : most;
+        const I8Plan p = i8_plan(W.rows, k, part);
+        __half* wide = reinterpret_cast<__half*>(ws + p.at_wide);
+        float* norms = reinterpret_cast<float*>(ws + p.at_norms);
+        const int64_t clear = (p.sums + kI8Clear - 1) / kI8Clear;
+        e = launch_ex(i8_widen_kernel, dim3((unsigned)(part + clear)), dim3(256), 0, s, false,
+                      reinterpret_cast<const uint4*>(a + t * k16), part, W.chunks, reinterpret_cast<uint4*>(wide), norms,
+                      reinterpret_cast<uint4*>(ws + p.at_sums), p.sums);
         if (e != cudaSuccess) return e;
-        CUtensorMap map;
-        const cuuint64_t dims[2] = {(cuuint64_t)k16, (cuuint64_t)part};
-        const cuuint64_t strides[1] = {(cuuint64_t)k16 * sizeof(__half)};
-        const cuuint32_t box[2] = {64, (cuuint32_t)p.bn};
-        const cuuint32_t elem[2] = {1, 1};
-        if (g_encode_tiled(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, wide, dims, strides, box, elem,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (!encode(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wide, (cuuint64_t)k16, (cuuint64_t)part, (cuuint64_t)k16 * 2,
+                    64, (cuuint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
         I8Gemm g{};
-        g.W = W, g.anorm = norms, g.sa = sa + t, g.m = (int)part, g.bn = p.bn;
-        g.token_tiles = p.token_tiles, g.tiles = p.tiles, g.kb = p.kb, g.stages = p.stages, g.buffers = p.buffers;
-        g.y_stride = y_stride, g.slots = reinterpret_cast<int32_t*>(ws + full.slots);
-        g.counters = reinterpret_cast<unsigned*>(ws), g.cut = p.cut, g.err = err;
-        const int64_t units = p.tiles * p.kb;
-        const int64_t ctas = p.cut ? (units < kI8Ctas ? units : kI8Ctas) : (p.tiles < kI8Ctas ? p.tiles : kI8Ctas);
-        e = launch_ex(i8_gemm_kernel<T>, dim3((unsigned)ctas), dim3(kI8Threads), (size_t)kI8Smem + 1024, s, true, g, map, wmap,
-                      y + t * y_stride);
+        g.W = W, g.anorm = norms, g.sa = sa + t, g.m = (int)part, g.bn = p.bn, g.token_tiles = p.token_tiles;
+        g.kb = p.kb, g.stages = p.stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
+        g.cutters = p.cutters, g.y_stride = y_stride, g.sums = reinterpret_cast<int32_t*>(ws + p.at_sums);
+        g.spare = reinterpret_cast<int32_t*>(ws + p.at_spare), g.counters = reinterpret_cast<unsigned*>(ws), g.err = err;
+        const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > p.cutters ? p.cut0 : p.cutters;
+        e = launch_ex(p.ks == 2 ? i8_gemm_kernel<T, 2> : i8_gemm_kernel<T, 1>, dim3((unsigned)ctas), dim3(kI8Threads),
+                      (size_t)kI8Smem + 1024, s, true, g, amap, wmap, y + t * y_stride);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
