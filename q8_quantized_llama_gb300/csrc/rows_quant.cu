@@ -11,14 +11,20 @@
 // a norm's codes need no second look at the row once M is known. The codes are
 // those of exact arithmetic: the f32 quotient t = v (127 / M) is off by a few
 // 2^-24 of itself, so a code is settled in f32 unless t lies within kWindow of a
-// half (a few elements in ten thousand), and those are decided in double from
-// the stored numbers, as is M (from the few elements within 2^-18 of the f32
-// maximum). Rows whose f32 numbers leave the normal range are done in double as
-// a whole.
+// half (a few elements in ten thousand). Those are settled at the end by the sign
+// of 254 |v| - (2 q + 1) M, from v and M in two-part f32 (exact for rows and norm,
+// to 2^-40 for silu), and where that is no more than the parts leave out, in
+// double (a double instruction takes 64 times an f32 one's turn, and exact halves
+// are common in 16-bit rows). The exact M comes from the elements next to the f32
+// maximum. Rows whose f32 numbers leave the normal range are done in double as a
+// whole.
 //
-// Bound: memory. One CTA of G threads (or one warp) per row keeps the row's v in
-// registers (16 values a thread), so every input is read once and every output
-// written once; rows of more than 16384 values are read twice.
+// Bound: memory, and with 16-bit types the f32 instructions (about 25 per element,
+// 30 with silu). A warp, or a CTA with as many threads as the row has values for,
+// keeps a row's v in registers (16 values a thread up to k = 8192, 32 up to 14336), so
+// every input is read once and every output written once; at least two CTAs share
+// an SM, so that one row's loads run under another's barriers; rows of more than
+// 14336 values are read twice.
 #include "kernels.cuh"
 #include "llama_q8.h"
 #include "ptx.cuh"
@@ -44,20 +50,21 @@ struct QuantArgs {
 
 struct BlockQ8 {};  // Q8_0 blocks as an element type
 
-constexpr int kPerThread = 16;             // values of a row that a thread keeps
-constexpr int kQuantMaxThreads = 1024;
+// threads of a CTA, at most: two such CTAs share an SM's registers (64 a thread; 72 with 32 values each)
+constexpr int kQuantThreads = 512, kQuantThreads32 = 448;
 constexpr float kMagic = 12582912.0f;       // 1.5 2^23: adding it rounds to an integer
 // Half width of the band around a half in which f32 does not settle a code. t = v (127 / M)
 // is at most 127 and off by the relative errors, in units of 2^-24, of: 127 / M 1, M 1, the
 // product by it 1, and v (rows 0, norm 1, silu: exp 4, 1 + e 1, the quotient 4, the product 1):
 // 127 * 13 * 2^-24 = 9.9e-5 for silu, 3.1e-5 for the others.
 template <int OP> constexpr float kWindow = OP == QUANT_SILU ? 1.6e-4f : 5e-5f;
-// v within this factor of the f32 maximum may be the exact maximum (2 * 11 * 2^-24 < 2^-19)
-constexpr float kNearMax = 1.0f - 1.0f / 262144.0f;
+// v within this factor of the f32 maximum may be the exact maximum: f32 products round in order (norm), silu's are off
+// by 10 * 2^-24 (2 * 10 * 2^-24 < 2^-19)
+template <int OP> constexpr float kNearMax = OP == QUANT_SILU ? 1.0f - 1.0f / 262144.0f : 1.0f;
 constexpr float kTiny = 7.9e-31f, kHuge = 1e36f;  // M outside: the row is done in double
 
 template <typename T> struct Piece { static constexpr int n = 16 / sizeof(T); };
-template <> struct Piece<BlockQ8> { static constexpr int n = 8; };
+template <> struct Piece<BlockQ8> { static constexpr int n = 16; };
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -77,41 +84,58 @@ template <> __device__ __forceinline__ float load_one<BlockQ8>(const void* x, in
     return d * (float)reinterpret_cast<const int8_t*>(blk)[2 + i % 32];
 }
 
+// Elements i .. i + n - 1 of a row as they lie in memory (i a multiple of n, 16-byte aligned), zeros past k.
+template <typename T> __device__ __forceinline__ uint4 load_raw(const void* x, int64_t row_at, int i, int k) {
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (i < k)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(reinterpret_cast<const T*>(x) + row_at + i));
+    return u;
+}
+template <typename T> __device__ __forceinline__ void from_raw(const uint4& u, float (&v)[Piece<T>::n]) {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int j = 0; j < Piece<T>::n; ++j) v[j] = to_f32(e[j]);
+}
+
 // Elements i .. i + n - 1 of a row (i a multiple of n), zeros past k. ALIGNED: 16-byte loads, k a multiple of n.
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void load_piece(const void* x, int64_t row_at, int i, int k, float (&v)[Piece<T>::n]) {
-    constexpr int n = Piece<T>::n;
     if constexpr (ALIGNED) {
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (i < k)
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                         : "l"(reinterpret_cast<const T*>(x) + row_at + i));
-        const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-        for (int j = 0; j < n; ++j) v[j] = to_f32(e[j]);
+        from_raw<T>(load_raw<T>(x, row_at, i, k), v);
     } else {
 #pragma unroll
-        for (int j = 0; j < n; ++j) v[j] = i + j < k ? load_one<T>(x, row_at, i + j) : 0.0f;
+        for (int j = 0; j < Piece<T>::n; ++j) v[j] = i + j < k ? load_one<T>(x, row_at, i + j) : 0.0f;
     }
 }
+// Half a Q8_0 block. Blocks lie on 2-byte boundaries: 16 codes are four words, or two bytes, three words and two bytes.
 template <>
-__device__ __forceinline__ void load_piece<BlockQ8, true>(const void* x, int64_t row_at, int i, int k, float (&v)[8]) {
-    // 8 codes of one block (blocks lie on 2-byte boundaries)
-    if (i >= k) {
+__device__ __forceinline__ void load_piece<BlockQ8, true>(const void* x, int64_t row_at, int i, int k, float (&v)[16]) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    float d = 0.0f;
+    if (i < k) {
+        const uint8_t* blk = reinterpret_cast<const uint8_t*>(x) + (row_at / 32 + i / 32) * 34;
+        const uint8_t* q = blk + 2 + i % 32;
+        d = __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short*>(blk)));
+        if (((uintptr_t)q & 2) == 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        return;
+            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(q + 4 * j);
+        } else {
+            uint32_t e[5];
+            e[0] = (uint32_t)*reinterpret_cast<const unsigned short*>(q) << 16;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) e[j + 1] = *reinterpret_cast<const uint32_t*>(q + 2 + 4 * j);
+            e[4] = *reinterpret_cast<const unsigned short*>(q + 14);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(e[j], e[j + 1], 16);
+        }
     }
-    const unsigned short* blk = reinterpret_cast<const unsigned short*>(
-        reinterpret_cast<const uint8_t*>(x) + (row_at / 32 + i / 32) * 34);
-    const float d = __half2float(__ushort_as_half(blk[0]));
-    const unsigned short* q = blk + 1 + (i % 32) / 2;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const unsigned short w = q[j];
-        v[2 * j] = d * (float)(int8_t)(w & 0xff);
-        v[2 * j + 1] = d * (float)(int8_t)(w >> 8);
+        const uint32_t u = w[j] ^ 0x80808080u;
+        const uint64_t a = codes2_f2<0>(u), b = codes2_f2<2>(u);
+        v[4 * j] = d * f2_lo(a), v[4 * j + 1] = d * f2_hi(a), v[4 * j + 2] = d * f2_lo(b), v[4 * j + 3] = d * f2_hi(b);
     }
 }
 
@@ -137,10 +161,65 @@ __device__ __forceinline__ void store_piece(void* x, int64_t row_at, int i, int 
 __device__ __noinline__ double silu_up_f64(float gate, float up) {
     return (double)gate / (1.0 + exp(-(double)gate)) * (double)up;
 }
-__device__ __forceinline__ float silu_up(float gate, float up) {
-    // below -80 the quotient's divisor passes the range of the quick division
-    if (gate < -80.0f) return (float)silu_up_f64(gate, up);
-    return __fdividef(gate, 1.0f + expf(-gate)) * up;
+__device__ __forceinline__ float silu_up(float gate, float up) { return __fdividef(gate, 1.0f + expf(-gate)) * up; }
+
+// ---- two-part f32 numbers: hi is the sum rounded to f32
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two two_renorm(float hi, float lo) {  // |hi| >= |lo|
+    const float s = hi + lo;
+    return {s, lo - (s - hi)};
+}
+__device__ __forceinline__ Two two_prod(float a, float b) {
+    const float p = a * b;
+    return {p, fmaf(a, b, -p)};
+}
+__device__ __forceinline__ Two two_of(double v) {
+    const float hi = (float)v;
+    return {hi, (float)(v - (double)hi)};
+}
+
+// silu(gate) up to about 2^-40 of itself, for gate >= -80: exp(x) = 2^n exp(r) with x = n ln 2 + r, ln 2 in three
+// parts of which n times the first is exact; exp(r), |r| <= ln 2 / 2, by its Taylor series to r^11 (what is left out is
+// below 2^-47), the terms up to r^5 in two parts.
+__device__ __noinline__ Two silu_up_two(float gate, float up) {
+    const float x = -gate;
+    Two y = {1.0f, 0.0f};  // 1 + exp(x)
+    if (x > -60.0f) {
+        const float n = rintf(x * 1.442695041f);
+        const float r1 = fmaf(-n, 0x1.62e4p-1f, x);
+        const Two p = two_prod(n, 0x1.7f7d1cp-20f);
+        Two r = two_sum(r1, -p.hi);
+        r = two_renorm(r.hi, r.lo - p.lo - n * 0x1.ef357ap-45f);
+        float q = 1.0f / 39916800.0f;
+        q = fmaf(q, r.hi, 1.0f / 3628800.0f);
+        q = fmaf(q, r.hi, 1.0f / 362880.0f);
+        q = fmaf(q, r.hi, 1.0f / 40320.0f);
+        q = fmaf(q, r.hi, 1.0f / 5040.0f);
+        q = fmaf(q, r.hi, 1.0f / 720.0f);
+        Two s = {q, 0.0f};
+        const Two c[6] = {{1.0f, 0.0f}, {1.0f, 0.0f}, {0.5f, 0.0f}, {0x1.555556p-3f, -0x1.555556p-28f},
+                          {0x1.555556p-5f, -0x1.555556p-30f}, {0x1.111112p-7f, -0x1.ddddep-32f}};  // 1 / i!
+#pragma unroll
+        for (int i = 5; i >= 0; --i) {
+            Two m = two_prod(s.hi, r.hi);
+            m.lo = fmaf(s.lo, r.hi, fmaf(s.hi, r.lo, m.lo));
+            const Two t = two_sum(c[i].hi, m.hi);
+            s = two_renorm(t.hi, t.lo + (c[i].lo + m.lo));
+        }
+        const float scale = pow2f((int)n);
+        y = two_sum(1.0f, s.hi * scale);
+        y = two_renorm(y.hi, y.lo + s.lo * scale);
+    }
+    const float q0 = __fdiv_rn(gate, y.hi);
+    const float q1 = __fdiv_rn(fmaf(-q0, y.lo, fmaf(-q0, y.hi, gate)), y.hi);
+    const Two v = two_prod(q0, up);
+    return two_renorm(v.hi, fmaf(q1, up, v.lo));
 }
 
 template <int OP, typename T, bool ALIGNED> struct Row {
@@ -149,56 +228,82 @@ template <int OP, typename T, bool ALIGNED> struct Row {
     int64_t xa, ba, oa;
     __device__ Row(const QuantArgs& args, int64_t r) : a(args), xa(r * args.xs), ba(r * args.bs), oa(r * args.os) {}
 
-    // h of elements i .. i + n - 1 as the first pass makes it; STORE writes it out
-    template <bool STORE> __device__ __forceinline__ void sums(int i, float (&h)[n]) const {
-        load_piece<T, ALIGNED>(a.x, xa, i, a.k, h);
-        if constexpr (OP == QUANT_NORM) {
-            if (a.b) {
-                float d[n];
-                load_piece<T, ALIGNED>(a.b, ba, i, a.k, d);
-#pragma unroll
-                for (int j = 0; j < n; ++j) h[j] = to_f32(from_f32<T>(h[j] + d[j]));
-            }
-            if (STORE && a.out) store_piece<T, ALIGNED>(a.out, oa, i, a.k, h);
-        }
+    // x (gate) and delta (up) of elements i .. i + n - 1
+    __device__ __forceinline__ void load(int i, float (&x)[n], float (&b)[n]) const {
+        load_piece<T, ALIGNED>(a.x, xa, i, a.k, x);
+        if (OP == QUANT_SILU || (OP == QUANT_NORM && a.b)) load_piece<T, ALIGNED>(a.b, ba, i, a.k, b);
     }
-    // v of the same elements, the sum of the squares of h added to ss
-    template <bool STORE> __device__ __forceinline__ void values(int i, float (&v)[n], float& ss) const {
+    // v from them, into x; a norm's h is written out and the sum of its squares added to ss
+    __device__ __forceinline__ void values(int i, float (&x)[n], const float (&b)[n], float& ss) const {
         if constexpr (OP == QUANT_SILU) {
-            float up[n];
-            load_piece<T, ALIGNED>(a.x, xa, i, a.k, v);
-            load_piece<T, ALIGNED>(a.b, ba, i, a.k, up);
+            float low = 0.0f;
 #pragma unroll
-            for (int j = 0; j < n; ++j) v[j] = silu_up(v[j], up[j]);
-        } else {
-            sums<STORE>(i, v);
-            if constexpr (OP == QUANT_NORM) {
-                float g[n];
+            for (int j = 0; j < n; ++j) low = fminf(low, x[j]);
+            if (low < -80.0f) {  // the quotient's divisor leaves the range of the quick division
 #pragma unroll
-                for (int j = 0; j < n; ++j) ss = fmaf(v[j], v[j], ss);
-                if constexpr (ALIGNED) {
+                for (int j = 0; j < n; ++j) x[j] = (float)silu_up_f64(x[j], b[j]);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < n; j += 4) {
-                        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (i < a.k) f = *reinterpret_cast<const float4*>(a.g + i + j);
-                        g[j] = f.x, g[j + 1] = f.y, g[j + 2] = f.z, g[j + 3] = f.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < n; ++j) g[j] = i + j < a.k ? a.g[i + j] : 0.0f;
-                }
-#pragma unroll
-                for (int j = 0; j < n; ++j) v[j] *= g[j];
+                for (int j = 0; j < n; ++j) x[j] = silu_up(x[j], b[j]);
             }
+        } else if constexpr (OP == QUANT_NORM) {
+            if (a.b) {
+#pragma unroll
+                for (int j = 0; j < n; ++j) x[j] = to_f32(from_f32<T>(x[j] + b[j]));
+            }
+            if (a.out) store_piece<T, ALIGNED>(a.out, oa, i, a.k, x);
+#pragma unroll
+            for (int j = 0; j < n; ++j) ss = fmaf(x[j], x[j], ss);
+            gained(i, x);
         }
     }
-    // h of element i after the first pass (which may have written it over x or delta)
+    // h times g
+    __device__ __forceinline__ void gained(int i, float (&x)[n]) const {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int j = 0; j < n; j += 4) {
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < a.k) f = __ldg(reinterpret_cast<const float4*>(a.g + i + j));
+                x[j] *= f.x, x[j + 1] *= f.y, x[j + 2] *= f.z, x[j + 3] *= f.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) x[j] *= i + j < a.k ? a.g[i + j] : 0.0f;
+        }
+    }
+    // v of elements i .. i + n - 1 after the first pass (which may have written h over x or delta)
+    __device__ __forceinline__ void again(int i, float (&v)[n]) const {
+        if constexpr (OP == QUANT_NORM) {
+            if (a.out) {
+                load_piece<T, ALIGNED>(a.out, oa, i, a.k, v);
+            } else {
+                float b[n];
+                load(i, v, b);
+                if (a.b) {
+#pragma unroll
+                    for (int j = 0; j < n; ++j) v[j] = to_f32(from_f32<T>(v[j] + b[j]));
+                }
+            }
+            gained(i, v);
+        } else {
+            float b[n], unused = 0.0f;
+            load(i, v, b);
+            values(i, v, b, unused);
+        }
+    }
+    // h of element i after the first pass
     __device__ __forceinline__ float h_again(int i) const {
         if (OP == QUANT_NORM && a.out) return load_one<T>(a.out, oa, i);
         float h = load_one<T>(a.x, xa, i);
         if constexpr (OP == QUANT_NORM)
             if (a.b) h = to_f32(from_f32<T>(h + load_one<T>(a.b, ba, i)));
         return h;
+    }
+    // v of element i (a gate of at least -80) in two parts
+    __device__ __forceinline__ Two v_two(int i) const {
+        if constexpr (OP == QUANT_SILU) return silu_up_two(load_one<T>(a.x, xa, i), load_one<T>(a.b, ba, i));
+        if constexpr (OP == QUANT_NORM) return two_prod(h_again(i), a.g[i]);
+        return {load_one<T>(a.x, xa, i), 0.0f};
     }
     // v of element i in double: exact for rows (one number) and norm (a product of two f32)
     __device__ double v_f64(int i) const {
@@ -207,16 +312,19 @@ template <int OP, typename T, bool ALIGNED> struct Row {
         return (double)load_one<T>(a.x, xa, i);
     }
 };
-// no element type but BlockQ8 stands only under rows_quant
+// Q8_0 blocks stand under rows_quant alone
 template <bool ALIGNED> struct Row<QUANT_ROWS, BlockQ8, ALIGNED> {
-    static constexpr int n = 8;
+    static constexpr int n = Piece<BlockQ8>::n;
     const QuantArgs& a;
     int64_t xa;
     __device__ Row(const QuantArgs& args, int64_t r) : a(args), xa(r * args.xs) {}
-    template <bool STORE> __device__ __forceinline__ void values(int i, float (&v)[n], float&) const {
-        load_piece<BlockQ8, true>(a.x, xa, i, a.k, v);
+    __device__ __forceinline__ void load(int i, float (&x)[n], float (&)[n]) const {
+        load_piece<BlockQ8, true>(a.x, xa, i, a.k, x);
     }
+    __device__ __forceinline__ void values(int, float (&)[n], const float (&)[n], float&) const {}
+    __device__ __forceinline__ void again(int i, float (&v)[n]) const { load_piece<BlockQ8, true>(a.x, xa, i, a.k, v); }
     __device__ __forceinline__ float h_again(int i) const { return load_one<BlockQ8>(a.x, xa, i); }
+    __device__ __forceinline__ Two v_two(int i) const { return {load_one<BlockQ8>(a.x, xa, i), 0.0f}; }
     __device__ double v_f64(int i) const { return (double)load_one<BlockQ8>(a.x, xa, i); }
 };
 
@@ -226,70 +334,93 @@ __device__ __forceinline__ bool above_half(double v, double M, float q) {
     const double odd = 2.0 * (double)q + 1.0, p = odd * M, e = fma(odd, M, -p);
     return fma(254.0, fabs(v), -p) - e >= 0.0;
 }
+// The same from two-part numbers: 1 or 0, or -1 where the difference is within what they leave out (2^-36 of either
+// product; nothing for one-part numbers).
+__device__ __forceinline__ int above_half(Two v, Two M, float q) {
+    const float odd = 2.0f * q + 1.0f, p = odd * M.hi, e = fmaf(odd, M.hi, -p);
+    const float lo = v.hi < 0.0f ? -v.lo : v.lo;
+    const float off = (fmaf(254.0f, fabsf(v.hi), -p) - e) + fmaf(254.0f, lo, -(odd * M.lo));
+    if (v.lo == 0.0f && M.lo == 0.0f) return off >= 0.0f;
+    return fabsf(off) <= p * 0x1p-36f ? -1 : off > 0.0f;
+}
 
-// The bits of a magnitude order like the magnitude, NaN above infinity.
-__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger magnitude; NaN if either is.
+__device__ __forceinline__ float max_magnitude(float a, float v) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(v)));
+    return a;
+}
 
 // One row's reduction area; a warp's or a CTA's.
 struct QuantShared {
-    uint32_t max[32];
-    float ss[32];
+    uint32_t max[kQuantThreads / 32];
+    float ss[kQuantThreads / 32];
     unsigned long long exact;  // the exact maximum as the bits of a double
     double ss64;
     int poison;
 };
 
-template <int G> __device__ __forceinline__ void row_sync() {
-    if constexpr (G == 32) __syncwarp();
+template <bool WARP> __device__ __forceinline__ void row_sync() {
+    if constexpr (WARP) __syncwarp();
     else __syncthreads();
 }
 
-// G threads per row (32: a warp; 128 / G rows per CTA below 128). LOOP: rows too long for the registers, read again.
-template <int OP, typename T, bool ALIGNED, int G, bool LOOP>
-__global__ void __launch_bounds__(G < 128 ? 128 : G) quant_kernel(const QuantArgs a) {
+// A row per warp (WARP, four per CTA) or per CTA; E values of it a thread. E == 0: rows too long for the registers, read
+// again.
+template <int OP, typename T, bool ALIGNED, int E, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : E == 32 ? kQuantThreads32 : kQuantThreads, WARP ? 6 : 2)
+    quant_kernel(const QuantArgs a) {
     using R = Row<OP, T, ALIGNED>;
-    constexpr int n = R::n, pieces = kPerThread / n;
-    constexpr int kRowsPerCta = G == 32 ? 4 : 1;
+    constexpr bool LOOP = E == 0;
+    constexpr int n = R::n, pieces = E / n;
+    constexpr int kRowsPerCta = WARP ? 4 : 1;
     __shared__ QuantShared shared[kRowsPerCta];
-    const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, warp = t >> 5;
-    QuantShared& sh = shared[G == 32 ? threadIdx.x >> 5 : 0];
-    const int64_t r = (int64_t)blockIdx.x * kRowsPerCta + (G == 32 ? threadIdx.x >> 5 : 0);
-    if (r >= a.rows) return;  // a whole warp (G == 32) or none
+    const int G = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, warp = t >> 5;
+    QuantShared& sh = shared[WARP ? threadIdx.x >> 5 : 0];
+    const int64_t r = (int64_t)blockIdx.x * kRowsPerCta + (WARP ? threadIdx.x >> 5 : 0);
+    if (r >= a.rows) return;  // a whole warp (WARP) or none
     const R row(a, r);
     const int k = a.k, k16 = (int)a.row_bytes;
     int8_t* codes = a.codes + r * a.row_bytes;
     if (t == 0) sh.exact = 0ull, sh.ss64 = 0.0, sh.poison = 0;
 
-    // the row once: v in registers, the largest magnitude, the sum of squares
-    float v[LOOP ? n : kPerThread];
-    float ss = 0.0f;
-    uint32_t mx = 0u;
+    // the row once: all its loads, then v in registers, the largest magnitude, the sum of squares
+    float v[LOOP ? n : E];
+    float ss = 0.0f, own = 0.0f;
     if constexpr (!LOOP) {
+        constexpr int batch = E == 32 && n == 4 ? 2 : E == 32 && n == 8 ? 2 : pieces;  // pieces whose loads are in flight
 #pragma unroll
-        for (int p = 0; p < pieces; ++p) {
-            float w[n];
-            row.template values<true>((p * G + t) * n, w, ss);
+        for (int p0 = 0; p0 < pieces; p0 += batch) {
+            float x[batch][n], b[batch][n];
 #pragma unroll
-            for (int j = 0; j < n; ++j) v[p * n + j] = w[j], mx = max(mx, magnitude_bits(w[j]));
+            for (int p = 0; p < batch; ++p) row.load(((p0 + p) * G + t) * n, x[p], b[p]);
+#pragma unroll
+            for (int p = 0; p < batch; ++p) {
+                row.values(((p0 + p) * G + t) * n, x[p], b[p], ss);
+#pragma unroll
+                for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j], own = max_magnitude(own, x[p][j]);
+            }
         }
     } else {
         float part[4] = {0.f, 0.f, 0.f, 0.f};  // short chains: a thread has many squares to add
         for (int i = t * n, p = 0; i < k; i += G * n, ++p) {
-            float w[n], s = 0.0f;
-            row.template values<true>(i, w, s);
+            float w[n], b[n], s = 0.0f;
+            row.load(i, w, b);
+            row.values(i, w, b, s);
             part[p & 3] += s;
 #pragma unroll
-            for (int j = 0; j < n; ++j) mx = max(mx, magnitude_bits(w[j]));
+            for (int j = 0; j < n; ++j) own = max_magnitude(own, w[j]);
         }
         ss = (part[0] + part[1]) + (part[2] + part[3]);
     }
+    uint32_t mx = __float_as_uint(own);  // the bits of magnitudes order like the magnitudes, NaN above infinity
     mx = __reduce_max_sync(0xffffffffu, mx);
     if constexpr (OP == QUANT_NORM) ss = warp_sum(ss);
-    if constexpr (G > 32) {
+    if constexpr (!WARP) {
         if (lane == 0) sh.max[warp] = mx, sh.ss[warp] = ss;
         __syncthreads();
-        mx = __reduce_max_sync(0xffffffffu, lane < G / 32 ? sh.max[lane] : 0u);
-        if constexpr (OP == QUANT_NORM) ss = warp_sum(lane < G / 32 ? sh.ss[lane] : 0.0f);
+        mx = __reduce_max_sync(0xffffffffu, lane < G >> 5 ? sh.max[lane] : 0u);
+        if constexpr (OP == QUANT_NORM) ss = warp_sum(lane < G >> 5 ? sh.ss[lane] : 0.0f);
     } else {
         __syncwarp();
     }
@@ -299,7 +430,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) quant_kernel(const QuantArg
         bool zero = true;
         if constexpr (OP != QUANT_ROWS) {
             for (int i = t; i < k; i += G) zero &= row.v_f64(i) == 0.0;
-            if constexpr (G == 32) zero = __all_sync(0xffffffffu, zero);
+            if constexpr (WARP) zero = __all_sync(0xffffffffu, zero);
             else zero = __syncthreads_and(zero);
         }
         if (zero) {
@@ -329,12 +460,12 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) quant_kernel(const QuantArg
         if constexpr (OP == QUANT_NORM) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            for (int w = 0; w < (G + 31) / 32; ++w) {
+            for (int w = 0; w < G >> 5; ++w) {
                 if (lane == 0 && warp == w) sh.ss64 += sum;
-                row_sync<G>();
+                row_sync<WARP>();
             }
         }
-        row_sync<G>();
+        row_sync<WARP>();
         const double M64 = __longlong_as_double((long long)sh.exact);
         const bool poison = sh.poison != 0;
         for (int i = t; i < k16; i += G) {
@@ -356,96 +487,112 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) quant_kernel(const QuantArg
         return;
     }
 
-    // v of elements i .. i + n - 1 once more (h from where the first pass left it)
-    auto again = [&](int i, float(&w)[n]) {
-        if constexpr (OP == QUANT_NORM) {
-#pragma unroll
-            for (int j = 0; j < n; ++j) w[j] = i + j < k ? row.h_again(i + j) * a.g[i + j] : 0.0f;
-        } else {
-            float unused = 0.0f;
-            row.template values<false>(i, w, unused);
-        }
-    };
     // the exact maximum, of the elements that may be it
-    double M64 = M;
     if constexpr (OP != QUANT_ROWS) {
-        const float near = M * kNearMax;
-        auto offer = [&](int i, float w) {
-            if (fabsf(w) >= near)
-                atomicMax(&sh.exact, (unsigned long long)__double_as_longlong(fabs(row.v_f64(i))));
-        };
-        if constexpr (!LOOP) {
+        const float near = M * kNearMax<OP>;
+        if (own >= near) {
+            auto offer = [&](int i, float w) {
+                if (fabsf(w) >= near)
+                    atomicMax(&sh.exact, (unsigned long long)__double_as_longlong(fabs(row.v_f64(i))));
+            };
+            if constexpr (!LOOP) {
 #pragma unroll
-            for (int p = 0; p < pieces; ++p)
+                for (int p = 0; p < pieces; ++p)
 #pragma unroll
-                for (int j = 0; j < n; ++j) offer((p * G + t) * n + j, v[p * n + j]);
-        } else {
-            for (int i = t * n; i < k; i += G * n) {
-                float w[n];
-                again(i, w);
+                    for (int j = 0; j < n; ++j) offer((p * G + t) * n + j, v[p * n + j]);
+            } else {
+                for (int i = t * n; i < k; i += G * n) {
+                    float w[n];
+                    row.again(i, w);
 #pragma unroll
-                for (int j = 0; j < n; ++j) offer(i + j, w[j]);
+                    for (int j = 0; j < n; ++j) offer(i + j, w[j]);
+                }
             }
         }
-        row_sync<G>();
-        M64 = __longlong_as_double((long long)sh.exact);
     }
 
-    // codes
+    // codes, rounded in f32; the elements next to a border are noted, as bits of a piece
     const float inv = __fdiv_rn(127.0f, M);
-    auto code = [&](int i, float w) -> uint32_t {
-        const float m = fmaf(w, inv, kMagic);  // rounded; its low byte is the code
-        const float off = fabsf(fmaf(w, inv, kMagic - m));
-        int c = __float_as_int(m);
-        if (off > 0.5f - kWindow<OP>) {
-            const float q = floorf(fabsf(w) * inv);
-            const int u = (int)q + (above_half(row.v_f64(i), M64, q) ? 1 : 0);
-            c = w < 0.0f ? -u : u;
-        }
-        return (uint32_t)c & 0xffu;
-    };
-    auto store = [&](int i, const float* w) {
-        uint32_t word[n / 4];
+    auto store = [&](int i, const float* w) -> uint32_t {
+        uint32_t word[n / 4], border = 0u;
+        float off = 0.0f;
 #pragma unroll
-        for (int j = 0; j < n / 4; ++j)
-            word[j] = code(i + 4 * j, w[4 * j]) | code(i + 4 * j + 1, w[4 * j + 1]) << 8 |
-                      code(i + 4 * j + 2, w[4 * j + 2]) << 16 | code(i + 4 * j + 3, w[4 * j + 3]) << 24;
+        for (int q = 0; q < n / 4; ++q) {
+            uint32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float m = fmaf(w[4 * q + j], inv, kMagic);  // rounded; its low byte is the code
+                off = fmaxf(off, fabsf(fmaf(w[4 * q + j], inv, kMagic - m)));
+                c[j] = __float_as_uint(m);
+            }
+            word[q] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        }
         if (i < k16) {
-            if constexpr (n == 8) *reinterpret_cast<uint2*>(codes + i) = make_uint2(word[0], word[1]);
+            if constexpr (n == 16) *reinterpret_cast<uint4*>(codes + i) = make_uint4(word[0], word[1], word[2], word[3]);
+            else if constexpr (n == 8) *reinterpret_cast<uint2*>(codes + i) = make_uint2(word[0], word[1]);
             else *reinterpret_cast<uint32_t*>(codes + i) = word[0];
+        }
+        if (off > 0.5f - kWindow<OP>) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const float m = fmaf(w[j], inv, kMagic);
+                if (fabsf(fmaf(w[j], inv, kMagic - m)) > 0.5f - kWindow<OP>) border |= 1u << j;
+            }
+        }
+        return border;
+    };
+    // the noted elements of the piece at i, with the exact maximum
+    auto settle = [&](int i, uint32_t border) {
+        const double M64 = OP == QUANT_ROWS ? (double)M : __longlong_as_double((long long)sh.exact);
+        const Two M2 = OP == QUANT_ROWS ? Two{M, 0.0f} : two_of(M64);
+#pragma unroll 1
+        while (border) {
+            const int at = i + __ffs(border) - 1;
+            border &= border - 1u;
+            const Two w = row.v_two(at);
+            const float q = floorf(fabsf(w.hi) * inv);
+            int up = above_half(w, M2, q);
+            if (up < 0) up = above_half(row.v_f64(at), M64, q);
+            const int c = (int)q + up;
+            codes[at] = (int8_t)(w.hi < 0.0f ? -c : c);
         }
     };
     if constexpr (!LOOP) {
+        uint32_t border = 0u;  // E <= 32
 #pragma unroll
-        for (int p = 0; p < pieces; ++p) store((p * G + t) * n, v + p * n);
+        for (int p = 0; p < pieces; ++p) border |= store((p * G + t) * n, v + p * n) << (p * n);
+        if constexpr (OP != QUANT_ROWS) row_sync<WARP>();
+#pragma unroll 1
+        for (int p = 0; border; ++p, border = n < 32 ? border >> n : 0u) {
+            const uint32_t bits = border & ((1u << n) - 1u);
+            if (bits) settle((p * G + t) * n, bits);
+        }
     } else {
+        row_sync<WARP>();
         for (int i = t * n; i < k16; i += G * n) {
             float w[n];
-            again(i, w);
-            store(i, w);
+            row.again(i, w);
+            const uint32_t bits = store(i, w);
+            if (bits) settle(i, bits);
         }
     }
-    if (t == 0) {
-        float d;
-        if constexpr (OP == QUANT_NORM) d = __fdiv_rn((float)M64, 127.0f * __fsqrt_rn(ss / (float)k + a.eps));
-        else d = __fdiv_rn((float)M64, 127.0f);
-        a.scale[r] = d;
+    if (t == 0) {  // M is the exact maximum rounded (silu: of the same row, to a few 2^-24)
+        const float top = OP == QUANT_SILU ? (float)__longlong_as_double((long long)sh.exact) : M;
+        a.scale[r] = __fdiv_rn(top, OP == QUANT_NORM ? 127.0f * __fsqrt_rn(ss / (float)k + a.eps) : 127.0f);
     }
 }
 
 template <int OP, typename T, bool ALIGNED>
 static cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s) {
-    const int threads = (int)((a.row_bytes + kPerThread - 1) / kPerThread);
-    auto go = [&](auto kernel, int rows_per_cta, int block) {
+    auto go = [&](auto kernel, int rows_per_cta, int64_t threads) {
         const unsigned grid = (unsigned)(((int64_t)a.rows + rows_per_cta - 1) / rows_per_cta);
-        return launch_ex(kernel, dim3(grid), dim3((unsigned)block), 0, s, false, a);
+        return launch_ex(kernel, dim3(grid), dim3((unsigned)((threads + 31) / 32 * 32)), 0, s, false, a);
     };
-    if (threads <= 32) return go(quant_kernel<OP, T, ALIGNED, 32, false>, 4, 128);
-    if (threads <= 128) return go(quant_kernel<OP, T, ALIGNED, 128, false>, 1, 128);
-    if (threads <= 256) return go(quant_kernel<OP, T, ALIGNED, 256, false>, 1, 256);
-    if (threads <= 512) return go(quant_kernel<OP, T, ALIGNED, 512, false>, 1, 512);
-    if (threads <= 1024) return go(quant_kernel<OP, T, ALIGNED, 1024, false>, 1, 1024);
-    return go(quant_kernel<OP, T, ALIGNED, 1024, true>, 1, 1024);
+    const int64_t k = a.row_bytes;
+    if (k <= 512) return go(quant_kernel<OP, T, ALIGNED, 16, true>, 4, 128);
+    if (k <= 16 * kQuantThreads) return go(quant_kernel<OP, T, ALIGNED, 16, false>, 1, k / 16);
+    if (k <= 32 * kQuantThreads32) return go(quant_kernel<OP, T, ALIGNED, 32, false>, 1, (k + 31) / 32);
+    return go(quant_kernel<OP, T, ALIGNED, 0, false>, 1, kQuantThreads);
 }
 
 // 16-byte loads and stores: k a multiple of a piece, rows and bases on 16-byte boundaries.
