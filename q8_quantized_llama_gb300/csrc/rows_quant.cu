@@ -30,6 +30,7 @@
 #include "ptx.cuh"
 
 #include <cuda_bf16.h>
+#include <type_traits>
 
 namespace lq8 {
 
@@ -53,11 +54,11 @@ struct BlockQ8 {};  // Q8_0 blocks as an element type
 // threads of a CTA, at most: two such CTAs share an SM's registers (64 a thread; 72 with 32 values each)
 constexpr int kQuantThreads = 512, kQuantThreads32 = 448;
 constexpr float kMagic = 12582912.0f;       // 1.5 2^23: adding it rounds to an integer
-// Half width of the band around a half in which f32 does not settle a code. t = v (127 / M)
-// is at most 127 and off by the relative errors, in units of 2^-24, of: 127 / M 1, M 1, the
-// product by it 1, and v (rows 0, norm 1, silu: exp 4, 1 + e 1, the quotient 4, the product 1):
-// 127 * 13 * 2^-24 = 9.9e-5 for silu, 3.1e-5 for the others.
-template <int OP> constexpr float kWindow = OP == QUANT_SILU ? 1.6e-4f : 5e-5f;
+// Half width of the band around a half in which f32 does not settle a code. t = v (127 / M) is at most 127 and off by
+// the relative errors, in units of 2^-24, of 127 / M (1), of M (rows 0, norm 1, silu as v) and of v (rows 0, norm 1, silu:
+// exp 4, 1 + e 1, the quotient 4, the product 1): 127 * 21 * 2^-24 = 1.6e-4 for silu, 127 * 3 * 2^-24 = 2.3e-5 for the
+// others; t itself is rounded at a few 2^-27 next to a half.
+template <int OP> constexpr float kWindow = OP == QUANT_SILU ? 1.7e-4f : 3e-5f;
 // v within this factor of the f32 maximum may be the exact maximum: f32 products round in order (norm), silu's are off
 // by 10 * 2^-24 (2 * 10 * 2^-24 < 2^-19)
 template <int OP> constexpr float kNearMax = OP == QUANT_SILU ? 1.0f - 1.0f / 262144.0f : 1.0f;
@@ -88,7 +89,7 @@ template <> __device__ __forceinline__ float load_one<BlockQ8>(const void* x, in
 template <typename T> __device__ __forceinline__ uint4 load_raw(const void* x, int64_t row_at, int i, int k) {
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (i < k)
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                      : "l"(reinterpret_cast<const T*>(x) + row_at + i));
     return u;
@@ -109,31 +110,31 @@ __device__ __forceinline__ void load_piece(const void* x, int64_t row_at, int i,
         for (int j = 0; j < Piece<T>::n; ++j) v[j] = i + j < k ? load_one<T>(x, row_at, i + j) : 0.0f;
     }
 }
-// Half a Q8_0 block. Blocks lie on 2-byte boundaries: 16 codes are four words, or two bytes, three words and two bytes.
-template <>
-__device__ __forceinline__ void load_piece<BlockQ8, true>(const void* x, int64_t row_at, int i, int k, float (&v)[16]) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    float d = 0.0f;
+// Half a Q8_0 block. Blocks lie on 2-byte boundaries, every other one off the words': its 16 codes are the words from two
+// bytes before them on, shifted, the last half word read by itself (nothing past the codes is touched).
+struct RawQ8 {
+    uint32_t w[5];
+    uint32_t d;  // the fp16 scale, and above it the shift
+};
+__device__ __forceinline__ RawQ8 load_raw_q8(const void* x, int64_t row_at, int i, int k) {
+    RawQ8 r = {};
     if (i < k) {
         const uint8_t* blk = reinterpret_cast<const uint8_t*>(x) + (row_at / 32 + i / 32) * 34;
         const uint8_t* q = blk + 2 + i % 32;
-        d = __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short*>(blk)));
-        if (((uintptr_t)q & 2) == 0) {
+        const uint32_t shift = ((uint32_t)(uintptr_t)q & 2u) * 8u;
+        const uint32_t* word = reinterpret_cast<const uint32_t*>((uintptr_t)q & ~(uintptr_t)3);
+        r.d = *reinterpret_cast<const unsigned short*>(blk) | shift << 16;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(q + 4 * j);
-        } else {
-            uint32_t e[5];
-            e[0] = (uint32_t)*reinterpret_cast<const unsigned short*>(q) << 16;
-#pragma unroll
-            for (int j = 0; j < 3; ++j) e[j + 1] = *reinterpret_cast<const uint32_t*>(q + 2 + 4 * j);
-            e[4] = *reinterpret_cast<const unsigned short*>(q + 14);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(e[j], e[j + 1], 16);
-        }
+        for (int j = 0; j < 4; ++j) r.w[j] = word[j];
+        if (shift) r.w[4] = *reinterpret_cast<const unsigned short*>(q + 14);
     }
+    return r;
+}
+__device__ __forceinline__ void from_raw_q8(const RawQ8& r, float (&v)[16]) {
+    const float d = __half2float(__ushort_as_half((unsigned short)(r.d & 0xffffu)));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint32_t u = w[j] ^ 0x80808080u;
+        const uint32_t u = __funnelshift_r(r.w[j], r.w[j + 1], r.d >> 16) ^ 0x80808080u;
         const uint64_t a = codes2_f2<0>(u), b = codes2_f2<2>(u);
         v[4 * j] = d * f2_lo(a), v[4 * j + 1] = d * f2_hi(a), v[4 * j + 2] = d * f2_lo(b), v[4 * j + 3] = d * f2_hi(b);
     }
@@ -233,6 +234,18 @@ template <int OP, typename T, bool ALIGNED> struct Row {
         load_piece<T, ALIGNED>(a.x, xa, i, a.k, x);
         if (OP == QUANT_SILU || (OP == QUANT_NORM && a.b)) load_piece<T, ALIGNED>(a.b, ba, i, a.k, b);
     }
+    // the same as they lie in memory (ALIGNED), and from there
+    struct Raw {
+        uint4 x, b;
+    };
+    __device__ __forceinline__ void load(int i, Raw& r) const {
+        r.x = load_raw<T>(a.x, xa, i, a.k);
+        if (OP == QUANT_SILU || (OP == QUANT_NORM && a.b)) r.b = load_raw<T>(a.b, ba, i, a.k);
+    }
+    __device__ __forceinline__ void open(const Raw& r, float (&x)[n], float (&b)[n]) const {
+        from_raw<T>(r.x, x);
+        from_raw<T>(r.b, b);  // not used where it was not read
+    }
     // v from them, into x; a norm's h is written out and the sum of its squares added to ss
     __device__ __forceinline__ void values(int i, float (&x)[n], const float (&b)[n], float& ss) const {
         if constexpr (OP == QUANT_SILU) {
@@ -299,6 +312,11 @@ template <int OP, typename T, bool ALIGNED> struct Row {
             if (a.b) h = to_f32(from_f32<T>(h + load_one<T>(a.b, ba, i)));
         return h;
     }
+    // whether v of element i is zero in fact
+    __device__ __forceinline__ bool zero(int i) const {
+        if (OP == QUANT_SILU) return load_one<T>(a.x, xa, i) == 0.0f || load_one<T>(a.b, ba, i) == 0.0f;
+        return h_again(i) == 0.0f || (OP == QUANT_NORM && a.g[i] == 0.0f);
+    }
     // v of element i (a gate of at least -80) in two parts
     __device__ __forceinline__ Two v_two(int i) const {
         if constexpr (OP == QUANT_SILU) return silu_up_two(load_one<T>(a.x, xa, i), load_one<T>(a.b, ba, i));
@@ -318,12 +336,12 @@ template <bool ALIGNED> struct Row<QUANT_ROWS, BlockQ8, ALIGNED> {
     const QuantArgs& a;
     int64_t xa;
     __device__ Row(const QuantArgs& args, int64_t r) : a(args), xa(r * args.xs) {}
-    __device__ __forceinline__ void load(int i, float (&x)[n], float (&)[n]) const {
-        load_piece<BlockQ8, true>(a.x, xa, i, a.k, x);
-    }
+    using Raw = RawQ8;
+    __device__ __forceinline__ void load(int i, float (&x)[n], float (&)[n]) const { again(i, x); }
     __device__ __forceinline__ void values(int, float (&)[n], const float (&)[n], float&) const {}
-    __device__ __forceinline__ void again(int i, float (&v)[n]) const { load_piece<BlockQ8, true>(a.x, xa, i, a.k, v); }
+    __device__ __forceinline__ void again(int i, float (&v)[n]) const { from_raw_q8(load_raw_q8(a.x, xa, i, a.k), v); }
     __device__ __forceinline__ float h_again(int i) const { return load_one<BlockQ8>(a.x, xa, i); }
+    __device__ __forceinline__ bool zero(int i) const { return h_again(i) == 0.0f; }
     __device__ __forceinline__ Two v_two(int i) const { return {load_one<BlockQ8>(a.x, xa, i), 0.0f}; }
     __device__ double v_f64(int i) const { return (double)load_one<BlockQ8>(a.x, xa, i); }
 };
@@ -350,12 +368,15 @@ __device__ __forceinline__ float max_magnitude(float a, float v) {
     return a;
 }
 
-// One row's reduction area; a warp's or a CTA's.
+// A row's reduction area; a warp's or a CTA's.
 struct QuantShared {
-    uint32_t max[kQuantThreads / 32];
-    float ss[kQuantThreads / 32];
-    unsigned long long exact;  // the exact maximum as the bits of a double
-    double ss64;
+    uint32_t max[32];
+    float ss[32];
+    unsigned long long exact;  // the exact maximum (key below)
+};
+struct QuantSharedF64 {
+    unsigned long long max;
+    double ss;
     int poison;
 };
 
@@ -364,136 +385,184 @@ template <bool WARP> __device__ __forceinline__ void row_sync() {
     else __syncthreads();
 }
 
-// A row per warp (WARP, four per CTA) or per CTA; E values of it a thread. E == 0: rows too long for the registers, read
-// again.
-template <int OP, typename T, bool ALIGNED, int E, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : E == 32 ? kQuantThreads32 : kQuantThreads, WARP ? 6 : 2)
-    quant_kernel(const QuantArgs a) {
-    using R = Row<OP, T, ALIGNED>;
-    constexpr bool LOOP = E == 0;
-    constexpr int n = R::n, pieces = E / n;
-    constexpr int kRowsPerCta = WARP ? 4 : 1;
-    __shared__ QuantShared shared[kRowsPerCta];
-    const int G = WARP ? 32 : blockDim.x;
-    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, warp = t >> 5;
-    QuantShared& sh = shared[WARP ? threadIdx.x >> 5 : 0];
-    const int64_t r = (int64_t)blockIdx.x * kRowsPerCta + (WARP ? threadIdx.x >> 5 : 0);
-    if (r >= a.rows) return;  // a whole warp (WARP) or none
+// A row whose numbers leave the range in which f32 settles codes, or are not finite, in double.
+template <int OP, bool WARP, typename R>
+__device__ __forceinline__ void quant_row_f64(const QuantArgs& a, int64_t r, int t, int G, QuantSharedF64& sh) {
     const R row(a, r);
     const int k = a.k, k16 = (int)a.row_bytes;
     int8_t* codes = a.codes + r * a.row_bytes;
-    if (t == 0) sh.exact = 0ull, sh.ss64 = 0.0, sh.poison = 0;
-
-    // the row once: all its loads, then v in registers, the largest magnitude, the sum of squares
-    float v[LOOP ? n : E];
-    float ss = 0.0f, own = 0.0f;
-    if constexpr (!LOOP) {
-        constexpr int batch = E == 32 && n == 4 ? 2 : E == 32 && n == 8 ? 2 : pieces;  // pieces whose loads are in flight
-#pragma unroll
-        for (int p0 = 0; p0 < pieces; p0 += batch) {
-            float x[batch][n], b[batch][n];
-#pragma unroll
-            for (int p = 0; p < batch; ++p) row.load(((p0 + p) * G + t) * n, x[p], b[p]);
-#pragma unroll
-            for (int p = 0; p < batch; ++p) {
-                row.values(((p0 + p) * G + t) * n, x[p], b[p], ss);
-#pragma unroll
-                for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j], own = max_magnitude(own, x[p][j]);
-            }
+    row_sync<WARP>();
+    if (t == 0) sh.max = 0ull, sh.ss = 0.0, sh.poison = 0;
+    row_sync<WARP>();
+    double top = 0.0, sum = 0.0;
+    bool bad = false;
+    for (int i = t; i < k; i += G) {
+        const double w = row.v_f64(i);
+        if (OP == QUANT_NORM) {
+            const double h = row.h_again(i);
+            sum += h * h;
+            bad |= !isfinite(h);
         }
-    } else {
-        float part[4] = {0.f, 0.f, 0.f, 0.f};  // short chains: a thread has many squares to add
-        for (int i = t * n, p = 0; i < k; i += G * n, ++p) {
-            float w[n], b[n], s = 0.0f;
-            row.load(i, w, b);
-            row.values(i, w, b, s);
-            part[p & 3] += s;
-#pragma unroll
-            for (int j = 0; j < n; ++j) own = max_magnitude(own, w[j]);
-        }
-        ss = (part[0] + part[1]) + (part[2] + part[3]);
+        bad |= !isfinite(w);
+        top = fmax(top, fabs(w));
     }
-    uint32_t mx = __float_as_uint(own);  // the bits of magnitudes order like the magnitudes, NaN above infinity
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if constexpr (OP == QUANT_NORM) ss = warp_sum(ss);
-    if constexpr (!WARP) {
-        if (lane == 0) sh.max[warp] = mx, sh.ss[warp] = ss;
-        __syncthreads();
-        mx = __reduce_max_sync(0xffffffffu, lane < G >> 5 ? sh.max[lane] : 0u);
-        if constexpr (OP == QUANT_NORM) ss = warp_sum(lane < G >> 5 ? sh.ss[lane] : 0.0f);
-    } else {
-        __syncwarp();
-    }
-    const float M = __uint_as_float(mx);
-    if (mx == 0u && (OP != QUANT_NORM || ss < kHuge)) {
-        // zeros (a norm whose sum of squares is NaN or beyond f32 is looked at below), or v below the smallest f32
-        bool zero = true;
-        if constexpr (OP != QUANT_ROWS) {
-            for (int i = t; i < k; i += G) zero &= row.v_f64(i) == 0.0;
-            if constexpr (WARP) zero = __all_sync(0xffffffffu, zero);
-            else zero = __syncthreads_and(zero);
-        }
-        if (zero) {
-            for (int i = t * 4; i < k16; i += G * 4) *reinterpret_cast<uint32_t*>(codes + i) = 0u;
-            if (t == 0) a.scale[r] = 0.0f;
-            return;
+    if (bad) atomicOr(&sh.poison, 1);
+    // the largest by its bits; the warps' sums in a fixed order, so that equal calls give equal bits
+    atomicMax(&sh.max, (unsigned long long)__double_as_longlong(top));
+    if constexpr (OP == QUANT_NORM) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int w = 0; w < G >> 5; ++w) {
+            if ((t & 31) == 0 && t >> 5 == w) sh.ss += sum;
+            row_sync<WARP>();
         }
     }
-
-    if (!(M >= kTiny && M <= kHuge) || (OP == QUANT_NORM && !(ss >= 1e-28f && ss <= kHuge))) {
-        // outside the range in which f32 settles codes (or not finite): the row in double
-        double top = 0.0, sum = 0.0;
-        bool bad = false;
-        for (int i = t; i < k; i += G) {
+    row_sync<WARP>();
+    const double M = __longlong_as_double((long long)sh.max);
+    const bool poison = sh.poison != 0;
+    for (int i = t; i < k16; i += G) {
+        int c = 0;
+        if (i < k && !poison && M > 0.0) {
             const double w = row.v_f64(i);
-            if (OP == QUANT_NORM) {
-                const double h = row.h_again(i);
-                sum += h * h;
-                bad |= !isfinite(h);
-            }
-            bad |= !isfinite(w);
-            top = fmax(top, fabs(w));
+            c = (int)fmax(floor(127.0 * fabs(w) / M - 0.25), 0.0);  // the code or the one below
+            while (c < 127 && above_half(w, M, (float)c)) ++c;
+            if (w < 0.0) c = -c;
         }
-        if (bad) atomicOr(&sh.poison, 1);
-        // the largest by its bits; the warps' sums in a fixed order, so that equal calls give equal bits
-        atomicMax(&sh.exact, (unsigned long long)__double_as_longlong(top));
-        if constexpr (OP == QUANT_NORM) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            for (int w = 0; w < G >> 5; ++w) {
-                if (lane == 0 && warp == w) sh.ss64 += sum;
-                row_sync<WARP>();
-            }
-        }
-        row_sync<WARP>();
-        const double M64 = __longlong_as_double((long long)sh.exact);
-        const bool poison = sh.poison != 0;
-        for (int i = t; i < k16; i += G) {
-            int c = 0;
-            if (i < k && !poison && M64 > 0.0) {
-                const double w = row.v_f64(i);
-                const float q = (float)floor(127.0 * fabs(w) / M64 - 0.25);  // the code or the one below
-                c = (int)fmaxf(q, 0.0f);
-                while (c < 127 && above_half(w, M64, (float)c)) ++c;
-                if (w < 0.0) c = -c;
-            }
-            codes[i] = (int8_t)c;
-        }
-        if (t == 0) {
-            double f = 1.0;
-            if constexpr (OP == QUANT_NORM) f = 1.0 / sqrt(sh.ss64 / k + (double)a.eps);
-            a.scale[r] = poison ? __int_as_float(0x7fffffff) : (float)(M64 == 0.0 ? 0.0 : M64 * f / 127.0);
-        }
-        return;
+        codes[i] = (int8_t)c;
     }
+    if (t == 0) {
+        const double f = OP == QUANT_NORM ? 1.0 / sqrt(sh.ss / k + (double)a.eps) : 1.0;
+        a.scale[r] = poison ? __int_as_float(0x7fffffff) : (float)(M == 0.0 ? 0.0 : M * f / 127.0);
+    }
+    row_sync<WARP>();
+}
 
-    // the exact maximum, of the elements that may be it
-    if constexpr (OP != QUANT_ROWS) {
+// The candidates for the exact maximum, ordered by one integer: the steps of f32 above `near` (they are few), the lower
+// part's sign and magnitude, the element's number (any of equal ones).
+__device__ __forceinline__ unsigned long long max_key(Two v, float near, int i) {
+    const float lo = v.hi < 0.0f ? -v.lo : v.lo;
+    return (unsigned long long)(__float_as_uint(fabsf(v.hi)) - __float_as_uint(near)) << 49 |
+           (unsigned long long)f32_order_key(lo) << 17 | (unsigned)i;
+}
+__device__ __forceinline__ Two max_of_key(unsigned long long key, float near) {
+    const uint32_t u = (uint32_t)(key >> 17);
+    return {__uint_as_float(__float_as_uint(near) + (uint32_t)(key >> 49)),
+            __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u)};
+}
+static_assert(LLAMA_Q8_I8_MAX_K <= 1 << 17, "an element's number in a key");
+
+// A row per warp (threads == 32, four per CTA) or per CTA of up to `threads`; E values of it a thread. E == 0: rows too
+// long for the registers, read again. AHEAD: a CTA takes several rows, and asks for the next one's values when it has
+// turned this one's into v.
+template <int OP, typename T, bool ALIGNED, int E, int threads, bool AHEAD>
+__global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ? 6 : threads > 512 ? 1 : 2)
+    quant_kernel(const QuantArgs a) {
+    using R = Row<OP, T, ALIGNED>;
+    constexpr bool WARP = threads == 32, LOOP = E == 0;
+    constexpr int n = R::n, pieces = E / n;
+    constexpr int kRowsPerCta = WARP ? 4 : 1;
+    __shared__ QuantShared shared[WARP ? 4 : 2];
+    __shared__ QuantSharedF64 shared64[kRowsPerCta];
+    const int G = WARP ? 32 : blockDim.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, warp = t >> 5;
+    const int k = a.k, k16 = (int)a.row_bytes;
+    int64_t r = (int64_t)blockIdx.x * kRowsPerCta + (WARP ? threadIdx.x >> 5 : 0);
+    if (r >= a.rows) return;  // a whole warp (WARP) or none
+    // two areas in turn: a row's first barrier is behind the last look at the area of the row before the last
+    int area = WARP ? threadIdx.x >> 5 : 0;
+    if (t == 0) {
+        shared[area].exact = 0ull;
+        if (!WARP) shared[1].exact = 0ull;
+    }
+    typename R::Raw raw[AHEAD ? pieces : 1];
+    if constexpr (AHEAD) {
+        const R row(a, r);
+#pragma unroll
+        for (int p = 0; p < pieces; ++p) row.load((p * G + t) * n, raw[p]);
+    }
+    for (;;) {
+        const R row(a, r);
+        QuantShared& sh = shared[area];
+        int8_t* codes = a.codes + r * a.row_bytes;
+
+        // the row once: v in registers, the largest magnitude, the sum of squares
+        float v[LOOP ? n : E];
+        float ss = 0.0f, own = 0.0f;
+        if constexpr (LOOP) {
+            float part[4] = {0.f, 0.f, 0.f, 0.f};  // short chains: a thread has many squares to add
+            for (int i = t * n, p = 0; i < k; i += G * n, ++p) {
+                float w[n], b[n], s = 0.0f;
+                row.load(i, w, b);
+                row.values(i, w, b, s);
+                part[p & 3] += s;
+#pragma unroll
+                for (int j = 0; j < n; ++j) own = max_magnitude(own, w[j]);
+            }
+            ss = (part[0] + part[1]) + (part[2] + part[3]);
+        } else {
+            constexpr int batch = E == 32 ? (n == 16 ? 1 : 2) : pieces;  // pieces whose loads are in flight together
+#pragma unroll
+            for (int p0 = 0; p0 < pieces; p0 += batch) {
+                float x[batch][n], b[batch][n];
+#pragma unroll
+                for (int p = 0; p < batch; ++p) {
+                    if constexpr (AHEAD) row.open(raw[p0 + p], x[p], b[p]);
+                    else row.load(((p0 + p) * G + t) * n, x[p], b[p]);
+                }
+#pragma unroll
+                for (int p = 0; p < batch; ++p) {
+                    row.values(((p0 + p) * G + t) * n, x[p], b[p], ss);
+#pragma unroll
+                    for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j], own = max_magnitude(own, x[p][j]);
+                }
+            }
+            if constexpr (AHEAD) {
+                if (r + gridDim.x < a.rows) {
+                    const R next(a, r + gridDim.x);
+#pragma unroll
+                    for (int p = 0; p < pieces; ++p) next.load((p * G + t) * n, raw[p]);
+                }
+            }
+        }
+        // the bits of magnitudes order like the magnitudes, NaN above infinity
+        uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(own));
+        if constexpr (OP == QUANT_NORM) ss = warp_sum(ss);
+        if constexpr (!WARP) {
+            if (lane == 0) sh.max[warp] = mx, sh.ss[warp] = ss;
+            __syncthreads();
+            mx = __reduce_max_sync(0xffffffffu, lane < G >> 5 ? sh.max[lane] : 0u);
+            if constexpr (OP == QUANT_NORM) ss = warp_sum(lane < G >> 5 ? sh.ss[lane] : 0.0f);
+            area ^= 1;
+            if (t == 0) shared[area].exact = 0ull;
+        } else {
+            __syncwarp();
+        }
+        const float M = __uint_as_float(mx);
+        if (!(M >= kTiny && M <= kHuge) || (OP == QUANT_NORM && !(ss >= 1e-28f && ss <= kHuge))) {
+            bool zero = mx == 0u && !(OP == QUANT_NORM && !(ss <= kHuge));
+            if (zero) {  // all zeros, or v below the smallest f32?
+                for (int i = t; i < k; i += G) zero &= row.zero(i);
+                if constexpr (WARP) zero = __all_sync(0xffffffffu, zero);
+                else zero = __syncthreads_and(zero);
+            }
+            if (zero) {
+                for (int i = t * 4; i < k16; i += G * 4) *reinterpret_cast<uint32_t*>(codes + i) = 0u;
+                if (t == 0) a.scale[r] = 0.0f;
+            } else {
+                quant_row_f64<OP, WARP, R>(a, r, t, G, shared64[WARP ? threadIdx.x >> 5 : 0]);
+            }
+            if (!AHEAD || (r += gridDim.x) >= a.rows) return;
+            continue;
+        }
+
+        // the exact maximum, of the elements that may be it
         const float near = M * kNearMax<OP>;
-        if (own >= near) {
+        if (OP != QUANT_ROWS && own >= near) {
             auto offer = [&](int i, float w) {
-                if (fabsf(w) >= near)
-                    atomicMax(&sh.exact, (unsigned long long)__double_as_longlong(fabs(row.v_f64(i))));
+                if (fabsf(w) >= near) {
+                    const Two e = row.v_two(i);
+                    if (fabsf(e.hi) >= near) atomicMax(&sh.exact, max_key(e, near, i));
+                }
             };
             if constexpr (!LOOP) {
 #pragma unroll
@@ -509,90 +578,104 @@ __global__ void __launch_bounds__(WARP ? 128 : E == 32 ? kQuantThreads32 : kQuan
                 }
             }
         }
-    }
 
-    // codes, rounded in f32; the elements next to a border are noted, as bits of a piece
-    const float inv = __fdiv_rn(127.0f, M);
-    auto store = [&](int i, const float* w) -> uint32_t {
-        uint32_t word[n / 4], border = 0u;
-        float off = 0.0f;
+        // codes, rounded in f32; the elements next to a border are noted, as bits of a piece
+        const float inv = __fdiv_rn(127.0f, M);
+        auto store = [&](int i, const float* w) -> uint32_t {
+            uint32_t word[n / 4], border = 0u;
+            float off = 0.0f;
 #pragma unroll
-        for (int q = 0; q < n / 4; ++q) {
-            uint32_t c[4];
+            for (int q = 0; q < n / 4; ++q) {
+                uint32_t c[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float m = fmaf(w[4 * q + j], inv, kMagic);  // rounded; its low byte is the code
-                off = fmaxf(off, fabsf(fmaf(w[4 * q + j], inv, kMagic - m)));
-                c[j] = __float_as_uint(m);
+                for (int j = 0; j < 4; ++j) {
+                    const float m = fmaf(w[4 * q + j], inv, kMagic);  // rounded; its low byte is the code
+                    off = fmaxf(off, fabsf(fmaf(w[4 * q + j], inv, kMagic - m)));
+                    c[j] = __float_as_uint(m);
+                }
+                word[q] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
             }
-            word[q] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-        }
-        if (i < k16) {
-            if constexpr (n == 16) *reinterpret_cast<uint4*>(codes + i) = make_uint4(word[0], word[1], word[2], word[3]);
-            else if constexpr (n == 8) *reinterpret_cast<uint2*>(codes + i) = make_uint2(word[0], word[1]);
-            else *reinterpret_cast<uint32_t*>(codes + i) = word[0];
-        }
-        if (off > 0.5f - kWindow<OP>) {
+            if (i < k16) {
+                if constexpr (n == 16)
+                    *reinterpret_cast<uint4*>(codes + i) = make_uint4(word[0], word[1], word[2], word[3]);
+                else if constexpr (n == 8) *reinterpret_cast<uint2*>(codes + i) = make_uint2(word[0], word[1]);
+                else *reinterpret_cast<uint32_t*>(codes + i) = word[0];
+            }
+            if (off > 0.5f - kWindow<OP>) {
 #pragma unroll
-            for (int j = 0; j < n; ++j) {
-                const float m = fmaf(w[j], inv, kMagic);
-                if (fabsf(fmaf(w[j], inv, kMagic - m)) > 0.5f - kWindow<OP>) border |= 1u << j;
+                for (int j = 0; j < n; ++j) {
+                    const float m = fmaf(w[j], inv, kMagic);
+                    if (fabsf(fmaf(w[j], inv, kMagic - m)) > 0.5f - kWindow<OP>) border |= 1u << j;
+                }
+            }
+            return border;
+        };
+        // the noted elements of the piece at i, with the exact maximum
+        auto settle = [&](int i, uint32_t border) {
+            const unsigned long long key = sh.exact;
+            const Two M2 = OP == QUANT_ROWS ? Two{M, 0.0f} : max_of_key(key, near);
+#pragma unroll 1
+            while (border) {
+                const int at = i + __ffs(border) - 1;
+                border &= border - 1u;
+                const Two w = row.v_two(at);
+                const float q = floorf(fabsf(w.hi) * inv);
+                int up = above_half(w, M2, q);
+                if (up < 0) up = above_half(row.v_f64(at), fabs(row.v_f64((int)(key & 0x1ffffu))), q);
+                const int c = (int)q + up;
+                codes[at] = (int8_t)(w.hi < 0.0f ? -c : c);
+            }
+        };
+        if constexpr (!LOOP) {
+            uint32_t border = 0u;  // E <= 32
+#pragma unroll
+            for (int p = 0; p < pieces; ++p) border |= store((p * G + t) * n, v + p * n) << (p * n);
+            if constexpr (OP != QUANT_ROWS) row_sync<WARP>();
+#pragma unroll 1
+            for (int p = 0; border; ++p, border >>= n) {
+                const uint32_t bits = border & ((1u << n) - 1u);
+                if (bits) settle((p * G + t) * n, bits);
+            }
+        } else {
+            row_sync<WARP>();
+            for (int i = t * n; i < k16; i += G * n) {
+                float w[n];
+                row.again(i, w);
+                const uint32_t bits = store(i, w);
+                if (bits) settle(i, bits);
             }
         }
-        return border;
-    };
-    // the noted elements of the piece at i, with the exact maximum
-    auto settle = [&](int i, uint32_t border) {
-        const double M64 = OP == QUANT_ROWS ? (double)M : __longlong_as_double((long long)sh.exact);
-        const Two M2 = OP == QUANT_ROWS ? Two{M, 0.0f} : two_of(M64);
-#pragma unroll 1
-        while (border) {
-            const int at = i + __ffs(border) - 1;
-            border &= border - 1u;
-            const Two w = row.v_two(at);
-            const float q = floorf(fabsf(w.hi) * inv);
-            int up = above_half(w, M2, q);
-            if (up < 0) up = above_half(row.v_f64(at), M64, q);
-            const int c = (int)q + up;
-            codes[at] = (int8_t)(w.hi < 0.0f ? -c : c);
+        if (t == 0) {  // a norm's M is the exact maximum rounded
+            const float top = OP == QUANT_SILU ? max_of_key(sh.exact, near).hi : M;
+            a.scale[r] = __fdiv_rn(top, OP == QUANT_NORM ? 127.0f * __fsqrt_rn(ss / (float)k + a.eps) : 127.0f);
         }
-    };
-    if constexpr (!LOOP) {
-        uint32_t border = 0u;  // E <= 32
-#pragma unroll
-        for (int p = 0; p < pieces; ++p) border |= store((p * G + t) * n, v + p * n) << (p * n);
-        if constexpr (OP != QUANT_ROWS) row_sync<WARP>();
-#pragma unroll 1
-        for (int p = 0; border; ++p, border = n < 32 ? border >> n : 0u) {
-            const uint32_t bits = border & ((1u << n) - 1u);
-            if (bits) settle((p * G + t) * n, bits);
-        }
-    } else {
-        row_sync<WARP>();
-        for (int i = t * n; i < k16; i += G * n) {
-            float w[n];
-            row.again(i, w);
-            const uint32_t bits = store(i, w);
-            if (bits) settle(i, bits);
-        }
-    }
-    if (t == 0) {  // M is the exact maximum rounded (silu: of the same row, to a few 2^-24)
-        const float top = OP == QUANT_SILU ? (float)__longlong_as_double((long long)sh.exact) : M;
-        a.scale[r] = __fdiv_rn(top, OP == QUANT_NORM ? 127.0f * __fsqrt_rn(ss / (float)k + a.eps) : 127.0f);
+        if (!AHEAD || (r += gridDim.x) >= a.rows) return;
     }
 }
 
 template <int OP, typename T, bool ALIGNED>
 static cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s) {
-    auto go = [&](auto kernel, int rows_per_cta, int64_t threads) {
-        const unsigned grid = (unsigned)(((int64_t)a.rows + rows_per_cta - 1) / rows_per_cta);
-        return launch_ex(kernel, dim3(grid), dim3((unsigned)((threads + 31) / 32 * 32)), 0, s, false, a);
+    auto go = [&](auto kernel, int64_t rows_per_cta, int64_t threads) {
+        const int64_t grid = (a.rows + rows_per_cta - 1) / rows_per_cta;
+        return launch_ex(kernel, dim3((unsigned)grid), dim3((unsigned)((threads + 31) / 32 * 32)), 0, s, false, a);
     };
     const int64_t k = a.row_bytes;
-    if (k <= 512) return go(quant_kernel<OP, T, ALIGNED, 16, true>, 4, 128);
-    if (k <= 16 * kQuantThreads) return go(quant_kernel<OP, T, ALIGNED, 16, false>, 1, k / 16);
-    if (k <= 32 * kQuantThreads32) return go(quant_kernel<OP, T, ALIGNED, 32, false>, 1, (k + 31) / 32);
-    return go(quant_kernel<OP, T, ALIGNED, 0, false>, 1, kQuantThreads);
+    if (k <= 16 * 32) return go(quant_kernel<OP, T, ALIGNED, 16, 32, false>, 4, 128);
+    // Several rows per CTA, as many CTAs as the SMs hold, where the next row's loads fit the registers beside v: not with
+    // two arrays of f32 (which keep memory busy without: norm of 8195 x 4096 64.9 us, the floor 64), and not where a row
+    // takes a whole SM's threads and is bound by what happens between its barriers (silu above 8192: 61 us in this form,
+    // 49 with two CTAs of 32 values a thread, 2048 x 14336 bf16), nor with Q8_0 blocks (28672 x 4096: 84 us, 73 without).
+    constexpr bool blocks = std::is_same<T, BlockQ8>::value;
+    constexpr bool ahead = ALIGNED && !blocks && (OP == QUANT_ROWS || sizeof(T) == 2);
+    constexpr bool wide = ahead && OP != QUANT_SILU;
+    const int64_t threads = (k / 16 + 31) / 32 * 32, ctas = 152 * (threads > 512 ? 1 : 1024 / threads);
+    const int64_t per = a.rows > ctas ? (a.rows + ctas - 1) / ctas : 1;
+    if (k <= 16 * kQuantThreads) return go(quant_kernel<OP, T, ALIGNED, 16, kQuantThreads, ahead>, ahead ? per : 1, k / 16);
+    if (k <= 32 * kQuantThreads32) {
+        if constexpr (wide) return go(quant_kernel<OP, T, ALIGNED, 16, 2 * kQuantThreads32, true>, per, threads);
+        else return go(quant_kernel<OP, T, ALIGNED, 32, kQuantThreads32, false>, 1, (k + 31) / 32);
+    }
+    return go(quant_kernel<OP, T, ALIGNED, 0, kQuantThreads, false>, 1, kQuantThreads);
 }
 
 // 16-byte loads and stores: k a multiple of a piece, rows and bases on 16-byte boundaries.
