@@ -724,7 +724,9 @@ llama_q8_status llama_q8_norm_quant(int32_t type, const void* x, int64_t x_strid
 /* Codes and a scale for each row of silu(gate) * up, silu(z) = z / (1 + exp(-z)), by the
  * rule of llama_q8_rows_quant. gate and up have the same row stride: columns 0 .. k - 1 and
  * k .. 2k - 1 of one product, or two arrays. A row with a NaN or an infinity in gate or up
- * has codes 0 and scale NaN. Enqueues one kernel. */
+ * has codes 0 and scale NaN. Products that lie within double precision of a half (those of one
+ * gate and several ups can be halves exactly) go the way that their quotient in double goes.
+ * Enqueues one kernel. */
 llama_q8_status llama_q8_silu_quant(int32_t type, const void* gate, const void* up, int64_t stride, int32_t rows,
                                     int32_t k, int8_t* codes, float* scale, void* stream);
 

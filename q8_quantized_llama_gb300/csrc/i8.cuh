@@ -51,7 +51,7 @@ template <typename T, typename S> __device__ __forceinline__ T i8_scaled(S sum, 
 }
 
 // i8_gemm.cu: m >= kI8GemmMin tokens on the tensor cores, in a workspace of i8_gemm_workspace bytes
-constexpr int kI8GemmMin = 9;
+constexpr int kI8GemmMin = 17;
 size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m);
 template <typename T>
 cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,

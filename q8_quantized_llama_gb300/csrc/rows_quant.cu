@@ -346,9 +346,11 @@ template <bool ALIGNED> struct Row<QUANT_ROWS, BlockQ8, ALIGNED> {
     __device__ double v_f64(int i) const { return (double)load_one<BlockQ8>(a.x, xa, i); }
 };
 
-// Whether 127 |v| / M is at least q + 1/2, from exact v and M: the sign of 254 |v| - (2 q + 1) M. Where the two
-// products are close their difference is exact, and so is the rounding error that is taken off.
-__device__ __forceinline__ bool above_half(double v, double M, float q) {
+// Whether 127 |v| / M is at least q + 1/2, in double. rows and norm have exact v and M: the sign of 254 |v| - (2 q + 1) M
+// (where the two products are close their difference is exact, and so is the rounding error that is taken off). silu's are
+// rounded, and halves that are exact in fact (one gate, two ups) are taken as the quotient in double has them.
+template <int OP> __device__ __forceinline__ bool above_half(double v, double M, float q) {
+    if constexpr (OP == QUANT_SILU) return 127.0 * fabs(v) / M - (double)q >= 0.5;
     const double odd = 2.0 * (double)q + 1.0, p = odd * M, e = fma(odd, M, -p);
     return fma(254.0, fabs(v), -p) - e >= 0.0;
 }
@@ -425,7 +427,7 @@ __device__ __forceinline__ void quant_row_f64(const QuantArgs& a, int64_t r, int
         if (i < k && !poison && M > 0.0) {
             const double w = row.v_f64(i);
             c = (int)fmax(floor(127.0 * fabs(w) / M - 0.25), 0.0);  // the code or the one below
-            while (c < 127 && above_half(w, M, (float)c)) ++c;
+            while (c < 127 && above_half<OP>(w, M, (float)c)) ++c;
             if (w < 0.0) c = -c;
         }
         codes[i] = (int8_t)c;
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
                 const Two w = row.v_two(at);
                 const float q = floorf(fabsf(w.hi) * inv);
                 int up = above_half(w, M2, q);
-                if (up < 0) up = above_half(row.v_f64(at), fabs(row.v_f64((int)(key & 0x1ffffu))), q);
+                if (up < 0) up = above_half<OP>(row.v_f64(at), fabs(row.v_f64((int)(key & 0x1ffffu))), q);
                 const int c = (int)q + up;
                 codes[at] = (int8_t)(w.hi < 0.0f ? -c : c);
             }

@@ -212,6 +212,25 @@ def test_silu_quant_near_halves(B, k):
     _check(codes, scale, 3, I.silu_quant(gate, up), 2 * U)
 
 
+def test_silu_quant_halves_of_one_gate(B):
+    """One gate and ups whose ratios are exact halves: either neighbour is as near; every other code is the nearest."""
+    rng = np.random.default_rng(5)
+    rows, k = 40, 300
+    gate = np.repeat((rng.standard_normal((rows, 1)) * 4.0).astype(np.float32), k, 1)
+    up = (rng.integers(-127, 127, (rows, k)) + 0.5).astype(np.float32)
+    up[:, 9] = 127.0
+    codes, scale = _outputs(rows, k)
+    B.llama_q8_silu_quant(0, torch.from_numpy(gate).cuda(), torch.from_numpy(up).cuda(), k, rows, k, codes, scale)
+    torch.cuda.synchronize()
+    got = codes[:rows, :k].cpu().numpy() * np.sign(gate)
+    assert (np.abs(got - up)[:, np.arange(k) != 9] == 0.5).all() and (got[:, 9] == 127).all()
+    off = np.nextafter(up, np.float32(np.inf))  # just past the halves: no choice is left
+    off[:, 9] = 127.0
+    B.llama_q8_silu_quant(0, torch.from_numpy(gate).cuda(), torch.from_numpy(off).cuda(), k, rows, k, codes, scale)
+    torch.cuda.synchronize()
+    assert np.array_equal(codes[:rows, :k].cpu().numpy() * np.sign(gate), np.where(off == 127, 127, np.floor(off + 0.5)))
+
+
 # ---- rows that f32 does not hold, zeros, NaN and infinities
 
 @pytest.mark.parametrize("k", [20, 576, 5000, 17000])
