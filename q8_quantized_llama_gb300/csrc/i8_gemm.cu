@@ -9,27 +9,29 @@
 // the others are read out as integers after every 1024 products (1024 * 128^2 =
 // 2^24).
 //
-// i8_widen_kernel turns the token rows into f16 once per call and notes their
-// norms. i8_gemm_kernel: CTA tile 128 channels (M) x bn tokens (N, a multiple of
-// 16 up to 256), one CTA per SM, persistent; a stage holds KS blocks of 64 codes of
-// k (two up to 128 tokens, where the products are shorter than what surrounds
-// them). Warp roles:
-//  - two producers: the f16 token tile (128-byte rows of 64 values, 128-byte swizzle:
-//    the K-major B operand, used in place) and the codes of the four 32-row tiles,
-//    each by one tensor copy per block;
+// i8_gemm_kernel: CTA tile 128 channels (M) x bn tokens (N, a multiple of 16 up to
+// 256), one CTA per SM, persistent; a stage holds KS blocks of 64 codes of k (two up
+// to 128 tokens, where the products are shorter than what surrounds them). More than
+// 64 tokens are turned into f16 once per call by i8_widen_kernel, which also notes
+// their norms; fewer (NARROW) are turned into f16 by every CTA for itself, which saves
+// the launch before and the wait for it (48 tokens over 4096 x 14336: 5 of 21 us).
+// Warp roles:
+//  - two producers: the token tile (f16: 128-byte rows of 64 values, 128-byte swizzle,
+//    the K-major B operand, used in place; NARROW: codes) and the codes of the four
+//    32-row tiles, by tensor copies;
 //  - two groups of 4 converter warps, one for the even and one for the odd stages: row
 //    r's codes as f16 into lane r of tensor memory (the A operand), one stage's columns
-//    next to the other's;
+//    next to the other's; NARROW: also the tokens' codes into the B operand;
 //  - MMA warp: one thread issues four 128 x bn x 16 products per block;
 //  - 8 accumulator warps read the finished sums (every second group of 16 columns
 //    each), apply the scales and store: a warp's 32 lanes hold 32 neighbouring
 //    channels of a token, 128 bytes of y.
 //
 // Work is dealt in whole tiles (tokens fastest, so that the CTAs that share a weight
-// tile run together). The tiles that do not fill a wave are cut into equal runs of
-// k-blocks, one per CTA, where that is shorter: their parts are added to sums in the
-// workspace (integers: in any order the same), and the CTA that brings the last part
-// of a tile stores it.
+// tile run together). The tiles that do not fill a wave are cut along k into parts,
+// one per CTA, where that is shorter: every CTA leaves its part's sums (integers) in
+// the workspace, and the one that brings a tile's last part adds the others to its
+// own and stores.
 #include "i8.cuh"
 #include "kernels.cuh"
 #include "llama_q8.h"
@@ -48,6 +50,7 @@ constexpr int kI8StagesMax = 8;
 constexpr int kI8CodeBytes = kI8BM * 64;  // a block's codes
 constexpr int kI8Smem = 220 * 1024;       // stages, in units of what a tile's width needs
 constexpr int kI8Exact = 16;              // blocks whose products cannot pass 2^24
+constexpr int kI8Narrow = 64;             // tokens up to which every CTA makes its own f16 of them
 constexpr int kI8ACols = 32;              // tensor-memory columns of a block's A
 
 struct I8Gemm {
@@ -56,12 +59,12 @@ struct I8Gemm {
     const float* sa;
     int m, bn, token_tiles, kb;
     int stages, buffers;
-    int64_t tiles, cut0;  // tiles from cut0 on are cut into runs for the first `cutters` CTAs
-    int cutters;
+    int64_t tiles, cut0;  // tiles from cut0 on are cut into `parts`, one for each of the first (tiles - cut0) parts CTAs
+    int parts;
     int64_t y_stride;
-    int32_t* sums;       // of the cut tiles, [tile][bn][128], zero at the start
+    int32_t* part;       // [CTA][bn][128]: the sums of its part
     int32_t* spare;      // [CTA][bn][128]: sums so far of a whole tile that is read out more than once
-    unsigned* counters;  // per cut tile: blocks that have arrived
+    unsigned* counters;  // per cut tile: parts that have arrived
     int32_t* err;
 };
 
@@ -117,26 +120,26 @@ __device__ __forceinline__ void i8_box(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
-// The segments of tiles that a CTA works on, the same for all its warps: its run of the cut tiles, then whole tiles.
+// The segments of tiles that a CTA works on, the same for all its warps: its part of a cut tile, then whole tiles.
 struct I8Segments {
     const I8Gemm& g;
-    int64_t at, end, whole, tile;
+    int64_t whole, tile;
     int k0, k1;
-    __device__ I8Segments(const I8Gemm& args) : g(args), at(0), end(0), whole(blockIdx.x) {
-        const int64_t units = (g.tiles - g.cut0) * g.kb;
-        if ((int)blockIdx.x < g.cutters)
-            at = units * blockIdx.x / g.cutters, end = units * (blockIdx.x + 1) / g.cutters;
-    }
+    bool cut;  // the segment to come or at hand is a part
+    __device__ I8Segments(const I8Gemm& args) : g(args), whole(-1) {}
     __device__ bool next() {
-        if (at < end) {
-            tile = at / g.kb, k0 = (int)(at % g.kb);
-            k1 = (int)(end - at < g.kb - k0 ? k0 + (end - at) : g.kb);
-            at += k1 - k0;
-            tile += g.cut0;
-            return true;
+        if (whole < 0) {
+            whole = blockIdx.x;
+            const int64_t at = g.cut0 + blockIdx.x / g.parts;
+            cut = g.parts > 1 && at < g.tiles;
+            if (cut) {
+                const int64_t p = blockIdx.x % g.parts;
+                tile = at, k0 = (int)(g.kb * p / g.parts), k1 = (int)(g.kb * (p + 1) / g.parts);
+                return true;
+            }
         }
         if (whole >= g.cut0) return false;
-        tile = whole, k0 = 0, k1 = g.kb;
+        cut = false, tile = whole, k0 = 0, k1 = g.kb;
         whole += gridDim.x;
         return true;
     }
@@ -181,7 +184,7 @@ __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int to
     return warp_max(w) * warp_max(a) <= 16777216.0f;
 }
 
-template <typename T, int KS>
+template <typename T, int KS, bool NARROW>
 __global__ void __launch_bounds__(kI8Threads, 1)
     i8_gemm_kernel(const I8Gemm g, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                    T* __restrict__ y) {
@@ -196,8 +199,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __shared__ unsigned arrived;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // a stage: KS token tiles, then KS blocks of codes
-    const int stages = g.stages, token_bytes = g.bn * 128, stage_bytes = KS * (token_bytes + kI8CodeBytes);
+    // a stage: KS token tiles, then KS blocks of codes, NARROW: then the tokens' codes
+    const int stages = g.stages, token_bytes = g.bn * 128;
+    const int stage_bytes = KS * (token_bytes + kI8CodeBytes) + (NARROW ? token_bytes : 0);
     if (tid == 0) {
         for (int s = 0; s < kI8StagesMax; ++s) {
             mbar_init(&full_bar[s], 2);
@@ -223,9 +227,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         // boxes are whole: codes past the last chunk or tile and tokens past the last arrive as zeros
         const bool codes = warp == kI8CodeWarp;
         const CUtensorMap* map = codes ? &wmap : &amap;
-        const uint32_t to = data + (codes ? KS * token_bytes : 0), size = codes ? kI8CodeBytes : token_bytes;
+        const uint32_t to = data + (codes ? KS * token_bytes : NARROW ? KS * (token_bytes + kI8CodeBytes) : 0);
+        const uint32_t size = codes ? kI8CodeBytes : token_bytes;
         const int step = codes ? 256 : 64;  // a block in the map's elements
-        if (!codes) pdl_wait();  // the codes do not depend on the kernel before
+        if (!NARROW && !codes) pdl_wait();  // the codes do not depend on the kernel before
         I8Segments seg(g);
         I8Ring ring(stages);
         bool again = false;  // past the first pass over the stages
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 }
                 if (i8_elect()) {
                     const uint32_t bar = full + s * 8, at = to + s * stage_bytes;
-                    const bool two = KS == 2 && kb + 1 < seg.k1;
+                    const bool two = KS == 2 && kb + 1 < seg.k1 && (codes || !NARROW);  // a box of token codes is a stage
                     i8_expect(bar, two ? 2 * size : size);
                     i8_box(at, map, kb * step, row, bar);
                     if (two) i8_box(at + size, map, (kb + 1) * step, row, bar);
@@ -249,14 +254,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             }
         }
         // every copy has landed before the CTA may exit: the last of each stage
-        if (codes) pdl_wait();
+        if (!NARROW && codes) pdl_wait();
         for (int i = 0; i < stages; ++i) {
             if (i >= ring.at && !again) break;
             i8_wait(full + i * 8, i < ring.at ? ring.parity : ring.parity ^ 1u, g.err);
         }
         __syncwarp();
     } else if (warp == kI8MmaWarp) {
-        pdl_wait();
+        if (!NARROW) pdl_wait();
         const uint32_t idesc = idesc_f16(kI8BM, (uint32_t)g.bn);
         const uint64_t desc0 = sw128_desc(data);
         I8Segments seg(g);
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         uint32_t last = 0, last_parity = 0;
         while (alive && seg.next()) {
             const int n = seg.k1 - seg.k0;
-            const bool one = n <= kI8Exact || i8_one_sum(g, seg.channel0(), seg.token0(), lane);
+            const bool one = n <= kI8Exact || (!NARROW && i8_one_sum(g, seg.channel0(), seg.token0(), lane));
             for (int left = n; left > 0 && alive;) {
                 int blocks = one ? left : min(left, kI8Exact);
                 left -= blocks;
@@ -337,22 +342,45 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     }
                     tmem_st16(base + (uint32_t)(s * KS * kI8ACols + h * 16), u);
                 }
+                if constexpr (NARROW) {
+                    // 16 codes of a token: two 16-byte pieces of its row, each swizzled by the row
+                    const uint32_t to = data + s * stage_bytes, codes = to + KS * (token_bytes + kI8CodeBytes);
+                    for (int i = (warp & 3) * 32 + lane; i < g.bn * 8; i += 128) {
+                        const int row = i >> 3, c = i & 7;
+                        uint4 q, lo, hi;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                     : "r"(codes + i * 16));
+                        codes_to_f16x2(q.x, lo.x, lo.y);
+                        codes_to_f16x2(q.y, lo.z, lo.w);
+                        codes_to_f16x2(q.z, hi.x, hi.y);
+                        codes_to_f16x2(q.w, hi.z, hi.w);
+                        const uint32_t at = to + (c >> 2) * token_bytes + row * 128, j = (uint32_t)((c & 3) * 2);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((j ^ (row & 7)) << 4)), "r"(lo.x),
+                                     "r"(lo.y), "r"(lo.z), "r"(lo.w)
+                                     : "memory");
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((j + 1) ^ (row & 7)) << 4)),
+                                     "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                                     : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read what was stored
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) i8_arrive(conv + s * 8);
             }
     } else {
-        pdl_wait();
+        if (!NARROW) pdl_wait();
         const int quarter = warp & 3, half = (warp - kI8AccWarp0) >> 2, groups = g.bn / 16;
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int64_t part = (int64_t)g.bn * kI8BM, off = quarter * 32 + lane;
         // a warp whose wait ran out still meets the others at their barriers
         I8Segments seg(g);
         I8Ring sums(g.buffers);
         while (seg.next()) {
             const int n = seg.k1 - seg.k0, channel0 = seg.channel0(), token0 = seg.token0();
-            const bool one = n <= kI8Exact || i8_one_sum(g, channel0, token0, lane);
-            const bool whole = n == g.kb;
+            const bool one = n <= kI8Exact || (!NARROW && i8_one_sum(g, channel0, token0, lane));
             const int channel = channel0 + quarter * 32 + lane;
             const bool mine = channel < g.W.rows;
             const float sw = mine ? g.W.scale[channel] : 0.0f;
@@ -372,55 +400,120 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                         if (mine && t0 + j < g.m) *at = i8_scaled<T>(v[j], __ldg(sa + j), sw);
                 }
             };
-            const int64_t part = (int64_t)g.bn * kI8BM, off = quarter * 32 + lane;
-            int32_t* sum = whole ? g.spare + blockIdx.x * part + off : g.sums + (seg.tile - g.cut0) * part + off;
             const int chunks = one ? 1 : (n + kI8Exact - 1) / kI8Exact;
-            for (int ch = 0; ch < chunks; ++ch, sums.next()) {
-                const int p = sums.at;
-                if (alive) alive = i8_wait(sfull + p * 8, sums.parity, g.err);
-                alive = __all_sync(0xffffffffu, alive);
-                if (!alive) break;
-                tc_fence_after();
-                for (int gr = half; gr < groups; gr += 2) {
-                    float v[16];
-                    tmem_ld16(base + (uint32_t)(p * g.bn + gr * 16), v);
-                    int32_t* at = sum + gr * 16 * kI8BM;
-                    if (whole && chunks == 1) {
-                        store(gr, v);
-                    } else if (!whole) {
+            // whether this CTA brings its cut tile's last part: the others' are in memory for it then
+            int32_t* const parts = g.part + off;
+            const int first = (int)(blockIdx.x - blockIdx.x % g.parts);
+            auto last_of_tile = [&] {
+                unsigned* counter = &g.counters[blockIdx.x / g.parts];
+                named_bar_sync(1, kI8AccWarps * 32);
+                if (tid == kI8AccWarp0 * 32) {
+                    arrived = take_ticket(counter) + 1;
+                    if (arrived == (unsigned)g.parts) *counter = 0u;
+                }
+                named_bar_sync(1, kI8AccWarps * 32);
+                return arrived == (unsigned)g.parts && alive;
+            };
+            if constexpr (NARROW) {
+                // up to 64 tokens: a warp's two groups of sums stay in registers
+                int sum[2][16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) atomicAdd(at + j * kI8BM, __float2int_rn(v[j]));
-                    } else {
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[h][j] = 0;
+                for (int ch = 0; ch < chunks; ++ch, sums.next()) {
+                    const int p = sums.at;
+                    if (alive) alive = i8_wait(sfull + p * 8, sums.parity, g.err);
+                    alive = __all_sync(0xffffffffu, alive);
+                    if (!alive) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (half + 2 * h >= groups) break;
+                        float v[16];
+                        tmem_ld16(base + (uint32_t)(p * g.bn + (half + 2 * h) * 16), v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[h][j] += __float2int_rn(v[j]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) i8_arrive(sempty + p * 8);
+                }
+                if (seg.cut) {
+                    int32_t* mypart = parts + blockIdx.x * part;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (half + 2 * h >= groups) break;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) mypart[((half + 2 * h) * 16 + j) * kI8BM] = sum[h][j];
+                    }
+                    if (!last_of_tile()) continue;
+                    for (int c = first; c < first + g.parts; ++c) {
+                        if (c == (int)blockIdx.x) continue;
+                        const int32_t* other = parts + c * part;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (half + 2 * h >= groups) break;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[h][j] += __ldcg(other + ((half + 2 * h) * 16 + j) * kI8BM);
+                        }
+                    }
+                }
+                if (!alive) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (half + 2 * h < groups) store(half + 2 * h, sum[h]);
+            } else {
+                int32_t* sum = seg.cut ? parts + blockIdx.x * part : g.spare + blockIdx.x * part + off;
+                for (int ch = 0; ch < chunks; ++ch, sums.next()) {
+                    const int p = sums.at;
+                    if (alive) alive = i8_wait(sfull + p * 8, sums.parity, g.err);
+                    alive = __all_sync(0xffffffffu, alive);
+                    if (!alive) break;
+                    tc_fence_after();
+                    for (int gr = half; gr < groups; gr += 2) {
+                        float v[16];
+                        tmem_ld16(base + (uint32_t)(p * g.bn + gr * 16), v);
+                        int32_t* at = sum + gr * 16 * kI8BM;
+                        if (chunks == 1 && !seg.cut) {
+                            store(gr, v);
+                            continue;
+                        }
                         int i[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) i[j] = __float2int_rn(v[j]) + (ch > 0 ? at[j * kI8BM] : 0);
-                        if (ch == chunks - 1) {
+                        if (ch == chunks - 1 && !seg.cut) {
                             store(gr, i);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) at[j * kI8BM] = i[j];
                         }
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) i8_arrive(sempty + p * 8);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) i8_arrive(sempty + p * 8);
-            }
-            if (!whole) {
-                // the part has been added; the CTA that brings the tile's last blocks stores it
-                named_bar_sync(1, kI8AccWarps * 32);
-                if (tid == kI8AccWarp0 * 32) arrived = take_ticket(&g.counters[seg.tile - g.cut0], (unsigned)n) + n;
-                named_bar_sync(1, kI8AccWarps * 32);
-                if (alive && arrived == (unsigned)g.kb) {
-                    if (tid == kI8AccWarp0 * 32) g.counters[seg.tile - g.cut0] = 0u;
-                    for (int gr = half; gr < groups; gr += 2) {
-                        int i[16];
+                if (!seg.cut || !last_of_tile()) continue;
+                // two groups' sums are asked for together
+                for (int gr = half; gr < groups; gr += 4) {
+                    int i[2][16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) i[j] = __ldcg(sum + gr * 16 * kI8BM + j * kI8BM);
-                        store(gr, i);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) i[h][j] = 0;
+                    for (int c = first; c < first + g.parts; ++c) {
+                        const int32_t* from = parts + c * part;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = gr + 2 * h < groups ? gr + 2 * h : gr;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) i[h][j] += __ldcg(from + (at * 16 + j) * kI8BM);
+                        }
                     }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (gr + 2 * h < groups) store(gr + 2 * h, i[h]);
                 }
-                named_bar_sync(1, kI8AccWarps * 32);  // `arrived` has been read
             }
         }
     }
@@ -429,20 +522,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     if (warp == kI8MmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The token rows as f16 and their norms, rounded up: one CTA per row. Further CTAs clear the sums of the cut tiles
-// (kI8Clear of 16 bytes each).
-constexpr int kI8Clear = 2048;
-__global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__ codes, int64_t rows, int64_t chunks,
-                                                       uint4* __restrict__ wide, float* __restrict__ norm,
-                                                       uint4* __restrict__ sums, int64_t n_sums) {
+// The token rows as f16 and their norms, rounded up: one CTA per row.
+__global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__ codes, int64_t chunks,
+                                                       uint4* __restrict__ wide, float* __restrict__ norm) {
     __shared__ uint32_t part[8];
     pdl_launch_dependents();
     const int64_t row = blockIdx.x;
-    if (row >= rows) {
-        const int64_t at = (row - rows) * kI8Clear, end = n_sums - at < kI8Clear ? n_sums - at : kI8Clear;
-        for (int64_t i = threadIdx.x; i < end; i += 256) sums[at + i] = make_uint4(0, 0, 0, 0);
-        return;
-    }
     int sum = 0;
     for (int64_t c = threadIdx.x; c < chunks; c += 256) {
         const uint4 q = codes[row * chunks + c];
@@ -471,11 +556,23 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__
 // ---- the plan of a call, from its sizes alone ------------------------------------------
 struct I8Plan {
     int64_t tokens;  // of one launch
-    int bn, ks, token_tiles, kb, stages, buffers, cutters;
+    int bn, ks, token_tiles, kb, stages, buffers, parts;
+    bool narrow;
     int64_t tiles, cut0;
-    int64_t sums;  // 16-byte pieces
-    size_t at_wide, at_norms, at_sums, at_spare, total;  // byte offsets in the workspace
+    size_t at_wide, at_norms, at_part, at_spare, total;  // byte offsets in the workspace
 };
+
+// Microseconds of a launch with token tiles of bn and `parts` parts of each tile past the last full wave, from what was
+// measured: a block takes 0.22 us and a little more for each token of the tile (0.25 at 64, 0.30 at 128, 0.36 at 256),
+// storing a tile 0.5 us and 1 / 100 us per token, a part's way through the workspace 2 us, and each further one's sums
+// another 1 us for every 64 tokens.
+static double i8_cost(int64_t tiles, int kb, int bn, int parts) {
+    const double block = bn <= 128 ? 0.20 + 0.0008 * bn : 0.24 + 0.00047 * bn, out = 0.5 + 0.01 * bn;
+    const int64_t rest = tiles % kI8Ctas;
+    double t = (double)(tiles / kI8Ctas) * (kb * block + out);
+    if (rest) t += (double)((kb + parts - 1) / parts) * block + out + (parts > 1 ? 2.0 + (parts - 1) * bn / 64.0 : 0.0);
+    return t;
+}
 
 static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
     I8Plan p{};
@@ -484,34 +581,38 @@ static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
     int64_t most = (512ll << 20) / (2 * k16) / 256 * 256;
     most = most < 2048 ? 2048 : most > 65536 ? 65536 : most;
     p.tokens = m < most ? m : most;
-    p.token_tiles = (int)((p.tokens + 255) / 256);
-    p.bn = (int)(((p.tokens + p.token_tiles - 1) / p.token_tiles + 15) / 16 * 16);
-    if (p.bn < 32) p.bn = 32;
-    p.tiles = (rows + kI8BM - 1) / kI8BM * p.token_tiles;
     p.kb = (int)((k16 + 63) / 64);
+    p.narrow = p.tokens <= kI8Narrow;
+    // token tiles from the fewest on, and parts
+    const int64_t row_tiles = (rows + kI8BM - 1) / kI8BM;
+    double best = 0.0;
+    for (int64_t tt = (p.tokens + 255) / 256, tries = 0; tries < 8; ++tt, ++tries) {
+        int bn = (int)(((p.tokens + tt - 1) / tt + 15) / 16 * 16);
+        if (bn < 32) bn = 32;
+        const int64_t tiles = row_tiles * tt, rest = tiles % kI8Ctas;
+        for (int parts = 1; parts == 1 || (rest && parts * rest <= kI8Ctas && parts <= 8 && p.kb >= 4 * parts); ++parts) {
+            const double t = i8_cost(tiles, p.kb, bn, parts);
+            if (p.bn == 0 || t < best)
+                best = t, p.bn = bn, p.token_tiles = (int)tt, p.tiles = tiles, p.parts = parts,
+                p.cut0 = parts > 1 ? tiles - rest : tiles;
+        }
+        if (bn == 32) break;
+    }
     p.ks = p.bn <= 128 ? 2 : 1;
-    p.stages = kI8Smem / (p.ks * (p.bn * 128 + kI8CodeBytes));
+    p.stages = kI8Smem / (p.ks * (p.bn * 128 + kI8CodeBytes) + (p.narrow ? p.bn * 128 : 0));
     if (p.stages > kI8StagesMax) p.stages = kI8StagesMax;
     // two buffers of sums where four stages still fit beside them
     const int cols = p.ks * kI8ACols;
     p.buffers = (512 - 2 * p.bn) / cols >= 4 ? 2 : 1;
     const int room = (512 - p.buffers * p.bn) / cols;
     if (p.stages > room) p.stages = room;
-    // The tiles past the last full wave, whole: kb blocks of time. Cut: their share and about 8 blocks for adding the
-    // parts up (runs of at least 4 blocks: each part costs as much as those).
-    const int64_t rest = p.tiles % kI8Ctas, units = rest * p.kb;
-    p.cut0 = p.tiles;
-    if (rest) {
-        int64_t runs = units / 4 < kI8Ctas ? units / 4 : kI8Ctas;
-        if (runs > rest && p.kb > (units + runs - 1) / runs + 8) p.cut0 = p.tiles - rest, p.cutters = (int)runs;
-    }
-    p.sums = (p.tiles - p.cut0) * p.bn * kI8BM / 4;
+    const size_t tile = (size_t)p.bn * kI8BM * 4;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p.at_wide = kCounterBytes;
-    p.at_norms = up(p.at_wide + (size_t)p.tokens * k16 * 2);
-    p.at_sums = up(p.at_norms + (size_t)p.tokens * 4);
-    p.at_spare = up(p.at_sums + (size_t)p.sums * 16);
-    p.total = up(p.at_spare + (p.kb > kI8Exact ? (size_t)kI8Ctas * p.bn * kI8BM * 4 : 0));
+    p.at_norms = up(p.at_wide + (p.narrow ? 0 : (size_t)p.tokens * k16 * 2));
+    p.at_part = up(p.at_norms + (p.narrow ? 0 : (size_t)p.tokens * 4));
+    p.at_spare = up(p.at_part + (p.parts > 1 ? (size_t)(p.tiles - p.cut0) * p.parts * tile : 0));
+    p.total = up(p.at_spare + (!p.narrow && p.kb > kI8Exact ? kI8Ctas * tile : 0));
     return p;
 }
 
@@ -524,10 +625,10 @@ static size_t i8_workspace(int64_t rows, int64_t k, int64_t m, const I8Plan& fir
 size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m) { return i8_workspace(rows, k, m, i8_plan(rows, k, m)); }
 
 template <typename T> static cudaError_t i8_gemm_attributes() {
-    cudaError_t e =
-        cudaFuncSetAttribute(i8_gemm_kernel<T, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(i8_gemm_kernel<T, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
+    cudaError_t e = cudaSuccess;
+    for (auto kernel : {i8_gemm_kernel<T, 1, false>, i8_gemm_kernel<T, 2, false>, i8_gemm_kernel<T, 2, true>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8Smem + 1024);
     return e;
 }
 cudaError_t init_i8_gemm_attributes() {
@@ -563,22 +664,28 @@ cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const
         const I8Plan p = i8_plan(W.rows, k, part);
         __half* wide = reinterpret_cast<__half*>(ws + p.at_wide);
         float* norms = reinterpret_cast<float*>(ws + p.at_norms);
-        const int64_t clear = (p.sums + kI8Clear - 1) / kI8Clear;
-        e = launch_ex(i8_widen_kernel, dim3((unsigned)(part + clear)), dim3(256), 0, s, false,
-                      reinterpret_cast<const uint4*>(a + t * k16), part, W.chunks, reinterpret_cast<uint4*>(wide), norms,
-                      reinterpret_cast<uint4*>(ws + p.at_sums), p.sums);
-        if (e != cudaSuccess) return e;
-        if (!encode(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wide, (cuuint64_t)k16, (cuuint64_t)part, (cuuint64_t)k16 * 2,
-                    64, (cuuint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B))
-            return cudaErrorInvalidValue;
+        const int8_t* tokens = a + t * k16;
+        if (!p.narrow) {
+            e = launch_ex(i8_widen_kernel, dim3((unsigned)part), dim3(256), 0, s, false,
+                          reinterpret_cast<const uint4*>(tokens), W.chunks, reinterpret_cast<uint4*>(wide), norms);
+            if (e != cudaSuccess) return e;
+        }
+        const bool mapped =
+            p.narrow ? encode(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT8, tokens, (cuuint64_t)k16, (cuuint64_t)part,
+                              (cuuint64_t)k16, 128, (cuuint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_NONE)
+                     : encode(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wide, (cuuint64_t)k16, (cuuint64_t)part,
+                              (cuuint64_t)k16 * 2, 64, (cuuint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (!mapped) return cudaErrorInvalidValue;
         I8Gemm g{};
         g.W = W, g.anorm = norms, g.sa = sa + t, g.m = (int)part, g.bn = p.bn, g.token_tiles = p.token_tiles;
         g.kb = p.kb, g.stages = p.stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
-        g.cutters = p.cutters, g.y_stride = y_stride, g.sums = reinterpret_cast<int32_t*>(ws + p.at_sums);
+        g.parts = p.parts, g.y_stride = y_stride, g.part = reinterpret_cast<int32_t*>(ws + p.at_part);
         g.spare = reinterpret_cast<int32_t*>(ws + p.at_spare), g.counters = reinterpret_cast<unsigned*>(ws), g.err = err;
-        const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > p.cutters ? p.cut0 : p.cutters;
-        e = launch_ex(p.ks == 2 ? i8_gemm_kernel<T, 2> : i8_gemm_kernel<T, 1>, dim3((unsigned)ctas), dim3(kI8Threads),
-                      (size_t)kI8Smem + 1024, s, true, g, amap, wmap, y + t * y_stride);
+        const int64_t cutters = p.parts > 1 ? (p.tiles - p.cut0) * p.parts : 0;
+        const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > cutters ? p.cut0 : cutters;
+        e = launch_ex(p.narrow ? i8_gemm_kernel<T, 2, true> : p.ks == 2 ? i8_gemm_kernel<T, 2, false> : i8_gemm_kernel<T, 1, false>,
+                      dim3((unsigned)ctas), dim3(kI8Threads), (size_t)kI8Smem + 1024, s, !p.narrow, g, amap, wmap,
+                      y + t * y_stride);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
