@@ -18,10 +18,11 @@
 // Warp roles:
 //  - two producers: the token tile (f16: 128-byte rows of 64 values, 128-byte swizzle,
 //    the K-major B operand, used in place; NARROW: codes) and the codes of the four
-//    32-row tiles, by tensor copies;
-//  - two groups of 4 converter warps, one for the even and one for the odd stages: row
-//    r's codes as f16 into lane r of tensor memory (the A operand), one stage's columns
-//    next to the other's; NARROW: also the tokens' codes into the B operand;
+//    32-row tiles, by tensor copies, each into a ring of its own: codes make room as soon
+//    as they are converted, tokens when they are multiplied;
+//  - two groups of 4 converter warps, taking stages in turn: row r's codes as f16 into
+//    lane r of tensor memory (the A operand), one stage's columns next to the other's;
+//    NARROW: 4 warps more for the tokens' codes;
 //  - MMA warp: one thread issues four 128 x bn x 16 products per block;
 //  - 8 accumulator warps read the finished sums (every second group of 16 columns
 //    each), apply the scales and store: a warp's 32 lanes hold 32 neighbouring
@@ -42,13 +43,14 @@ namespace lq8 {
 
 constexpr int kI8BM = 128;
 constexpr int kI8Ctas = 152;       // SMs of a GB300; the plan does not depend on the device at hand
-constexpr int kI8ConvWarps = 8, kI8AccWarps = 8;
-constexpr int kI8AccWarp0 = kI8ConvWarps, kI8TokenWarp = kI8AccWarp0 + kI8AccWarps, kI8CodeWarp = kI8TokenWarp + 1,
-              kI8MmaWarp = kI8CodeWarp + 1;
-constexpr int kI8Threads = (kI8MmaWarp + 1) * 32;
+constexpr int kI8AccWarps = 8;
+// warps: accumulators, code converters, producers of tokens and of codes, MMA issuer, NARROW: token converters
+constexpr int kI8ConvWarp0 = kI8AccWarps, kI8TokenWarp = kI8ConvWarp0 + 8, kI8CodeWarp = kI8TokenWarp + 1,
+              kI8MmaWarp = kI8CodeWarp + 1, kI8WidenWarp0 = kI8MmaWarp + 1;
+constexpr int i8_threads(bool narrow) { return (kI8WidenWarp0 + (narrow ? 4 : 0)) * 32; }
 constexpr int kI8StagesMax = 8;
 constexpr int kI8CodeBytes = kI8BM * 64;  // a block's codes
-constexpr int kI8Smem = 220 * 1024;       // stages, in units of what a tile's width needs
+constexpr int kI8Smem = 224 * 1024;       // both rings
 constexpr int kI8Exact = 16;              // blocks whose products cannot pass 2^24
 constexpr int kI8Narrow = 64;             // tokens up to which every CTA makes its own f16 of them
 constexpr int kI8ACols = 32;              // tensor-memory columns of a block's A
@@ -58,7 +60,7 @@ struct I8Gemm {
     const float* anorm;  // per token
     const float* sa;
     int m, bn, token_tiles, kb;
-    int stages, buffers;
+    int stages, code_stages, buffers;
     int64_t tiles, cut0;  // tiles from cut0 on are cut into `parts`, one for each of the first (tiles - cut0) parts CTAs
     int parts;
     int64_t y_stride;
@@ -185,27 +187,31 @@ __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int to
 }
 
 template <typename T, int KS, bool NARROW>
-__global__ void __launch_bounds__(kI8Threads, 1)
+__global__ void __launch_bounds__(i8_threads(NARROW), 1)
     i8_gemm_kernel(const I8Gemm g, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                    T* __restrict__ y) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full_bar[kI8StagesMax];  // copies landed
-    __shared__ __align__(8) uint64_t conv_bar[kI8StagesMax];  // A in tensor memory
-    __shared__ __align__(8) uint64_t done_bar[kI8StagesMax];  // products of the stage complete
-    __shared__ __align__(8) uint64_t sum_full[2];             // a chunk's sums complete
-    __shared__ __align__(8) uint64_t sum_empty[2];            // and read
+    __shared__ __align__(8) uint64_t tok_full[kI8StagesMax];    // token copies landed
+    __shared__ __align__(8) uint64_t code_full[kI8StagesMax];   // code copies landed
+    __shared__ __align__(8) uint64_t code_empty[kI8StagesMax];  // and read
+    __shared__ __align__(8) uint64_t conv_bar[kI8StagesMax];    // A in tensor memory (NARROW: B in shared memory)
+    __shared__ __align__(8) uint64_t done_bar[kI8StagesMax];    // products of the stage complete
+    __shared__ __align__(8) uint64_t sum_full[2];               // a chunk's sums complete
+    __shared__ __align__(8) uint64_t sum_empty[2];              // and read
     __shared__ uint32_t tmem_holder;
     __shared__ unsigned arrived;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // a stage: KS token tiles, then KS blocks of codes, NARROW: then the tokens' codes
-    const int stages = g.stages, token_bytes = g.bn * 128;
-    const int stage_bytes = KS * (token_bytes + kI8CodeBytes) + (NARROW ? token_bytes : 0);
+    // a stage's tokens: KS tiles, NARROW: then their codes; the code ring follows the token ring
+    const int stages = g.stages, token_bytes = g.bn * 128, tok_bytes = (KS + (NARROW ? 1 : 0)) * token_bytes;
+    constexpr int code_bytes = KS * kI8CodeBytes;
     if (tid == 0) {
         for (int s = 0; s < kI8StagesMax; ++s) {
-            mbar_init(&full_bar[s], 2);
-            mbar_init(&conv_bar[s], 4);
+            mbar_init(&tok_full[s], 1);
+            mbar_init(&code_full[s], 1);
+            mbar_init(&code_empty[s], 4);
+            mbar_init(&conv_bar[s], NARROW ? 8 : 4);
             mbar_init(&done_bar[s], 1);
         }
         for (int p = 0; p < 2; ++p) {
@@ -219,31 +225,32 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_holder, tmem_a = tmem + (uint32_t)(g.buffers * g.bn);
-    const uint32_t data = smem_u32(smem), full = smem_u32(full_bar), conv = smem_u32(conv_bar), done = smem_u32(done_bar),
-                   sfull = smem_u32(sum_full), sempty = smem_u32(sum_empty);
+    const uint32_t data = smem_u32(smem), code_data = data + stages * tok_bytes, tfull = smem_u32(tok_full),
+                   cfull = smem_u32(code_full), cempty = smem_u32(code_empty), conv = smem_u32(conv_bar),
+                   done = smem_u32(done_bar), sfull = smem_u32(sum_full), sempty = smem_u32(sum_empty);
     bool alive = true;  // cleared by a wait that ran out; the role then ends
 
     if (warp == kI8TokenWarp || warp == kI8CodeWarp) {
         // boxes are whole: codes past the last chunk or tile and tokens past the last arrive as zeros
         const bool codes = warp == kI8CodeWarp;
         const CUtensorMap* map = codes ? &wmap : &amap;
-        const uint32_t to = data + (codes ? KS * token_bytes : NARROW ? KS * (token_bytes + kI8CodeBytes) : 0);
-        const uint32_t size = codes ? kI8CodeBytes : token_bytes;
+        const uint32_t to = codes ? code_data : data + (NARROW ? KS * token_bytes : 0), slot = codes ? code_bytes : tok_bytes;
+        const uint32_t size = codes ? kI8CodeBytes : token_bytes, full = codes ? cfull : tfull, empty = codes ? cempty : done;
         const int step = codes ? 256 : 64;  // a block in the map's elements
         if (!NARROW && !codes) pdl_wait();  // the codes do not depend on the kernel before
         I8Segments seg(g);
-        I8Ring ring(stages);
-        bool again = false;  // past the first pass over the stages
+        I8Ring ring(codes ? g.code_stages : stages);
+        bool again = false;  // past the first pass over the ring
         while (alive && seg.next()) {
             const int row = codes ? seg.channel0() / 32 : seg.token0();
             for (int kb = seg.k0; kb < seg.k1; kb += KS) {
                 const int s = ring.at;
                 if (again) {
-                    alive = __all_sync(0xffffffffu, i8_wait(done + s * 8, ring.parity ^ 1u, g.err));
+                    alive = __all_sync(0xffffffffu, i8_wait(empty + s * 8, ring.parity ^ 1u, g.err));
                     if (!alive) break;
                 }
                 if (i8_elect()) {
-                    const uint32_t bar = full + s * 8, at = to + s * stage_bytes;
+                    const uint32_t bar = full + s * 8, at = to + s * slot;
                     const bool two = KS == 2 && kb + 1 < seg.k1 && (codes || !NARROW);  // a box of token codes is a stage
                     i8_expect(bar, two ? 2 * size : size);
                     i8_box(at, map, kb * step, row, bar);
@@ -253,9 +260,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 again |= ring.at == 0;
             }
         }
-        // every copy has landed before the CTA may exit: the last of each stage
+        // every copy has landed before the CTA may exit: the last of each slot
         if (!NARROW && codes) pdl_wait();
-        for (int i = 0; i < stages; ++i) {
+        for (int i = 0; i < ring.n; ++i) {
             if (i >= ring.at && !again) break;
             i8_wait(full + i * 8, i < ring.at ? ring.parity : ring.parity ^ 1u, g.err);
         }
@@ -267,6 +274,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         I8Segments seg(g);
         I8Ring ring(stages), sums(g.buffers);
         bool again = false;  // past the first pass over the sum buffers
+        bool ready = false;  // the next stage is known to be
         uint32_t last = 0, last_parity = 0;
         while (alive && seg.next()) {
             const int n = seg.k1 - seg.k0;
@@ -279,11 +287,14 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 uint32_t accumulate = 0;
                 for (; blocks > 0 && alive; blocks -= KS) {
                     const int s = ring.at;
-                    // the converters arrive after the stage's copies: the token tile has landed too
-                    alive = __all_sync(0xffffffffu, i8_wait(conv + s * 8, ring.parity, g.err));
+                    if (!ready) {
+                        bool ok = i8_wait(conv + s * 8, ring.parity, g.err);
+                        if (!NARROW) ok = i8_wait(tfull + s * 8, ring.parity, g.err) && ok;
+                        alive = __all_sync(0xffffffffu, ok);
+                    }
                     if (!alive) break;
                     tc_fence_after();
-                    const uint64_t b = desc0 + (uint32_t)(s * stage_bytes >> 4);
+                    const uint64_t b = desc0 + (uint32_t)(s * tok_bytes >> 4);
                     const uint32_t a = tmem_a + (uint32_t)(s * KS * kI8ACols);
                     if (i8_elect()) {
                         mma_f16_ts(d, a, b, idesc, accumulate);  // 16 k: 8 columns of A, 32 bytes of B's rows
@@ -303,6 +314,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     accumulate = 1u;
                     last = done + s * 8, last_parity = ring.parity;
                     ring.next();
+                    // asked for while the products are on their way to the tensor cores
+                    ready = i8_test(conv + ring.at * 8, ring.parity);
+                    if (!NARROW) ready &= i8_test(tfull + ring.at * 8, ring.parity);
+                    ready = __all_sync(0xffffffffu, ready);
                 }
                 sums.next();
                 again |= sums.at == 0;
@@ -311,68 +326,99 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         // products in flight read shared memory and write tensor memory: the last is complete before the CTA exits
         if (last) i8_wait(last, last_parity, g.err);
         __syncwarp();
-    } else if (warp < kI8ConvWarps) {
-        // a stage is always converted by the same group, so that a wait never meets a barrier two phases behind
-        const int quarter = warp & 3, group = warp >> 2;
-        const uint32_t base = tmem_a + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t from = data + KS * token_bytes + quarter * 2048 + lane * 16;
+    } else if (NARROW && warp >= kI8WidenWarp0) {
+        // the tokens' codes as f16: 16 codes are two 16-byte pieces of a token's row, each swizzled by the row
         I8Segments seg(g);
         I8Ring ring(stages);
         while (alive && seg.next())
             for (int n = seg.k1 - seg.k0; n > 0; n -= KS, ring.next()) {
                 const int s = ring.at;
-                if ((s & 1) != group) continue;
-                alive = __all_sync(0xffffffffu, i8_wait(full + s * 8, ring.parity, g.err));
+                alive = __all_sync(0xffffffffu, i8_wait(tfull + s * 8, ring.parity, g.err));
                 if (!alive) break;
-                tc_fence_after();  // the products that read the stage's columns before are complete: its copies followed them
+                const uint32_t to = data + s * tok_bytes, codes = to + KS * token_bytes;
+                uint4 q[kI8Narrow / 16];  // all loads first
 #pragma unroll
-                for (int h = 0; h < 2 * KS; ++h) {
-                    if (KS == 2 && h == 2 && n == 1) break;
-                    uint32_t u[16];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint4 q;
+                for (int p = 0; p < kI8Narrow / 16; ++p) {
+                    const int i = tid - kI8WidenWarp0 * 32 + p * 128;
+                    if (i < g.bn * 8)
                         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                                     : "r"(from + s * stage_bytes + (h >> 1) * kI8CodeBytes + (h & 1) * 1024 + c * 512));
-                        codes_to_f16x2(q.x, u[8 * c + 0], u[8 * c + 1]);
-                        codes_to_f16x2(q.y, u[8 * c + 2], u[8 * c + 3]);
-                        codes_to_f16x2(q.z, u[8 * c + 4], u[8 * c + 5]);
-                        codes_to_f16x2(q.w, u[8 * c + 6], u[8 * c + 7]);
-                    }
-                    tmem_st16(base + (uint32_t)(s * KS * kI8ACols + h * 16), u);
-                }
-                if constexpr (NARROW) {
-                    // 16 codes of a token: two 16-byte pieces of its row, each swizzled by the row
-                    const uint32_t to = data + s * stage_bytes, codes = to + KS * (token_bytes + kI8CodeBytes);
-                    for (int i = (warp & 3) * 32 + lane; i < g.bn * 8; i += 128) {
-                        const int row = i >> 3, c = i & 7;
-                        uint4 q, lo, hi;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                     : "=r"(q[p].x), "=r"(q[p].y), "=r"(q[p].z), "=r"(q[p].w)
                                      : "r"(codes + i * 16));
-                        codes_to_f16x2(q.x, lo.x, lo.y);
-                        codes_to_f16x2(q.y, lo.z, lo.w);
-                        codes_to_f16x2(q.z, hi.x, hi.y);
-                        codes_to_f16x2(q.w, hi.z, hi.w);
-                        const uint32_t at = to + (c >> 2) * token_bytes + row * 128, j = (uint32_t)((c & 3) * 2);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((j ^ (row & 7)) << 4)), "r"(lo.x),
-                                     "r"(lo.y), "r"(lo.z), "r"(lo.w)
-                                     : "memory");
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((j + 1) ^ (row & 7)) << 4)),
-                                     "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                                     : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read what was stored
                 }
-                tmem_wait_st();
-                tc_fence_before();
+#pragma unroll
+                for (int p = 0; p < kI8Narrow / 16; ++p) {
+                    const int i = tid - kI8WidenWarp0 * 32 + p * 128, row = i >> 3, c = i & 7;
+                    if (i >= g.bn * 8) break;
+                    uint4 lo, hi;
+                    codes_to_f16x2(q[p].x, lo.x, lo.y);
+                    codes_to_f16x2(q[p].y, lo.z, lo.w);
+                    codes_to_f16x2(q[p].z, hi.x, hi.y);
+                    codes_to_f16x2(q[p].w, hi.z, hi.w);
+                    const uint32_t at = to + (c >> 2) * token_bytes + row * 128, j = (uint32_t)((c & 3) * 2);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((j ^ (row & 7)) << 4)), "r"(lo.x),
+                                 "r"(lo.y), "r"(lo.z), "r"(lo.w)
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((j + 1) ^ (row & 7)) << 4)),
+                                 "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read what was stored
                 __syncwarp();
                 if (lane == 0) i8_arrive(conv + s * 8);
             }
+    } else if (warp >= kI8ConvWarp0) {
+        // The groups take stages in turn. The code ring's slots are an even number, so that each is always read by the same
+        // group and a wait never meets a barrier two phases behind (products complete in order, so those of the slot's
+        // stage before the last are complete when a group waits for the last's).
+        const int quarter = warp & 3, group = (warp - kI8ConvWarp0) >> 2;
+        const uint32_t base = tmem_a + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t from = code_data + quarter * 2048 + lane * 16;
+        I8Segments seg(g);
+        I8Ring ring(stages), slots(g.code_stages);
+        bool again = false, mine = group == 0;
+        while (alive && seg.next())
+            for (int n = seg.k1 - seg.k0; n > 0; n -= KS) {
+                if (mine) {
+                    const int s = ring.at, c = slots.at;
+                    alive = __all_sync(0xffffffffu, i8_wait(cfull + c * 8, slots.parity, g.err));
+                    if (!alive) break;
+                    uint4 q[4 * KS];
+#pragma unroll
+                    for (int i = 0; i < 4 * KS; ++i)  // the second block may be missing: not used
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                                     : "r"(from + c * code_bytes + (i >> 2) * kI8CodeBytes + (i & 3) * 512));
+                    // the products that read the columns before
+                    if (again) alive = __all_sync(0xffffffffu, i8_wait(done + s * 8, ring.parity ^ 1u, g.err));
+                    if (!alive) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2 * KS; ++h) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            codes_to_f16x2(q[2 * h + i].x, u[8 * i + 0], u[8 * i + 1]);
+                            codes_to_f16x2(q[2 * h + i].y, u[8 * i + 2], u[8 * i + 3]);
+                            codes_to_f16x2(q[2 * h + i].z, u[8 * i + 4], u[8 * i + 5]);
+                            codes_to_f16x2(q[2 * h + i].w, u[8 * i + 6], u[8 * i + 7]);
+                        }
+                        tmem_st16(base + (uint32_t)(s * KS * kI8ACols + h * 16), u);
+                    }
+                    __syncwarp();
+                    if (lane == 0) i8_arrive(cempty + c * 8);  // the codes are in registers, and converted
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) i8_arrive(conv + s * 8);
+                }
+                mine = !mine;
+                ring.next();
+                slots.next();
+                again |= ring.at == 0;
+            }
     } else {
         if (!NARROW) pdl_wait();
-        const int quarter = warp & 3, half = (warp - kI8AccWarp0) >> 2, groups = g.bn / 16;
+        const int quarter = warp & 3, half = warp >> 2, groups = g.bn / 16;
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
         const int64_t part = (int64_t)g.bn * kI8BM, off = quarter * 32 + lane;
         // a warp whose wait ran out still meets the others at their barriers
@@ -407,7 +453,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             auto last_of_tile = [&] {
                 unsigned* counter = &g.counters[blockIdx.x / g.parts];
                 named_bar_sync(1, kI8AccWarps * 32);
-                if (tid == kI8AccWarp0 * 32) {
+                if (tid == 0) {
                     arrived = take_ticket(counter) + 1;
                     if (arrived == (unsigned)g.parts) *counter = 0u;
                 }
@@ -556,7 +602,7 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__
 // ---- the plan of a call, from its sizes alone ------------------------------------------
 struct I8Plan {
     int64_t tokens;  // of one launch
-    int bn, ks, token_tiles, kb, stages, buffers, parts;
+    int bn, ks, token_tiles, kb, stages, code_stages, buffers, parts;
     bool narrow;
     int64_t tiles, cut0;
     size_t at_wide, at_norms, at_part, at_spare, total;  // byte offsets in the workspace
@@ -599,13 +645,15 @@ static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
         if (bn == 32) break;
     }
     p.ks = p.bn <= 128 ? 2 : 1;
-    p.stages = kI8Smem / (p.ks * (p.bn * 128 + kI8CodeBytes) + (p.narrow ? p.bn * 128 : 0));
-    if (p.stages > kI8StagesMax) p.stages = kI8StagesMax;
-    // two buffers of sums where four stages still fit beside them
-    const int cols = p.ks * kI8ACols;
+    // the token ring: as many stages as tensor memory has columns for their A beside the sums (two buffers of them where
+    // four stages still fit); the code ring: the rest, an even number of stages, four at least
+    const int cols = p.ks * kI8ACols, token = (p.ks + (p.narrow ? 1 : 0)) * p.bn * 128, code = p.ks * kI8CodeBytes;
     p.buffers = (512 - 2 * p.bn) / cols >= 4 ? 2 : 1;
-    const int room = (512 - p.buffers * p.bn) / cols;
-    if (p.stages > room) p.stages = room;
+    p.stages = (512 - p.buffers * p.bn) / cols;
+    p.stages = p.stages < kI8StagesMax ? p.stages : kI8StagesMax;
+    while (p.stages * token + 4 * code > kI8Smem) --p.stages;
+    p.code_stages = (kI8Smem - p.stages * token) / code / 2 * 2;
+    p.code_stages = p.code_stages < kI8StagesMax ? p.code_stages : kI8StagesMax;
     const size_t tile = (size_t)p.bn * kI8BM * 4;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p.at_wide = kCounterBytes;
@@ -678,13 +726,13 @@ cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const
         if (!mapped) return cudaErrorInvalidValue;
         I8Gemm g{};
         g.W = W, g.anorm = norms, g.sa = sa + t, g.m = (int)part, g.bn = p.bn, g.token_tiles = p.token_tiles;
-        g.kb = p.kb, g.stages = p.stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
+        g.kb = p.kb, g.stages = p.stages, g.code_stages = p.code_stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
         g.parts = p.parts, g.y_stride = y_stride, g.part = reinterpret_cast<int32_t*>(ws + p.at_part);
         g.spare = reinterpret_cast<int32_t*>(ws + p.at_spare), g.counters = reinterpret_cast<unsigned*>(ws), g.err = err;
         const int64_t cutters = p.parts > 1 ? (p.tiles - p.cut0) * p.parts : 0;
         const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > cutters ? p.cut0 : cutters;
         e = launch_ex(p.narrow ? i8_gemm_kernel<T, 2, true> : p.ks == 2 ? i8_gemm_kernel<T, 2, false> : i8_gemm_kernel<T, 1, false>,
-                      dim3((unsigned)ctas), dim3(kI8Threads), (size_t)kI8Smem + 1024, s, !p.narrow, g, amap, wmap,
+                      dim3((unsigned)ctas), dim3(i8_threads(p.narrow)), (size_t)kI8Smem + 1024, s, !p.narrow, g, amap, wmap,
                       y + t * y_stride);
         if (e != cudaSuccess) return e;
     }
