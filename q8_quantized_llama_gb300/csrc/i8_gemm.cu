@@ -186,6 +186,25 @@ __device__ __forceinline__ bool i8_one_sum(const I8Gemm& g, int channel0, int to
     return warp_max(w) * warp_max(a) <= 16777216.0f;
 }
 
+// The products of stage s: 16 k each, 8 columns of A and 32 bytes of B's rows on.
+template <int KS>
+__device__ __forceinline__ void i8_stage(uint32_t d, uint32_t tmem_a, uint64_t desc0, int s, int tok_bytes, int token_bytes,
+                                         uint32_t idesc, uint32_t accumulate, bool two) {
+    const uint64_t b = desc0 + (uint32_t)(s * tok_bytes >> 4);
+    const uint32_t a = tmem_a + (uint32_t)(s * KS * kI8ACols);
+    mma_f16_ts(d, a, b, idesc, accumulate);
+    mma_f16_ts(d, a + 8, b + 2, idesc, 1u);
+    mma_f16_ts(d, a + 16, b + 4, idesc, 1u);
+    mma_f16_ts(d, a + 24, b + 6, idesc, 1u);
+    if (KS == 2 && two) {
+        const uint64_t b1 = b + (uint32_t)(token_bytes >> 4);
+        mma_f16_ts(d, a + 32, b1, idesc, 1u);
+        mma_f16_ts(d, a + 40, b1 + 2, idesc, 1u);
+        mma_f16_ts(d, a + 48, b1 + 4, idesc, 1u);
+        mma_f16_ts(d, a + 56, b1 + 6, idesc, 1u);
+    }
+}
+
 template <typename T, int KS, bool NARROW>
 __global__ void __launch_bounds__(i8_threads(NARROW), 1)
     i8_gemm_kernel(const I8Gemm g, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
@@ -274,7 +293,8 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
         I8Segments seg(g);
         I8Ring ring(stages), sums(g.buffers);
         bool again = false;  // past the first pass over the sum buffers
-        bool ready = false;  // the next stage is known to be
+        bool ready = false;  // the next stages are known to be
+        constexpr int U = KS == 1 ? 2 : 1;  // stages issued together: what is around the products takes half as long as they
         uint32_t last = 0, last_parity = 0;
         while (alive && seg.next()) {
             const int n = seg.k1 - seg.k0;
@@ -285,38 +305,44 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                 if (again) alive = __all_sync(0xffffffffu, i8_wait(sempty + sums.at * 8, sums.parity ^ 1u, g.err));
                 const uint32_t d = tmem + (uint32_t)(sums.at * g.bn);
                 uint32_t accumulate = 0;
-                for (; blocks > 0 && alive; blocks -= KS) {
-                    const int s = ring.at;
+                for (; blocks > 0 && alive; blocks -= U * KS) {
+                    const bool more = U == 2 && blocks > KS;  // a second stage
+                    const int s0 = ring.at;
+                    const uint32_t parity0 = ring.parity;
+                    ring.next();
+                    const int s1 = ring.at;
                     if (!ready) {
-                        bool ok = i8_wait(conv + s * 8, ring.parity, g.err);
-                        if (!NARROW) ok = i8_wait(tfull + s * 8, ring.parity, g.err) && ok;
+                        bool ok = i8_wait(conv + s0 * 8, parity0, g.err);
+                        if (!NARROW) ok = i8_wait(tfull + s0 * 8, parity0, g.err) && ok;
+                        if (more) {
+                            ok = i8_wait(conv + s1 * 8, ring.parity, g.err) && ok;
+                            if (!NARROW) ok = i8_wait(tfull + s1 * 8, ring.parity, g.err) && ok;
+                        }
                         alive = __all_sync(0xffffffffu, ok);
                     }
                     if (!alive) break;
                     tc_fence_after();
-                    const uint64_t b = desc0 + (uint32_t)(s * tok_bytes >> 4);
-                    const uint32_t a = tmem_a + (uint32_t)(s * KS * kI8ACols);
                     if (i8_elect()) {
-                        mma_f16_ts(d, a, b, idesc, accumulate);  // 16 k: 8 columns of A, 32 bytes of B's rows
-                        mma_f16_ts(d, a + 8, b + 2, idesc, 1u);
-                        mma_f16_ts(d, a + 16, b + 4, idesc, 1u);
-                        mma_f16_ts(d, a + 24, b + 6, idesc, 1u);
-                        if (KS == 2 && blocks > 1) {
-                            const uint64_t b1 = b + (uint32_t)(token_bytes >> 4);
-                            mma_f16_ts(d, a + 32, b1, idesc, 1u);
-                            mma_f16_ts(d, a + 40, b1 + 2, idesc, 1u);
-                            mma_f16_ts(d, a + 48, b1 + 4, idesc, 1u);
-                            mma_f16_ts(d, a + 56, b1 + 6, idesc, 1u);
+                        i8_stage<KS>(d, tmem_a, desc0, s0, tok_bytes, token_bytes, idesc, accumulate, blocks > 1);
+                        i8_commit(done + s0 * 8);
+                        if (more) {
+                            i8_stage<KS>(d, tmem_a, desc0, s1, tok_bytes, token_bytes, idesc, 1u, true);
+                            i8_commit(done + s1 * 8);
                         }
-                        i8_commit(done + s * 8);
-                        if (blocks <= KS) i8_commit(sfull + sums.at * 8);
+                        if (blocks <= U * KS) i8_commit(sfull + sums.at * 8);
                     }
                     accumulate = 1u;
-                    last = done + s * 8, last_parity = ring.parity;
-                    ring.next();
+                    last = done + (more ? s1 : s0) * 8, last_parity = more ? ring.parity : parity0;
+                    if (more) ring.next();
                     // asked for while the products are on their way to the tensor cores
-                    ready = i8_test(conv + ring.at * 8, ring.parity);
-                    if (!NARROW) ready &= i8_test(tfull + ring.at * 8, ring.parity);
+                    I8Ring then = ring;
+                    ready = i8_test(conv + then.at * 8, then.parity);
+                    if (!NARROW) ready &= i8_test(tfull + then.at * 8, then.parity);
+                    if (U == 2) {
+                        then.next();
+                        ready &= i8_test(conv + then.at * 8, then.parity);
+                        if (!NARROW) ready &= i8_test(tfull + then.at * 8, then.parity);
+                    }
                     ready = __all_sync(0xffffffffu, ready);
                 }
                 sums.next();
