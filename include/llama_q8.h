@@ -748,7 +748,8 @@ llama_q8_status llama_q8_i8_pack(const int8_t* codes, const float* scale, int64_
  * are kept the same way. Calls that share one (or graphs that captured such calls) must not
  * overlap on the GPU. y overlaps nothing else. err (device int32, may be NULL, zeroed by the
  * caller) receives LQ8_ERR_CUDA if a wait inside the kernel ran out, which leaves y
- * undefined. */
+ * undefined. Enqueues one kernel, or two from 65 tokens on (for every 65536 tokens, or
+ * 512 MB of their codes as f16). */
 size_t llama_q8_i8_matmul_workspace_bytes(int64_t rows, int64_t k, int64_t m);
 llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, const int8_t* codes,
                                    const float* scale, int64_t m, int32_t type, void* y, int64_t y_stride,

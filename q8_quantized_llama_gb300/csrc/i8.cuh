@@ -7,6 +7,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "llama_q8.h"
+
 namespace lq8 {
 
 // Rows in tiles of 32 (padded with zero rows), k in chunks of 16 (padded with
@@ -50,11 +52,12 @@ template <typename T, typename S> __device__ __forceinline__ T i8_scaled(S sum, 
     return i8_round<T>((float)sum * sa * sw);
 }
 
-// i8_gemm.cu: m >= kI8GemmMin tokens on the tensor cores, in a workspace of i8_gemm_workspace bytes
+// i8_gemm.cu: m >= kI8GemmMin tokens on the tensor cores, in a workspace of i8_gemm_workspace bytes (LQ8_ERR_ARG if it is
+// smaller)
 constexpr int kI8GemmMin = 17;
 size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m);
 template <typename T>
-cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
-                           int64_t y_stride, void* workspace, int32_t* err, cudaStream_t s);
+llama_q8_status launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
+                               int64_t y_stride, void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t s);
 
 }  // namespace lq8

@@ -594,14 +594,15 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
     if (warp == kI8MmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// The token rows as f16 and their norms, rounded up: one CTA per row.
-__global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__ codes, int64_t chunks,
+// The token rows as f16 and their norms, rounded up: one CTA per row, a thread per 16 codes as far as there are threads.
+constexpr int kWidenThreads = 1024;
+__global__ void __launch_bounds__(kWidenThreads) i8_widen_kernel(const uint4* __restrict__ codes, int64_t chunks,
                                                        uint4* __restrict__ wide, float* __restrict__ norm) {
-    __shared__ uint32_t part[8];
+    __shared__ uint32_t part[kWidenThreads / 32];
     pdl_launch_dependents();
     const int64_t row = blockIdx.x;
     int sum = 0;
-    for (int64_t c = threadIdx.x; c < chunks; c += 256) {
+    for (int64_t c = threadIdx.x; c < chunks; c += blockDim.x) {
         const uint4 q = codes[row * chunks + c];
         uint4 lo, hi;
         codes_to_f16x2(q.x, lo.x, lo.y);
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(256) i8_widen_kernel(const uint4* __restrict__
     __syncthreads();
     if (threadIdx.x == 0) {
         uint32_t all = 0;
-        for (int w = 0; w < 8; ++w) all += part[w];  // at most 131056 * 2^14 < 2^31
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) all += part[w];  // at most 131056 * 2^14 < 2^31
         norm[row] = __fsqrt_ru(__uint2float_ru(all));
     }
 }
@@ -712,64 +713,68 @@ cudaError_t init_i8_gemm_attributes() {
     return e;
 }
 
-template <typename T>
-cudaError_t launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
-                           int64_t y_stride, void* workspace, int32_t* err, cudaStream_t s) {
-    const int64_t most = i8_plan(W.rows, k, m).tokens;
-    cudaError_t e = get_encode_tiled();
-    if (e != cudaSuccess) return e;
-    uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
-    auto encode = [](CUtensorMap* map, CUtensorMapDataType type, const void* base, cuuint64_t width, cuuint64_t rows,
-                     cuuint64_t row_bytes, cuuint32_t box_x, cuuint32_t box_y, CUtensorMapSwizzle swizzle) {
-        const cuuint64_t dims[2] = {width, rows}, strides[1] = {row_bytes};
-        const cuuint32_t box[2] = {box_x, box_y}, elem[2] = {1, 1};
-        return g_encode_tiled(map, type, 2, const_cast<void*>(base), dims, strides, box, elem,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
-    // the packed codes as rows of 8-byte words, a row per 32-row tile: boxes of 4 tiles x 64 k (2 KB of a row)
-    const int64_t k16 = W.chunks * 16;
-    CUtensorMap wmap, amap;
-    if (!encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, W.codes, (cuuint64_t)W.chunks * 64, (cuuint64_t)W.rows_pad / 32,
-                (cuuint64_t)W.chunks * 512, 256, 4, CU_TENSOR_MAP_SWIZZLE_NONE))
-        return cudaErrorInvalidValue;
-    for (int64_t t = 0; t < m; t += most) {
-        const int64_t part = m - t < most ? m - t : most;
-        const I8Plan p = i8_plan(W.rows, k, part);
-        __half* wide = reinterpret_cast<__half*>(ws + p.at_wide);
-        float* norms = reinterpret_cast<float*>(ws + p.at_norms);
-        const int8_t* tokens = a + t * k16;
-        if (!p.narrow) {
-            e = launch_ex(i8_widen_kernel, dim3((unsigned)part), dim3(256), 0, s, false,
-                          reinterpret_cast<const uint4*>(tokens), W.chunks, reinterpret_cast<uint4*>(wide), norms);
-            if (e != cudaSuccess) return e;
-        }
-        const bool mapped =
-            p.narrow ? encode(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT8, tokens, (cuuint64_t)k16, (cuuint64_t)part,
-                              (cuuint64_t)k16, 128, (cuuint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_NONE)
-                     : encode(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wide, (cuuint64_t)k16, (cuuint64_t)part,
-                              (cuuint64_t)k16 * 2, 64, (cuuint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B);
-        if (!mapped) return cudaErrorInvalidValue;
-        I8Gemm g{};
-        g.W = W, g.anorm = norms, g.sa = sa + t, g.m = (int)part, g.bn = p.bn, g.token_tiles = p.token_tiles;
-        g.kb = p.kb, g.stages = p.stages, g.code_stages = p.code_stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
-        g.parts = p.parts, g.y_stride = y_stride, g.part = reinterpret_cast<int32_t*>(ws + p.at_part);
-        g.spare = reinterpret_cast<int32_t*>(ws + p.at_spare), g.counters = reinterpret_cast<unsigned*>(ws), g.err = err;
-        const int64_t cutters = p.parts > 1 ? (p.tiles - p.cut0) * p.parts : 0;
-        const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > cutters ? p.cut0 : cutters;
-        e = launch_ex(p.narrow ? i8_gemm_kernel<T, 2, true> : p.ks == 2 ? i8_gemm_kernel<T, 2, false> : i8_gemm_kernel<T, 1, false>,
-                      dim3((unsigned)ctas), dim3(i8_threads(p.narrow)), (size_t)kI8Smem + 1024, s, !p.narrow, g, amap, wmap,
-                      y + t * y_stride);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+// A tensor map of rows of 8-byte words, f16 numbers or bytes: boxes of box_x x box_y.
+static bool i8_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows,
+                   int64_t row_bytes, int box_x, int box_y, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y}, elem[2] = {1, 1};
+    return g_encode_tiled(map, type, 2, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template cudaError_t launch_i8_gemm<float>(const I8Weights&, int64_t, const int8_t*, const float*, int64_t,
-                                           float*, int64_t, void*, int32_t*, cudaStream_t);
-template cudaError_t launch_i8_gemm<__half>(const I8Weights&, int64_t, const int8_t*, const float*, int64_t,
-                                            __half*, int64_t, void*, int32_t*, cudaStream_t);
-template cudaError_t launch_i8_gemm<__nv_bfloat16>(const I8Weights&, int64_t, const int8_t*, const float*,
-                                                   int64_t, __nv_bfloat16*, int64_t, void*, int32_t*, cudaStream_t);
+// One launch: tokens a[m] by the plan.
+template <typename T>
+static cudaError_t i8_gemm_part(const I8Plan& p, const I8Weights& W, const int8_t* a, const float* sa, int m, T* y,
+                                int64_t y_stride, uint8_t* ws, int32_t* err, cudaStream_t s) {
+    __half* wide = reinterpret_cast<__half*>(ws + p.at_wide);
+    float* norms = reinterpret_cast<float*>(ws + p.at_norms);
+    const int64_t k16 = W.chunks * 16;
+    // the packed codes: a row per 32-row tile, boxes of 4 tiles x 64 k (2 KB of a row)
+    CUtensorMap wmap, amap;
+    const bool mapped =
+        i8_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, W.codes, W.chunks * 64, W.rows_pad / 32, W.chunks * 512, 256, 4,
+               CU_TENSOR_MAP_SWIZZLE_NONE) &&
+        (p.narrow ? i8_map(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, k16, m, k16, 128, p.bn, CU_TENSOR_MAP_SWIZZLE_NONE)
+                  : i8_map(&amap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, wide, k16, m, k16 * 2, 64, p.bn, CU_TENSOR_MAP_SWIZZLE_128B));
+    if (!mapped) return cudaErrorInvalidValue;
+    if (!p.narrow) {
+        const int64_t threads = W.chunks < kWidenThreads ? (W.chunks + 31) / 32 * 32 : kWidenThreads;
+        const cudaError_t e = launch_ex(i8_widen_kernel, dim3((unsigned)m), dim3((unsigned)threads), 0, s, false,
+                                        reinterpret_cast<const uint4*>(a), W.chunks, reinterpret_cast<uint4*>(wide), norms);
+        if (e != cudaSuccess) return e;
+    }
+    I8Gemm g{};
+    g.W = W, g.anorm = norms, g.sa = sa, g.m = m, g.bn = p.bn, g.token_tiles = p.token_tiles, g.kb = p.kb;
+    g.stages = p.stages, g.code_stages = p.code_stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
+    g.parts = p.parts, g.y_stride = y_stride, g.part = reinterpret_cast<int32_t*>(ws + p.at_part);
+    g.spare = reinterpret_cast<int32_t*>(ws + p.at_spare), g.counters = reinterpret_cast<unsigned*>(ws), g.err = err;
+    const int64_t cutters = p.parts > 1 ? (p.tiles - p.cut0) * p.parts : 0;
+    const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > cutters ? p.cut0 : cutters;
+    return launch_ex(p.narrow ? i8_gemm_kernel<T, 2, true> : p.ks == 2 ? i8_gemm_kernel<T, 2, false> : i8_gemm_kernel<T, 1, false>,
+                     dim3((unsigned)ctas), dim3(i8_threads(p.narrow)), (size_t)kI8Smem + 1024, s, !p.narrow, g, amap, wmap, y);
+}
+
+template <typename T>
+llama_q8_status launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
+                               int64_t y_stride, void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t s) {
+    const I8Plan first = i8_plan(W.rows, k, m);
+    if (!workspace || workspace_bytes < i8_workspace(W.rows, k, m, first)) return LQ8_ERR_ARG;
+    if (ensure_kernel_attributes() != cudaSuccess || get_encode_tiled() != cudaSuccess) return LQ8_ERR_CUDA;
+    for (int64_t t = 0; t < m; t += first.tokens) {
+        const int64_t part = m - t < first.tokens ? m - t : first.tokens;
+        const cudaError_t e = i8_gemm_part(part == first.tokens ? first : i8_plan(W.rows, k, part), W, a + t * W.chunks * 16,
+                                           sa + t, (int)part, y + t * y_stride, y_stride,
+                                           reinterpret_cast<uint8_t*>(workspace), err, s);
+        if (e != cudaSuccess) return LQ8_ERR_CUDA;
+    }
+    return LQ8_OK;
+}
+
+template llama_q8_status launch_i8_gemm<float>(const I8Weights&, int64_t, const int8_t*, const float*, int64_t,
+                                           float*, int64_t, void*, size_t, int32_t*, cudaStream_t);
+template llama_q8_status launch_i8_gemm<__half>(const I8Weights&, int64_t, const int8_t*, const float*, int64_t,
+                                            __half*, int64_t, void*, size_t, int32_t*, cudaStream_t);
+template llama_q8_status launch_i8_gemm<__nv_bfloat16>(const I8Weights&, int64_t, const int8_t*, const float*,
+                                                   int64_t, __nv_bfloat16*, int64_t, void*, size_t, int32_t*, cudaStream_t);
 
 }  // namespace lq8

@@ -248,13 +248,12 @@ static cudaError_t launch_i8_few(const I8Weights& W, const int8_t* a, const floa
 }
 
 template <typename T>
-static cudaError_t launch_i8_matmul(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
-                                    int64_t y_stride, void* workspace, int32_t* err, cudaStream_t s) {
-    const cudaError_t e = ensure_kernel_attributes();
-    if (e != cudaSuccess) return e;
-    if (m < kI8GemmMin)
-        return launch_i8_few<T>(W, a, sa, (int)m, y, y_stride, s);
-    return launch_i8_gemm<T>(W, k, a, sa, m, y, y_stride, workspace, err, s);
+static llama_q8_status launch_i8_matmul(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, void* y,
+                                        int64_t y_stride, void* workspace, size_t workspace_bytes, int32_t* err,
+                                        cudaStream_t s) {
+    if (m >= kI8GemmMin)
+        return launch_i8_gemm(W, k, a, sa, m, reinterpret_cast<T*>(y), y_stride, workspace, workspace_bytes, err, s);
+    return launch_i8_few(W, a, sa, (int)m, reinterpret_cast<T*>(y), y_stride, s) == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
 
 static bool i8_sizes_ok(int64_t rows, int64_t k) {
@@ -300,16 +299,14 @@ llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, 
     if (((uintptr_t)scale | (uintptr_t)err) & 3 || ((uintptr_t)y & (type == LLAMA_Q8_GGUF_F32 ? 3 : 1)))
         return LQ8_ERR_ARG;
     if (!i8_sizes_ok(rows, k) || m > (1ll << 30)) return LQ8_ERR_UNSUPPORTED;
-    const size_t need = llama_q8_i8_matmul_workspace_bytes(rows, k, m);
-    if (workspace_bytes < need || (need && !workspace)) return LQ8_ERR_ARG;
     if (m == 0) return LQ8_OK;
     const I8Weights w = i8_view(packed, rows, k);
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    if (type == LLAMA_Q8_GGUF_F32) e = launch_i8_matmul(w, k, codes, scale, m, (float*)y, y_stride, workspace, err, s);
-    else if (type == LLAMA_Q8_GGUF_F16) e = launch_i8_matmul(w, k, codes, scale, m, (__half*)y, y_stride, workspace, err, s);
-    else e = launch_i8_matmul(w, k, codes, scale, m, (__nv_bfloat16*)y, y_stride, workspace, err, s);
-    return e == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
+    if (type == LLAMA_Q8_GGUF_F32)
+        return launch_i8_matmul<float>(w, k, codes, scale, m, y, y_stride, workspace, workspace_bytes, err, s);
+    if (type == LLAMA_Q8_GGUF_F16)
+        return launch_i8_matmul<__half>(w, k, codes, scale, m, y, y_stride, workspace, workspace_bytes, err, s);
+    return launch_i8_matmul<__nv_bfloat16>(w, k, codes, scale, m, y, y_stride, workspace, workspace_bytes, err, s);
 }
 
 }  // extern "C"
