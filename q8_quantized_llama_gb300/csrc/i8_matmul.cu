@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 6)
     if (gridDim.y > 1) few_cluster_store(W, part, 1, tile, sa, y, y_stride);
 }
 
-// Two to sixteen tokens: a warp multiplies 32 channels with 8 NT tokens by f16 matrix instructions (m16n8k16; codes are
-// exact in f16, and sums of 1024 products in f32).
+// Two to sixteen tokens, and more with small matrices: a warp multiplies 32 channels with 8 NT tokens by f16 matrix
+// instructions (m16n8k16; codes are exact in f16, and sums of 1024 products in f32).
 //
 // A block is 64 k. Lane 4 g + t holds chunk t (16 codes) of rows g, g + 8, g + 16
 // and g + 24 and of token g: the word w of each is the lane's part of step w, whose
@@ -117,9 +117,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 
 // S warps per tile, of a CTA (which then has kFewWarps / S tiles) or, S = kFewWarps, of each CTA of a cluster.
 template <int NT, typename T>
-__global__ void __launch_bounds__(kFewWarps * 32, 6)
+__global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 6 : 4)
     i8_few_kernel(const I8Weights W, const int8_t* __restrict__ a, const float* __restrict__ sa, int m, int S,
                   T* __restrict__ y, int64_t y_stride) {
+    // tokens in groups of 8 NT along grid.z
+    a += (int64_t)blockIdx.z * 8 * NT * W.chunks * 16, sa += blockIdx.z * 8 * NT, y += blockIdx.z * 8 * NT * y_stride;
+    m = min(m - (int)blockIdx.z * 8 * NT, 8 * NT);
     constexpr int D = kFewDeep<NT>;
     __shared__ int part[kFewWarps][8 * NT][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -209,11 +212,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, 6)
     }
 }
 
-// grid.x CTAs in clusters of `size` along y
+// grid.x CTAs in clusters of `size` along y, and z of those
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_few(void (*kernel)(KArgs...), int64_t x, int64_t size, int threads, cudaStream_t s, Args... args) {
+static cudaError_t launch_few(void (*kernel)(KArgs...), int64_t x, int64_t size, int64_t z, int threads, cudaStream_t s,
+                              Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)x, (unsigned)size);
+    cfg.gridDim = dim3((unsigned)x, (unsigned)size, (unsigned)z);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -238,20 +242,32 @@ static cudaError_t launch_i8_few(const I8Weights& W, const int8_t* a, const floa
         const int64_t fit = 152 * 4 / tiles, k = blocks / (least * warps), c = fit < k ? fit : k;
         return c < 1 ? 1 : c > 8 ? 8 : c;
     };
-    if (m == 1) return launch_few(i8_row_kernel<T>, tiles, cluster(kRowWarps, 1), kRowWarps * 32, s, W, a, sa, y, y_stride);
+    if (m == 1) return launch_few(i8_row_kernel<T>, tiles, cluster(kRowWarps, 1), 1, kRowWarps * 32, s, W, a, sa, y, y_stride);
     // warps of a CTA on one tile: two blocks each while the SMs are not full, else eight
     int S = 1;
     while (S < kFewWarps && blocks >= (tiles * 2 * S > 152 * 24 ? 8 : 2) * S) S *= 2;
     const int64_t c = S == kFewWarps ? cluster(kFewWarps, 2) : 1, x = (tiles * S + kFewWarps - 1) / kFewWarps;
-    return m <= 8 ? launch_few(i8_few_kernel<1, T>, x, c, kFewWarps * 32, s, W, a, sa, m, S, y, y_stride)
-                  : launch_few(i8_few_kernel<2, T>, x, c, kFewWarps * 32, s, W, a, sa, m, S, y, y_stride);
+    auto go = [&](auto kernel, int each) {
+        return launch_few(kernel, x, c, (m + each - 1) / each, kFewWarps * 32, s, W, a, sa, m, S, y, y_stride);
+    };
+    return m <= 8 ? go(i8_few_kernel<1, T>, 8) : m <= 16 ? go(i8_few_kernel<2, T>, 16) : go(i8_few_kernel<4, T>, 32);
+}
+
+// Whether a product goes to the tensor cores' matrix kernel (i8_gemm.cu). Up to 16 tokens the kernels above are as fast or
+// faster; with small matrices, which the groups of 32 tokens read again from L2, further on, as they take no launch, ring
+// and tensor memory to set up (matrix kernel / these, in us: 32 tokens over 4096 x 4096, 8192 blocks of 32 channels x 64 k,
+// 11.1 / 10.5, over 6144 x 4096 12.2 / 13.1; 64 over 2048 x 2048 8.5 / 7.7, over 4096 x 4096 12.8 / 18.9; 128 over 576 x
+// 1536, 432 blocks, 9.3 / 6.6, over 2048 x 2048 11.2 / 14.4).
+static bool i8_on_gemm(int64_t rows, int64_t k, int64_t m) {
+    const int64_t blocks = (rows + 31) / 32 * ((k + 63) / 64);
+    return m > 16 && (m > 32 ? m > 128 || (m + 31) / 32 * blocks > 4096 : blocks > 8192);
 }
 
 template <typename T>
 static llama_q8_status launch_i8_matmul(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, void* y,
                                         int64_t y_stride, void* workspace, size_t workspace_bytes, int32_t* err,
                                         cudaStream_t s) {
-    if (m >= kI8GemmMin)
+    if (i8_on_gemm(W.rows, k, m))
         return launch_i8_gemm(W, k, a, sa, m, reinterpret_cast<T*>(y), y_stride, workspace, workspace_bytes, err, s);
     return launch_i8_few(W, a, sa, (int)m, reinterpret_cast<T*>(y), y_stride, s) == cudaSuccess ? LQ8_OK : LQ8_ERR_CUDA;
 }
@@ -286,7 +302,7 @@ llama_q8_status llama_q8_i8_pack(const int8_t* codes, const float* scale, int64_
 }
 
 size_t llama_q8_i8_matmul_workspace_bytes(int64_t rows, int64_t k, int64_t m) {
-    return !i8_sizes_ok(rows, k) || m < kI8GemmMin || m > (1ll << 30) ? 0 : i8_gemm_workspace(rows, k, m);
+    return !i8_sizes_ok(rows, k) || m > (1ll << 30) || !i8_on_gemm(rows, k, m) ? 0 : i8_gemm_workspace(rows, k, m);
 }
 
 llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, const int8_t* codes,

@@ -412,6 +412,30 @@ def test_matmul_rows_that_are_not_finite_spoil_themselves_alone(B, m):
     assert torch.equal(y[rest][:, keep], clean[:m, :n][rest][:, keep])
 
 
+# sizes at which the matrix kernel takes few tokens, too: whole and cut tiles, an odd last block of k, the last tile's
+# channels, several reads of the sums of a long k, a last group of tokens
+@pytest.mark.parametrize("m", [17, 31, 33, 48, 50, 64, 65, 100, 127, 128])
+@pytest.mark.parametrize("n,k", [(9000, 2000), (20001, 1025), (8200, 4111), (1301, 14336), (2600, 7000)])
+def test_matmul_of_few_tokens_on_the_matrix_kernel(B, m, n, k):
+    gen = torch.Generator(device="cuda").manual_seed(m * n)
+    a = torch.randint(-128, 128, (m, k), generator=gen, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    # rows whose sums pass 2^24 on the way, and cancel
+    w[5], w[n - 1], a[m - 1] = 127, -128, 127
+    a[1, ::2], a[1, 1::2] = 127, -128
+    pad = torch.zeros((m, I.row_bytes(k)), dtype=torch.int8, device="cuda")
+    wpad = torch.zeros((n, I.row_bytes(k)), dtype=torch.int8, device="cuda")
+    pad[:, :k], wpad[:, :k] = a, w
+    one = torch.ones(max(m, n), device="cuda")
+    p = Product(B, wpad.cpu().numpy(), one[:n].cpu().numpy(), k, m)
+    y = torch.full((m + 1, n + 3), 3.0, device="cuda")
+    p(pad, one[:m], "f32", n + 3, y)
+    torch.cuda.synchronize()
+    assert int(p.err.item()) == 0
+    assert torch.equal(y[:m, :n], (a.double() @ w.double().T).float())
+    assert (y[m] == 3.0).all() and (y[:, n:] == 3.0).all()
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 14336), (6, 28672, 576), (16, 49152, 576), (48, 4096, 14336),
                                    (512, 6144, 4096), (203, 1536, 576), (1000, 4096, 4096), (2049, 640, 1536)])
 def test_matmul_model_shapes(B, m, n, k):
@@ -520,7 +544,8 @@ def test_mlp_captured_and_replayed_on_a_stream(B, rows):
 
 
 def test_one_workspace_for_products_of_many_sizes(B):
-    shapes = [(40, 960, 576), (300, 4096, 300), (9, 576, 4100), (64, 96, 1536), (130, 2048, 2048), (33, 33, 33)]
+    shapes = [(40, 960, 576), (300, 4096, 300), (9, 576, 4100), (64, 96, 1536), (130, 2048, 2048), (33, 33, 33),
+              (40, 4096, 4500), (200, 700, 3000)]
     size = max(B.llama_q8_i8_matmul_workspace_bytes(n, k, m) for m, n, k in shapes)
     ws = torch.zeros(max(16, size), dtype=torch.uint8, device="cuda")
     for seed in (0, 1):

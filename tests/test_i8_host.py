@@ -100,11 +100,10 @@ def test_matmul_refusals(B, kw, status):
                                       f["stride"], f["ws"], f["ws_bytes"], f["err"], None) == _status(B, status)
 
 
-@pytest.mark.parametrize("rows,k,m", [(100, 200, 40), (4096, 14336, 48), (28672, 4096, 512), (960, 576, 64)])
+@pytest.mark.parametrize("rows,k,m", [(100, 200, 140), (4096, 14336, 48), (28672, 4096, 512), (28672, 4096, 17)])
 def test_matmul_refuses_a_short_workspace(B, rows, k, m):
     need = B.llama_q8_i8_matmul_workspace_bytes(rows, k, m)
-    if need == 0:
-        return
+    assert need > 0
     for ws, n in ((WS, need - 1), (WS, 0), (None, need)):
         assert B.lib().llama_q8_i8_matmul(PACKED, rows, k, CODES, SCALE, m, 0, Y, rows, ws, n, None,
                                           None) == B.LQ8_ERR_ARG
