@@ -742,14 +742,15 @@ llama_q8_status llama_q8_i8_pack(const int8_t* codes, const float* scale, int64_
  * and wscale packed by llama_q8_i8_pack. The sum is exact; it is turned into f32 and
  * multiplied by the token's and the channel's scale in f32, then rounded to `type`. y rows
  * are y_stride >= rows elements apart; what lies between them is not written. m <= 2^30.
- * workspace: llama_q8_i8_matmul_workspace_bytes(rows, k, m) bytes (may be 0; 0 also for sizes
- * out of range), 16-byte aligned, zeroed before its first use; it can be used by calls of any
- * sizes that it is large enough for, in turn, and by other operators' calls whose workspaces
- * are kept the same way. Calls that share one (or graphs that captured such calls) must not
+ * workspace: llama_q8_i8_matmul_workspace_bytes(rows, k, m) bytes (0, and then not used, for
+ * few tokens and small matrices; 0 also for sizes out of range), 16-byte aligned, zeroed before
+ * its first use. The size never falls as rows, k or m grow: one for the largest matrix and
+ * the most tokens serves every call, in turn, and other operators' calls whose workspaces are
+ * kept the same way. Calls that share one (or graphs that captured such calls) must not
  * overlap on the GPU. y overlaps nothing else. err (device int32, may be NULL, zeroed by the
  * caller) receives LQ8_ERR_CUDA if a wait inside the kernel ran out, which leaves y
- * undefined. Enqueues one kernel, or two from 65 tokens on (for every 65536 tokens, or
- * 512 MB of their codes as f16). */
+ * undefined. Enqueues one kernel, or two from 65 tokens on (small matrices: 129), for every
+ * 65536 tokens or 512 MB of their codes as f16. */
 size_t llama_q8_i8_matmul_workspace_bytes(int64_t rows, int64_t k, int64_t m);
 llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, const int8_t* codes,
                                    const float* scale, int64_t m, int32_t type, void* y, int64_t y_stride,

@@ -54,7 +54,7 @@ template <typename T, typename S> __device__ __forceinline__ T i8_scaled(S sum, 
 
 // i8_gemm.cu: any number of tokens on the tensor cores, in a workspace of i8_gemm_workspace bytes (LQ8_ERR_ARG if it is
 // smaller)
-size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m);
+size_t i8_gemm_workspace(int64_t k, int64_t m);
 template <typename T>
 llama_q8_status launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
                                int64_t y_stride, void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t s);

@@ -632,11 +632,31 @@ struct I8Plan {
     int bn, ks, token_tiles, kb, stages, code_stages, buffers, parts;
     bool narrow;
     int64_t tiles, cut0;
-    size_t at_wide, at_norms, at_part, at_spare, total;  // byte offsets in the workspace
+    size_t at_wide, at_norms, at_part, at_spare;  // byte offsets in the workspace
 };
 
+// tokens of one launch: 512 MB of f16, and enough of them to fill the GPU
+constexpr int64_t kI8Wide = 512ll << 20, kI8MinTokens = 2048, kI8MaxTokens = 65536;
+static int64_t i8_launch_tokens(int64_t k16, int64_t m) {
+    const int64_t fit = kI8Wide / (2 * k16) / 256 * 256;
+    const int64_t most = fit < kI8MinTokens ? kI8MinTokens : fit > kI8MaxTokens ? kI8MaxTokens : fit;
+    return m < most ? m : most;
+}
+static size_t i8_up256(size_t x) { return (x + 255) / 256 * 256; }
+// The workspace of any plan for up to m tokens: counters, a launch's tokens as f16 and their norms, a tile of sums per CTA
+// for the parts and one for sums so far. It never falls as m or k grows (a launch's tokens may, as k grows: hence bounds
+// in their place), so that one workspace serves many sizes.
+size_t i8_gemm_workspace(int64_t k, int64_t m) {
+    const int64_t k16 = (k + 15) / 16 * 16, tokens = m < kI8MaxTokens ? m : kI8MaxTokens;
+    const int64_t bn = tokens < 32 ? 32 : tokens > 256 ? 256 : (tokens + 15) / 16 * 16;
+    const size_t slots = (size_t)kI8Ctas * bn * kI8BM * 4;
+    if (m <= kI8Narrow) return kCounterBytes + slots;
+    const int64_t all = tokens * k16 * 2, most = kI8MinTokens * k16 * 2 > kI8Wide ? kI8MinTokens * k16 * 2 : kI8Wide;
+    return i8_up256(kCounterBytes + (size_t)(all < most ? all : most)) + i8_up256((size_t)tokens * 4) + 2 * slots;
+}
+
 // Microseconds of a launch with token tiles of bn and `parts` parts of each tile past the last full wave, from what was
-// measured: a block takes 0.22 us and a little more for each token of the tile (0.25 at 64, 0.30 at 128, 0.36 at 256),
+// measured: a block takes 0.25 us with 64 tokens, 0.30 with 128 and 0.36 with 256 (whose products alone are 0.33),
 // storing a tile 0.5 us and 1 / 100 us per token, a part's way through the workspace 2 us, and each further one's sums
 // another 1 us for every 64 tokens.
 static double i8_cost(int64_t tiles, int kb, int bn, int parts) {
@@ -650,10 +670,7 @@ static double i8_cost(int64_t tiles, int kb, int bn, int parts) {
 static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
     I8Plan p{};
     const int64_t k16 = (k + 15) / 16 * 16;
-    // tokens widened at a time: 512 MB of f16, and enough of them to fill the GPU
-    int64_t most = (512ll << 20) / (2 * k16) / 256 * 256;
-    most = most < 2048 ? 2048 : most > 65536 ? 65536 : most;
-    p.tokens = m < most ? m : most;
+    p.tokens = i8_launch_tokens(k16, m);
     p.kb = (int)((k16 + 63) / 64);
     p.narrow = p.tokens <= kI8Narrow;
     // token tiles from the fewest on, and parts
@@ -681,23 +698,12 @@ static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
     while (p.stages * token + 4 * code > kI8Smem) --p.stages;
     p.code_stages = (kI8Smem - p.stages * token) / code / 2 * 2;
     p.code_stages = p.code_stages < kI8StagesMax ? p.code_stages : kI8StagesMax;
-    const size_t tile = (size_t)p.bn * kI8BM * 4;
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p.at_wide = kCounterBytes;
-    p.at_norms = up(p.at_wide + (p.narrow ? 0 : (size_t)p.tokens * k16 * 2));
-    p.at_part = up(p.at_norms + (p.narrow ? 0 : (size_t)p.tokens * 4));
-    p.at_spare = up(p.at_part + (p.parts > 1 ? (size_t)(p.tiles - p.cut0) * p.parts * tile : 0));
-    p.total = up(p.at_spare + (!p.narrow && p.kb > kI8Exact ? kI8Ctas * tile : 0));
+    p.at_norms = i8_up256(p.at_wide + (p.narrow ? 0 : (size_t)p.tokens * k16 * 2));
+    p.at_part = i8_up256(p.at_norms + (p.narrow ? 0 : (size_t)p.tokens * 4));
+    p.at_spare = p.at_part + (p.parts > 1 ? (size_t)(p.tiles - p.cut0) * p.parts * p.bn * kI8BM * 4 : 0);
     return p;
 }
-
-// The largest of the workspaces of a call's launches (the last may have fewer tokens and another plan).
-static size_t i8_workspace(int64_t rows, int64_t k, int64_t m, const I8Plan& first) {
-    const int64_t tail = m % first.tokens;
-    const size_t last = tail ? i8_plan(rows, k, tail).total : 0;
-    return last > first.total ? last : first.total;
-}
-size_t i8_gemm_workspace(int64_t rows, int64_t k, int64_t m) { return i8_workspace(rows, k, m, i8_plan(rows, k, m)); }
 
 template <typename T> static cudaError_t i8_gemm_attributes() {
     cudaError_t e = cudaSuccess;
@@ -758,7 +764,7 @@ template <typename T>
 llama_q8_status launch_i8_gemm(const I8Weights& W, int64_t k, const int8_t* a, const float* sa, int64_t m, T* y,
                                int64_t y_stride, void* workspace, size_t workspace_bytes, int32_t* err, cudaStream_t s) {
     const I8Plan first = i8_plan(W.rows, k, m);
-    if (!workspace || workspace_bytes < i8_workspace(W.rows, k, m, first)) return LQ8_ERR_ARG;
+    if (!workspace || workspace_bytes < i8_gemm_workspace(k, m)) return LQ8_ERR_ARG;
     if (ensure_kernel_attributes() != cudaSuccess || get_encode_tiled() != cudaSuccess) return LQ8_ERR_CUDA;
     for (int64_t t = 0; t < m; t += first.tokens) {
         const int64_t part = m - t < first.tokens ? m - t : first.tokens;

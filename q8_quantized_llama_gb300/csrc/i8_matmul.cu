@@ -302,7 +302,7 @@ llama_q8_status llama_q8_i8_pack(const int8_t* codes, const float* scale, int64_
 }
 
 size_t llama_q8_i8_matmul_workspace_bytes(int64_t rows, int64_t k, int64_t m) {
-    return !i8_sizes_ok(rows, k) || m > (1ll << 30) || !i8_on_gemm(rows, k, m) ? 0 : i8_gemm_workspace(rows, k, m);
+    return !i8_sizes_ok(rows, k) || m > (1ll << 30) || !i8_on_gemm(rows, k, m) ? 0 : i8_gemm_workspace(k, m);
 }
 
 llama_q8_status llama_q8_i8_matmul(const void* packed, int64_t rows, int64_t k, const int8_t* codes,

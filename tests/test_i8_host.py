@@ -100,6 +100,24 @@ def test_matmul_refusals(B, kw, status):
                                       f["stride"], f["ws"], f["ws_bytes"], f["err"], None) == _status(B, status)
 
 
+# one workspace, of the largest matrix and the most tokens, serves all
+def test_matmul_workspace_never_falls(B):
+    sizes = B.llama_q8_i8_matmul_workspace_bytes
+    ms = [1, 16, 17, 32, 33, 64, 65, 100, 128, 129, 255, 256, 257, 300, 512, 777, 1024, 2048, 4096, 65536, 65537, 200000]
+    rows, ks = [1, 33, 576, 4096, 28672, 128256], [1, 16, 576, 4096, 14336, 131056]
+    for n in rows:
+        for k in ks:
+            found = [sizes(n, k, m) for m in ms]
+            assert found == sorted(found)
+    for m in ms:
+        for k in ks:
+            found = [sizes(n, k, m) for n in rows]
+            assert found == sorted(found)
+        for n in rows:
+            found = [sizes(n, k, m) for k in ks]
+            assert found == sorted(found)
+
+
 @pytest.mark.parametrize("rows,k,m", [(100, 200, 140), (4096, 14336, 48), (28672, 4096, 512), (28672, 4096, 17)])
 def test_matmul_refuses_a_short_workspace(B, rows, k, m):
     need = B.llama_q8_i8_matmul_workspace_bytes(rows, k, m)
