@@ -19,8 +19,9 @@
 // maximum. Rows whose f32 numbers leave the normal range are done in double as a
 // whole.
 //
-// Bound: memory, and with 16-bit types the f32 instructions (about 25 per element,
-// 30 with silu). A warp, or a CTA with as many threads as the row has values for,
+// Bound: memory (norm of 8195 x 4096 f32 65 us, 6.7 TB/s), and with 16-bit types the
+// instructions (an element of rows takes 16, of norm 28, of silu 26 with its share of
+// the row's reductions) and the chain from a row's maximum to its last code. A warp, or a CTA with as many threads as the row has values for,
 // keeps a row's v in registers (16 values a thread up to k = 8192, 32 up to 14336), so
 // every input is read once and every output written once; at least two CTAs share
 // an SM, so that one row's loads run under another's barriers; rows of more than
@@ -55,12 +56,12 @@ struct BlockQ8 {};  // Q8_0 blocks as an element type
 constexpr int kQuantThreads = 512, kQuantThreads32 = 448;
 constexpr float kMagic = 12582912.0f;       // 1.5 2^23: adding it rounds to an integer
 // Half width of the band around a half in which f32 does not settle a code. t = v (127 / M) is at most 127 and off by
-// the relative errors, in units of 2^-24, of 127 / M (1), of M (rows 0, norm 1, silu as v) and of v (rows 0, norm 1, silu:
-// exp 4, 1 + e 1, the quotient 4, the product 1): 127 * 21 * 2^-24 = 1.6e-4 for silu, 127 * 3 * 2^-24 = 2.3e-5 for the
-// others; t itself is rounded at a few 2^-27 next to a half.
-template <int OP> constexpr float kWindow = OP == QUANT_SILU ? 1.7e-4f : 3e-5f;
+// the relative errors, in units of 2^-24, of 127 / M (1), of M (rows 0, norm 1, silu as v) and of v (rows 0, norm 1, silu
+// 9: see silu_up): 127 * 19 * 2^-24 = 1.44e-4 for silu, 127 * 3 * 2^-24 = 2.3e-5 for the others; t itself is rounded at a
+// few 2^-27 next to a half.
+template <int OP> constexpr float kWindow = OP == QUANT_SILU ? 1.5e-4f : 3e-5f;
 // v within this factor of the f32 maximum may be the exact maximum: f32 products round in order (norm), silu's are off
-// by 10 * 2^-24 (2 * 10 * 2^-24 < 2^-19)
+// by 9 * 2^-24 (2 * 9 * 2^-24 < 2^-19)
 template <int OP> constexpr float kNearMax = OP == QUANT_SILU ? 1.0f - 1.0f / 262144.0f : 1.0f;
 constexpr float kTiny = 7.9e-31f, kHuge = 1e36f;  // M outside: the row is done in double
 
@@ -74,6 +75,25 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// two numbers rounded to the type, as they lie in a word of memory (f32: not used), and back
+template <typename T> __device__ __forceinline__ uint32_t pair_raw(uint64_t v) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(f2_lo(v), f2_hi(v));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <typename T> __device__ __forceinline__ void pair_open(uint32_t u, float& lo, float& hi) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        lo = f.x, hi = f.y;
+    } else {
+        lo = __uint_as_float(u << 16), hi = __uint_as_float(u & 0xffff0000u);
+    }
+}
 
 // Element i of a row (any i < k).
 template <typename T> __device__ __forceinline__ float load_one(const void* x, int64_t row_at, int i) {
@@ -95,9 +115,12 @@ template <typename T> __device__ __forceinline__ uint4 load_raw(const void* x, i
     return u;
 }
 template <typename T> __device__ __forceinline__ void from_raw(const uint4& u, float (&v)[Piece<T>::n]) {
-    const T* e = reinterpret_cast<const T*>(&u);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < Piece<T>::n; ++j) v[j] = to_f32(e[j]);
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) v[j] = __uint_as_float(w[j]);
+        else pair_open<T>(w[j], v[2 * j], v[2 * j + 1]);
+    }
 }
 
 // Elements i .. i + n - 1 of a row (i a multiple of n), zeros past k. ALIGNED: 16-byte loads, k a multiple of n.
@@ -158,11 +181,32 @@ __device__ __forceinline__ void store_piece(void* x, int64_t row_at, int i, int 
     }
 }
 
+// The largest magnitude of three; NaN if any is (its sign is left open).
+__device__ __forceinline__ float max_magnitude(float a, float v, float w) {
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(v), "f"(w));
+    return a;
+}
+__device__ __forceinline__ float min3(float a, float v, float w) {
+    asm("min.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(v), "f"(w));
+    return a;
+}
+
 // silu(gate) up in double
 __device__ __noinline__ double silu_up_f64(float gate, float up) {
     return (double)gate / (1.0 + exp(-(double)gate)) * (double)up;
 }
-__device__ __forceinline__ float silu_up(float gate, float up) { return __fdividef(gate, 1.0f + expf(-gate)) * up; }
+// The same in f32 for gate >= -80: exp(x) = 2^h (1 + r) with h = x / ln 2 rounded and r what the rounding left, in six
+// operations and two approximations (expf and a division take 12 more instructions per element). Off by 6.6 * 2^-24 of itself
+// at most for any gate of -80 .. 80 (up = 1; measured over all f32 numbers of 1e-9 and more, against double), and by the
+// last product's rounding.
+__device__ __forceinline__ float silu_up(float gate, float up) {
+    const float h = gate * -1.442695041f, r = fmaf(-h, 0.6931471806f, -gate);
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
+    e = fmaf(e, r, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+    return gate * q * up;
+}
 
 // ---- two-part f32 numbers: hi is the sum rounded to f32
 struct Two {
@@ -251,8 +295,8 @@ template <int OP, typename T, bool ALIGNED> struct Row {
         if constexpr (OP == QUANT_SILU) {
             float low = 0.0f;
 #pragma unroll
-            for (int j = 0; j < n; ++j) low = fminf(low, x[j]);
-            if (low < -80.0f) {  // the quotient's divisor leaves the range of the quick division
+            for (int j = 0; j < n; j += 2) low = min3(low, x[j], x[j + 1]);
+            if (low < -80.0f) {  // outside of silu_up's range
 #pragma unroll
                 for (int j = 0; j < n; ++j) x[j] = (float)silu_up_f64(x[j], b[j]);
             } else {
@@ -260,11 +304,24 @@ template <int OP, typename T, bool ALIGNED> struct Row {
                 for (int j = 0; j < n; ++j) x[j] = silu_up(x[j], b[j]);
             }
         } else if constexpr (OP == QUANT_NORM) {
-            if (a.b) {
+            if constexpr (ALIGNED && sizeof(T) == 2) {
+                uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < n; ++j) x[j] = to_f32(from_f32<T>(x[j] + b[j]));
+                for (int j = 0; j < 4; ++j) {
+                    uint64_t h = pack_f2(x[2 * j], x[2 * j + 1]);
+                    if (a.b) h = add_f2(h, pack_f2(b[2 * j], b[2 * j + 1]));
+                    w[j] = pair_raw<T>(h);
+                    pair_open<T>(w[j], x[2 * j], x[2 * j + 1]);
+                }
+                if (a.out && i < a.k)
+                    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + oa + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                if (a.b) {
+#pragma unroll
+                    for (int j = 0; j < n; ++j) x[j] = to_f32(from_f32<T>(x[j] + b[j]));
+                }
+                if (a.out) store_piece<T, ALIGNED>(a.out, oa, i, a.k, x);
             }
-            if (a.out) store_piece<T, ALIGNED>(a.out, oa, i, a.k, x);
 #pragma unroll
             for (int j = 0; j < n; ++j) ss = fmaf(x[j], x[j], ss);
             gained(i, x);
@@ -364,11 +421,6 @@ __device__ __forceinline__ int above_half(Two v, Two M, float q) {
     return fabsf(off) <= p * 0x1p-36f ? -1 : off > 0.0f;
 }
 
-// The larger magnitude; NaN if either is.
-__device__ __forceinline__ float max_magnitude(float a, float v) {
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(v)));
-    return a;
-}
 
 // A row's reduction area; a warp's or a CTA's.
 struct QuantShared {
@@ -498,7 +550,7 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
                 row.values(i, w, b, s);
                 part[p & 3] += s;
 #pragma unroll
-                for (int j = 0; j < n; ++j) own = max_magnitude(own, w[j]);
+                for (int j = 0; j < n; j += 2) own = max_magnitude(own, w[j], w[j + 1]);
             }
             ss = (part[0] + part[1]) + (part[2] + part[3]);
         } else {
@@ -515,7 +567,9 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
                 for (int p = 0; p < batch; ++p) {
                     row.values(((p0 + p) * G + t) * n, x[p], b[p], ss);
 #pragma unroll
-                    for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j], own = max_magnitude(own, x[p][j]);
+                    for (int j = 0; j < n; j += 2) own = max_magnitude(own, x[p][j], x[p][j + 1]);
+#pragma unroll
+                    for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j];
                 }
             }
             if constexpr (AHEAD) {
@@ -527,6 +581,7 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
             }
         }
         // the bits of magnitudes order like the magnitudes, NaN above infinity
+        own = fabsf(own);
         uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(own));
         if constexpr (OP == QUANT_NORM) ss = warp_sum(ss);
         if constexpr (!WARP) {
@@ -583,17 +638,29 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
 
         // codes, rounded in f32; the elements next to a border are noted, as bits of a piece
         const float inv = __fdiv_rn(127.0f, M);
+        // two elements an instruction where the registers' pairs come for nothing (norm of 8195 x 4096 bf16 49 -> 42 us, but
+        // Q8_0 rows 74 -> 80, silu of 2048 x 14336 bf16 43 -> 46)
+        constexpr bool packed = OP == QUANT_NORM && sizeof(T) == 2;
         auto store = [&](int i, const float* w) -> uint32_t {
             uint32_t word[n / 4], border = 0u;
             float off = 0.0f;
+            const uint64_t inv2 = pack_f2(inv, inv), magic = pack_f2(kMagic, kMagic);
 #pragma unroll
             for (int q = 0; q < n / 4; ++q) {
                 uint32_t c[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float m = fmaf(w[4 * q + j], inv, kMagic);  // rounded; its low byte is the code
-                    off = fmaxf(off, fabsf(fmaf(w[4 * q + j], inv, kMagic - m)));
-                    c[j] = __float_as_uint(m);
+                for (int j = 0; j < 4; j += 2) {
+                    const float x0 = w[4 * q + j], x1 = w[4 * q + j + 1];
+                    if constexpr (packed) {
+                        const uint64_t x = pack_f2(x0, x1), m = fma_f2(x, inv2, magic);
+                        const uint64_t r = fma_f2(x, inv2, sub_f2(magic, m));
+                        off = max_magnitude(off, f2_lo(r), f2_hi(r));
+                        c[j] = (uint32_t)m, c[j + 1] = (uint32_t)(m >> 32);
+                    } else {
+                        const float m0 = fmaf(x0, inv, kMagic), m1 = fmaf(x1, inv, kMagic);  // rounded; the low byte is the code
+                        off = max_magnitude(off, fmaf(x0, inv, kMagic - m0), fmaf(x1, inv, kMagic - m1));
+                        c[j] = __float_as_uint(m0), c[j + 1] = __float_as_uint(m1);
+                    }
                 }
                 word[q] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
             }
@@ -603,7 +670,7 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
                 else if constexpr (n == 8) *reinterpret_cast<uint2*>(codes + i) = make_uint2(word[0], word[1]);
                 else *reinterpret_cast<uint32_t*>(codes + i) = word[0];
             }
-            if (off > 0.5f - kWindow<OP>) {
+            if (fabsf(off) > 0.5f - kWindow<OP>) {
 #pragma unroll
                 for (int j = 0; j < n; ++j) {
                     const float m = fmaf(w[j], inv, kMagic);
@@ -612,39 +679,61 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
             }
             return border;
         };
-        // the noted elements of the piece at i, with the exact maximum
-        auto settle = [&](int i, uint32_t border) {
+        // a noted element, with the exact maximum
+        auto settle = [&](int at, Two w) {
             const unsigned long long key = sh.exact;
             const Two M2 = OP == QUANT_ROWS ? Two{M, 0.0f} : max_of_key(key, near);
-#pragma unroll 1
-            while (border) {
-                const int at = i + __ffs(border) - 1;
-                border &= border - 1u;
-                const Two w = row.v_two(at);
-                const float q = floorf(fabsf(w.hi) * inv);
-                int up = above_half(w, M2, q);
-                if (up < 0) up = above_half<OP>(row.v_f64(at), fabs(row.v_f64((int)(key & 0x1ffffu))), q);
-                const int c = (int)q + up;
-                codes[at] = (int8_t)(w.hi < 0.0f ? -c : c);
-            }
+            const float q = floorf(fabsf(w.hi) * inv);
+            int up = above_half(w, M2, q);
+            if (up < 0) up = above_half<OP>(row.v_f64(at), fabs(row.v_f64((int)(key & 0x1ffffu))), q);
+            const int c = (int)q + up;
+            codes[at] = (int8_t)(w.hi < 0.0f ? -c : c);
         };
         if constexpr (!LOOP) {
             uint32_t border = 0u;  // E <= 32
 #pragma unroll
             for (int p = 0; p < pieces; ++p) border |= store((p * G + t) * n, v + p * n) << (p * n);
-            if constexpr (OP != QUANT_ROWS) row_sync<WARP>();
+            auto place = [&] {
+                const int bit = __ffs(border) - 1;
+                border &= border - 1u;
+                return (bit / n * G + t) * n + bit % n;
+            };
+            if constexpr (OP == QUANT_SILU) {
+                // a thread's first noted element is looked up while the exact maximum is still on its way
+                int first = -1;
+                Two w = {0.0f, 0.0f};
+                if (border) first = place(), w = row.v_two(first);
+                row_sync<WARP>();
+                if (first >= 0) settle(first, w);
+            } else if constexpr (OP == QUANT_NORM) {
+                row_sync<WARP>();
+            }
+            if constexpr (OP == QUANT_NORM) {  // piece by piece (8195 x 14336 bf16: 134 us, as below 180)
 #pragma unroll 1
-            for (int p = 0; border; ++p, border >>= n) {
-                const uint32_t bits = border & ((1u << n) - 1u);
-                if (bits) settle((p * G + t) * n, bits);
+                for (int p = 0; border; ++p, border >>= n)
+#pragma unroll 1
+                    for (uint32_t bits = border & ((1u << n) - 1u); bits; bits &= bits - 1u) {
+                        const int at = (p * G + t) * n + __ffs(bits) - 1;
+                        settle(at, row.v_two(at));
+                    }
+            } else {
+#pragma unroll 1
+                while (border) {
+                    const int at = place();
+                    settle(at, row.v_two(at));
+                }
             }
         } else {
             row_sync<WARP>();
             for (int i = t * n; i < k16; i += G * n) {
                 float w[n];
                 row.again(i, w);
-                const uint32_t bits = store(i, w);
-                if (bits) settle(i, bits);
+                uint32_t bits = store(i, w);
+#pragma unroll 1
+                for (; bits; bits &= bits - 1u) {
+                    const int at = i + __ffs(bits) - 1;
+                    settle(at, row.v_two(at));
+                }
             }
         }
         if (t == 0) {  // a norm's M is the exact maximum rounded
