@@ -21,11 +21,11 @@
 //
 // Bound: memory (norm of 8195 x 4096 f32 65 us, 6.7 TB/s), and with 16-bit types the
 // instructions (an element of rows takes 16, of norm 28, of silu 26 with its share of
-// the row's reductions) and the chain from a row's maximum to its last code. A warp, or a CTA with as many threads as the row has values for,
-// keeps a row's v in registers (16 values a thread up to k = 8192, 32 up to 14336), so
-// every input is read once and every output written once; at least two CTAs share
-// an SM, so that one row's loads run under another's barriers; rows of more than
-// 14336 values are read twice.
+// the row's reductions) and the chain from a row's maximum to its last code. A warp,
+// or a CTA with as many threads as the row has values for, keeps a row's v in registers
+// (16 values a thread, or 32, up to 14336), so every input is read once and
+// every output written once; at least two CTAs share an SM, so that one row's loads run
+// under another's barriers; rows of more than 14336 values are read twice.
 #include "kernels.cuh"
 #include "llama_q8.h"
 #include "ptx.cuh"
@@ -752,19 +752,22 @@ static cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s) {
     };
     const int64_t k = a.row_bytes;
     if (k <= 16 * 32) return go(quant_kernel<OP, T, ALIGNED, 16, 32, false>, 4, 128);
-    // Several rows per CTA, as many CTAs as the SMs hold, where the next row's loads fit the registers beside v: not with
-    // two arrays of f32 (which keep memory busy without: norm of 8195 x 4096 64.9 us, the floor 64), and not where a row
-    // takes a whole SM's threads and is bound by what happens between its barriers (silu above 8192: 61 us in this form,
-    // 49 with two CTAs of 32 values a thread, 2048 x 14336 bf16), nor with Q8_0 blocks (28672 x 4096: 84 us, 73 without).
-    constexpr bool blocks = std::is_same<T, BlockQ8>::value;
-    constexpr bool ahead = ALIGNED && !blocks && (OP == QUANT_ROWS || sizeof(T) == 2);
-    constexpr bool wide = ahead && OP != QUANT_SILU;
-    const int64_t threads = (k / 16 + 31) / 32 * 32, ctas = 152 * (threads > 512 ? 1 : 1024 / threads);
-    const int64_t per = a.rows > ctas ? (a.rows + ctas - 1) / ctas : 1;
-    if (k <= 16 * kQuantThreads) return go(quant_kernel<OP, T, ALIGNED, 16, kQuantThreads, ahead>, ahead ? per : 1, k / 16);
-    if (k <= 32 * kQuantThreads32) {
-        if constexpr (wide) return go(quant_kernel<OP, T, ALIGNED, 16, 2 * kQuantThreads32, true>, per, threads);
-        else return go(quant_kernel<OP, T, ALIGNED, 32, kQuantThreads32, false>, 1, (k + 31) / 32);
+    // 16 values a thread, or 32 with rows by themselves where 16 would take more than one wave of CTAs: half the warps share
+    // the row's reductions (28672 x 4096 bf16 84 -> 63 us, f32 91 -> 82, Q8_0 74 -> 71; 512 x 4096 f32 4.1 -> 4.2 us; silu
+    // of f32 loses more registers than it gains: 8195 x 1536 22.5 -> 33 us).
+    const bool half = OP == QUANT_ROWS && ALIGNED && k > 2048 && a.rows * (k / 16) > 152 * 1024;
+    // Several rows per CTA, as many CTAs as the SMs hold, for norms of 16-bit types, whose next row fits the registers beside
+    // v (8195 x 4096 bf16 67 -> 42 us). Two arrays of f32 do not, and keep memory busy without; silu is bound by the chain
+    // between its barriers, which more CTAs hide better (8195 x 4096 bf16 51.6 us in this form, 47.1 without).
+    constexpr bool ahead = ALIGNED && OP == QUANT_NORM && sizeof(T) == 2;
+    if constexpr (ahead) {
+        const int64_t threads = (k / 16 + 31) / 32 * 32, ctas = 152 * (threads > 512 ? 1 : 1024 / threads);
+        const int64_t per = a.rows > ctas ? (a.rows + ctas - 1) / ctas : 1;
+        if (k <= 16 * kQuantThreads) return go(quant_kernel<OP, T, ALIGNED, 16, kQuantThreads, true>, per, threads);
+        if (k <= 32 * kQuantThreads32) return go(quant_kernel<OP, T, ALIGNED, 16, 2 * kQuantThreads32, true>, per, threads);
+    } else {
+        if (k <= 16 * kQuantThreads && !half) return go(quant_kernel<OP, T, ALIGNED, 16, kQuantThreads, false>, 1, k / 16);
+        if (k <= 32 * kQuantThreads32) return go(quant_kernel<OP, T, ALIGNED, 32, kQuantThreads32, false>, 1, (k + 31) / 32);
     }
     return go(quant_kernel<OP, T, ALIGNED, 0, kQuantThreads, false>, 1, kQuantThreads);
 }
