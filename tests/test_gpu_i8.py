@@ -152,6 +152,56 @@ def test_rows_quant_blocks(B, k):
     _check(codes, scale, rows, I.rows_quant(I.q8_0_values(packed.cpu().numpy(), k)), 0.0)
 
 
+# more rows than the GPU takes at once, in every form for them, with rows among them that leave the usual way
+@pytest.mark.parametrize("op", ["rows", "norm", "silu"])
+@pytest.mark.parametrize("kind,rows,k", [("bf16", 1300, 4096), ("f16", 400, 10000), ("bf16", 5000, 520), ("f32", 2500, 2080),
+                                         ("f32", 200, 14336), ("f16", 1301, 2049)])
+def test_many_long_rows(B, op, kind, rows, k):
+    t, dtype = TYPES[kind]
+    tiny = 2.0 ** -110 if kind != "f16" else 2.0 ** -20
+    x, y = _rand(rows, rows, k, scale=2.0), _rand(k, rows, k)
+    for at in (3, min(307, rows - 4), rows // 2, rows - 1):
+        x[at], x[at - 1, k // 2], x[at - 2] = 0.0, float("nan"), x[at - 2] * tiny
+        y[at], y[at - 2] = 0.0, y[at - 2] * tiny
+    x[rows // 3, 5] = float("inf")
+    x, y = x.to(dtype).cuda(), y.to(dtype).cuda()
+    codes, scale = _outputs(rows, k)
+    if op == "rows":
+        B.llama_q8_rows_quant(t, x, k, rows, k, codes, scale)
+        return _check(codes, scale, rows, I.rows_quant(_host(x)), 0.0)
+    if op == "silu":
+        B.llama_q8_silu_quant(t, x, y, k, rows, k, codes, scale)
+        want = I.silu_quant(_host(x), _host(y))
+        # A gate of a 16-bit type comes twice in a row, and its ups may have the ratio (2 q + 1) / 254: 127 v / M is then
+        # q + 1/2 in fact, in double q + 1/2 off by three roundings of 2^-53 of at most 127, and the code follows it: q or
+        # q + 1. Everything else is settled (numbers that are no halves lie further off than 1e-12 but for 1e-12 of them).
+        v = _host(x) / (1.0 + np.exp(-_host(x))) * _host(y)
+        with np.errstate(all="ignore"):
+            a = 127.0 * np.abs(v) / np.abs(v).max(1, keepdims=True)
+            half = np.abs(a - np.floor(a) - 0.5) < 1e-12
+        got = codes[:rows, :k].cpu().numpy()
+        assert half.sum() < 1e-4 * half.size and (np.abs(np.abs(got[half]) - np.floor(a[half]) - 0.5) == 0.5).all()
+        want[0][:, :k][half] = got[half]
+        # a scale of 2^-220 is 0 in f32: the wanted one is rounded too, by U at most
+        return _check(codes, scale, rows, (want[0], want[1].astype(np.float32)), 3 * U)
+    g = (1.0 + 0.2 * _rand(1, k)).cuda()
+    h = (x.float() + y.float()).to(dtype)
+    B.llama_q8_norm_quant(t, x, k, y, k, x, k, g, 1e-5, rows, k, codes, scale)
+    _check(codes, scale, rows, I.norm_quant(_host(h), _host(g), float(np.float32(1e-5))), 20 * U)
+    assert torch.equal(x.nan_to_num(9.0), h.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("rows,k", [(700, 4096), (1300, 2080)])
+def test_many_rows_of_blocks(B, rows, k):
+    blocks = torch.empty((rows, k // 32 * 34), dtype=torch.uint8, device="cuda")
+    w = _rand(k, rows, k, scale=0.02)
+    w[3] = 0.0
+    B.llama_q8_quantize(w.cuda(), rows, k, blocks)
+    codes, scale = _outputs(rows, k)
+    B.llama_q8_rows_quant(8, blocks, k, rows, k, codes, scale)
+    _check(codes, scale, rows, I.rows_quant(I.q8_0_values(blocks.cpu().numpy(), k)), 0.0)
+
+
 # ---- values next to the border between two codes
 
 def test_rows_quant_ties(B):
