@@ -513,6 +513,24 @@ def test_matmul_offsets_past_32_bits(B):
     assert int(p.err.item()) == 0
 
 
+@pytest.mark.parametrize("more", [1, 20, 70, 300])
+def test_matmul_of_two_launches(B, more):
+    """The tokens behind the first launch's 65536 go by a plan of their own."""
+    m, n, k = 65536 + more, 300, 600
+    gen = torch.Generator(device="cuda").manual_seed(more)
+    pad = torch.zeros((m, I.row_bytes(k)), dtype=torch.int8, device="cuda")
+    pad[:, :k] = torch.randint(-128, 128, (m, k), generator=gen, device="cuda", dtype=torch.int8)
+    w = torch.zeros((n, I.row_bytes(k)), dtype=torch.int8, device="cuda")
+    w[:, :k] = torch.randint(-128, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    p = Product(B, w.cpu().numpy(), np.ones(n, np.float32), k, m)
+    y = torch.full((m + 1, n), 3.0, device="cuda")
+    p(pad, torch.ones(m, device="cuda"), "f32", n, y)
+    torch.cuda.synchronize()
+    assert int(p.err.item()) == 0
+    assert torch.equal(y[:m], (pad.double() @ w.double().T).float())
+    assert (y[m] == 3.0).all()
+
+
 # ---- a run of them together, streams, graphs, workspaces
 
 def _mlp(B, rows, h, f, seed):
