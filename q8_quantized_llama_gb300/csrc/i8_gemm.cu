@@ -14,7 +14,7 @@
 // to 128 tokens, where the products are shorter than what surrounds them). More than
 // 64 tokens are turned into f16 once per call by i8_widen_kernel, which also notes
 // their norms; fewer (NARROW) are turned into f16 by every CTA for itself, which saves
-// the launch before and the wait for it (48 tokens over 4096 x 14336: 5 of 21 us).
+// the launch before and the wait for it (48 tokens over 4096 x 14336: 5 of 19 us).
 // Warp roles:
 //  - two producers: the token tile (f16: 128-byte rows of 64 values, 128-byte swizzle,
 //    the K-major B operand, used in place; NARROW: codes) and the codes of the four
@@ -30,13 +30,16 @@
 //
 // Work is dealt in whole tiles (tokens fastest, so that the CTAs that share a weight
 // tile run together). The tiles that do not fill a wave are cut along k into parts,
-// one per CTA, where that is shorter: every CTA leaves its part's sums (integers) in
-// the workspace, and the one that brings a tile's last part adds the others to its
-// own and stores.
+// one per CTA, where that is shorter. Where all tiles are cut, the CTAs of a tile are a
+// cluster: each leaves its sums (integers) in its shared memory and stores a share of the
+// tile's tokens (512 tokens over 4096 x 14336 56 -> 49 us, 65 26 -> 20, against the other
+// way). Behind whole tiles each leaves them in the workspace, and the one that brings a
+// tile's last part adds the others to its own and stores.
 #include "i8.cuh"
 #include "kernels.cuh"
 #include "llama_q8.h"
 #include "paged.cuh"
+#include "ptx.cuh"
 #include "tc.cuh"
 
 namespace lq8 {
@@ -54,6 +57,7 @@ constexpr int kI8Smem = 224 * 1024;       // both rings
 constexpr int kI8Exact = 16;              // blocks whose products cannot pass 2^24
 constexpr int kI8Narrow = 64;             // tokens up to which every CTA makes its own f16 of them
 constexpr int kI8ACols = 32;              // tensor-memory columns of a block's A
+static_assert(256 * kI8BM * 4 <= kI8Smem, "a tile's sums fit in the rings' place");
 
 struct I8Gemm {
     I8Weights W;
@@ -63,6 +67,7 @@ struct I8Gemm {
     int stages, code_stages, buffers;
     int64_t tiles, cut0;  // tiles from cut0 on are cut into `parts`, one for each of the first (tiles - cut0) parts CTAs
     int parts;
+    bool cluster;  // every tile is cut, and a tile's CTAs are a cluster
     int64_t y_stride;
     int32_t* part;       // [CTA][bn][128]: the sums of its part
     int32_t* spare;      // [CTA][bn][128]: sums so far of a whole tile that is read out more than once
@@ -475,6 +480,7 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
             const int chunks = one ? 1 : (n + kI8Exact - 1) / kI8Exact;
             // whether this CTA brings its cut tile's last part: the others' are in memory for it then
             int32_t* const parts = g.part + off;
+            int32_t* const staged = reinterpret_cast<int32_t*>(smem) + off;  // the rings are done with when it is written
             const int first = (int)(blockIdx.x - blockIdx.x % g.parts);
             auto last_of_tile = [&] {
                 unsigned* counter = &g.counters[blockIdx.x / g.parts];
@@ -511,6 +517,15 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                     __syncwarp();
                     if (lane == 0) i8_arrive(sempty + p * 8);
                 }
+                if (g.cluster) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (half + 2 * h >= groups) break;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) staged[((half + 2 * h) * 16 + j) * kI8BM] = sum[h][j];
+                    }
+                    continue;
+                }
                 if (seg.cut) {
                     int32_t* mypart = parts + blockIdx.x * part;
 #pragma unroll
@@ -536,7 +551,7 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                 for (int h = 0; h < 2; ++h)
                     if (half + 2 * h < groups) store(half + 2 * h, sum[h]);
             } else {
-                int32_t* sum = seg.cut ? parts + blockIdx.x * part : g.spare + blockIdx.x * part + off;
+                int32_t* sum = seg.cut && !g.cluster ? parts + blockIdx.x * part : g.spare + blockIdx.x * part + off;
                 for (int ch = 0; ch < chunks; ++ch, sums.next()) {
                     const int p = sums.at;
                     if (alive) alive = i8_wait(sfull + p * 8, sums.parity, g.err);
@@ -557,6 +572,7 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                         if (ch == chunks - 1 && !seg.cut) {
                             store(gr, i);
                         } else {
+                            if (ch == chunks - 1 && g.cluster) at = staged + gr * 16 * kI8BM;
 #pragma unroll
                             for (int j = 0; j < 16; ++j) at[j * kI8BM] = i[j];
                         }
@@ -565,7 +581,7 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                     __syncwarp();
                     if (lane == 0) i8_arrive(sempty + p * 8);
                 }
-                if (!seg.cut || !last_of_tile()) continue;
+                if (!seg.cut || g.cluster || !last_of_tile()) continue;
                 // two groups' sums are asked for together
                 for (int gr = half; gr < groups; gr += 4) {
                     int i[2][16];
@@ -588,6 +604,37 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                 }
             }
         }
+    }
+    if (g.cluster) {
+        // the tile's tokens are dealt over its CTAs and their warps
+        __syncwarp();
+        cluster_sync();
+        const int64_t tile = blockIdx.x / g.parts;
+        const int rank = blockIdx.x % g.parts, channel = (int)(tile / g.token_tiles) * kI8BM + lane;
+        const int token0 = (int)(tile % g.token_tiles) * g.bn;
+        float sw[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sw[q] = channel + q * 32 < g.W.rows ? g.W.scale[channel + q * 32] : 0.0f;
+        for (int t = rank + g.parts * warp; t < g.bn && token0 + t < g.m; t += g.parts * (int)(blockDim.x >> 5)) {
+            int s[4] = {0, 0, 0, 0};
+#pragma unroll 4
+            for (int c = 0; c < g.parts; ++c) {
+                uint32_t from;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(data + (t * kI8BM + lane) * 4), "r"(c));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    int v;
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(from + q * 128) : "memory");
+                    s[q] += v;
+                }
+            }
+            const float sa = __ldg(g.sa + token0 + t);
+            T* at = y + (int64_t)(token0 + t) * g.y_stride + channel;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (channel + q * 32 < g.W.rows) at[q * 32] = i8_scaled<T>(s[q], sa, sw[q]);
+        }
+        cluster_sync();  // nobody leaves while its sums are read
     }
     tc_fence_before();
     __syncthreads();
@@ -630,7 +677,7 @@ __global__ void __launch_bounds__(kWidenThreads) i8_widen_kernel(const uint4* __
 struct I8Plan {
     int64_t tokens;  // of one launch
     int bn, ks, token_tiles, kb, stages, code_stages, buffers, parts;
-    bool narrow;
+    bool narrow, cluster;
     int64_t tiles, cut0;
     size_t at_wide, at_norms, at_part, at_spare;  // byte offsets in the workspace
 };
@@ -655,15 +702,23 @@ size_t i8_gemm_workspace(int64_t k, int64_t m) {
     return i8_up256(kCounterBytes + (size_t)(all < most ? all : most)) + i8_up256((size_t)tokens * 4) + 2 * slots;
 }
 
+// Clusters of so many CTAs that a GB300 holds at once, a CTA taking an SM (what cudaOccupancyMaxActiveClusters reports).
+constexpr int kI8Clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+static bool i8_clusters(int64_t tiles, int parts) { return parts > 1 && tiles <= kI8Clusters[parts]; }
+
 // Microseconds of a launch with token tiles of bn and `parts` parts of each tile past the last full wave, from what was
-// measured: a block takes 0.25 us with 64 tokens, 0.30 with 128 and 0.36 with 256 (whose products alone are 0.33),
-// storing a tile 0.5 us and 1 / 100 us per token, a part's way through the workspace 2 us, and each further one's sums
-// another 1 us for every 64 tokens.
+// measured: a block takes 0.20 us with 32 tokens, 0.23 with 128 and 0.32 with 256, storing a tile 0.5 us and 1 / 100 us per
+// token. Parts that meet in a cluster share the stores, all in all 2.25 us, 1 / 64 us per token and 0.45 us for each part
+// after the second; through the workspace they take 2 us and another 1 us for every 64 tokens of each part after the first.
 static double i8_cost(int64_t tiles, int kb, int bn, int parts) {
-    const double block = bn <= 128 ? 0.20 + 0.0008 * bn : 0.24 + 0.00047 * bn, out = 0.5 + 0.01 * bn;
+    const double block = bn <= 128 ? 0.19 + 0.0003 * bn : 0.24 + 0.00033 * bn, out = 0.5 + 0.01 * bn;
     const int64_t rest = tiles % kI8Ctas;
     double t = (double)(tiles / kI8Ctas) * (kb * block + out);
-    if (rest) t += (double)((kb + parts - 1) / parts) * block + out + (parts > 1 ? 2.0 + (parts - 1) * bn / 64.0 : 0.0);
+    if (rest) {
+        t += (double)((kb + parts - 1) / parts) * block;
+        t += i8_clusters(tiles, parts) ? 2.25 + bn / 64.0 + (parts - 2) * 0.45
+                                       : out + (parts > 1 ? 2.0 + (parts - 1) * bn / 64.0 : 0.0);
+    }
     return t;
 }
 
@@ -688,6 +743,7 @@ static I8Plan i8_plan(int64_t rows, int64_t k, int64_t m) {
         }
         if (bn == 32) break;
     }
+    p.cluster = i8_clusters(p.tiles, p.parts);
     p.ks = p.bn <= 128 ? 2 : 1;
     // the token ring: as many stages as tensor memory has columns for their A beside the sums (two buffers of them where
     // four stages still fit); the code ring: the rest, an even number of stages, four at least
@@ -752,12 +808,29 @@ static cudaError_t i8_gemm_part(const I8Plan& p, const I8Weights& W, const int8_
     I8Gemm g{};
     g.W = W, g.anorm = norms, g.sa = sa, g.m = m, g.bn = p.bn, g.token_tiles = p.token_tiles, g.kb = p.kb;
     g.stages = p.stages, g.code_stages = p.code_stages, g.buffers = p.buffers, g.tiles = p.tiles, g.cut0 = p.cut0;
-    g.parts = p.parts, g.y_stride = y_stride, g.part = reinterpret_cast<int32_t*>(ws + p.at_part);
+    g.parts = p.parts, g.cluster = p.cluster, g.y_stride = y_stride, g.part = reinterpret_cast<int32_t*>(ws + p.at_part);
     g.spare = reinterpret_cast<int32_t*>(ws + p.at_spare), g.counters = reinterpret_cast<unsigned*>(ws), g.err = err;
     const int64_t cutters = p.parts > 1 ? (p.tiles - p.cut0) * p.parts : 0;
     const int64_t ctas = p.cut0 >= kI8Ctas ? kI8Ctas : p.cut0 > cutters ? p.cut0 : cutters;
-    return launch_ex(p.narrow ? i8_gemm_kernel<T, 2, true> : p.ks == 2 ? i8_gemm_kernel<T, 2, false> : i8_gemm_kernel<T, 1, false>,
-                     dim3((unsigned)ctas), dim3(i8_threads(p.narrow)), (size_t)kI8Smem + 1024, s, !p.narrow, g, amap, wmap, y);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(i8_threads(p.narrow));
+    cfg.dynamicSmemBytes = (size_t)kI8Smem + 1024;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    if (!p.narrow) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (p.cluster) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)p.parts;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    return cudaLaunchKernelEx(&cfg, p.narrow ? i8_gemm_kernel<T, 2, true> : p.ks == 2 ? i8_gemm_kernel<T, 2, false> : i8_gemm_kernel<T, 1, false>,
+                              g, amap, wmap, y);
 }
 
 template <typename T>

@@ -255,12 +255,12 @@ static cudaError_t launch_i8_few(const I8Weights& W, const int8_t* a, const floa
 
 // Whether a product goes to the tensor cores' matrix kernel (i8_gemm.cu). Up to 16 tokens the kernels above are as fast or
 // faster; with small matrices, which the groups of 32 tokens read again from L2, further on, as they take no launch, ring
-// and tensor memory to set up (matrix kernel / these, in us: 32 tokens over 4096 x 4096, 8192 blocks of 32 channels x 64 k,
-// 11.1 / 10.5, over 6144 x 4096 12.2 / 13.1; 64 over 2048 x 2048 8.5 / 7.7, over 4096 x 4096 12.8 / 18.9; 128 over 576 x
-// 1536, 432 blocks, 9.3 / 6.6, over 2048 x 2048 11.2 / 14.4).
+// and tensor memory to set up (matrix kernel / these, in us: 32 tokens over 4096 x 2048, 4096 blocks of 32 channels x 64 k,
+// 8.3 / 7.7, over 4096 x 4096 10.2 / 10.5; 64 over 2048 x 2048 7.9 / 7.7, over 4096 x 2048 9.1 / 14.4; 128 over 576 x 1536,
+// 432 blocks, 7.8 / 6.5, over 2048 x 2048 9.7 / 14.4).
 static bool i8_on_gemm(int64_t rows, int64_t k, int64_t m) {
     const int64_t blocks = (rows + 31) / 32 * ((k + 63) / 64);
-    return m > 16 && (m > 32 ? m > 128 || (m + 31) / 32 * blocks > 4096 : blocks > 8192);
+    return m > 16 && (m > 32 ? m > 128 || (m + 31) / 32 * blocks > 4096 : blocks >= 8192);
 }
 
 template <typename T>

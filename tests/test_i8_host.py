@@ -118,7 +118,7 @@ def test_matmul_workspace_never_falls(B):
             assert found == sorted(found)
 
 
-@pytest.mark.parametrize("rows,k,m", [(100, 200, 140), (4096, 14336, 48), (28672, 4096, 512), (28672, 4096, 17)])
+@pytest.mark.parametrize("rows,k,m", [(100, 200, 140), (4096, 14336, 48), (28672, 4096, 512), (28672, 4096, 17), (4096, 4096, 32)])
 def test_matmul_refuses_a_short_workspace(B, rows, k, m):
     need = B.llama_q8_i8_matmul_workspace_bytes(rows, k, m)
     assert need > 0
