@@ -14,7 +14,7 @@
 // to 128 tokens, where the products are shorter than what surrounds them). More than
 // 64 tokens are turned into f16 once per call by i8_widen_kernel, which also notes
 // their norms; fewer (NARROW) are turned into f16 by every CTA for itself, which saves
-// the launch before and the wait for it (48 tokens over 4096 x 14336: 5 of 19 us).
+// the launch before and the wait for it (48 tokens over 4096 x 14336: 5 of 24 us).
 // Warp roles:
 //  - two producers: the token tile (f16: 128-byte rows of 64 values, 128-byte swizzle,
 //    the K-major B operand, used in place; NARROW: codes) and the codes of the four
@@ -248,6 +248,10 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (NARROW) {
+        pdl_wait();
+        pdl_launch_dependents();  // behind the allocation, too: a kernel that waits for this one cannot hold its columns
+    }
     const uint32_t tmem = tmem_holder, tmem_a = tmem + (uint32_t)(g.buffers * g.bn);
     const uint32_t data = smem_u32(smem), code_data = data + stages * tok_bytes, tfull = smem_u32(tok_full),
                    cfull = smem_u32(code_full), cempty = smem_u32(code_empty), conv = smem_u32(conv_bar),
@@ -465,16 +469,18 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
             auto store = [&](int gr, const auto* v) {
                 const int t0 = token0 + gr * 16;
                 T* at = y + (int64_t)t0 * g.y_stride + channel;
-                const float* sa = g.sa + t0;
+                float sa[16];  // before the stores, which the compiler takes for possible writes to them
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sa[j] = t0 + j < g.m ? __ldca(g.sa + t0 + j) : 0.0f;
                 if (t0 + 16 <= g.m) {
                     if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j, at += g.y_stride) *at = i8_scaled<T>(v[j], __ldg(sa + j), sw);
+                        for (int j = 0; j < 16; ++j, at += g.y_stride) *at = i8_scaled<T>(v[j], sa[j], sw);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j, at += g.y_stride)
-                        if (mine && t0 + j < g.m) *at = i8_scaled<T>(v[j], __ldg(sa + j), sw);
+                        if (mine && t0 + j < g.m) *at = i8_scaled<T>(v[j], sa[j], sw);
                 }
             };
             const int chunks = one ? 1 : (n + kI8Exact - 1) / kI8Exact;
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(i8_threads(NARROW), 1)
                     s[q] += v;
                 }
             }
-            const float sa = __ldg(g.sa + token0 + t);
+            const float sa = __ldca(g.sa + token0 + t);
             T* at = y + (int64_t)(token0 + t) * g.y_stride + channel;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -819,10 +825,8 @@ static cudaError_t i8_gemm_part(const I8Plan& p, const I8Weights& W, const int8_
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    if (!p.narrow) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     if (p.cluster) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
         attr[cfg.numAttrs].val.clusterDim.x = (unsigned)p.parts;

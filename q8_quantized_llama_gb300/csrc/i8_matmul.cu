@@ -56,19 +56,21 @@ __device__ __forceinline__ void few_cluster_store(const I8Weights& W, const int 
         int s = 0;
         for (int i = 0; i < (int)gridDim.y; ++i)
             s += __float_as_int(ld_dsmem_f32(reinterpret_cast<const float*>(&mine[tok][threadIdx.x & 31]), (uint32_t)i));
-        if (channel < W.rows) y[tok * y_stride + channel] = i8_scaled<T>(s, sa[tok], W.scale[channel]);
+        if (channel < W.rows) y[tok * y_stride + channel] = i8_scaled<T>(s, __ldca(sa + tok), W.scale[channel]);
     }
     cluster_sync();  // nobody leaves while its sums are read
 }
 
 // One token: lane = row, four codes of both sides through one integer dot product (its rate, 16 lanes a clock and SM,
-// would be too low for four tokens: 28672 x 4096 34 us; one 19.2), each of the cluster's warps a chunk in turn.
+// would be too low for four tokens: 28672 x 4096 34 us; one 18.8), each of the cluster's warps a chunk in turn.
 constexpr int kRowWarps = 8;
 template <typename T>
 __global__ void __launch_bounds__(kRowWarps * 32, 6)
     i8_row_kernel(const I8Weights W, const int8_t* __restrict__ a, const float* __restrict__ sa, T* __restrict__ y,
                   int64_t y_stride) {
     __shared__ int part[kRowWarps][33];
+    pdl_wait();
+    pdl_launch_dependents();  // behind the wait: what is launched next may rely on everything before this kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tile = blockIdx.x, channel = tile * 32 + lane;
     const int chunks = (int)W.chunks, step = kRowWarps * gridDim.y;
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 6)
     int acc = 0;
 #pragma unroll 4
     for (int c = blockIdx.y * kRowWarps + warp; c < chunks; c += step) {
-        const uint4 q = ld_stream_u4(w + (int64_t)c * 32), v = __ldg(x + c);
+        const uint4 q = ld_stream_u4(w + (int64_t)c * 32), v = __ldca(x + c);
         acc = __dp4a((int)q.x, (int)v.x, acc);
         acc = __dp4a((int)q.y, (int)v.y, acc);
         acc = __dp4a((int)q.z, (int)v.z, acc);
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 6)
 #pragma unroll
         for (int i = 0; i < kRowWarps; ++i) s += part[i][lane];
         if (gridDim.y > 1) part[0][lane] = s;
-        else if (channel < W.rows) y[channel] = i8_scaled<T>(s, sa[0], W.scale[channel]);
+        else if (channel < W.rows) y[channel] = i8_scaled<T>(s, __ldca(sa), W.scale[channel]);
     }
     if (gridDim.y > 1) few_cluster_store(W, part, 1, tile, sa, y, y_stride);
 }
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 6)
 // 16 k are words w of the four chunks (any order of k serves, if it is the same for
 // both operands). Two blocks' loads are in flight, one with 16 tokens, as the
 // registers of 24 warps an SM allow (28672 x 4096, 8 tokens: 21.6 us, 22.1 with four
-// blocks and 12 warps, 23.4 with one and 40; 16 tokens: 24.1 us, 29.0 with two and 16).
+// blocks and 12 warps, 23.4 with one and 40; 16 tokens: 23.8 us, 29.0 with two and 16).
 constexpr int kFewWarps = 4;
 template <int NT> constexpr int kFewDeep = NT == 1 ? 2 : 1;
 
@@ -120,6 +122,7 @@ template <int NT, typename T>
 __global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 6 : 4)
     i8_few_kernel(const I8Weights W, const int8_t* __restrict__ a, const float* __restrict__ sa, int m, int S,
                   T* __restrict__ y, int64_t y_stride) {
+    pdl_wait();
     // tokens in groups of 8 NT along grid.z
     a += (int64_t)blockIdx.z * 8 * NT * W.chunks * 16, sa += blockIdx.z * 8 * NT, y += blockIdx.z * 8 * NT * y_stride;
     m = min(m - (int)blockIdx.z * 8 * NT, 8 * NT);
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 6 : 4)
             q[u][i] = in ? ld_stream_u4(w + (int64_t)b * 128 + i * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            p[u][j] = in && j * 8 + g < m ? __ldg(x + (int64_t)(j * 8 + g) * chunks + 4 * b) : make_uint4(0, 0, 0, 0);
+            p[u][j] = in && j * 8 + g < m ? __ldca(x + (int64_t)(j * 8 + g) * chunks + 4 * b) : make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
     for (int u = 0; u < D; ++u) load(u, u);
@@ -208,11 +211,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 6 : 4)
     for (int tok = share; tok < m; tok += S) {
         int s = 0;
         for (int i = 0; i < S; ++i) s += part[own * S + i][tok][lane];
-        y[tok * y_stride + channel] = i8_scaled<T>(s, sa[tok], W.scale[channel]);
+        y[tok * y_stride + channel] = i8_scaled<T>(s, __ldca(sa + tok), W.scale[channel]);
     }
 }
 
-// grid.x CTAs in clusters of `size` along y, and z of those
+// grid.x CTAs in clusters of `size` along y, and z of those. The launch may overlap the end of the kernel before, whose
+// outputs are read behind pdl_wait, and not by read-only loads. i8_row_kernel lets the next launch overlap all of its own
+// (28672 x 4096 19.2 -> 18.7 us, 960 x 576 2.1 -> 1.8); after i8_few_kernel its CTAs would take the places that come free
+// first, and leave SMs with too many and too few (8 tokens over 4096 x 14336 14.3 us, so 16.4).
 template <typename... KArgs, typename... Args>
 static cudaError_t launch_few(void (*kernel)(KArgs...), int64_t x, int64_t size, int64_t z, int threads, cudaStream_t s,
                               Args... args) {
@@ -220,14 +226,17 @@ static cudaError_t launch_few(void (*kernel)(KArgs...), int64_t x, int64_t size,
     cfg.gridDim = dim3((unsigned)x, (unsigned)size, (unsigned)z);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (size > 1) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 1;
-        attr[0].val.clusterDim.y = (unsigned)size;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = (unsigned)size;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
@@ -237,7 +246,7 @@ static cudaError_t launch_i8_few(const I8Weights& W, const int8_t* a, const floa
                                  cudaStream_t s) {
     const int64_t tiles = W.rows_pad / 32, blocks = (W.chunks + 3) / 4;
     // A cluster per tile where the tiles leave SMs empty, of CTAs enough for four per SM, with at least `least` blocks of
-    // k for each warp (4096 x 14336, one token: 42 us without clusters, 13.3 us with 4 CTAs, 17.9 with 8).
+    // k for each warp (4096 x 14336, one token: 42 us without clusters, 12.8 us with 4 CTAs, 17.9 with 8).
     auto cluster = [&](int warps, int64_t least) {
         const int64_t fit = 152 * 4 / tiles, k = blocks / (least * warps), c = fit < k ? fit : k;
         return c < 1 ? 1 : c > 8 ? 8 : c;

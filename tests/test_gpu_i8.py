@@ -611,6 +611,52 @@ def test_mlp_captured_and_replayed_on_a_stream(B, rows):
     _mlp_check(st, rows, h, f)
 
 
+@pytest.mark.parametrize("kind,rows,k", [("f32", 1, 576), ("bf16", 1, 4096), ("f32", 8, 1000), ("f16", 24, 576),
+                                         ("f32", 48, 4160), ("bf16", 90, 4160)])
+def test_a_chain_of_calls_on_a_stream_equals_single_steps(B, kind, rows, k):
+    """Each kernel reads what the one before it wrote, and its launch may overlap that one's end."""
+    t, dtype = TYPES[kind]
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    w = torch.randn((k, k), generator=gen, device="cuda")
+    wc, ws = torch.zeros((k, I.row_bytes(k)), dtype=torch.int8, device="cuda"), torch.zeros(k, device="cuda")
+    B.llama_q8_rows_quant(0, w, k, k, k, wc, ws)
+    packed = torch.zeros(B.llama_q8_i8_packed_bytes(k, k), dtype=torch.uint8, device="cuda")
+    B.llama_q8_i8_pack(wc, ws, k, k, packed)
+    n_ws = B.llama_q8_i8_matmul_workspace_bytes(k, k, rows)
+    work = torch.zeros(max(16, n_ws), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.full((k,), 0.01, device="cuda")
+    start = torch.randn((rows, k), generator=gen, device="cuda").to(dtype)
+
+    def run(wait):
+        x, y = start.clone(), torch.zeros((rows, k), dtype=dtype, device="cuda")
+        codes, scale = _outputs(rows, k, 0)
+        for _ in range(40):
+            B.llama_q8_norm_quant(t, x, k, y, k, x, k, g, 1e-5, rows, k, codes, scale)
+            wait()
+            B.llama_q8_i8_matmul(packed, k, k, codes, scale, rows, t, y, k, work, n_ws, err)
+            wait()
+            B.llama_q8_silu_quant(t, y, x, k, rows, k, codes, scale)
+            wait()
+            B.llama_q8_i8_matmul(packed, k, k, codes, scale, rows, t, y, k, work, n_ws, err)
+            wait()
+            B.llama_q8_rows_quant(t, y, k, rows, k, codes, scale)
+            wait()
+            B.llama_q8_i8_matmul(packed, k, k, codes, scale, rows, t, y, k, work, n_ws, err)
+            wait()
+            y.mul_(1e-4)
+            wait()
+        torch.cuda.synchronize()
+        return x.clone(), y.clone(), codes.clone()
+
+    want = run(torch.cuda.synchronize)
+    assert all(torch.isfinite(v.float()).all() for v in want)
+    for _ in range(5):
+        for got, w_ in zip(run(lambda: None), want):
+            assert torch.equal(got, w_)
+    assert int(err.item()) == 0
+
+
 def test_one_workspace_for_products_of_many_sizes(B):
     shapes = [(40, 960, 576), (300, 4096, 300), (9, 576, 4100), (64, 96, 1536), (130, 2048, 2048), (33, 33, 33),
               (40, 4096, 4500), (200, 700, 3000)]
