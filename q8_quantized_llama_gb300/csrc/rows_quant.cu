@@ -374,9 +374,12 @@ template <int OP, typename T, bool ALIGNED> struct Row {
         if (OP == QUANT_SILU) return load_one<T>(a.x, xa, i) == 0.0f || load_one<T>(a.b, ba, i) == 0.0f;
         return h_again(i) == 0.0f || (OP == QUANT_NORM && a.g[i] == 0.0f);
     }
-    // v of element i (a gate of at least -80) in two parts
+    // v of element i in two parts
     __device__ __forceinline__ Two v_two(int i) const {
-        if constexpr (OP == QUANT_SILU) return silu_up_two(load_one<T>(a.x, xa, i), load_one<T>(a.b, ba, i));
+        if constexpr (OP == QUANT_SILU) {
+            const float gate = load_one<T>(a.x, xa, i), up = load_one<T>(a.b, ba, i);
+            return gate < -80.0f ? two_of(silu_up_f64(gate, up)) : silu_up_two(gate, up);
+        }
         if constexpr (OP == QUANT_NORM) return two_prod(h_again(i), a.g[i]);
         return {load_one<T>(a.x, xa, i), 0.0f};
     }

@@ -1,0 +1,70 @@
+"""The 8-bit quantisers against the CPU definitions where f32 reaches its ends, and to the last bit of their scales."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import i8_oracle as I
+from tests.gpu_helpers import binding, require_gpu
+from tests.test_gpu_i8 import TYPES, U, _check, _host, _outputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    require_gpu()
+    return binding()
+
+
+def _silu(gate):
+    gate = gate.astype(np.longdouble)
+    with np.errstate(over="ignore"):
+        return gate / (1 + np.exp(-gate))
+
+
+def _near_halves(rng, gate, at, top, kind):
+    """(gate, up) of a row in a type: the product at `at` is the largest, about `top`, the others lie as near to halves of its
+    127th as the type's ups allow. None is closer than 1e-11 to one, so that the definition in f64 knows every code."""
+    dtype = TYPES[kind][1]
+    gate = torch.from_numpy(gate.astype(np.float32)).to(dtype).double().numpy()
+    silu = _silu(gate)
+    q = rng.integers(0, 127, gate.size) + 0.5
+    q[at] = 127.0
+    with np.errstate(all="ignore"):
+        up = torch.from_numpy((q * top / 127.0 / silu).astype(np.float64)).to(dtype).double().numpy()
+        up[~np.isfinite(up)] = 0.0
+        v = np.abs(silu * up.astype(np.longdouble))
+        t = 127.0 * v / v[at]
+        t[at] = 0.0
+        up[(t > 127.0) | (np.abs(t - np.floor(t) - 0.5) < 1e-11)] = 0.0
+    assert up[at] != 0.0
+    return gate, up
+
+
+def _check_silu(B, kind, rows):
+    gate, up = (np.stack(x) for x in zip(*rows))
+    n, k = gate.shape
+    dtype = TYPES[kind][1]
+    codes, scale = _outputs(n, k)
+    B.llama_q8_silu_quant(TYPES[kind][0], torch.from_numpy(gate).to(dtype).cuda(), torch.from_numpy(up).to(dtype).cuda(), k,
+                          n, k, codes, scale)
+    _check(codes, scale, n, I.silu_quant(gate, up), 2 * U)
+
+
+# the row's largest product has a gate below -80, and others next to a half have one
+FAR = [(-80.5, 1e-3), (-82, 2e-4), (-85, 1e-10), (-88, 5e-5), (-88.5, 3e-7), (-90, 7e-8), (-90, 0.07), (-96, 1e-9),
+       (-100, 4e-6), (-104, 2e-7)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [40, 600, 4096, 17000])
+def test_silu_largest_product_of_a_far_gate(B, kind, k):
+    rng = np.random.default_rng(k)
+    rows = []
+    for far, top in FAR:
+        gate = rng.standard_normal(k) * 4.0
+        gate = np.where(rng.random(k) < 0.3, rng.choice([-82.0, -84.5, -88.0, -88.5, -90.0, -97.0], k), gate)
+        at = int(rng.integers(k))
+        gate[at] = far
+        rows.append(_near_halves(rng, gate, at, top, kind))
+    _check_silu(B, kind, rows)
