@@ -197,15 +197,17 @@ __device__ __noinline__ double silu_up_f64(float gate, float up) {
 }
 // The same in f32 for gate >= -80: exp(x) = 2^h (1 + r) with h = x / ln 2 rounded and r what the rounding left, in six
 // operations and two approximations (expf and a division take 12 more instructions per element). Off by 6.6 * 2^-24 of itself
-// at most for any gate of -80 .. 80 (up = 1; measured over all f32 numbers of 1e-9 and more, against double), and by the
-// last product's rounding.
+// at most for any gate of -80 .. 80 (up = 1; measured over all f32 numbers of 1e-9 and more, against double), and by one
+// product's rounding. up comes before gate: gate times the quotient loses bits where gate lies next to the subnormal range, and an
+// up of 1e20 brings what is left back among the row's numbers. The quotient times up is that small only where the whole is
+// far below a row's smallest code, or the quotient is 1.
 __device__ __forceinline__ float silu_up(float gate, float up) {
     const float h = gate * -1.442695041f, r = fmaf(-h, 0.6931471806f, -gate);
     float e, q;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
     e = fmaf(e, r, e);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
-    return gate * q * up;
+    return gate * (q * up);
 }
 
 // ---- two-part f32 numbers: hi is the sum rounded to f32
@@ -229,7 +231,8 @@ __device__ __forceinline__ Two two_of(double v) {
     return {hi, (float)(v - (double)hi)};
 }
 
-// silu(gate) up to about 2^-40 of itself, for gate >= -80: exp(x) = 2^n exp(r) with x = n ln 2 + r, ln 2 in three
+// silu(gate) up to about 2^-40 of itself, for gate >= -80 and |gate| >= 2^-100 (below, the division's remainder falls under the
+// smallest f32), by the range reduction of Cody and Waite: exp(x) = 2^n exp(r) with x = n ln 2 + r, ln 2 in three
 // parts of which n times the first is exact; exp(r), |r| <= ln 2 / 2, by its Taylor series to r^11 (what is left out is
 // below 2^-47), the terms up to r^5 in two parts.
 __device__ __noinline__ Two silu_up_two(float gate, float up) {
@@ -378,7 +381,8 @@ template <int OP, typename T, bool ALIGNED> struct Row {
     __device__ __forceinline__ Two v_two(int i) const {
         if constexpr (OP == QUANT_SILU) {
             const float gate = load_one<T>(a.x, xa, i), up = load_one<T>(a.b, ba, i);
-            return gate < -80.0f ? two_of(silu_up_f64(gate, up)) : silu_up_two(gate, up);
+            if (gate < -80.0f || fabsf(gate) < 0x1p-100f) return two_of(silu_up_f64(gate, up));  // out of its range
+            return silu_up_two(gate, up);
         }
         if constexpr (OP == QUANT_NORM) return two_prod(h_again(i), a.g[i]);
         return {load_one<T>(a.x, xa, i), 0.0f};

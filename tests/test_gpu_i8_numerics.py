@@ -68,3 +68,20 @@ def test_silu_largest_product_of_a_far_gate(B, kind, k):
         gate[at] = far
         rows.append(_near_halves(rng, gate, at, top, kind))
     _check_silu(B, kind, rows)
+
+
+# gates in or next to the subnormal range with ups that bring the products back, and the reverse
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [40, 600, 4096, 9000, 17000])
+def test_silu_gates_and_ups_at_the_ends_of_f32(B, kind, k):
+    rng = np.random.default_rng(k + 1)
+    rows = []
+    for low, high, top in ((-44.5, -38.5, 1e-7), (-43, -42, 1e-20), (-42, -37, 1e-20), (-39, -34, 1e-3), (-38.2, -37.7, 1.0),
+                           (-33, -28, 1e6), (28, 34, 1e-7), (30, 31, 1e-12 if kind == "f32" else 1e-8)):
+        least = 1.5e-45 if kind == "f32" else 1e-40
+        gate = np.maximum(10.0 ** rng.uniform(low, high, k), least) * rng.choice([-1.0, 1.0] if low < 0 else [1.0], k)
+        gate = np.where(rng.random(k) < 0.2, rng.standard_normal(k) * 3.0, gate)
+        at = int(rng.integers(k))
+        gate[at] = max(10.0 ** ((low + high) / 2), least)
+        rows.append(_near_halves(rng, gate, at, top, kind))
+    _check_silu(B, kind, rows)
