@@ -63,7 +63,9 @@ template <int OP> constexpr float kWindow = OP == QUANT_SILU ? 1.5e-4f : 3e-5f;
 // v within this factor of the f32 maximum may be the exact maximum: f32 products round in order (norm), silu's are off
 // by 9 * 2^-24 (2 * 9 * 2^-24 < 2^-19)
 template <int OP> constexpr float kNearMax = OP == QUANT_SILU ? 1.0f - 1.0f / 262144.0f : 1.0f;
-constexpr float kTiny = 7.9e-31f, kHuge = 1e36f;  // M outside: the row is done in double
+// M outside: the row is done in double. Above kTiny the products next to a half are 2^-100 and more, and the part of a norm's
+// h g below f32 is a multiple of the smallest f32, 2^-149.
+constexpr float kTiny = 0x1p-92f, kHuge = 1e36f;
 
 template <typename T> struct Piece { static constexpr int n = 16 / sizeof(T); };
 template <> struct Piece<BlockQ8> { static constexpr int n = 16; };

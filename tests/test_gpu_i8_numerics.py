@@ -85,3 +85,25 @@ def test_silu_gates_and_ups_at_the_ends_of_f32(B, kind, k):
         gate[at] = max(10.0 ** ((low + high) / 2), least)
         rows.append(_near_halves(rng, gate, at, top, kind))
     _check_silu(B, kind, rows)
+
+
+# h g a step of 2^-46 below q + 1/2 in 127ths of the largest product, which f32 alone takes for the half itself. Of a product of
+# about 2^-107 the part below f32 is under the smallest f32 number. The last rows are 2^6, 2^8 and 2^30 times as large.
+@pytest.mark.parametrize("k", [30, 900, 9000, 17000])
+def test_norm_products_whose_second_part_is_below_f32(B, k):
+    pairs = [(8388607, 8388609, 46), (4783982, 14709241, 46), (4374971, 16084391, 46), (13911026, 15175461, 46),
+             (13140607, 13387651, 45), (12582911, 12582913, 44), (12653911, 15292825, 44)]  # odd 2^bits - 1 to 6
+    h, g = np.zeros(k), np.zeros(k)
+    h[3], g[3] = 254.0 * 2.0 ** -40, 2.0 ** -67
+    for i, (a, b, bits) in enumerate(pairs):
+        odd = round(a * b / 2.0 ** bits)
+        assert odd % 2 == 1 and 0 < odd * 2 ** bits - a * b < 8
+        at = (7 + i * (k // 8)) % k
+        h[at], g[at] = a * 2.0 ** -60, b * 2.0 ** (-47 - bits)
+        h[(at + 1) % k], g[(at + 1) % k] = -h[at], g[at]
+    rows = np.stack([h, h * 0.5, h * 2.0 ** 6, h * 2.0 ** 8, h * 2.0 ** 30]).astype(np.float32)
+    g = g.astype(np.float32)
+    codes, scale = _outputs(5, k)
+    B.llama_q8_norm_quant(0, torch.from_numpy(rows).cuda(), k, None, 0, None, 0, torch.from_numpy(g).cuda(), 0.0, 5, k,
+                          codes, scale)
+    _check(codes, scale, 5, I.norm_quant(rows, g, 0.0), 20 * U)
