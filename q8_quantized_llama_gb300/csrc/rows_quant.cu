@@ -573,14 +573,16 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
                     if constexpr (AHEAD) row.open(raw[p0 + p], x[p], b[p]);
                     else row.load(((p0 + p) * G + t) * n, x[p], b[p]);
                 }
+                float part = 0.0f;  // 16 squares at most in a chain
 #pragma unroll
                 for (int p = 0; p < batch; ++p) {
-                    row.values(((p0 + p) * G + t) * n, x[p], b[p], ss);
+                    row.values(((p0 + p) * G + t) * n, x[p], b[p], part);
 #pragma unroll
                     for (int j = 0; j < n; j += 2) own = max_magnitude(own, x[p][j], x[p][j + 1]);
 #pragma unroll
                     for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j];
                 }
+                ss += part;
             }
             if constexpr (AHEAD) {
                 if (r + gridDim.x < a.rows) {

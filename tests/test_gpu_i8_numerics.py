@@ -107,3 +107,21 @@ def test_norm_products_whose_second_part_is_below_f32(B, k):
     B.llama_q8_norm_quant(0, torch.from_numpy(rows).cuda(), k, None, 0, None, 0, torch.from_numpy(g).cuda(), 0.0, 5, k,
                           codes, scale)
     _check(codes, scale, 5, I.norm_quant(rows, g, 0.0), 20 * U)
+
+
+def test_norm_scale_of_a_sum_that_loses_every_small_square(B):
+    """One thread has a large square and then small ones, each a little under half a step of the sum, which an addition to it
+    drops; so do the additions of lanes and of warps. 30 additions deep a scale is off by 20 * 2^-24 at most."""
+    k, tiny = 13952, 2.0 ** -12 * (1 - 2.0 ** -10)
+    x = np.zeros((8, 448, 4), np.float32)  # pieces of four values, dealt over 448 threads
+    x[:, 0, :] = tiny
+    x[0, 0, 0] = 1.0
+    x[0, [1, 2, 4, 8, 16], 0] = tiny
+    x[0, [32, 64, 128, 256], 0] = tiny
+    x = x.reshape(1, -1)[:, :k]
+    g = np.ones(k, np.float32)
+    g[0] = 1.25
+    codes, scale = _outputs(1, k)
+    B.llama_q8_norm_quant(0, torch.from_numpy(x).cuda(), k, None, 0, None, 0, torch.from_numpy(g).cuda(), 0.0, 1, k, codes,
+                          scale)
+    _check(codes, scale, 1, I.norm_quant(x, g, 0.0), 20 * U)
