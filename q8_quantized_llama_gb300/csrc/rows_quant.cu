@@ -749,8 +749,13 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
             }
         }
         if (t == 0) {  // a norm's M is the exact maximum rounded
-            const float top = OP == QUANT_SILU ? max_of_key(sh.exact, near).hi : M;
-            a.scale[r] = __fdiv_rn(top, OP == QUANT_NORM ? 127.0f * __fsqrt_rn(ss / (float)k + a.eps) : 127.0f);
+            if constexpr (OP == QUANT_SILU) {  // both parts, rounded once
+                const Two top = max_of_key(sh.exact, near);
+                const float q = __fdiv_rn(top.hi, 127.0f);
+                a.scale[r] = fmaf(fmaf(-q, 127.0f, top.hi) + top.lo, 1.0f / 127.0f, q);
+            } else {
+                a.scale[r] = __fdiv_rn(M, OP == QUANT_NORM ? 127.0f * __fsqrt_rn(ss / (float)k + a.eps) : 127.0f);
+            }
         }
         if (!AHEAD || (r += gridDim.x) >= a.rows) return;
     }

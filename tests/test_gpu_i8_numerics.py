@@ -125,3 +125,21 @@ def test_norm_scale_of_a_sum_that_loses_every_small_square(B):
     B.llama_q8_norm_quant(0, torch.from_numpy(x).cuda(), k, None, 0, None, 0, torch.from_numpy(g).cuda(), 0.0, 1, k, codes,
                           scale)
     _check(codes, scale, 1, I.norm_quant(x, g, 0.0), 20 * U)
+
+
+@pytest.mark.parametrize("kind", sorted(TYPES))
+@pytest.mark.parametrize("k", [9, 700, 17000])
+def test_silu_scale_is_rounded_once(B, kind, k):
+    """M / 127, M known to 2^-40, rounded to f32: off by half a step, and by that 2^-40 where it decides."""
+    dtype = TYPES[kind][1]
+    gen = torch.Generator(device="cuda").manual_seed(k)
+    rows = 400 if k < 1000 else 30
+    gate = (torch.randn((rows, k), generator=gen, device="cuda") * 3).to(dtype)
+    up = torch.randn((rows, k), generator=gen, device="cuda").to(dtype)
+    codes, scale = _outputs(rows, k)
+    B.llama_q8_silu_quant(TYPES[kind][0], gate, up, k, rows, k, codes, scale)
+    torch.cuda.synchronize()
+    want = np.abs(_silu(_host(gate)) * _host(up)).max(1) / 127
+    got = _host(scale[:rows])
+    step = np.spacing(want.astype(np.float32)).astype(np.float64)  # of the binade: a half step is at most U of the value
+    assert (np.abs(got - want) <= step * (0.5 + 2.0 ** -15)).all()
