@@ -200,15 +200,18 @@ __device__ __noinline__ double silu_up_f64(float gate, float up) {
 // The same in f32 for gate >= -80: exp(x) = 2^h (1 + r) with h = x / ln 2 rounded and r what the rounding left, in six
 // operations and two approximations (expf and a division take 12 more instructions per element). Off by 6.6 * 2^-24 of itself
 // at most for any gate of -80 .. 80 (up = 1; measured over all f32 numbers of 1e-9 and more, against double), and by one
-// product's rounding. up comes before gate: gate times the quotient loses bits where gate lies next to the subnormal range, and an
-// up of 1e20 brings what is left back among the row's numbers. The quotient times up is that small only where the whole is
-// far below a row's smallest code, or the quotient is 1.
-__device__ __forceinline__ float silu_up(float gate, float up) {
+// product's rounding. gate and the quotient alone do not make the first product: it would lose bits where gate lies next to the
+// subnormal range, which an up of 1e20 brings back among the row's numbers. Gate times up does so only where all of v is
+// far below a row's smallest code (or leaves the range above, and the row goes through double), and so does the quotient
+// times up, unless the quotient is 1. 16-bit types have the better time with the first order (2048 x 14336 bf16 42.6 us,
+// 45.8 with the second), f32 with the second (61.4 us, 64.5).
+template <typename T> __device__ __forceinline__ float silu_up(float gate, float up) {
     const float h = gate * -1.442695041f, r = fmaf(-h, 0.6931471806f, -gate);
     float e, q;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
     e = fmaf(e, r, e);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+    if constexpr (sizeof(T) == 2) return gate * up * q;
     return gate * (q * up);
 }
 
@@ -228,15 +231,12 @@ __device__ __forceinline__ Two two_prod(float a, float b) {
     const float p = a * b;
     return {p, fmaf(a, b, -p)};
 }
-__device__ __forceinline__ Two two_of(double v) {
-    const float hi = (float)v;
-    return {hi, (float)(v - (double)hi)};
-}
 
-// silu(gate) up to about 2^-40 of itself, for gate >= -80 and |gate| >= 2^-100 (below, the division's remainder falls under the
-// smallest f32), by the range reduction of Cody and Waite: exp(x) = 2^n exp(r) with x = n ln 2 + r, ln 2 in three
-// parts of which n times the first is exact; exp(r), |r| <= ln 2 / 2, by its Taylor series to r^11 (what is left out is
-// below 2^-47), the terms up to r^5 in two parts.
+// silu(gate) up to about 2^-40 of itself, for the elements that a row's maximum and codes are settled by (of 2^-101 and more):
+// exp(x) = 2^n exp(r) with x = n ln 2 + r, ln 2 in three parts of which n times the first is exact (the range reduction of
+// Cody and Waite); exp(r), |r| <= ln 2 / 2, by its Taylor series to r^11 (what is left out is below 2^-47), the terms up to
+// r^5 in two parts. Powers of two go from one factor to the other where a quotient's remainder would fall under the smallest f32:
+// 2^n of a far gate (1 beside it is nothing) and 2^64 of a tiny one. An up that brings such a gate back is large.
 __device__ __noinline__ Two silu_up_two(float gate, float up) {
     const float x = -gate;
     Two y = {1.0f, 0.0f};  // 1 + exp(x)
@@ -262,10 +262,16 @@ __device__ __noinline__ Two silu_up_two(float gate, float up) {
             const Two t = two_sum(c[i].hi, m.hi);
             s = two_renorm(t.hi, t.lo + (c[i].lo + m.lo));
         }
-        const float scale = pow2f((int)n);
-        y = two_sum(1.0f, s.hi * scale);
-        y = two_renorm(y.hi, y.lo + s.lo * scale);
+        if (n < 60.0f) {
+            const float scale = pow2f((int)n);
+            y = two_sum(1.0f, s.hi * scale);
+            y = two_renorm(y.hi, y.lo + s.lo * scale);
+        } else {
+            const int half = (int)n >> 1;
+            y = s, up = up * pow2f(-half) * pow2f(half - (int)n);
+        }
     }
+    if (fabsf(gate) < 0x1p-100f) gate *= 0x1p64f, up *= 0x1p-64f;
     const float q0 = __fdiv_rn(gate, y.hi);
     const float q1 = __fdiv_rn(fmaf(-q0, y.lo, fmaf(-q0, y.hi, gate)), y.hi);
     const Two v = two_prod(q0, up);
@@ -306,7 +312,7 @@ template <int OP, typename T, bool ALIGNED> struct Row {
                 for (int j = 0; j < n; ++j) x[j] = (float)silu_up_f64(x[j], b[j]);
             } else {
 #pragma unroll
-                for (int j = 0; j < n; ++j) x[j] = silu_up(x[j], b[j]);
+                for (int j = 0; j < n; ++j) x[j] = silu_up<T>(x[j], b[j]);
             }
         } else if constexpr (OP == QUANT_NORM) {
             if constexpr (ALIGNED && sizeof(T) == 2) {
@@ -382,9 +388,7 @@ template <int OP, typename T, bool ALIGNED> struct Row {
     // v of element i in two parts
     __device__ __forceinline__ Two v_two(int i) const {
         if constexpr (OP == QUANT_SILU) {
-            const float gate = load_one<T>(a.x, xa, i), up = load_one<T>(a.b, ba, i);
-            if (gate < -80.0f || fabsf(gate) < 0x1p-100f) return two_of(silu_up_f64(gate, up));  // out of its range
-            return silu_up_two(gate, up);
+            return silu_up_two(load_one<T>(a.x, xa, i), load_one<T>(a.b, ba, i));
         }
         if constexpr (OP == QUANT_NORM) return two_prod(h_again(i), a.g[i]);
         return {load_one<T>(a.x, xa, i), 0.0f};
@@ -573,7 +577,8 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
                     if constexpr (AHEAD) row.open(raw[p0 + p], x[p], b[p]);
                     else row.load(((p0 + p) * G + t) * n, x[p], b[p]);
                 }
-                float part = 0.0f;  // 16 squares at most in a chain
+                // 16 squares at most in a chain (a sum beside ss where one batch is all: 8195 x 14336 bf16 133 -> 143 us)
+                float batch_ss = 0.0f, &part = batch == pieces ? ss : batch_ss;
 #pragma unroll
                 for (int p = 0; p < batch; ++p) {
                     row.values(((p0 + p) * G + t) * n, x[p], b[p], part);
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(threads == 32 ? 128 : threads, threads == 32 ?
 #pragma unroll
                     for (int j = 0; j < n; ++j) v[(p0 + p) * n + j] = x[p][j];
                 }
-                ss += part;
+                if constexpr (batch != pieces) ss += part;
             }
             if constexpr (AHEAD) {
                 if (r + gridDim.x < a.rows) {
