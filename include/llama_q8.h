@@ -712,9 +712,9 @@ llama_q8_status llama_q8_rows_quant(int32_t type, const void* x, int64_t x_strid
 /* The residual's addition, RMSNorm, and codes with a scale for each row: h = x + delta
  * (added in f32, rounded to the type; delta NULL: h = x), stored to x_out unless that is
  * NULL, y = h g / sqrt(mean(h^2) + eps) with f32 g[k], and codes and scale of y by the
- * rule of llama_q8_rows_quant (y itself is not rounded: the codes depend on h g alone, and
- * the scale is rounded to f32 at the end; the sum of squares is kept in f32, in double where
- * that would leave the range of f32). x_out may be x or delta (with the same stride); no
+ * rule of llama_q8_rows_quant (y itself is not rounded: the codes depend on h g alone and are
+ * those of exact arithmetic; the scale lies within 20 * 2^-24 of the exact one, as the largest
+ * h g, the sum of squares and the root are f32, or double where they would leave its range). x_out may be x or delta (with the same stride); no
  * other arrays overlap. A row whose h or h g is not finite has codes 0 and scale NaN; eps >=
  * 0 and finite. Enqueues one kernel. */
 llama_q8_status llama_q8_norm_quant(int32_t type, const void* x, int64_t x_stride, const void* delta,
@@ -722,10 +722,12 @@ llama_q8_status llama_q8_norm_quant(int32_t type, const void* x, int64_t x_strid
                                     int32_t rows, int32_t k, int8_t* codes, float* scale, void* stream);
 
 /* Codes and a scale for each row of silu(gate) * up, silu(z) = z / (1 + exp(-z)), by the
- * rule of llama_q8_rows_quant. gate and up have the same row stride: columns 0 .. k - 1 and
- * k .. 2k - 1 of one product, or two arrays. A row with a NaN or an infinity in gate or up
- * has codes 0 and scale NaN. Products that lie within double precision of a half (those of one
- * gate and several ups can be halves exactly) go the way that their quotient in double goes.
+ * rule of llama_q8_rows_quant (M, known to 2^-40, is divided by 127 and rounded once). gate and
+ * up have the same row stride: columns 0 .. k - 1 and k .. 2k - 1 of one product, or two
+ * arrays. A row with a NaN or an infinity in gate or up has codes 0 and scale NaN. Products that
+ * lie within double precision of a half (those of one gate and several ups can be halves
+ * exactly) go the way that their quotient in double goes. Products of gates below -709, less
+ * than 2^-880 in magnitude, may count as 0.
  * Enqueues one kernel. */
 llama_q8_status llama_q8_silu_quant(int32_t type, const void* gate, const void* up, int64_t stride, int32_t rows,
                                     int32_t k, int8_t* codes, float* scale, void* stream);

@@ -21,7 +21,8 @@
 //
 // Bound: memory (norm of 8195 x 4096 f32 65 us, 6.7 TB/s), and with 16-bit types the
 // instructions (an element of rows takes 16, of norm 28, of silu 26 with its share of
-// the row's reductions) and the chain from a row's maximum to its last code. A warp,
+// the row's reductions; they fill half to two thirds of the issue slots) and the chain from
+// a row's maximum to its last code. A warp,
 // or a CTA with as many threads as the row has values for, keeps a row's v in registers
 // (16 values a thread, or 32, up to 14336), so every input is read once and
 // every output written once; at least two CTAs share an SM, so that one row's loads run

@@ -143,3 +143,16 @@ def test_silu_scale_is_rounded_once(B, kind, k):
     got = _host(scale[:rows])
     step = np.spacing(want.astype(np.float32)).astype(np.float64)  # of the binade: a half step is at most U of the value
     assert (np.abs(got - want) <= step * (0.5 + 2.0 ** -15)).all()
+
+
+def test_silu_products_below_any_scale(B):
+    """Gates so far down that no f32 scale holds their products: zeros, alone in a row or beside others."""
+    k = 40
+    gate, up = np.full((2, k), -1000.0, np.float32), np.full((2, k), 3e38, np.float32)
+    gate[0, ::3], gate[1, 5], up[1, 5] = -1e30, 2.0, 1.0
+    codes, scale = _outputs(2, k)
+    B.llama_q8_silu_quant(0, torch.from_numpy(gate).cuda(), torch.from_numpy(up).cuda(), k, 2, k, codes, scale)
+    torch.cuda.synchronize()
+    assert not codes[0].any() and float(scale[0]) == 0.0
+    assert int(codes[1, 5]) == 127 and int(codes[1].count_nonzero()) == 1
+    assert abs(float(scale[1]) * 127 / float(_silu(np.float32([2.0]))[0]) - 1) <= 1.001 * U
